@@ -13,6 +13,9 @@
  *   5. bf16      the forward-pass parameter is the nearest-even bf16 of the
  *                new master                                          (3-5: zero1_adamw_step)
  *   1-5 fused over a ragged per-tensor list: zero1_mta_plan + zero1_mta_step.
+ * Beside AdamW, for weight matrices that a rank owns whole: the Muon step
+ * (momentum, orthogonalisation by Newton-Schulz products, update), at the end
+ * of this header.
  *
  * Sources (web pages; section names as they appear on each page):
  *   "并行训练" (notes.cassieliang.com):
@@ -36,7 +39,8 @@
  *     surfaces at the caller's next synchronization.  Setting the environment
  *     variable ZERO1_SYNC_CHECK=1 makes each call synchronize and check (tests;
  *     on a stream under graph capture it checks the launches only).
- *   - Graph capture: apart from zero1_mta_plan (a synchronous table upload),
+ *   - Graph capture: apart from zero1_mta_plan and zero1_muon_plan (synchronous
+ *     table uploads),
  *     the entry points only launch kernels
  *     (no memset, copy or synchronization), so their work can be captured into
  *     a HIP graph.  The fp32 scalars derived from zero1_hparams -- the step t
@@ -71,7 +75,7 @@
 extern "C" {
 #endif
 
-#define ZERO1_ABI_VERSION 4
+#define ZERO1_ABI_VERSION 5
 #define ZERO1_MAX_W 128          /* largest number of replicas per call */
 
 typedef enum zero1_status {
@@ -453,6 +457,136 @@ typedef struct zero1_arena_layout {
 #define ZERO1_ARENA_SPACING ((size_t)40 << 30)   /* preferred spacing D */
 
 zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout* out);
+
+/* ---------------------------------------------------------------- Muon
+ * The Muon step on weight matrices that this rank owns whole (the embedding,
+ * the head, gains and biases take the AdamW step above).  Per matrix, with g
+ * the replicas' reduced gradient:
+ *   1. momentum       m = mu m + g;  u = g + mu m                (zero1_muon_momentum)
+ *   2. orthogonalise  X = u / (||u||_F + eps);  ns_steps times
+ *                     A = X X^T, B = b A + c A A, X = a X + B X;
+ *                     o = X                                      (zero1_orthogonalize)
+ *   3. update         p = (p - lr scale o) * (1 - lr weight_decay);
+ *                     param = bf16(p)                            (zero1_muon_update)
+ *   1-3 in one call: zero1_muon_step.
+ * A step maps every singular value s of X to a s + b s^3 + c s^5: the default
+ * coefficients bring those above about 0.002 into 0.68-1.2 in five steps, so
+ * o is close to U V^T of u = U S V^T.  (A tall u is iterated as its transpose:
+ * the result is the same.)
+ *
+ * Types: gradients bf16; m fp32 (bf16 with ZERO1_MV_BF16); u bf16 (fp32 with
+ * ZERO1_U_F32); o bf16; master fp32; param bf16.
+ * Arithmetic: momentum and update, like the AdamW step, one binary32 operation
+ * at a time (eta = fp32(lr) * scale is one of them).  The norm is fp64.  The
+ * products multiply fp16 operands on the matrix cores and add in fp32; X is
+ * held as two fp16 halves (22 bits), A and B as one.  o is within about 0.2 %
+ * (2-norm) of the iteration in 64 bits before its rounding to bf16; for single
+ * rows and other matrices of few singular values within about 0.5 %.  Results
+ * do not depend on the other matrices of the plan, and a rerun gives the same
+ * bits.
+ * Non-finite values: a matrix whose u holds an infinity or a NaN gets NaN in
+ * the whole of its o (as the formulas give); the other matrices do not. */
+
+/* Flags of the Muon entry points only. */
+#define ZERO1_U_F32        0x200u /* plan: u is fp32                                 */
+#define ZERO1_NO_NESTEROV  0x400u /* momentum: u = m                                 */
+
+/* One weight matrix.  A stride of 0 stands for cols.  Buffers that no call made
+ * with the plan uses may be NULL, for all its matrices alike: momentum uses m
+ * and u; orthogonalize u and o; update master, param_bf16 and o; step master,
+ * param_bf16, m and u. */
+typedef struct zero1_matrix {
+    int64_t rows, cols;     /* >= 1; the smaller at most 32768                  */
+    int64_t ld;             /* row stride (elements) of gradients, param, master, m */
+    int64_t shard_offset;   /* position of element (0, 0) inside the shard      */
+    float scale;            /* o's factor beside lr, e.g. sqrt(max(1, rows/cols)) or
+                               0.2 sqrt(max(rows, cols))                        */
+    uint16_t* param_bf16;   /* written                                          */
+    float* master;          /* read and written                                 */
+    void* m;                /* momentum, read and written; zero at first        */
+    void* u;                /* written by momentum, read by orthogonalize       */
+    int64_t ldu;            /* row stride of u                                  */
+    uint16_t* o;            /* written by orthogonalize, read by update; may be a
+                               bf16 u itself (same address and stride)          */
+    int64_t ldo;            /* row stride of o                                  */
+} zero1_matrix;
+
+/* A validated list of matrices uploaded by zero1_muon_plan.  Plain data owned
+ * by the caller; valid as long as the table memory is. */
+typedef struct zero1_matrix_plan {
+    void* table;
+    int64_t elems;          /* sum of rows * cols                               */
+    int64_t off_tiles, off_groups, off_list, area_bytes;
+    int32_t n_mats, n_tiles, n_groups, max_sym, max_full;
+    uint32_t flags;         /* ZERO1_MV_BF16, ZERO1_U_F32                       */
+    uint32_t has;           /* which buffers the matrices have                  */
+    int32_t device;         /* calls are made with this device current          */
+} zero1_matrix_plan;
+
+/* Hyper-parameters of one Muon step (host struct). */
+typedef struct zero1_muon_hparams {
+    double lr;              /* >= 0                                             */
+    double momentum;        /* in [0, 1)                                        */
+    double weight_decay;    /* >= 0                                             */
+    double max_norm;        /* > 0; read where rank_sumsq is given              */
+    double ns_a, ns_b, ns_c;/* coefficients, e.g. 3.4445, -4.7750, 2.0315       */
+    double ns_eps;          /* >= 0, added to the norm, e.g. 1e-7               */
+    int32_t ns_steps;       /* 1..64, e.g. 5                                    */
+    int32_t reserved;
+    const void* device_scalars; /* NULL, or a zero1_muon_scalars on the device (8-byte
+                               aligned), read when the kernels run in place of lr,
+                               momentum, weight_decay and max_norm              */
+} zero1_muon_hparams;
+
+/* The per-step values derived from zero1_muon_hparams, for a captured step's
+ * device_scalars.  24 bytes. */
+typedef struct zero1_muon_scalars {
+    float lr, momentum;
+    float decay;            /* fp32(1 - lr * weight_decay)                      */
+    float reserved;
+    double max_norm;
+} zero1_muon_scalars;
+
+zero1_status zero1_muon_scalars_derive(const zero1_muon_hparams* hp, zero1_muon_scalars* out);
+
+/* zero1_muon_table_bytes: device bytes of the plan's table, by the sizes and by
+ *   which buffers there are (0: rejected, see zero1_last_error).
+ * zero1_muon_plan: validates the matrices (sizes, strides, no two buffers
+ *   sharing an element; blocks of columns of one array are told apart by their
+ *   common stride) and copies the table into `table` (device, 256-byte
+ *   aligned).  Synchronous, once per list.  `flags`: ZERO1_MV_BF16, ZERO1_U_F32.
+ * zero1_muon_workspace_bytes: workspace of zero1_orthogonalize and
+ *   zero1_muon_step (256-byte aligned): the iteration's buffers of one group of
+ *   matrices at a time (about 512 MiB, or one matrix where it needs more) and
+ *   the norms.  Every byte is written before it is read.
+ * zero1_muon_momentum: grads, W, begin as for zero1_shard_reduce: element (i, j)
+ *   of a matrix has its gradients at grads[w][begin + shard_offset + i*ld + j].
+ *   flags: ZERO1_SUM_ONLY, ZERO1_G_BF16, ZERO1_CLIP_EPS, ZERO1_NO_NESTEROV.
+ *   rank_sumsq: n_ranks doubles as for zero1_adamw_step (g is clipped by the
+ *   global norm and info_out written), or NULL: no clipping (info_out NULL).
+ * zero1_orthogonalize: o from u.  ZERO1_EINVAL for coefficients that let
+ *   singular values grow beyond 3 or B's eigenvalues beyond 12 (the range of
+ *   the fp16 operands).
+ * zero1_muon_update: flags: ZERO1_DECAY_FIRST (p = p*decay - lr scale o).
+ * zero1_muon_step: the three together; o is not rounded to bf16 on its way to
+ *   the update and not written; u is. */
+size_t zero1_muon_table_bytes(const zero1_matrix* mats, int n_mats);
+zero1_status zero1_muon_plan(const zero1_matrix* mats, int n_mats, uint32_t flags,
+                             void* table, size_t table_bytes, zero1_matrix_plan* plan_out);
+size_t zero1_muon_workspace_bytes(const zero1_matrix_plan* plan);
+zero1_status zero1_muon_momentum(const uint16_t* const* grads, int W, int64_t begin,
+                                 const zero1_matrix_plan* plan, const zero1_muon_hparams* hp,
+                                 const double* rank_sumsq, int n_ranks, uint32_t flags,
+                                 zero1_norm_info* info_out, void* stream);
+zero1_status zero1_orthogonalize(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp,
+                                 uint32_t flags, void* ws, size_t ws_bytes, void* stream);
+zero1_status zero1_muon_update(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp,
+                               uint32_t flags, void* stream);
+zero1_status zero1_muon_step(const uint16_t* const* grads, int W, int64_t begin,
+                             const zero1_matrix_plan* plan, const zero1_muon_hparams* hp,
+                             const double* rank_sumsq, int n_ranks, uint32_t flags,
+                             zero1_norm_info* info_out, void* ws, size_t ws_bytes,
+                             void* stream);
 
 #ifdef __cplusplus
 }

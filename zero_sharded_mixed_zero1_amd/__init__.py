@@ -13,6 +13,8 @@ from .binding import (  # noqa: F401
     mta_table_bytes, mta_plan, mta_workspace_bytes, mta_reduce, mta_update, mta_design, mta_step,
     mta_step_static, mta_reduce_range, partials_sum,
     arena_plan, step_scalars_derive, time_next_launch,
+    Matrix, MatrixPlan, MuonHParams, MuonScalars, U_F32, NO_NESTEROV, matrix, muon_scalars_derive,
+    muon_table_bytes, muon_plan, muon_workspace_bytes, muon_momentum, orthogonalize, muon_update, muon_step,
     lib, lib_path,
 )
 from .layout import shard_pieces  # noqa: F401

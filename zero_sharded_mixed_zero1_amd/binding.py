@@ -22,11 +22,13 @@ STORE_G = 0x8
 DECAY_FIRST = 0x20
 CLIP_EPS = 0x40
 G_BF16 = 0x80
+U_F32 = 0x200
+NO_NESTEROV = 0x400
 MAX_W = 128
 STATIC_MAX_G_ELEMS = 16777216
 # the layout of the structures below and the signatures set in lib(); a
 # library that reports another ZERO1_ABI_VERSION is refused at load time
-ABI_VERSION = 4
+ABI_VERSION = 5
 
 P = ctypes.c_void_p
 i64 = ctypes.c_int64
@@ -84,6 +86,30 @@ class ArenaLayout(ctypes.Structure):
                 ("ws", ctypes.c_size_t), ("ws_bytes", ctypes.c_size_t),
                 ("master", ctypes.c_size_t), ("m", ctypes.c_size_t), ("v", ctypes.c_size_t),
                 ("params", ctypes.c_size_t), ("grads", ctypes.c_size_t * 128)]
+
+
+class Matrix(ctypes.Structure):
+    _fields_ = [("rows", i64), ("cols", i64), ("ld", i64), ("shard_offset", i64), ("scale", ctypes.c_float),
+                ("param_bf16", P), ("master", P), ("m", P), ("u", P), ("ldu", i64), ("o", P), ("ldo", i64)]
+
+
+class MatrixPlan(ctypes.Structure):
+    _fields_ = [("table", P), ("elems", i64), ("off_tiles", i64), ("off_groups", i64), ("off_list", i64),
+                ("area_bytes", i64), ("n_mats", ctypes.c_int32), ("n_tiles", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("max_sym", ctypes.c_int32), ("max_full", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("has", ctypes.c_uint32), ("device", ctypes.c_int32)]
+
+
+class MuonHParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("ns_a", ctypes.c_double), ("ns_b", ctypes.c_double),
+                ("ns_c", ctypes.c_double), ("ns_eps", ctypes.c_double), ("ns_steps", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("device_scalars", P)]
+
+
+class MuonScalars(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("decay", ctypes.c_float),
+                ("reserved", ctypes.c_float), ("max_norm", ctypes.c_double)]
 
 
 _lib = None
@@ -155,6 +181,24 @@ def lib():
         L.zero1_arena_plan.restype = i32
         L.zero1_time_next_launch.argtypes = [P, P]
         L.zero1_time_next_launch.restype = i32
+        L.zero1_muon_scalars_derive.argtypes = [ctypes.POINTER(MuonHParams), ctypes.POINTER(MuonScalars)]
+        L.zero1_muon_scalars_derive.restype = i32
+        L.zero1_muon_table_bytes.argtypes = [ctypes.POINTER(Matrix), i32]
+        L.zero1_muon_table_bytes.restype = szt
+        L.zero1_muon_plan.argtypes = [ctypes.POINTER(Matrix), i32, u32, P, szt, ctypes.POINTER(MatrixPlan)]
+        L.zero1_muon_plan.restype = i32
+        L.zero1_muon_workspace_bytes.argtypes = [ctypes.POINTER(MatrixPlan)]
+        L.zero1_muon_workspace_bytes.restype = szt
+        L.zero1_muon_momentum.argtypes = [P, i32, i64, ctypes.POINTER(MatrixPlan), ctypes.POINTER(MuonHParams),
+                                          P, i32, u32, P, P]
+        L.zero1_muon_momentum.restype = i32
+        L.zero1_orthogonalize.argtypes = [ctypes.POINTER(MatrixPlan), ctypes.POINTER(MuonHParams), u32, P, szt, P]
+        L.zero1_orthogonalize.restype = i32
+        L.zero1_muon_update.argtypes = [ctypes.POINTER(MatrixPlan), ctypes.POINTER(MuonHParams), u32, P]
+        L.zero1_muon_update.restype = i32
+        L.zero1_muon_step.argtypes = [P, i32, i64, ctypes.POINTER(MatrixPlan), ctypes.POINTER(MuonHParams),
+                                      P, i32, u32, P, P, szt, P]
+        L.zero1_muon_step.restype = i32
         _lib = L
     return _lib
 
@@ -385,3 +429,101 @@ def time_next_launch(start=None, stop=None):
     (zero1_time_next_launch): start.elapsed_time(stop) is that kernel's own
     duration.  Events need enable_timing=True."""
     _check(lib().zero1_time_next_launch(_event(start), _event(stop)))
+
+
+# ------------------------------------------------------------------ Muon
+def matrix(rows: int, cols: int, ld: int = 0, shard_offset: int = 0, scale: float = 1.0, param=None, master=None,
+           m=None, u=None, ldu: int = 0, o=None, ldo: int = 0) -> Matrix:
+    """One weight matrix of a Muon plan (zero1_matrix); buffers are tensors or
+    device addresses of element (0, 0), strides of 0 stand for cols."""
+    return Matrix(rows, cols, ld, shard_offset, scale, _addr(param), _addr(master), _addr(m), _addr(u), ldu,
+                  _addr(o), ldo)
+
+
+def _matrices(mats):
+    if isinstance(mats, ctypes.Array):
+        return mats
+    arr = (Matrix * len(mats))()
+    for k, q in enumerate(mats):
+        arr[k] = q
+    return arr
+
+
+def _muon_hp(hp) -> MuonHParams:
+    """From a MuonHParams, or a dict with lr, momentum, weight_decay and
+    optionally max_norm (inf), ns_steps (5), ns_a, ns_b, ns_c (3.4445, -4.7750,
+    2.0315), ns_eps (1e-7) and device_scalars (a device address or tensor
+    holding a MuonScalars; lr, momentum, weight_decay and max_norm are then
+    not read)."""
+    if isinstance(hp, MuonHParams):
+        return hp
+    dev = hp.get("device_scalars")
+    h = MuonHParams(0.0, 0.0, 0.0, float("inf"), hp.get("ns_a", 3.4445), hp.get("ns_b", -4.7750),
+                    hp.get("ns_c", 2.0315), hp.get("ns_eps", 1e-7), int(hp.get("ns_steps", 5)), 0, None)
+    if dev is not None:
+        h.device_scalars = _addr(dev)
+    else:
+        h.lr, h.momentum, h.weight_decay = hp["lr"], hp["momentum"], hp["weight_decay"]
+        h.max_norm = hp.get("max_norm", float("inf"))
+    return h
+
+
+def muon_scalars_derive(hp) -> MuonScalars:
+    """The per-step scalars the Muon calls derive from hp (zero1_muon_scalars_derive)."""
+    out = MuonScalars()
+    h = _muon_hp(hp)
+    _check(lib().zero1_muon_scalars_derive(ctypes.byref(h), ctypes.byref(out)))
+    return out
+
+
+def muon_table_bytes(mats) -> int:
+    arr = _matrices(mats)
+    n = lib().zero1_muon_table_bytes(arr, len(arr))
+    if n == 0:
+        raise Zero1Error(1, "ZERO1_EINVAL", last_error())
+    return n
+
+
+def muon_plan(mats, table, table_bytes=None, flags: int = 0) -> MatrixPlan:
+    """mats: Matrix structs (see matrix())."""
+    arr = _matrices(mats)
+    plan = MatrixPlan()
+    t, tb = _ws(table, table_bytes)
+    _check(lib().zero1_muon_plan(arr, len(arr), flags, t, tb, ctypes.byref(plan)))
+    return plan
+
+
+def muon_workspace_bytes(plan: MatrixPlan) -> int:
+    return lib().zero1_muon_workspace_bytes(ctypes.byref(plan))
+
+
+def muon_momentum(grads, begin: int, plan: MatrixPlan, hp, rank_sumsq=None, n_ranks: int = 0, flags: int = 0,
+                  info_out=None, stream=None):
+    """m = mu m + g, u = g + mu m over the plan's matrices (zero1_muon_momentum)."""
+    arr = _ptrs(grads)
+    h = _muon_hp(hp)
+    _check(lib().zero1_muon_momentum(ctypes.cast(arr, P), len(grads), begin, ctypes.byref(plan), ctypes.byref(h),
+                                     _addr(rank_sumsq), n_ranks, flags, _addr(info_out), _stream(stream)))
+
+
+def orthogonalize(plan: MatrixPlan, hp, flags: int = 0, ws=None, ws_bytes=None, stream=None):
+    """o from u by Newton-Schulz products (zero1_orthogonalize)."""
+    w, wb = _ws(ws, ws_bytes)
+    h = _muon_hp(hp)
+    _check(lib().zero1_orthogonalize(ctypes.byref(plan), ctypes.byref(h), flags, w, wb, _stream(stream)))
+
+
+def muon_update(plan: MatrixPlan, hp, flags: int = 0, stream=None):
+    """master and the bf16 parameter from o (zero1_muon_update)."""
+    h = _muon_hp(hp)
+    _check(lib().zero1_muon_update(ctypes.byref(plan), ctypes.byref(h), flags, _stream(stream)))
+
+
+def muon_step(grads, begin: int, plan: MatrixPlan, hp, rank_sumsq=None, n_ranks: int = 0, flags: int = 0,
+              info_out=None, ws=None, ws_bytes=None, stream=None):
+    """momentum, orthogonalisation and update in one call (zero1_muon_step)."""
+    arr = _ptrs(grads)
+    w, wb = _ws(ws, ws_bytes)
+    h = _muon_hp(hp)
+    _check(lib().zero1_muon_step(ctypes.cast(arr, P), len(grads), begin, ctypes.byref(plan), ctypes.byref(h),
+                                 _addr(rank_sumsq), n_ranks, flags, _addr(info_out), w, wb, _stream(stream)))

@@ -1,0 +1,175 @@
+// muon.h -- declarations shared by the Muon entry points' host code
+// (muon_api.cpp) and kernels (muon.hip, newton_schulz.hip).  Not part of the
+// public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace z1 {
+
+// Streaming kernels (momentum, update, sum of squares): a workgroup's tile is
+// 512 quads, a quad being up to four neighbouring elements of one row.
+constexpr int kQuadsPerTile = 512;
+// Side of the square tiles that the products' operands are padded to.
+constexpr int kPad = 128;
+// Power of two that X, A and B carry in fp16 (see newton_schulz.hip).
+constexpr float kNsScale = 4096.0f;
+
+// One matrix.  "x" is the matrix the iteration works on: u, or u transposed
+// when u is tall, so that k = min(rows, cols) rows of n = max(rows, cols).
+struct MatDesc {
+    int64_t rows, cols, ld, shard_offset, ldu, ldo;
+    uint16_t* param;
+    float* master;
+    void* m;
+    void* u;
+    uint16_t* o;
+    float scale;
+    int32_t tall;
+    int32_t k, n, kp, np;          // kp, np: k, n rounded up to kPad
+    // the streaming kernels' view: vrows rows of vcols elements, qpr quads each
+    // (one row when the matrix and its u and o are contiguous)
+    int64_t vcols, qpr;
+    int32_t vrows;
+    int32_t tile0, n_tiles;        // its streaming tiles
+    int32_t reserved;
+    // byte offsets inside the workspace's group area
+    int64_t x[2], lo, a, b;
+};
+static_assert(sizeof(MatDesc) == 184, "matrix descriptor layout");
+
+// A streaming tile: quads [512 idx, +512) of matrix `mat`, the first of them
+// quad q0 of row row0.
+struct StreamTile {
+    int32_t mat, idx, row0, q0;
+};
+
+// A tile of one matrix's product: block row i, block column j.
+struct ProdTile {
+    int32_t mat, i, j, reserved;
+};
+
+// Matrices that are iterated together, and their tiles in the list of
+// ProdTiles: A and B (upper triangle), X (all).
+struct GroupDesc {
+    int64_t sym0, full0;
+    int32_t n_sym, n_full;
+    int64_t reserved;
+};
+
+// Norm of one matrix's u as the iteration uses it: S / (norm + eps) = 2^e r
+// with r in [1, 2); r is NaN when the quotient is not finite.
+struct NormRec {
+    float r;
+    int32_t e;
+};
+
+// Per-step scalars (zero1_muon_scalars).
+struct MuonScal {
+    float lr, mu, delta, reserved;
+    double max_norm;
+};
+
+struct MuonArgs {
+    float lr, mu, delta;
+    const MuonScal* dev;           // non-null: read lr, mu, delta, max_norm from here
+    int decay_first;
+};
+
+// Clip prologue; rank_sumsq null: no clipping.
+struct MuonClip {
+    const double* rank_sumsq;
+    int n_ranks;
+    double max_norm;
+    int clip_eps;
+    NormInfo* info_out;
+};
+
+struct NsArgs {
+    const MatDesc* mats;
+    const GroupDesc* groups;
+    const ProdTile* list;
+    int group;
+    char* area;                    // the workspace's group area
+    const NormRec* norms;
+    float a, b, c;
+};
+
+enum NsLast : int { kNsMid = 0, kNsWriteO = 1, kNsUpdate = 2 };
+
+hipError_t launch_momentum(const Reduce& r, const MatDesc* mats, const StreamTile* tiles, int n_tiles, bool m_bf16,
+                           bool u_f32, bool nesterov, const MuonArgs& ma, const MuonClip& mc, double* partials,
+                           int nblocks, int split, hipStream_t s);
+hipError_t launch_u_sumsq(const MatDesc* mats, const StreamTile* tiles, int n_tiles, bool u_f32, double* partials,
+                          int nblocks, int split, hipStream_t s);
+hipError_t launch_ns_norms(const MatDesc* mats, int n_mats, const double* partials, double eps, NormRec* norms,
+                           hipStream_t s);
+hipError_t launch_muon_update(const MatDesc* mats, const StreamTile* tiles, int n_tiles, const MuonArgs& ma,
+                              int nblocks, int split, hipStream_t s);
+
+hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, int grid, hipStream_t s);
+hipError_t launch_ns_gram(const NsArgs& g, int it, int grid, hipStream_t s);
+hipError_t launch_ns_poly(const NsArgs& g, int grid, hipStream_t s);
+hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, int grid,
+                           hipStream_t s);
+
+#ifdef __HIPCC__
+// ------------------------------------------------------------------ device
+namespace dev {
+
+template <typename T>
+using gptr = __attribute__((address_space(1))) T*;
+
+// Vectors of four elements at any element's address: rows of an odd stride
+// start anywhere, and gfx950 loads and stores them whole all the same.
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef u16x4 u16x4u __attribute__((aligned(2)));
+typedef f32x4 f32x4u __attribute__((aligned(4)));
+
+__device__ __forceinline__ u16x4 ld4(const uint16_t* p)
+{
+    return __builtin_nontemporal_load((gptr<const u16x4u>)p);
+}
+__device__ __forceinline__ f32x4 ld4(const float* p) { return __builtin_nontemporal_load((gptr<const f32x4u>)p); }
+__device__ __forceinline__ void st4(uint16_t* p, u16x4 v) { __builtin_nontemporal_store(v, (gptr<u16x4u>)p); }
+__device__ __forceinline__ void st4(float* p, f32x4 v) { __builtin_nontemporal_store(v, (gptr<f32x4u>)p); }
+
+__device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+// Nearest-even bf16; NaNs stay quiet NaNs with their sign.
+__device__ __forceinline__ uint16_t bf16_rne(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    return (uint16_t)(((u & 0x7fffffffu) > 0x7f800000u) ? ((u >> 16) | 0x40u) : r);
+}
+
+__device__ __forceinline__ void use_device_scalars(MuonArgs& a, double* max_norm)
+{
+    if (a.dev) {
+        const MuonScal d = *a.dev;
+        a.lr = d.lr;
+        a.mu = d.mu;
+        a.delta = d.delta;
+        if (max_norm) *max_norm = d.max_norm;
+    }
+}
+
+// p moves by eta*o and is multiplied by the decay factor (decay_first swaps
+// the two); eta = lr * the matrix's scale.
+__device__ __forceinline__ float muon_elem(float p, float o, float eta, const MuonArgs& a)
+{
+#pragma clang fp contract(off)
+    if (a.decay_first) return p * a.delta - eta * o;
+    return (p - eta * o) * a.delta;
+}
+
+}  // namespace dev
+#endif
+
+}  // namespace z1

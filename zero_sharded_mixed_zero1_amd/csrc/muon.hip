@@ -1,0 +1,364 @@
+// muon.hip -- the streaming kernels of the Muon step on gfx950: momentum over
+// the W replicas' gradients, the sum of squares of u, and the update of the
+// master with the bf16 parameter.
+//
+// All are HBM-bound (under one flop per byte).  A workgroup takes a tile of
+// 512 quads (2048 elements) of one matrix; lane l handles quads l and 256 + l,
+// so a wave's load covers one contiguous run of a row.  A quad is up to four
+// neighbouring elements of one row: rows may start at any element (odd column
+// counts, blocks cut out of wider matrices), because gfx950's vector loads and
+// stores need no more than the element's alignment, and only the last quad of
+// a row is taken element by element.  Matrices that are contiguous in all
+// their arrays are one long row.
+//
+// Arithmetic: one binary32 operation at a time (no contraction), gradients
+// summed in rank order as the reduce of the AdamW step does; sums of squares
+// in fp64 over a fixed tree, so a rerun gives the same bits.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "muon.h"
+
+#pragma clang fp contract(off)
+
+namespace z1 {
+namespace {
+
+using namespace dev;
+
+// Tiles [lo, hi) with a stride for this workgroup; split = 8 gives each XCD
+// (workgroup b runs on XCD b % 8) one contiguous eighth.
+struct Walk {
+    int64_t lo, hi, step;
+};
+
+__device__ __forceinline__ Walk walk(int64_t n, int split)
+{
+    const int64_t G = gridDim.x, b = blockIdx.x;
+    const int64_t nx = (split > 1 && G % split == 0) ? split : 1;
+    const int64_t per = (n + nx - 1) / nx, lo = (b % nx) * per;
+    return Walk{lo + b / nx, lo + per < n ? lo + per : n, G / nx};
+}
+
+// A lane's quad: its row and first column, and how many elements it has.
+struct Quad {
+    int64_t row, col;
+    int n;
+};
+
+__device__ __forceinline__ Quad quad_at(const MatDesc& d, const StreamTile& t, int lane_quad)
+{
+    Quad q;
+    if (d.vrows == 1) {
+        q.row = 0;
+        q.col = 4 * ((int64_t)t.idx * kQuadsPerTile + lane_quad);
+    } else {   // qpr < 2^30 (cols < 2^31), so 32-bit division
+        const uint32_t x = (uint32_t)t.q0 + (uint32_t)lane_quad, per = (uint32_t)d.qpr;
+        const uint32_t r = x / per;
+        q.row = (int64_t)t.row0 + r;
+        q.col = 4 * (int64_t)(x - r * per);
+    }
+    const int64_t left = d.vcols - q.col;
+    q.n = q.row < d.vrows ? (left >= 4 ? 4 : (left > 0 ? (int)left : 0)) : 0;
+    return q;
+}
+
+// Loads and stores of a quad's n elements; four at once when all are there.
+__device__ __forceinline__ void load_quad(const uint16_t* p, int n, float (&x)[4])
+{
+    if (n == 4) {
+        const u16x4 v = ld4(p);
+        x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = j < n ? widen(p[j]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void load_quad(const float* p, int n, float (&x)[4])
+{
+    if (n == 4) {
+        const f32x4 v = ld4(p);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = j < n ? p[j] : 0.0f;
+    }
+}
+
+// Stores in the array's type; x becomes the values as stored.
+__device__ __forceinline__ void store_quad(uint16_t* p, int n, float (&x)[4])
+{
+    u16x4 v;
+    v.x = bf16_rne(x[0]); v.y = bf16_rne(x[1]); v.z = bf16_rne(x[2]); v.w = bf16_rne(x[3]);
+    x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
+    if (n == 4) {
+        st4(p, v);
+    } else {
+        if (n > 0) p[0] = v.x;
+        if (n > 1) p[1] = v.y;
+        if (n > 2) p[2] = v.z;
+    }
+}
+
+__device__ __forceinline__ void store_quad(float* p, int n, float (&x)[4])
+{
+    if (n == 4) {
+        st4(p, f32x4{x[0], x[1], x[2], x[3]});
+    } else {
+        if (n > 0) p[0] = x[0];
+        if (n > 1) p[1] = x[1];
+        if (n > 2) p[2] = x[2];
+    }
+}
+
+// Fixed-order workgroup sum; the total is in thread 0.  `sh` alternates
+// between two buffers from tile to tile, so one barrier a tile is enough.
+__device__ __forceinline__ double tile_sum(double x, double* sh)
+{
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return ((sh[0] + sh[1]) + sh[2]) + sh[3];
+}
+
+// The reduced gradient of the lane's two quads: slices added in rank order,
+// the loads of up to four slices in flight together; then the average.
+__device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at)[2], const int (&n)[2],
+                                             float (&g)[2][4])
+{
+    for (int w0 = 0; w0 < r.W; w0 += 4) {
+        float x[4][2][4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (w0 + w < r.W) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) load_quad(r.gp.p[w0 + w] + at[h], n[h], x[w][h]);
+            }
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (w0 + w < r.W) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) g[h][j] = (w0 + w == 0) ? x[w][h][j] : g[h][j] + x[w][h][j];
+            }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float v = g[h][j];
+            if (r.mode == kAvgMulPow2) v = v * r.inv_w;
+            else if (r.mode == kAvgDiv) v = v / r.f_w;
+            if (r.round_bf16) v = widen(bf16_rne(v));
+            g[h][j] = v;
+        }
+}
+
+// m = mu m + g; u = g + mu m (Nesterov) or m.  Moves 2W + 2 sizeof(m) +
+// sizeof(u) bytes an element.
+template <typename M, typename U, bool NORM>
+__global__ __launch_bounds__(kThreads) void momentum_kernel(Reduce r, const MatDesc* __restrict__ mats,
+                                                            const StreamTile* __restrict__ tiles, int n_tiles,
+                                                            int nesterov, MuonArgs ma, MuonClip mc,
+                                                            double* __restrict__ partials, int split)
+{
+    __shared__ NormInfo ni;
+    __shared__ double sums[2][kThreads / 64];
+    use_device_scalars(ma, &mc.max_norm);
+    bool clip = false;
+    float coef = 1.0f;
+    if (mc.rank_sumsq) {   // the clip decision, as the AdamW update forms it
+        if (threadIdx.x == 0) {
+            double tot = 0.0;
+            for (int q = 0; q < mc.n_ranks; ++q) tot = tot + mc.rank_sumsq[q];
+            const double norm = sqrt(tot);
+            const double c = mc.clip_eps ? mc.max_norm / (norm + 1e-6) : mc.max_norm / norm;
+            const bool cl = mc.clip_eps ? (c < 1.0) : (norm > mc.max_norm);
+            ni = NormInfo{tot, norm, cl ? (float)c : 1.0f, cl ? 1 : 0, (isnan(norm) || isinf(norm)) ? 1 : 0, 0};
+            if (blockIdx.x == 0 && mc.info_out) *mc.info_out = ni;
+        }
+        __syncthreads();
+        clip = ni.clip != 0;
+        coef = ni.clip_coef;
+    }
+    const Walk wk = walk(n_tiles, split);
+    int buf = 0;
+    for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
+        const StreamTile tile = tiles[t];
+        const MatDesc& d = mats[tile.mat];
+        Quad q[2];
+        int64_t at[2];
+        int n[2];
+        float g[2][4], m[2][4], u[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            q[h] = quad_at(d, tile, (int)threadIdx.x + h * kThreads);
+            n[h] = q[h].n;
+            at[h] = q[h].row * d.ld + q[h].col;
+            load_quad(static_cast<const M*>(d.m) + at[h], n[h], m[h]);
+        }
+        const int64_t ga[2] = {d.shard_offset + at[0], d.shard_offset + at[1]};
+        reduce_quads(r, ga, n, g);
+        double acc = 0.0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float gj = clip ? g[h][j] * coef : g[h][j];
+                const float mj = ma.mu * m[h][j] + gj;
+                m[h][j] = mj;
+                u[h][j] = nesterov ? gj + ma.mu * mj : mj;
+            }
+            store_quad(static_cast<M*>(d.m) + at[h], n[h], m[h]);
+            store_quad(static_cast<U*>(d.u) + (q[h].row * d.ldu + q[h].col), n[h], u[h]);
+            if constexpr (NORM) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < n[h]) acc = fma((double)u[h][j], (double)u[h][j], acc);
+            }
+        }
+        if constexpr (NORM) {
+            const double b = tile_sum(acc, sums[buf]);
+            buf ^= 1;
+            if (threadIdx.x == 0) partials[t] = b;
+        }
+    }
+}
+
+template <typename U>
+__global__ __launch_bounds__(kThreads) void u_sumsq_kernel(const MatDesc* __restrict__ mats,
+                                                           const StreamTile* __restrict__ tiles, int n_tiles,
+                                                           double* __restrict__ partials, int split)
+{
+    __shared__ double sums[2][kThreads / 64];
+    const Walk wk = walk(n_tiles, split);
+    int buf = 0;
+    for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
+        const StreamTile tile = tiles[t];
+        const MatDesc& d = mats[tile.mat];
+        double acc = 0.0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const Quad q = quad_at(d, tile, (int)threadIdx.x + h * kThreads);
+            float u[4];
+            load_quad(static_cast<const U*>(d.u) + (q.row * d.ldu + q.col), q.n, u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc = fma((double)u[j], (double)u[j], acc);
+        }
+        const double b = tile_sum(acc, sums[buf]);
+        buf ^= 1;
+        if (threadIdx.x == 0) partials[t] = b;
+    }
+}
+
+// One workgroup a matrix: the norm from its tiles' partials in a fixed order,
+// and the scale the iteration starts with.
+__global__ __launch_bounds__(kThreads) void ns_norms_kernel(const MatDesc* __restrict__ mats,
+                                                            const double* __restrict__ partials, double eps,
+                                                            NormRec* __restrict__ norms)
+{
+    __shared__ double sums[kThreads / 64];
+    const MatDesc& d = mats[blockIdx.x];
+    double a = 0.0;
+    for (int i = threadIdx.x; i < d.n_tiles; i += kThreads) a = a + partials[d.tile0 + i];
+    const double tot = tile_sum(a, sums);
+    if (threadIdx.x == 0) {
+        const double f = (double)kNsScale / (sqrt(tot) + eps);
+        NormRec n;
+        // a norm that is infinite, NaN, or zero with eps = 0: u / (norm + eps)
+        // holds a NaN, and the iteration spreads it over the whole matrix
+        if (!(f > 0.0) || isinf(f)) {
+            n.r = __builtin_nanf("");
+            n.e = 0;
+        } else {
+            n.e = ilogb(f);
+            n.r = (float)ldexp(f, -n.e);
+        }
+        norms[blockIdx.x] = n;
+    }
+}
+
+// p = (p - eta o) delta, the bf16 parameter from the new p: 12 bytes an element.
+__global__ __launch_bounds__(kThreads) void muon_update_kernel(const MatDesc* __restrict__ mats,
+                                                               const StreamTile* __restrict__ tiles, int n_tiles,
+                                                               MuonArgs ma, int split)
+{
+    use_device_scalars(ma, nullptr);
+    const Walk wk = walk(n_tiles, split);
+    for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
+        const StreamTile tile = tiles[t];
+        const MatDesc& d = mats[tile.mat];
+        const float eta = ma.lr * d.scale;
+        Quad q[2];
+        int64_t at[2];
+        float p[2][4], o[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            q[h] = quad_at(d, tile, (int)threadIdx.x + h * kThreads);
+            at[h] = q[h].row * d.ld + q[h].col;
+            load_quad(d.master + at[h], q[h].n, p[h]);
+            load_quad(d.o + (q[h].row * d.ldo + q[h].col), q[h].n, o[h]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[h][j] = muon_elem(p[h][j], o[h][j], eta, ma);
+            store_quad(d.master + at[h], q[h].n, p[h]);
+            store_quad(d.param + at[h], q[h].n, p[h]);
+        }
+    }
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ launchers
+hipError_t launch_momentum(const Reduce& r, const MatDesc* mats, const StreamTile* tiles, int n_tiles, bool m_bf16,
+                           bool u_f32, bool nesterov, const MuonArgs& ma, const MuonClip& mc, double* partials,
+                           int nblocks, int split, hipStream_t s)
+{
+#define Z1_MOM(M, U, N)                                                                                          \
+    momentum_kernel<M, U, N><<<dim3(nblocks), dim3(kThreads), 0, s>>>(r, mats, tiles, n_tiles, nesterov ? 1 : 0, \
+                                                                      ma, mc, partials, split)
+#define Z1_MOM_N(M, U)                  \
+    do {                                \
+        if (partials) Z1_MOM(M, U, true); \
+        else Z1_MOM(M, U, false);       \
+    } while (0)
+    if (m_bf16) {
+        if (u_f32) Z1_MOM_N(uint16_t, float);
+        else Z1_MOM_N(uint16_t, uint16_t);
+    } else {
+        if (u_f32) Z1_MOM_N(float, float);
+        else Z1_MOM_N(float, uint16_t);
+    }
+#undef Z1_MOM_N
+#undef Z1_MOM
+    return hipGetLastError();
+}
+
+hipError_t launch_u_sumsq(const MatDesc* mats, const StreamTile* tiles, int n_tiles, bool u_f32, double* partials,
+                          int nblocks, int split, hipStream_t s)
+{
+    if (u_f32) u_sumsq_kernel<float><<<dim3(nblocks), dim3(kThreads), 0, s>>>(mats, tiles, n_tiles, partials, split);
+    else u_sumsq_kernel<uint16_t><<<dim3(nblocks), dim3(kThreads), 0, s>>>(mats, tiles, n_tiles, partials, split);
+    return hipGetLastError();
+}
+
+hipError_t launch_ns_norms(const MatDesc* mats, int n_mats, const double* partials, double eps, NormRec* norms,
+                           hipStream_t s)
+{
+    ns_norms_kernel<<<dim3(n_mats), dim3(kThreads), 0, s>>>(mats, partials, eps, norms);
+    return hipGetLastError();
+}
+
+hipError_t launch_muon_update(const MatDesc* mats, const StreamTile* tiles, int n_tiles, const MuonArgs& ma,
+                              int nblocks, int split, hipStream_t s)
+{
+    muon_update_kernel<<<dim3(nblocks), dim3(kThreads), 0, s>>>(mats, tiles, n_tiles, ma, split);
+    return hipGetLastError();
+}
+
+}  // namespace z1

@@ -1,0 +1,704 @@
+// muon_api.cpp -- the Muon entry points of the C ABI (declared in
+// include/zero1.h): argument checks, the plan over a rank's matrices (tiles of
+// the streaming kernels and of the products, groups, workspace layout) and the
+// launch sequences.  No entry point allocates device memory or synchronizes
+// (except zero1_muon_plan, which copies its table once, and
+// ZERO1_SYNC_CHECK=1).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <exception>
+#include <mutex>
+#include <vector>
+
+#include "../../include/zero1.h"
+#include "internal.h"
+#include "muon.h"
+
+using namespace z1;
+
+static_assert(sizeof(MuonScal) == sizeof(zero1_muon_scalars) && sizeof(MuonScal) == 24 &&
+                  offsetof(MuonScal, max_norm) == offsetof(zero1_muon_scalars, max_norm) &&
+                  offsetof(MuonScal, delta) == offsetof(zero1_muon_scalars, decay),
+              "muon scalars layout");
+
+namespace {
+
+// ------------------------------------------------------------------ errors
+zero1_status fail(zero1_status st, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_error(st, buf);
+    return st;
+}
+
+zero1_status ok()
+{
+    set_error(ZERO1_OK, "");
+    return ZERO1_OK;
+}
+
+#define Z1_HIP(call)                                                                      \
+    do {                                                                                  \
+        hipError_t e_ = (call);                                                           \
+        if (e_ != hipSuccess)                                                             \
+            return fail(ZERO1_EHIP, "%s failed: %s", #call, hipGetErrorString(e_));      \
+    } while (0)
+
+zero1_status finish(hipStream_t s)
+{
+    static const bool sync = [] {
+        const char* e = std::getenv("ZERO1_SYNC_CHECK");
+        return e && e[0] && e[0] != '0';
+    }();
+    if (sync) {
+        hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+        Z1_HIP(hipStreamIsCapturing(s, &cs));
+        if (cs == hipStreamCaptureStatusNone) Z1_HIP(hipStreamSynchronize(s));
+        Z1_HIP(hipGetLastError());
+    }
+    return ok();
+}
+
+// ------------------------------------------------------------------ device
+std::mutex g_mu;
+int g_cus[64];   // CUs of each device once probed; -1: not gfx950
+
+zero1_status current_device(int& dev, int& cus)
+{
+    Z1_HIP(hipGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return fail(ZERO1_ENOTSUPPORTED, "device index %d out of range", dev);
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (g_cus[dev] == 0) {
+        hipDeviceProp_t p;
+        Z1_HIP(hipGetDeviceProperties(&p, dev));
+        g_cus[dev] = std::strncmp(p.gcnArchName, "gfx950", 6) == 0 ? p.multiProcessorCount : -1;
+    }
+    if (g_cus[dev] < 0) return fail(ZERO1_ENOTSUPPORTED, "device %d is not a gfx950", dev);
+    cus = g_cus[dev];
+    return ZERO1_OK;
+}
+
+// The device the call runs on has to be the one that holds the plan's table.
+zero1_status plan_device(const zero1_matrix_plan* plan, int& cus)
+{
+    int dev = 0;
+    if (zero1_status st = current_device(dev, cus)) return st;
+    if (dev != plan->device)
+        return fail(ZERO1_EINVAL, "the plan was made on device %d, the current device is %d", plan->device, dev);
+    return ZERO1_OK;
+}
+
+// ------------------------------------------------------------------ checks
+constexpr uint32_t kPlanFlags = ZERO1_MV_BF16 | ZERO1_U_F32;
+constexpr uint32_t kMuonFlags = ZERO1_SUM_ONLY | ZERO1_MV_BF16 | ZERO1_RECOMPUTE_G | ZERO1_STORE_G |
+                                ZERO1_DECAY_FIRST | ZERO1_CLIP_EPS | ZERO1_G_BF16 | ZERO1_U_F32 |
+                                ZERO1_NO_NESTEROV;
+constexpr int64_t kMaxSide = ((int64_t)1 << 31) - 256;   // rows, cols
+constexpr int64_t kMaxInner = 32768;                     // the smaller of the two
+constexpr int kMaxSteps = 64;
+
+enum Has : uint32_t { kHasMaster = 1, kHasM = 2, kHasU = 4, kHasO = 8 };
+
+zero1_status check_flags(uint32_t flags, const char* fn)
+{
+    if (flags & ~kMuonFlags) return fail(ZERO1_EINVAL, "%s: unknown flag bits 0x%x", fn, flags & ~kMuonFlags);
+    return ZERO1_OK;
+}
+
+zero1_status check_plan(const zero1_matrix_plan* plan, uint32_t need, const char* fn)
+{
+    if (!plan || !plan->table) return fail(ZERO1_EINVAL, "plan is NULL or has no table");
+    if ((need & kHasM) && !(plan->has & kHasM)) return fail(ZERO1_EINVAL, "%s: the plan's matrices have no m", fn);
+    if ((need & kHasU) && !(plan->has & kHasU)) return fail(ZERO1_EINVAL, "%s: the plan's matrices have no u", fn);
+    if ((need & kHasO) && !(plan->has & kHasO)) return fail(ZERO1_EINVAL, "%s: the plan's matrices have no o", fn);
+    if ((need & kHasMaster) && !(plan->has & kHasMaster))
+        return fail(ZERO1_EINVAL, "%s: the plan's matrices have no master and param_bf16", fn);
+    return ZERO1_OK;
+}
+
+zero1_status check_scalars(const zero1_muon_hparams* hp)
+{
+    if (!(hp->lr >= 0.0) || std::isinf(hp->lr)) return fail(ZERO1_EINVAL, "lr=%g must be finite and >= 0", hp->lr);
+    if (!(hp->momentum >= 0.0 && hp->momentum < 1.0))
+        return fail(ZERO1_EINVAL, "momentum=%g must be in [0, 1)", hp->momentum);
+    if (!(hp->weight_decay >= 0.0) || std::isinf(hp->weight_decay))
+        return fail(ZERO1_EINVAL, "weight_decay=%g must be finite and >= 0", hp->weight_decay);
+    if (!(hp->max_norm > 0.0))
+        return fail(ZERO1_EINVAL, "max_norm=%g must be > 0 (inf disables clipping)", hp->max_norm);
+    return ZERO1_OK;
+}
+
+zero1_status check_hparams(const zero1_muon_hparams* hp)
+{
+    if (!hp) return fail(ZERO1_EINVAL, "hp is NULL");
+    if (hp->device_scalars) {
+        if (reinterpret_cast<uintptr_t>(hp->device_scalars) % 8)
+            return fail(ZERO1_EINVAL, "hp->device_scalars must be 8-byte aligned");
+        return ZERO1_OK;
+    }
+    return check_scalars(hp);
+}
+
+// The singular values s <= 1 of the normalised matrix go through
+// p(s) = a s + b s^3 + c s^5 a step.  What bounds them bounds every entry of
+// X, A and B, which fp16 holds times 2^12: 3, 9 and 12 leave a third of its
+// range for roundings.
+zero1_status check_iteration(const zero1_muon_hparams* hp)
+{
+    if (hp->ns_steps < 1 || hp->ns_steps > kMaxSteps)
+        return fail(ZERO1_EINVAL, "ns_steps=%d must be in [1, %d]", hp->ns_steps, kMaxSteps);
+    if (!(hp->ns_eps >= 0.0) || std::isinf(hp->ns_eps))
+        return fail(ZERO1_EINVAL, "ns_eps=%g must be finite and >= 0", hp->ns_eps);
+    const double a = hp->ns_a, b = hp->ns_b, c = hp->ns_c;
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+        return fail(ZERO1_EINVAL, "ns_a, ns_b and ns_c must be finite");
+    double top = 1.0;
+    for (int it = 0; it < hp->ns_steps; ++it) {
+        // on t = s^2 in [0, top^2]: |b t + c t^2| (B's eigenvalues) and |p(s)|
+        const double tt = top * top;
+        auto beta = [&](double t) { return std::fabs(b * t + c * t * t); };
+        auto poly = [&](double t) { return std::sqrt(t) * std::fabs(a + b * t + c * t * t); };
+        double most_b = beta(tt), most_p = poly(tt);
+        if (c != 0.0) {
+            const double tb = -b / (2.0 * c);
+            if (tb > 0.0 && tb < tt) most_b = std::max(most_b, beta(tb));
+            const double disc = 9.0 * b * b - 20.0 * a * c;
+            if (disc >= 0.0)
+                for (int sgn = -1; sgn <= 1; sgn += 2) {
+                    const double tp = (-3.0 * b + sgn * std::sqrt(disc)) / (10.0 * c);
+                    if (tp > 0.0 && tp < tt) most_p = std::max(most_p, poly(tp));
+                }
+        } else if (b != 0.0) {
+            const double tp = -a / (3.0 * b);
+            if (tp > 0.0 && tp < tt) most_p = std::max(most_p, poly(tp));
+        }
+        if (!(most_b <= 12.0) || !(most_p <= 3.0))
+            return fail(ZERO1_EINVAL,
+                        "ns_a=%g, ns_b=%g, ns_c=%g let singular values reach %g (|b s^2 + c s^4| %g) in step %d; at most 3 "
+                        "(12) is supported",
+                        a, b, c, most_p, most_b, it + 1);
+        top = std::max(most_p, 1e-30);
+    }
+    return ZERO1_OK;
+}
+
+MuonArgs muon_args(const zero1_muon_hparams* hp, uint32_t flags)
+{
+    MuonArgs m;
+    std::memset(&m, 0, sizeof m);
+    m.decay_first = (flags & ZERO1_DECAY_FIRST) ? 1 : 0;
+    if (hp->device_scalars) {
+        m.dev = static_cast<const MuonScal*>(hp->device_scalars);
+        return m;
+    }
+    m.lr = (float)hp->lr;
+    m.mu = (float)hp->momentum;
+    m.delta = (float)(1.0 - hp->lr * hp->weight_decay);
+    return m;
+}
+
+zero1_status check_grads(const uint16_t* const* grads, int W, int64_t begin, uint32_t flags, Reduce& r)
+{
+    if (W < 1 || W > kMaxW) return fail(ZERO1_EINVAL, "W=%d must be in [1, %d]", W, kMaxW);
+    if (begin < 0) return fail(ZERO1_EINVAL, "begin=%lld is negative", (long long)begin);
+    if (!grads) return fail(ZERO1_EINVAL, "grads (host array of W pointers) is NULL");
+    std::memset(&r, 0, sizeof r);
+    for (int w = 0; w < W; ++w) {
+        if (!grads[w]) return fail(ZERO1_EINVAL, "grads[%d] is NULL", w);
+        r.gp.p[w] = grads[w] + begin;
+    }
+    r.W = W;
+    r.round_bf16 = (flags & ZERO1_G_BF16) ? 1 : 0;
+    if ((flags & ZERO1_SUM_ONLY) || W == 1) {
+        r.mode = kAvgNone;
+    } else if ((W & (W - 1)) == 0) {
+        r.mode = kAvgMulPow2;
+        r.inv_w = 1.0f / (float)W;
+    } else {
+        r.mode = kAvgDiv;
+        r.f_w = (float)W;
+    }
+    return ZERO1_OK;
+}
+
+// ------------------------------------------------------------------ overlap
+// rows x cols elements of `esize` bytes with a row stride of ld elements.
+struct Block {
+    uintptr_t lo, hi;   // first byte, one past the last
+    int64_t rows, cols, ld;
+    size_t esize;
+    const char* what;
+    int idx;
+};
+
+Block block(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t esize, const char* what, int idx)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return Block{lo, lo + (uintptr_t)((rows - 1) * ld + cols) * esize, rows, cols, ld, esize, what, idx};
+}
+
+// Whether two blocks whose byte ranges overlap (a.lo <= b.lo < a.hi) share an
+// element.  Blocks cut out of one array (the same stride and element size) are
+// told apart by rows and columns; others are taken to share.
+bool share(const Block& a, const Block& b)
+{
+    if (a.esize != b.esize || a.ld != b.ld || (b.lo - a.lo) % a.esize) return true;
+    const int64_t delta = (int64_t)((b.lo - a.lo) / a.esize);
+    const int64_t q = delta / a.ld, r = delta % a.ld;   // b starts at row q, column r of a's array
+    if (r < a.cols && q < a.rows) return true;
+    // b's columns past the array's row end continue at column 0 of the next row
+    return r + b.cols > a.ld && q + 1 < a.rows;
+}
+
+zero1_status check_blocks(std::vector<Block>& v)
+{
+    std::sort(v.begin(), v.end(), [](const Block& a, const Block& b) { return a.lo < b.lo; });
+    std::vector<size_t> open;   // earlier blocks that may reach this one
+    for (size_t i = 0; i < v.size(); ++i) {
+        size_t kept = 0;
+        for (size_t k = 0; k < open.size(); ++k)
+            if (v[open[k]].hi > v[i].lo) open[kept++] = open[k];
+        open.resize(kept);
+        for (size_t k : open)
+            if (share(v[k], v[i]))
+                return fail(ZERO1_EINVAL, "buffers overlap: %s[%d] and %s[%d]", v[k].what, v[k].idx, v[i].what,
+                            v[i].idx);
+        open.push_back(i);
+    }
+    return ZERO1_OK;
+}
+
+// ------------------------------------------------------------------ plan
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+int64_t round_up64(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+// Matrices share a group until their iteration buffers pass this: enough
+// tiles in a launch to fill the chip several times, little enough to stay
+// near the 256 MB MALL.
+constexpr int64_t kGroupBytes = (int64_t)512 << 20;
+
+struct Host {
+    std::vector<MatDesc> mats;
+    std::vector<StreamTile> tiles;
+    std::vector<GroupDesc> groups;
+    std::vector<ProdTile> list;
+    int64_t area = 0;
+    int32_t max_sym = 0, max_full = 0;
+    uint32_t has = 0;
+    int64_t elems = 0;
+    size_t off_tiles() const { return round_up(sizeof(MatDesc) * mats.size(), 256); }
+    size_t off_groups() const { return off_tiles() + round_up(sizeof(StreamTile) * tiles.size(), 256); }
+    size_t off_list() const { return off_groups() + round_up(sizeof(GroupDesc) * groups.size(), 256); }
+    size_t bytes() const { return off_list() + sizeof(ProdTile) * list.size(); }
+};
+
+uint32_t buffers_of(const zero1_matrix& q)
+{
+    return (q.master ? kHasMaster : 0) | (q.m ? kHasM : 0) | (q.u ? kHasU : 0) | (q.o ? kHasO : 0);
+}
+
+// What the sizes of a plan's parts depend on.
+zero1_status check_shape(const zero1_matrix& q, int i, uint32_t has0)
+{
+    if (q.rows < 1 || q.cols < 1 || q.rows > kMaxSide || q.cols > kMaxSide)
+        return fail(ZERO1_EINVAL, "matrix %d: %lld x %lld: rows and cols must be in [1, %lld]", i, (long long)q.rows,
+                    (long long)q.cols, (long long)kMaxSide);
+    if (std::min(q.rows, q.cols) > kMaxInner)
+        return fail(ZERO1_EINVAL, "matrix %d: %lld x %lld: the smaller side is at most %lld", i, (long long)q.rows,
+                    (long long)q.cols, (long long)kMaxInner);
+    const int64_t strides[3] = {q.ld, q.ldu, q.ldo};
+    const char* names[3] = {"ld", "ldu", "ldo"};
+    for (int k = 0; k < 3; ++k)
+        if (strides[k] != 0 && (strides[k] < q.cols || strides[k] > kMaxSide))
+            return fail(ZERO1_EINVAL, "matrix %d: %s=%lld must be 0 or in [cols=%lld, %lld]", i, names[k],
+                        (long long)strides[k], (long long)q.cols, (long long)kMaxSide);
+    const uint32_t has = buffers_of(q);
+    if (!has) return fail(ZERO1_EINVAL, "matrix %d has no buffer", i);
+    if (i > 0 && has != has0)
+        return fail(ZERO1_EINVAL, "matrix %d: every matrix of a plan has the same buffers (NULL or not)", i);
+    return ZERO1_OK;
+}
+
+zero1_status check_matrix(const zero1_matrix& q, int i, uint32_t flags)
+{
+    if (q.shard_offset < 0) return fail(ZERO1_EINVAL, "matrix %d: negative shard_offset", i);
+    if (!std::isfinite(q.scale)) return fail(ZERO1_EINVAL, "matrix %d: scale must be finite", i);
+    if (!q.master != !q.param_bf16)
+        return fail(ZERO1_EINVAL, "matrix %d: master and param_bf16 go together", i);
+    const size_t align[5] = {sizeof(float), 2, (flags & ZERO1_MV_BF16) ? (size_t)2 : 4,
+                             (flags & ZERO1_U_F32) ? (size_t)4 : 2, 2};
+    const void* p[5] = {q.master, q.param_bf16, q.m, q.u, q.o};
+    const char* pn[5] = {"master", "param_bf16", "m", "u", "o"};
+    for (int k = 0; k < 5; ++k)
+        if (reinterpret_cast<uintptr_t>(p[k]) % align[k])
+            return fail(ZERO1_EINVAL, "matrix %d: %s is not aligned to its elements", i, pn[k]);
+    return ZERO1_OK;
+}
+
+// The buffers: values, alignment, and that no two share an element.
+zero1_status check_buffers(const zero1_matrix* mats, int n, uint32_t flags)
+{
+    const size_t mb = (flags & ZERO1_MV_BF16) ? 2 : 4, ub = (flags & ZERO1_U_F32) ? 4 : 2;
+    std::vector<Block> blocks;
+    for (int i = 0; i < n; ++i) {
+        const zero1_matrix& q = mats[i];
+        if (zero1_status st = check_matrix(q, i, flags)) return st;
+        const int64_t ld = q.ld ? q.ld : q.cols, ldu = q.ldu ? q.ldu : q.cols, ldo = q.ldo ? q.ldo : q.cols;
+        if (q.master) {
+            blocks.push_back(block(q.param_bf16, q.rows, q.cols, ld, 2, "param_bf16", i));
+            blocks.push_back(block(q.master, q.rows, q.cols, ld, 4, "master", i));
+        }
+        if (q.m) blocks.push_back(block(q.m, q.rows, q.cols, ld, mb, "m", i));
+        if (q.u) blocks.push_back(block(q.u, q.rows, q.cols, ldu, ub, "u", i));
+        // o in place of a bf16 u is the one overlap that is allowed
+        const bool in_place = q.o && (const void*)q.o == q.u && ub == 2 && ldo == ldu;
+        if (q.o && !in_place) blocks.push_back(block(q.o, q.rows, q.cols, ldo, 2, "o", i));
+    }
+    return check_blocks(blocks);
+}
+
+zero1_status build(const zero1_matrix* mats, int n, Host& h)
+{
+    if (!mats || n < 1) return fail(ZERO1_EINVAL, "need at least one matrix");
+    h.has = buffers_of(mats[0]);
+    std::vector<int> order(n);
+    for (int i = 0; i < n; ++i) {
+        if (zero1_status st = check_shape(mats[i], i, h.has)) return st;
+        h.elems += mats[i].rows * mats[i].cols;
+        order[i] = i;
+    }
+    // largest products first: the tiles that run longest are dispatched first
+    auto small = [&](int i) { return std::min(mats[i].rows, mats[i].cols); };
+    auto large = [&](int i) { return std::max(mats[i].rows, mats[i].cols); };
+    std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
+        return small(a) != small(b) ? small(a) > small(b) : large(a) > large(b);
+    });
+    int64_t used = 0;
+    size_t group_first = 0;
+    auto close_group = [&](size_t end) {
+        GroupDesc g;
+        std::memset(&g, 0, sizeof g);
+        g.sym0 = (int64_t)h.list.size();
+        for (size_t m = group_first; m < end; ++m)
+            for (int i = 0; i < h.mats[m].kp / kPad; ++i)
+                for (int j = i; j < h.mats[m].kp / kPad; ++j) h.list.push_back(ProdTile{(int32_t)m, i, j, 0});
+        g.n_sym = (int32_t)(h.list.size() - g.sym0);
+        g.full0 = (int64_t)h.list.size();
+        for (size_t m = group_first; m < end; ++m)
+            for (int j = 0; j < h.mats[m].np / kPad; ++j)
+                for (int i = 0; i < h.mats[m].kp / kPad; ++i) h.list.push_back(ProdTile{(int32_t)m, i, j, 0});
+        g.n_full = (int32_t)(h.list.size() - g.full0);
+        h.groups.push_back(g);
+        h.max_sym = std::max(h.max_sym, g.n_sym);
+        h.max_full = std::max(h.max_full, g.n_full);
+        h.area = std::max(h.area, used);
+        group_first = end;
+        used = 0;
+    };
+    for (int k = 0; k < n; ++k) {
+        const zero1_matrix& q = mats[order[k]];
+        MatDesc d;
+        std::memset(&d, 0, sizeof d);
+        d.rows = q.rows;
+        d.cols = q.cols;
+        d.ld = q.ld ? q.ld : q.cols;
+        d.ldu = q.ldu ? q.ldu : q.cols;
+        d.ldo = q.ldo ? q.ldo : q.cols;
+        d.shard_offset = q.shard_offset;
+        d.param = q.param_bf16;
+        d.master = q.master;
+        d.m = q.m;
+        d.u = q.u;
+        d.o = q.o;
+        d.scale = q.scale;
+        d.tall = q.rows > q.cols ? 1 : 0;
+        d.k = (int32_t)std::min(q.rows, q.cols);
+        d.n = (int32_t)std::max(q.rows, q.cols);
+        d.kp = (int32_t)round_up64(d.k, kPad);
+        d.np = (int32_t)round_up64(d.n, kPad);
+        const bool flat = q.rows == 1 || (d.ld == q.cols && d.ldu == q.cols && d.ldo == q.cols);
+        d.vrows = flat ? 1 : (int32_t)q.rows;
+        d.vcols = flat ? q.rows * q.cols : q.cols;
+        d.qpr = (d.vcols + 3) / 4;
+        const int64_t quads = d.vrows * d.qpr, nt = (quads + kQuadsPerTile - 1) / kQuadsPerTile;
+        if ((int64_t)h.tiles.size() + nt > INT32_MAX) return fail(ZERO1_EINVAL, "too many elements in one plan");
+        d.tile0 = (int32_t)h.tiles.size();
+        d.n_tiles = (int32_t)nt;
+        for (int64_t t = 0; t < nt; ++t) {
+            StreamTile s{k, (int32_t)t, 0, 0};
+            if (!flat) {
+                s.row0 = (int32_t)(t * kQuadsPerTile / d.qpr);
+                s.q0 = (int32_t)(t * kQuadsPerTile % d.qpr);
+            }
+            h.tiles.push_back(s);
+        }
+        if (h.has & kHasU) {   // its place in a group's buffers
+            const int64_t x = round_up64((int64_t)d.kp * d.np * 2, 256), a = round_up64((int64_t)d.kp * d.kp * 2, 256);
+            if (used > 0 && used + 3 * x + 2 * a > kGroupBytes) close_group(h.mats.size());
+            d.x[0] = used;
+            d.x[1] = used + x;
+            d.lo = used + 2 * x;
+            d.a = used + 3 * x;
+            d.b = d.a + a;
+            used = d.b + a;
+        }
+        h.mats.push_back(d);
+    }
+    if (h.has & kHasU) {
+        close_group(h.mats.size());
+        if ((int64_t)h.list.size() > INT32_MAX) return fail(ZERO1_EINVAL, "too many tiles in one plan");
+    }
+    return ZERO1_OK;
+}
+
+// Workspace: the streaming tiles' partial sums of squares, the norms, then a
+// group's iteration buffers.
+size_t ws_norms(const zero1_matrix_plan* p) { return round_up(sizeof(double) * (size_t)p->n_tiles, 256); }
+size_t ws_area(const zero1_matrix_plan* p) { return ws_norms(p) + round_up(sizeof(NormRec) * (size_t)p->n_mats, 256); }
+
+zero1_status check_ws(const zero1_matrix_plan* plan, const void* ws, size_t bytes)
+{
+    const size_t need = zero1_muon_workspace_bytes(plan);
+    if (!ws) return fail(ZERO1_EWORKSPACE, "workspace is NULL (need %zu bytes)", need);
+    if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(ZERO1_EWORKSPACE, "workspace must be 256-byte aligned");
+    if (bytes < need) return fail(ZERO1_EWORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
+    return ZERO1_OK;
+}
+
+const MatDesc* plan_mats(const zero1_matrix_plan* p) { return static_cast<const MatDesc*>(p->table); }
+const StreamTile* plan_tiles(const zero1_matrix_plan* p)
+{
+    return reinterpret_cast<const StreamTile*>(static_cast<const char*>(p->table) + p->off_tiles);
+}
+
+// The streaming kernels' grid, as the AdamW update's: a workgroup a tile up
+// to kMaxPartials tiles, then 8 a CU with each XCD on its own eighth.
+struct Shape {
+    int grid, split;
+};
+
+Shape stream_shape(int n_tiles, int cus)
+{
+    if (n_tiles <= kMaxPartials) return Shape{n_tiles, 1};
+    return Shape{cus * 8 / 8 * 8, 8};
+}
+
+zero1_status momentum(const uint16_t* const* grads, int W, int64_t begin, const zero1_matrix_plan* plan,
+                      const zero1_muon_hparams* hp, const double* rank_sumsq, int n_ranks, uint32_t flags,
+                      zero1_norm_info* info_out, double* partials, int cus, hipStream_t s)
+{
+    Reduce r;
+    if (zero1_status st = check_grads(grads, W, begin, flags, r)) return st;
+    if (rank_sumsq && n_ranks < 1) return fail(ZERO1_EINVAL, "n_ranks=%d must be >= 1", n_ranks);
+    if (info_out && !rank_sumsq) return fail(ZERO1_EINVAL, "info_out needs rank_sumsq");
+    const MuonClip mc{rank_sumsq, n_ranks, hp->max_norm, (flags & ZERO1_CLIP_EPS) ? 1 : 0,
+                      reinterpret_cast<NormInfo*>(info_out)};
+    const Shape sh = stream_shape(plan->n_tiles, cus);
+    Z1_HIP(launch_momentum(r, plan_mats(plan), plan_tiles(plan), plan->n_tiles, (plan->flags & ZERO1_MV_BF16) != 0,
+                           (plan->flags & ZERO1_U_F32) != 0, !(flags & ZERO1_NO_NESTEROV), muon_args(hp, flags), mc,
+                           partials, sh.grid, sh.split, s));
+    return ZERO1_OK;
+}
+
+// The iteration over every group, from u and its tiles' partials; `last` says
+// what becomes of the result.
+zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp, uint32_t flags, NsLast last,
+                     char* ws, hipStream_t s)
+{
+    const double* partials = reinterpret_cast<const double*>(ws);
+    NormRec* norms = reinterpret_cast<NormRec*>(ws + ws_norms(plan));
+    Z1_HIP(launch_ns_norms(plan_mats(plan), plan->n_mats, partials, hp->ns_eps, norms, s));
+    const char* tb = static_cast<const char*>(plan->table);
+    NsArgs g;
+    std::memset(&g, 0, sizeof g);
+    g.mats = plan_mats(plan);
+    g.groups = reinterpret_cast<const GroupDesc*>(tb + plan->off_groups);
+    g.list = reinterpret_cast<const ProdTile*>(tb + plan->off_list);
+    g.area = ws + ws_area(plan);
+    g.norms = norms;
+    g.a = (float)hp->ns_a;
+    g.b = (float)hp->ns_b;
+    g.c = (float)hp->ns_c;
+    const bool u_f32 = (plan->flags & ZERO1_U_F32) != 0;
+    const MuonArgs ma = muon_args(hp, flags);
+    for (g.group = 0; g.group < plan->n_groups; ++g.group) {
+        Z1_HIP(launch_ns_prepare(g, u_f32, plan->max_full, s));
+        for (int it = 0; it < hp->ns_steps; ++it) {
+            Z1_HIP(launch_ns_gram(g, it, plan->max_sym, s));
+            Z1_HIP(launch_ns_poly(g, plan->max_sym, s));
+            Z1_HIP(launch_ns_apply(g, it, u_f32, it + 1 == hp->ns_steps ? last : kNsMid, ma, plan->max_full, s));
+        }
+    }
+    return ZERO1_OK;
+}
+
+}  // namespace
+
+// ====================================================================== ABI
+extern "C" {
+
+size_t zero1_muon_table_bytes(const zero1_matrix* mats, int n_mats)
+{
+    try {
+        Host h;
+        return build(mats, n_mats, h) == ZERO1_OK ? h.bytes() : 0;
+    } catch (const std::exception& e) {
+        fail(ZERO1_EINVAL, "zero1_muon_table_bytes: %s", e.what());
+        return 0;
+    }
+}
+
+zero1_status zero1_muon_plan(const zero1_matrix* mats, int n_mats, uint32_t flags, void* table, size_t table_bytes,
+                             zero1_matrix_plan* plan_out)
+{
+    try {
+        zero1_status st;
+        if ((st = check_flags(flags, "zero1_muon_plan"))) return st;
+        if (!plan_out) return fail(ZERO1_EINVAL, "plan_out is NULL");
+        Host h;
+        if ((st = build(mats, n_mats, h)) || (st = check_buffers(mats, n_mats, flags))) return st;
+        const size_t need = h.bytes();
+        if (!table) return fail(ZERO1_EWORKSPACE, "table is NULL (need %zu bytes)", need);
+        if (reinterpret_cast<uintptr_t>(table) % 256) return fail(ZERO1_EWORKSPACE, "table must be 256-byte aligned");
+        if (table_bytes < need) return fail(ZERO1_EWORKSPACE, "table has %zu bytes, needs %zu", table_bytes, need);
+        int dev = 0, cus = 0;
+        if ((st = current_device(dev, cus))) return st;
+        std::vector<char> host(need, 0);
+        std::memcpy(host.data(), h.mats.data(), sizeof(MatDesc) * h.mats.size());
+        std::memcpy(host.data() + h.off_tiles(), h.tiles.data(), sizeof(StreamTile) * h.tiles.size());
+        if (!h.groups.empty()) {
+            std::memcpy(host.data() + h.off_groups(), h.groups.data(), sizeof(GroupDesc) * h.groups.size());
+            std::memcpy(host.data() + h.off_list(), h.list.data(), sizeof(ProdTile) * h.list.size());
+        }
+        Z1_HIP(hipMemcpy(table, host.data(), need, hipMemcpyHostToDevice));
+        zero1_matrix_plan p;
+        std::memset(&p, 0, sizeof p);
+        p.table = table;
+        p.elems = h.elems;
+        p.off_tiles = (int64_t)h.off_tiles();
+        p.off_groups = (int64_t)h.off_groups();
+        p.off_list = (int64_t)h.off_list();
+        p.area_bytes = h.area;
+        p.n_mats = n_mats;
+        p.n_tiles = (int32_t)h.tiles.size();
+        p.n_groups = (int32_t)h.groups.size();
+        p.max_sym = h.max_sym;
+        p.max_full = h.max_full;
+        p.flags = flags & kPlanFlags;
+        p.has = h.has;
+        p.device = dev;
+        *plan_out = p;
+        return ok();
+    } catch (const std::exception& e) {
+        return fail(ZERO1_EINVAL, "zero1_muon_plan: %s", e.what());
+    }
+}
+
+size_t zero1_muon_workspace_bytes(const zero1_matrix_plan* plan)
+{
+    if (!plan || !plan->table) return 0;
+    return ws_area(plan) + round_up((size_t)plan->area_bytes, 256);
+}
+
+zero1_status zero1_muon_scalars_derive(const zero1_muon_hparams* hp, zero1_muon_scalars* out)
+{
+    if (!hp || !out) return fail(ZERO1_EINVAL, "hp or out is NULL");
+    if (zero1_status st = check_scalars(hp)) return st;
+    zero1_muon_hparams h = *hp;
+    h.device_scalars = nullptr;
+    const MuonArgs a = muon_args(&h, 0);
+    zero1_muon_scalars o;
+    std::memset(&o, 0, sizeof o);
+    o.lr = a.lr;
+    o.momentum = a.mu;
+    o.decay = a.delta;
+    o.max_norm = hp->max_norm;
+    *out = o;
+    return ok();
+}
+
+zero1_status zero1_muon_momentum(const uint16_t* const* grads, int W, int64_t begin, const zero1_matrix_plan* plan,
+                                 const zero1_muon_hparams* hp, const double* rank_sumsq, int n_ranks, uint32_t flags,
+                                 zero1_norm_info* info_out, void* stream)
+{
+    zero1_status st;
+    int cus = 0;
+    if ((st = check_flags(flags, "zero1_muon_momentum"))) return st;
+    if ((st = check_plan(plan, kHasM | kHasU, "zero1_muon_momentum"))) return st;
+    if ((st = check_hparams(hp))) return st;
+    Reduce r;
+    if ((st = check_grads(grads, W, begin, flags, r))) return st;
+    if ((st = plan_device(plan, cus))) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = momentum(grads, W, begin, plan, hp, rank_sumsq, n_ranks, flags, info_out, nullptr, cus, s))) return st;
+    return finish(s);
+}
+
+zero1_status zero1_orthogonalize(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp, uint32_t flags, void* ws,
+                                 size_t ws_bytes, void* stream)
+{
+    zero1_status st;
+    int cus = 0;
+    if ((st = check_flags(flags, "zero1_orthogonalize"))) return st;
+    if ((st = check_plan(plan, kHasU | kHasO, "zero1_orthogonalize"))) return st;
+    if (!hp) return fail(ZERO1_EINVAL, "hp is NULL");
+    if ((st = check_iteration(hp))) return st;
+    if ((st = check_ws(plan, ws, ws_bytes))) return st;
+    if ((st = plan_device(plan, cus))) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const Shape sh = stream_shape(plan->n_tiles, cus);
+    Z1_HIP(launch_u_sumsq(plan_mats(plan), plan_tiles(plan), plan->n_tiles, (plan->flags & ZERO1_U_F32) != 0,
+                          static_cast<double*>(ws), sh.grid, sh.split, s));
+    if ((st = iterate(plan, hp, flags, kNsWriteO, static_cast<char*>(ws), s))) return st;
+    return finish(s);
+}
+
+zero1_status zero1_muon_update(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp, uint32_t flags,
+                               void* stream)
+{
+    zero1_status st;
+    int cus = 0;
+    if ((st = check_flags(flags, "zero1_muon_update"))) return st;
+    if ((st = check_plan(plan, kHasMaster | kHasO, "zero1_muon_update"))) return st;
+    if ((st = check_hparams(hp))) return st;
+    if ((st = plan_device(plan, cus))) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const Shape sh = stream_shape(plan->n_tiles, cus);
+    Z1_HIP(launch_muon_update(plan_mats(plan), plan_tiles(plan), plan->n_tiles, muon_args(hp, flags), sh.grid,
+                              sh.split, s));
+    return finish(s);
+}
+
+zero1_status zero1_muon_step(const uint16_t* const* grads, int W, int64_t begin, const zero1_matrix_plan* plan,
+                             const zero1_muon_hparams* hp, const double* rank_sumsq, int n_ranks, uint32_t flags,
+                             zero1_norm_info* info_out, void* ws, size_t ws_bytes, void* stream)
+{
+    zero1_status st;
+    int cus = 0;
+    if ((st = check_flags(flags, "zero1_muon_step"))) return st;
+    if ((st = check_plan(plan, kHasMaster | kHasM | kHasU, "zero1_muon_step"))) return st;
+    if ((st = check_hparams(hp))) return st;
+    if ((st = check_iteration(hp))) return st;
+    Reduce r;
+    if ((st = check_grads(grads, W, begin, flags, r))) return st;
+    if ((st = check_ws(plan, ws, ws_bytes))) return st;
+    if ((st = plan_device(plan, cus))) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if ((st = momentum(grads, W, begin, plan, hp, rank_sumsq, n_ranks, flags, info_out, static_cast<double*>(ws), cus,
+                       s)))
+        return st;
+    if ((st = iterate(plan, hp, flags, kNsUpdate, static_cast<char*>(ws), s))) return st;
+    return finish(s);
+}
+
+}  // extern "C"
