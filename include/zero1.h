@@ -511,16 +511,25 @@ typedef struct zero1_matrix {
     int64_t ldo;            /* row stride of o                                  */
 } zero1_matrix;
 
+/* Matrices of a plan that are iterated together: their launches' sizes and tile
+ * shapes. */
+#define ZERO1_MUON_MAX_GROUPS 64
+typedef struct zero1_matrix_group {
+    int32_t n_sym, n_full, n_blocks;
+    int16_t sym_tile, full_tile;
+} zero1_matrix_group;
+
 /* A validated list of matrices uploaded by zero1_muon_plan.  Plain data owned
  * by the caller; valid as long as the table memory is. */
 typedef struct zero1_matrix_plan {
     void* table;
     int64_t elems;          /* sum of rows * cols                               */
     int64_t off_tiles, off_groups, off_list, area_bytes;
-    int32_t n_mats, n_tiles, n_groups, max_sym, max_full;
+    int32_t n_mats, n_tiles, n_groups;
     uint32_t flags;         /* ZERO1_MV_BF16, ZERO1_U_F32                       */
     uint32_t has;           /* which buffers the matrices have                  */
     int32_t device;         /* calls are made with this device current          */
+    zero1_matrix_group groups[ZERO1_MUON_MAX_GROUPS];
 } zero1_matrix_plan;
 
 /* Hyper-parameters of one Muon step (host struct). */

@@ -30,7 +30,7 @@ def _mat(rows=10, cols=20, at=FAKE, **kw):
 
 
 def _plan(**kw):
-    d = dict(table=FAKE, elems=200, n_mats=1, n_tiles=1, n_groups=1, max_sym=1, max_full=1, has=15,
+    d = dict(table=FAKE, elems=200, n_mats=1, n_tiles=1, n_groups=1, has=15,
              area_bytes=1 << 17)
     d.update(kw)
     return z.MatrixPlan(**d)
@@ -50,10 +50,11 @@ def _valid(mats, flags=0):
 
 def test_table_bytes_and_layout():
     # 184 bytes a matrix; streaming tiles of 512 quads (16 bytes each); one
-    # group; 128-wide product tiles: A's upper triangle and X (16 bytes each)
-    assert z.muon_table_bytes([_mat()]) == 256 + 256 + 256 + 16 * (1 + 1)
-    # 300 x 700: 3 x 6 tiles of X, 6 of A's 3 x 3; 52500 quads
-    assert z.muon_table_bytes([_mat(300, 700)]) == 256 + -(-103 * 16 // 256) * 256 + 256 + 16 * (6 + 18)
+    # group; product tiles of 128 x 128: A's upper triangle, X; X's blocks of
+    # 64 x 64 (16 bytes each)
+    assert z.muon_table_bytes([_mat()]) == 256 + 256 + 256 + 16 * (1 + 1 + 1)
+    # 300 x 700: 3 x 6 tiles of X, 6 of A's 3 x 3, 5 x 11 blocks; 52500 quads
+    assert z.muon_table_bytes([_mat(300, 700)]) == 256 + -(-103 * 16 // 256) * 256 + 256 + 16 * (6 + 18 + 55)
     # without u there is nothing to iterate
     assert z.muon_table_bytes([_mat(u=None)]) == 256 + 256
     # a tall matrix has the tiles of its transpose

@@ -14,8 +14,8 @@ namespace z1 {
 // Streaming kernels (momentum, update, sum of squares): a workgroup's tile is
 // 512 quads, a quad being up to four neighbouring elements of one row.
 constexpr int kQuadsPerTile = 512;
-// Side of the square tiles that the products' operands are padded to.
-constexpr int kPad = 128;
+// Side of the square blocks that X, A and B are laid out in and padded to.
+constexpr int kPad = 64;
 // Power of two that X, A and B carry in fp16 (see newton_schulz.hip).
 constexpr float kNsScale = 4096.0f;
 
@@ -48,18 +48,20 @@ struct StreamTile {
     int32_t mat, idx, row0, q0;
 };
 
-// A tile of one matrix's product: block row i, block column j.
+// A tile of one matrix's product: its first block row i and block column j.
 struct ProdTile {
     int32_t mat, i, j, reserved;
 };
 
-// Matrices that are iterated together, and their tiles in the list of
-// ProdTiles: A and B (upper triangle), X (all).
+// Matrices that are iterated together, and what there is of them in the list
+// of ProdTiles: tiles of A and B (upper triangle), tiles of X, blocks of X.
 struct GroupDesc {
-    int64_t sym0, full0;
-    int32_t n_sym, n_full;
-    int64_t reserved;
+    int64_t sym0, full0, blocks0;
+    int32_t n_sym, n_full, n_blocks, reserved;
 };
+
+// Shapes of the products' tiles.
+enum TileShape : int { kTile128 = 0, kTile192 = 1, kTile256 = 2 };
 
 // Norm of one matrix's u as the iteration uses it: S / (norm + eps) = 2^e r
 // with r in [1, 2); r is NaN when the quotient is not finite.
@@ -112,10 +114,10 @@ hipError_t launch_muon_update(const MatDesc* mats, const StreamTile* tiles, int 
                               int nblocks, int split, hipStream_t s);
 
 hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, int grid, hipStream_t s);
-hipError_t launch_ns_gram(const NsArgs& g, int it, int grid, hipStream_t s);
-hipError_t launch_ns_poly(const NsArgs& g, int grid, hipStream_t s);
-hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, int grid,
-                           hipStream_t s);
+hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hipStream_t s);
+hipError_t launch_ns_poly(const NsArgs& g, TileShape tile, int grid, hipStream_t s);
+hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, TileShape tile,
+                           int grid, hipStream_t s);
 
 #ifdef __HIPCC__
 // ------------------------------------------------------------------ device
@@ -167,6 +169,55 @@ __device__ __forceinline__ float muon_elem(float p, float o, float eta, const Mu
 #pragma clang fp contract(off)
     if (a.decay_first) return p * a.delta - eta * o;
     return (p - eta * o) * a.delta;
+}
+
+// Loads and stores of a quad's n elements; four at once when all are there.
+__device__ __forceinline__ void load_quad(const uint16_t* p, int n, float (&x)[4])
+{
+    if (n == 4) {
+        const u16x4 v = ld4(p);
+        x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = j < n ? widen(p[j]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void load_quad(const float* p, int n, float (&x)[4])
+{
+    if (n == 4) {
+        const f32x4 v = ld4(p);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = j < n ? p[j] : 0.0f;
+    }
+}
+
+// Stores in the array's type; x becomes the values as stored.
+__device__ __forceinline__ void store_quad(uint16_t* p, int n, float (&x)[4])
+{
+    u16x4 v;
+    v.x = bf16_rne(x[0]); v.y = bf16_rne(x[1]); v.z = bf16_rne(x[2]); v.w = bf16_rne(x[3]);
+    x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
+    if (n == 4) {
+        st4(p, v);
+    } else {
+        if (n > 0) p[0] = v.x;
+        if (n > 1) p[1] = v.y;
+        if (n > 2) p[2] = v.z;
+    }
+}
+
+__device__ __forceinline__ void store_quad(float* p, int n, float (&x)[4])
+{
+    if (n == 4) {
+        st4(p, f32x4{x[0], x[1], x[2], x[3]});
+    } else {
+        if (n > 0) p[0] = x[0];
+        if (n > 1) p[1] = x[1];
+        if (n > 2) p[2] = x[2];
+    }
 }
 
 }  // namespace dev

@@ -63,55 +63,6 @@ __device__ __forceinline__ Quad quad_at(const MatDesc& d, const StreamTile& t, i
     return q;
 }
 
-// Loads and stores of a quad's n elements; four at once when all are there.
-__device__ __forceinline__ void load_quad(const uint16_t* p, int n, float (&x)[4])
-{
-    if (n == 4) {
-        const u16x4 v = ld4(p);
-        x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = j < n ? widen(p[j]) : 0.0f;
-    }
-}
-
-__device__ __forceinline__ void load_quad(const float* p, int n, float (&x)[4])
-{
-    if (n == 4) {
-        const f32x4 v = ld4(p);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = j < n ? p[j] : 0.0f;
-    }
-}
-
-// Stores in the array's type; x becomes the values as stored.
-__device__ __forceinline__ void store_quad(uint16_t* p, int n, float (&x)[4])
-{
-    u16x4 v;
-    v.x = bf16_rne(x[0]); v.y = bf16_rne(x[1]); v.z = bf16_rne(x[2]); v.w = bf16_rne(x[3]);
-    x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
-    if (n == 4) {
-        st4(p, v);
-    } else {
-        if (n > 0) p[0] = v.x;
-        if (n > 1) p[1] = v.y;
-        if (n > 2) p[2] = v.z;
-    }
-}
-
-__device__ __forceinline__ void store_quad(float* p, int n, float (&x)[4])
-{
-    if (n == 4) {
-        st4(p, f32x4{x[0], x[1], x[2], x[3]});
-    } else {
-        if (n > 0) p[0] = x[0];
-        if (n > 1) p[1] = x[1];
-        if (n > 2) p[2] = x[2];
-    }
-}
-
 // Fixed-order workgroup sum; the total is in thread 0.  `sh` alternates
 // between two buffers from tile to tile, so one barrier a tile is enough.
 __device__ __forceinline__ double tile_sum(double x, double* sh)

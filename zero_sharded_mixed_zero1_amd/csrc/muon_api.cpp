@@ -284,16 +284,43 @@ int64_t round_up64(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 // Matrices share a group until their iteration buffers pass this: enough
 // tiles in a launch to fill the chip several times, little enough to stay
-// near the 256 MB MALL.
+// near the 256 MB MALL.  Larger plans take larger groups, so that a plan holds
+// at most ZERO1_MUON_MAX_GROUPS of them.
 constexpr int64_t kGroupBytes = (int64_t)512 << 20;
+
+// Tile shapes (by TileShape) and what they take, in us: `start` a round of
+// tiles for its first loads and its epilogue, then for every 64 of the inner
+// dimension `one` where a tile has the chip to itself and `all` where every
+// slot holds one (the chip's clock falls with the load).  Measured on MI355X:
+//   matrix        product (inner)  128 x 128   192 x 192   256 x 256
+//   4096 x 11008  gram (11008)        262 us      201 us      229 us
+//                 apply (4096)        384         428         362
+//   1111 x 2501   gram (2501)          29          47          60   (3 matrices)
+//                 apply (1111)         40          34          41
+//   768 x 768     gram (768)           14          23          29   (12 matrices)
+struct TileCost {
+    int side;       // blocks
+    int slots;      // tiles the chip holds at once
+    double start, one, all;
+};
+constexpr TileCost kTiles[3] = {{2, 512, 6.0, 0.44, 0.98}, {3, 256, 9.0, 0.87, 1.15}, {4, 256, 11.0, 1.10, 1.72}};
+constexpr int kXcds = 8;
+
+double tile_time(const TileCost& c, double tiles, int inner)
+{
+    const double full = std::floor(tiles / c.slots), rest = tiles - full * c.slots;
+    double t = full * (c.start + inner * c.all);
+    if (rest > 0) t += c.start + inner * (c.one + (c.all - c.one) * rest / c.slots);
+    return t;
+}
 
 struct Host {
     std::vector<MatDesc> mats;
     std::vector<StreamTile> tiles;
     std::vector<GroupDesc> groups;
     std::vector<ProdTile> list;
+    std::vector<zero1_matrix_group> shape;
     int64_t area = 0;
-    int32_t max_sym = 0, max_full = 0;
     uint32_t has = 0;
     int64_t elems = 0;
     size_t off_tiles() const { return round_up(sizeof(MatDesc) * mats.size(), 256); }
@@ -367,6 +394,94 @@ zero1_status check_buffers(const zero1_matrix* mats, int n, uint32_t flags)
     return check_blocks(blocks);
 }
 
+int64_t group_bytes(int64_t k, int64_t n)
+{
+    const int64_t kp = round_up64(k, kPad), np = round_up64(n, kPad);
+    return 2 * (3 * kp * np + 2 * kp * kp);
+}
+
+// Block rows and columns of X, or of A and B.
+struct Blocks {
+    int rows, cols;
+};
+
+Blocks blocks_of(const MatDesc& d, bool sym) { return Blocks{d.kp / kPad, (sym ? d.kp : d.np) / kPad}; }
+
+// Appends a group's tiles of `side` blocks: all of X, or (sym) those of A and B
+// that reach above the diagonal.  Workgroup b runs on XCD b % 8, which has an
+// L2 of its own: of matrices alike, each XCD takes one contiguous eighth of the
+// tiles, walked in strips of 8 tile columns, so that the 32 tiles it works on
+// at once share 4 rows and 8 columns of the operands.
+int32_t add_tiles(Host& h, size_t first, size_t end, int side, bool sym)
+{
+    const size_t start = h.list.size();
+    std::vector<ProdTile> seq;
+    for (size_t m = first; m < end;) {
+        seq.clear();
+        size_t e = m;
+        for (; e < end && h.mats[e].kp == h.mats[m].kp && h.mats[e].np == h.mats[m].np; ++e) {
+            const Blocks b = blocks_of(h.mats[e], sym);
+            const int strip = 8 * side;
+            for (int js = 0; js < b.cols; js += strip)
+                for (int i = 0; i < b.rows; i += side)
+                    for (int j = js; j < std::min(js + strip, b.cols); j += side)
+                        if (!sym || j >= i) seq.push_back(ProdTile{(int32_t)e, i, j, 0});
+        }
+        const size_t base = h.list.size() - start;
+        h.list.resize(h.list.size() + seq.size());
+        size_t next = 0;
+        for (size_t x = 0; x < kXcds; ++x)
+            for (size_t t = (x + kXcds - base % kXcds) % kXcds; t < seq.size(); t += kXcds)
+                h.list[start + base + t] = seq[next++];
+        m = e;
+    }
+    return (int32_t)(h.list.size() - start);
+}
+
+// The tile shape that takes least for a group's symmetric products (gram and
+// poly) or for its apply.
+int16_t best_tile(const Host& h, size_t first, size_t end, bool sym)
+{
+    int16_t best = 0;
+    double least = 0.0;
+    for (int16_t s = 0; s < 3; ++s) {
+        const int side = kTiles[s].side;
+        double tiles = 0, gram = 0, apply = 0;
+        for (size_t m = first; m < end; ++m) {
+            const Blocks b = blocks_of(h.mats[m], sym);
+            const double r = (b.rows + side - 1) / side, c = (b.cols + side - 1) / side;
+            tiles += sym ? r * (r + 1) / 2 : r * c;
+            gram = std::max(gram, (double)h.mats[m].np / kPad);
+            apply = std::max(apply, (double)h.mats[m].kp / kPad);
+        }
+        double t = tile_time(kTiles[s], tiles, (int)apply);
+        if (sym) t += tile_time(kTiles[s], tiles, (int)gram);
+        if (s == 0 || t < least) {
+            best = s;
+            least = t;
+        }
+    }
+    return best;
+}
+
+void add_group(Host& h, size_t first, size_t end)
+{
+    zero1_matrix_group z;
+    std::memset(&z, 0, sizeof z);
+    z.sym_tile = best_tile(h, first, end, true);
+    z.full_tile = best_tile(h, first, end, false);
+    GroupDesc g;
+    std::memset(&g, 0, sizeof g);
+    g.sym0 = (int64_t)h.list.size();
+    g.n_sym = z.n_sym = add_tiles(h, first, end, kTiles[z.sym_tile].side, true);
+    g.full0 = (int64_t)h.list.size();
+    g.n_full = z.n_full = add_tiles(h, first, end, kTiles[z.full_tile].side, false);
+    g.blocks0 = (int64_t)h.list.size();
+    g.n_blocks = z.n_blocks = add_tiles(h, first, end, 1, false);
+    h.groups.push_back(g);
+    h.shape.push_back(z);
+}
+
 zero1_status build(const zero1_matrix* mats, int n, Host& h)
 {
     if (!mats || n < 1) return fail(ZERO1_EINVAL, "need at least one matrix");
@@ -383,24 +498,12 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
     std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
         return small(a) != small(b) ? small(a) > small(b) : large(a) > large(b);
     });
-    int64_t used = 0;
+    int64_t used = 0, total = 0;
+    for (int i = 0; i < n; ++i) total += group_bytes(small(i), large(i));
+    const int64_t budget = std::max(kGroupBytes, total / (ZERO1_MUON_MAX_GROUPS / 2 - 1));
     size_t group_first = 0;
     auto close_group = [&](size_t end) {
-        GroupDesc g;
-        std::memset(&g, 0, sizeof g);
-        g.sym0 = (int64_t)h.list.size();
-        for (size_t m = group_first; m < end; ++m)
-            for (int i = 0; i < h.mats[m].kp / kPad; ++i)
-                for (int j = i; j < h.mats[m].kp / kPad; ++j) h.list.push_back(ProdTile{(int32_t)m, i, j, 0});
-        g.n_sym = (int32_t)(h.list.size() - g.sym0);
-        g.full0 = (int64_t)h.list.size();
-        for (size_t m = group_first; m < end; ++m)
-            for (int j = 0; j < h.mats[m].np / kPad; ++j)
-                for (int i = 0; i < h.mats[m].kp / kPad; ++i) h.list.push_back(ProdTile{(int32_t)m, i, j, 0});
-        g.n_full = (int32_t)(h.list.size() - g.full0);
-        h.groups.push_back(g);
-        h.max_sym = std::max(h.max_sym, g.n_sym);
-        h.max_full = std::max(h.max_full, g.n_full);
+        add_group(h, group_first, end);
         h.area = std::max(h.area, used);
         group_first = end;
         used = 0;
@@ -444,7 +547,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         }
         if (h.has & kHasU) {   // its place in a group's buffers
             const int64_t x = round_up64((int64_t)d.kp * d.np * 2, 256), a = round_up64((int64_t)d.kp * d.kp * 2, 256);
-            if (used > 0 && used + 3 * x + 2 * a > kGroupBytes) close_group(h.mats.size());
+            if (used > 0 && used + 3 * x + 2 * a > budget) close_group(h.mats.size());
             d.x[0] = used;
             d.x[1] = used + x;
             d.lo = used + 2 * x;
@@ -457,6 +560,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
     if (h.has & kHasU) {
         close_group(h.mats.size());
         if ((int64_t)h.list.size() > INT32_MAX) return fail(ZERO1_EINVAL, "too many tiles in one plan");
+        if (h.groups.size() > ZERO1_MUON_MAX_GROUPS) return fail(ZERO1_EINVAL, "too many groups in one plan");
     }
     return ZERO1_OK;
 }
@@ -532,11 +636,13 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
     const bool u_f32 = (plan->flags & ZERO1_U_F32) != 0;
     const MuonArgs ma = muon_args(hp, flags);
     for (g.group = 0; g.group < plan->n_groups; ++g.group) {
-        Z1_HIP(launch_ns_prepare(g, u_f32, plan->max_full, s));
+        const zero1_matrix_group& q = plan->groups[g.group];
+        const TileShape sym = (TileShape)q.sym_tile, full = (TileShape)q.full_tile;
+        Z1_HIP(launch_ns_prepare(g, u_f32, q.n_blocks, s));
         for (int it = 0; it < hp->ns_steps; ++it) {
-            Z1_HIP(launch_ns_gram(g, it, plan->max_sym, s));
-            Z1_HIP(launch_ns_poly(g, plan->max_sym, s));
-            Z1_HIP(launch_ns_apply(g, it, u_f32, it + 1 == hp->ns_steps ? last : kNsMid, ma, plan->max_full, s));
+            Z1_HIP(launch_ns_gram(g, it, sym, q.n_sym, s));
+            Z1_HIP(launch_ns_poly(g, sym, q.n_sym, s));
+            Z1_HIP(launch_ns_apply(g, it, u_f32, it + 1 == hp->ns_steps ? last : kNsMid, ma, full, q.n_full, s));
         }
     }
     return ZERO1_OK;
@@ -592,8 +698,7 @@ zero1_status zero1_muon_plan(const zero1_matrix* mats, int n_mats, uint32_t flag
         p.n_mats = n_mats;
         p.n_tiles = (int32_t)h.tiles.size();
         p.n_groups = (int32_t)h.groups.size();
-        p.max_sym = h.max_sym;
-        p.max_full = h.max_full;
+        std::copy(h.shape.begin(), h.shape.end(), p.groups);
         p.flags = flags & kPlanFlags;
         p.has = h.has;
         p.device = dev;

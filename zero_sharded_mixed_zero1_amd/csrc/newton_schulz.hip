@@ -21,8 +21,12 @@
 // The norm enters as a power of two 2^e, exact on the way into fp16, and a
 // factor r in [1, 2) folded into the first step: X = r Xs / S.
 //
-// Operands are padded with zeros to multiples of 128, so no product checks
-// bounds; a zero row stays zero through the iteration.
+// Layout: X, A and B lie in blocks of 64 x 64 (8 KiB), block rows one after the
+// other, rows of 128 bytes inside a block with their 16-byte slots permuted
+// (slot_key).  A block is what the products stage: eight loads of 1 KiB go from
+// memory to LDS as they lie, and from there both directions read without bank
+// conflicts: along rows (ds_read_b128) and, for X in B X, down columns
+// (ds_read_b64_tr_b16).  The padding up to 64 is zero and stays zero.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -36,174 +40,344 @@ using namespace dev;
 typedef _Float16 half_t;
 typedef half_t h4 __attribute__((ext_vector_type(4)));
 typedef half_t h8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
 
-constexpr int kT = kPad;           // tile side
+constexpr int kB = kPad;                 // block side
+constexpr int kBlock = kB * kB;          // elements of a block
+
+// What the 16-byte slots of row r are XORed with, so that what sixteen lanes
+// read at once falls into different banks (64 banks: 256 bytes, two rows).
+// Along rows they read one slot of 16 neighbouring rows: the key takes each
+// value once over (r >> 1) & 7.  Down columns they read 32 bytes of 4
+// neighbouring rows, the four groups of a wave rows 8 apart: bits 0 and 2 of
+// r >> 1 select the 32-byte unit.  (A key over r & 7 costs the second kind 19 %
+// more LDS cycles.)
+__device__ __forceinline__ int slot_key(int r)
+{
+    const int v = r >> 1;
+    return ((v >> 1) & 1) | ((v & 1) << 1) | (v & 4);
+}
+
+// Element (i, j) of a matrix of `cb` blocks a row.
+__device__ __forceinline__ int64_t elem_at(int i, int j, int cb)
+{
+    const int r = i & (kB - 1), c = j & (kB - 1);
+    return ((int64_t)(i >> 6) * cb + (j >> 6)) * kBlock + r * kB + (((c >> 3) ^ slot_key(r)) << 3) + (c & 7);
+}
 
 __device__ __forceinline__ float to_f32(uint16_t h) { return widen(h); }
 __device__ __forceinline__ float to_f32(float x) { return x; }
 
 // ------------------------------------------------------------- prepare
 // Xs = 2^e u as hi (and lo where u is fp32: a bf16 u fits hi exactly), u
-// transposed if tall, zeros in the padding.  One workgroup a 128 x 128 tile;
-// a tall u goes through LDS so that both sides are read and written by rows.
+// transposed if tall, zeros in the padding.  One workgroup a block.
 template <typename U>
 __global__ __launch_bounds__(kThreads) void ns_prepare_kernel(NsArgs g)
 {
     constexpr bool LO = sizeof(U) == 4;
-    __shared__ float sh[kT / 2][kT + 1];
+    __shared__ float sh[kB][kB + 1];
     const GroupDesc& gd = g.groups[g.group];
-    if ((int)blockIdx.x >= gd.n_full) return;
-    const ProdTile pt = g.list[gd.full0 + blockIdx.x];
+    if ((int)blockIdx.x >= gd.n_blocks) return;
+    const ProdTile pt = g.list[gd.blocks0 + blockIdx.x];
     const MatDesc& d = g.mats[pt.mat];
     const int e = g.norms[pt.mat].e;
     const U* u = static_cast<const U*>(d.u);
-    half_t* hi = reinterpret_cast<half_t*>(g.area + d.x[0]);
-    half_t* lo = reinterpret_cast<half_t*>(g.area + d.lo);
-    const int i0 = pt.i * kT, j0 = pt.j * kT;
+    const int i0 = pt.i * kB, j0 = pt.j * kB;
+    // rows of u are rows of X, or columns when u is tall
+    const int a0 = d.tall ? j0 : i0, b0 = d.tall ? i0 : j0;
     const int c = threadIdx.x & 63, r0 = threadIdx.x >> 6;
-    auto put = [&](int i, int j, float x) {
-        const int64_t at = (int64_t)i * d.np + j;
-        const half_t h = (half_t)x;
-        hi[at] = h;
-        if constexpr (LO) lo[at] = (half_t)(x - (float)h);
-    };
-    if (!d.tall) {
-        for (int r = r0; r < kT; r += 4)
-            for (int cc = c; cc < kT; cc += 64) {
-                const int i = i0 + r, j = j0 + cc;
-                const bool in = i < d.k && j < d.n;
-                put(i, j, in ? ldexpf(to_f32(u[(int64_t)i * d.ldu + j]), e) : 0.0f);
-            }
-    } else {
-        for (int half = 0; half < 2; ++half) {   // rows of u = columns j of X
-            const int jb = j0 + half * (kT / 2);
-            for (int r = r0; r < kT / 2; r += 4)
-                for (int cc = c; cc < kT; cc += 64) {
-                    const int j = jb + r, i = i0 + cc;
-                    const bool in = i < d.k && j < d.n;
-                    sh[r][cc] = in ? ldexpf(to_f32(u[(int64_t)j * d.ldu + i]), e) : 0.0f;
-                }
-            __syncthreads();
-            for (int r = r0; r < kT; r += 4) put(i0 + r, jb + c, sh[c][r]);
-            __syncthreads();
+#pragma unroll 4
+    for (int r = r0; r < kB; r += 4) {
+        const bool in = a0 + r < d.rows && b0 + c < d.cols;
+        const float x = in ? ldexpf(to_f32(u[(int64_t)(a0 + r) * d.ldu + b0 + c]), e) : 0.0f;
+        if (d.tall) sh[c][r] = x;
+        else sh[r][c] = x;
+    }
+    __syncthreads();
+    const int64_t at = ((int64_t)pt.i * (d.np / kB) + pt.j) * kBlock;
+    half_t* hi = reinterpret_cast<half_t*>(g.area + d.x[0]) + at;
+    half_t* lo = reinterpret_cast<half_t*>(g.area + d.lo) + at;
+#pragma unroll
+    for (int h = 0; h < kBlock / 8 / kThreads; ++h) {
+        const int slot = threadIdx.x + h * kThreads, r = slot >> 3, j = ((slot & 7) ^ slot_key(r)) << 3;
+        h8 vh, vl;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            vh[q] = (half_t)sh[r][j + q];
+            vl[q] = (half_t)(sh[r][j + q] - (float)vh[q]);
         }
+        *reinterpret_cast<h8*>(hi + slot * 8) = vh;
+        if constexpr (LO) *reinterpret_cast<h8*>(lo + slot * 8) = vl;
     }
 }
 
 // ------------------------------------------------------------- products
-// C = P Q^T of a 128 x 128 tile, four waves of 64 x 64, 32 of the inner
-// dimension at a time.  P and Q are read by rows along the inner dimension;
-// QT: Q is given transposed (inner dimension by rows).  The operands of the
-// MFMA are swapped, so that a lane holds four neighbouring columns of C:
+// C = P Q^T of a tile of (64 MB WR) x (64 WC): WR x WC waves, each of 64 MB
+// rows and 64 columns in MFMAs of 16 x 16 x 32.  The operands of the MFMA are
+// swapped, so that a lane holds four neighbouring columns of C:
 // acc[x][y][r] = C[16 x + (lane & 15)][16 y + 4 (lane >> 4) + r].
-constexpr int kInner = 32, kLdsRow = kInner + 8;
+//
+// S stages of 64 of the inner dimension lie in LDS: while one is multiplied,
+// the loads of the next S - 1 are under way.
+template <int WR, int WC, int MB, int S>
+struct Tile {
+    static constexpr int kWaves = WR * WC, kThr = 64 * kWaves;
+    static constexpr int kRowBlocks = WR * MB, kColBlocks = WC, kBlocks = kRowBlocks + kColBlocks;
+    static constexpr int kStage = kBlocks * kBlock;            // elements of a stage
+    static constexpr int kLoads = (kBlocks * 8 + kWaves - 1) / kWaves;   // 1 KiB loads a wave issues a stage
+    static constexpr bool kEven = kBlocks * 8 % kWaves == 0;
+    // the epilogue's staging of one block a wave, rows padded by 16 bytes
+    static constexpr int kOutRow = kB + 4;
+    static constexpr int kOut = kB * kOutRow;                  // floats a wave
+    static constexpr size_t kStages = (size_t)S * kStage * 2, kOuts = (size_t)kWaves * kOut * 4;
+    static constexpr size_t kLds = kStages > kOuts ? kStages : kOuts;
+    static_assert(kLds <= 160 * 1024, "LDS of a CU");
+    static constexpr int kMinBlocks = kLds <= 80 * 1024 ? 2 : 1;   // workgroups a CU holds
+};
 
-typedef half_t Stage[kT][kLdsRow];
-
-template <bool QT>
-__device__ __forceinline__ void product(const half_t* P, int64_t ldp, const half_t* Q, int64_t ldq, int inner,
-                                        Stage* sp, Stage* sq, f32x4 (&acc)[4][4])
+// One wave copies 1 KiB from memory to LDS: lane l its 16 bytes at base +
+// 16 l, to lds + 16 l.  No register receives the data; whoever reads it waits
+// (stage_wait) first.
+__device__ __forceinline__ void load_1k(const half_t* base, uint32_t lane_off, uint32_t lds)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wi = (wave >> 1) * 64, wj = (wave & 1) * 64;
-    h8 rp[2], rq[2];
-    auto fetch = [&](int k0) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(lane_off), "s"(base)
+                 : "memory");
+}
+
+// All of this wave's loads but the N youngest have reached LDS.
+template <int N>
+__device__ __forceinline__ void stage_wait()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt is six bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// P: block row p0 of a matrix of `pc` blocks a row and `pr` block rows, read
+// along its rows; Q: block row q0 of one of `qr` by `qc` likewise, or, with QT,
+// block column q0, read down its columns.  `steps` blocks of the inner
+// dimension.  Tiles past the last block row or column repeat it (their results
+// are not stored).
+template <typename T, int WR, int WC, int MB, int S, bool QT>
+__device__ __forceinline__ void product(const half_t* P, int p0, int pr, int pc, const half_t* Q, int q0, int qr,
+                                        int qc, int steps, half_t* sh, f32x4 (&acc)[4 * MB][4])
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wi = wave / WC, wj = wave % WC;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) half_t*)sh;
+    const half_t* src[T::kLoads];
+    int64_t adv[T::kLoads];
+    uint32_t dst[T::kLoads];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int ch = tid + h * kThreads;
-            rp[h] = *reinterpret_cast<const h8*>(P + (int64_t)(ch >> 2) * ldp + k0 + (ch & 3) * 8);
-            if constexpr (!QT) rq[h] = *reinterpret_cast<const h8*>(Q + (int64_t)(ch >> 2) * ldq + k0 + (ch & 3) * 8);
-            else rq[h] = *reinterpret_cast<const h8*>(Q + (int64_t)(k0 + (ch >> 4)) * ldq + (ch & 15) * 8);
+    for (int l = 0; l < T::kLoads; ++l) {
+        // (where the loads do not divide evenly, the last waves repeat the last)
+        const int idx = T::kEven ? wave * T::kLoads + l : min(wave * T::kLoads + l, T::kBlocks * 8 - 1);
+        const int blk = idx >> 3, part = idx & 7;
+        if (blk < T::kRowBlocks) {
+            const int b = p0 + blk < pr ? p0 + blk : pr - 1;
+            src[l] = P + (int64_t)b * pc * kBlock + part * 512;
+            adv[l] = kBlock;
+        } else if (!QT) {
+            const int b = q0 + blk - T::kRowBlocks < qr ? q0 + blk - T::kRowBlocks : qr - 1;
+            src[l] = Q + (int64_t)b * qc * kBlock + part * 512;
+            adv[l] = kBlock;
+        } else {
+            const int b = q0 + blk - T::kRowBlocks < qc ? q0 + blk - T::kRowBlocks : qc - 1;
+            src[l] = Q + (int64_t)b * kBlock + part * 512;
+            adv[l] = (int64_t)qc * kBlock;
+        }
+        dst[l] = lds0 + idx * 1024;
+    }
+    auto issue = [&](int buf) {
+#pragma unroll
+        for (int l = 0; l < T::kLoads; ++l) {
+            load_1k(src[l], lane * 16, dst[l] + buf * (T::kStage * 2));
+            src[l] += adv[l];
         }
     };
-    auto stash = [&](int b) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int ch = tid + h * kThreads;
-            *reinterpret_cast<h8*>(&sp[b][ch >> 2][(ch & 3) * 8]) = rp[h];
-            if constexpr (!QT) *reinterpret_cast<h8*>(&sq[b][ch >> 2][(ch & 3) * 8]) = rq[h];
-            else {
+    for (int x = 0; x < 4 * MB; ++x)
 #pragma unroll
-                for (int v = 0; v < 8; ++v) sq[b][(ch & 15) * 8 + v][ch >> 4] = rq[h][v];
+        for (int y = 0; y < 4; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
+    // lane's place in a block: row lane & 15 (of 16), slot lane >> 4 (+ 4 for
+    // the second half of the inner block); rows 16 apart have the same key
+    const int row = lane & 15, key = slot_key(row);
+    const int off[2] = {row * kB + (((lane >> 4) ^ key) << 3), row * kB + (((4 + (lane >> 4)) ^ key) << 3)};
+    // down columns: the lane's row inside a group of 4, and its 8 bytes of the
+    // group's 32
+    const int trow = 8 * (lane >> 4) + ((lane & 15) >> 2), tq = lane & 3;
+    struct Frag {
+        h8 p[4 * MB], q[4];
+    };
+    // the wave's operands for half h of the stage in buffer `buf`
+    auto read = [&](Frag& f, int buf, int h) {
+        const half_t* sp = sh + buf * T::kStage + wi * MB * kBlock;
+        const half_t* sq = sh + buf * T::kStage + (T::kRowBlocks + wj) * kBlock;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if constexpr (!QT) {
+                f.q[y] = *reinterpret_cast<const h8*>(sq + y * 16 * kB + off[h]);
+            } else {
+                // columns 16 y + 4 tq.. of rows 32 h + trow and 4 below
+                typedef __attribute__((address_space(3))) s4 lds_s4;
+                union { s4 s[2]; h8 v; } both;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int r = 32 * h + trow + 4 * z, c = 16 * y + 4 * tq;
+                    const half_t* a = sq + r * kB + (((c >> 3) ^ slot_key(r)) << 3) + (c & 7);
+                    both.s[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)a);
+                }
+                f.q[y] = both.v;
             }
         }
+#pragma unroll
+        for (int x = 0; x < 4 * MB; ++x) f.p[x] = *reinterpret_cast<const h8*>(sp + x * 16 * kB + off[h]);
     };
+    auto multiply = [&](const Frag& f) {
+#pragma unroll
+        for (int x = 0; x < 4 * MB; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.q[y], f.p[x], acc[x][y], 0, 0, 0);
+    };
+    // the order that a half is scheduled in: its MFMAs with the LDS reads of the
+    // next spread between them
+    auto spread = [] {
+        constexpr int kMfma = 16 * MB, kReads = 4 * MB + (QT ? 8 : 4), kEach = kMfma / kReads;
+#pragma unroll
+        for (int i = 0; i < kReads; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kMfma - kReads * kEach, 0);
+    };
+    // each half's operands are read from LDS while the half before is
+    // multiplied; the barrier lies between the halves, when this wave's reads
+    // of stage t are done and its loads of stage t + 1 have arrived
+    int put = 0, get = 0;   // buffers: the next one to load into, the one to read
+    auto next = [](int b) { return b + 1 == S ? 0 : b + 1; };
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+        if (k < steps) {
+            issue(put);
+            put = next(put);
+        }
+    Frag f0, f1;
+    if (steps > S - 1) stage_wait<(S - 1) * T::kLoads>();
+    else stage_wait<0>();
+    __syncthreads();
+    read(f0, get, 0);
+    for (int t = 0; t < steps; ++t) {
+        read(f1, get, 1);
+        multiply(f0);
+        spread();
+        if (t + 1 < steps) {
+            if (t + S - 1 < steps) stage_wait<(S - 2) * T::kLoads>();   // stages t + 2 .. t + S - 1 may be under way
+            else stage_wait<0>();
+            __syncthreads();
+            if (t + S < steps) {
+                issue(put);
+                put = next(put);
+            }
+            get = next(get);
+        }
+        // (the last round reads the last stage again: the loop stays one block)
+        read(f0, get, 0);
+        multiply(f1);
+        spread();
+    }
+    __syncthreads();   // the stages are free for the epilogue
+}
+
+// LDS accesses of one wave execute in order; this keeps the compiler from
+// moving them past each other.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// One 64 x 64 block of the wave's accumulators into its staging area.
+template <int ROW>
+__device__ __forceinline__ void stage_block(const f32x4 (*acc)[4], float* out)
+{
+    const int lane = threadIdx.x & 63;
+    wave_sync();
 #pragma unroll
     for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
-    fetch(0);
-    stash(0);
-    __syncthreads();
-    int b = 0;
-    for (int k0 = 0; k0 < inner; k0 += kInner, b ^= 1) {
-        const bool more = k0 + kInner < inner;
-        if (more) fetch(k0 + kInner);
-        h8 p[4], q[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            p[x] = *reinterpret_cast<const h8*>(&sp[b][wi + 16 * x + (lane & 15)][(lane >> 4) * 8]);
-            q[x] = *reinterpret_cast<const h8*>(&sq[b][wj + 16 * x + (lane & 15)][(lane >> 4) * 8]);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[y], p[x], acc[x][y], 0, 0, 0);
-        if (more) stash(b ^ 1);
-        __syncthreads();
-    }
+        for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<f32x4*>(out + (16 * x + (lane & 15)) * ROW + 16 * y + 4 * (lane >> 4)) = acc[x][y];
+    wave_sync();
 }
 
 enum Op : int { kGram = 0, kPoly = 1 };
 
-// A = X X^T or B = b A + c A A: the tiles of the upper triangle, each stored
+// A = X X^T or B = b A + c A A: the blocks of the upper triangle, each stored
 // with its mirror image.
-template <int OP>
-__global__ __launch_bounds__(kThreads) void ns_sym_kernel(NsArgs g, int it)
+template <int OP, int WR, int WC, int MB, int S>
+__global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) void ns_sym_kernel(NsArgs g, int it)
 {
-    __shared__ Stage sp[2], sq[2];
+    using T = Tile<WR, WC, MB, S>;
+    __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
     const GroupDesc& gd = g.groups[g.group];
     if ((int)blockIdx.x >= gd.n_sym) return;
     const ProdTile pt = g.list[gd.sym0 + blockIdx.x];
     const MatDesc& d = g.mats[pt.mat];
     const half_t* src = reinterpret_cast<const half_t*>(g.area + (OP == kGram ? d.x[it & 1] : d.a));
     half_t* dst = reinterpret_cast<half_t*>(g.area + (OP == kGram ? d.a : d.b));
-    const int64_t lds = OP == kGram ? d.np : d.kp;
-    f32x4 acc[4][4];
-    product<false>(src + (int64_t)pt.i * kT * lds, lds, src + (int64_t)pt.j * kT * lds, lds, (int)lds, sp, sq, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int bi = pt.i * kT + (wave >> 1) * 64 + (lane & 15), bj = pt.j * kT + (wave & 1) * 64 + (lane >> 4) * 4;
+    const int kb = d.kp / kB, inner = OP == kGram ? d.np / kB : kb;
+    f32x4 acc[4 * MB][4];
+    product<T, WR, WC, MB, S, false>(src, pt.i, kb, inner, src, pt.j, kb, inner, inner, reinterpret_cast<half_t*>(lds),
+                                  acc);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    float* out = reinterpret_cast<float*>(lds) + wave * T::kOut;
     const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
     const float f = OP == kGram ? r * r / kNsScale : g.c / kNsScale;
+    const int bj = pt.j + wave % WC;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int m = 0; m < MB; ++m) {
+        const int bi = pt.i + (wave / WC) * MB + m;
+        if (bi > bj || bi >= kb || bj >= kb) continue;   // below the diagonal, or past the end
+        stage_block<T::kOutRow>(acc + 4 * m, out);
+        const int64_t at = ((int64_t)bi * kb + bj) * kBlock, mirror = ((int64_t)bj * kb + bi) * kBlock;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int i = bi + 16 * x, j = bj + 16 * y;
-            h4 v;
-            h4 av{};
-            if constexpr (OP == kPoly) av = *reinterpret_cast<const h4*>(src + (int64_t)i * d.kp + j);
+        for (int h = 0; h < 8; ++h) {
+            const int slot = lane + 64 * h, row = slot >> 3, j = ((slot & 7) ^ slot_key(row)) << 3;
+            h8 av{}, v;
+            if constexpr (OP == kPoly) av = *reinterpret_cast<const h8*>(src + at + slot * 8);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float z = f * acc[x][y][q];
+            for (int q = 0; q < 8; ++q) {
+                float z = f * out[row * T::kOutRow + j + q];
                 if constexpr (OP == kPoly) z += g.b * (float)av[q];
                 v[q] = (half_t)z;
             }
-            *reinterpret_cast<h4*>(dst + (int64_t)i * d.kp + j) = v;
-            if (pt.i != pt.j) {
+            *reinterpret_cast<h8*>(dst + at + slot * 8) = v;
+            if (bi != bj) {
+                // the block (bj, bi): row `row` of it is column `row` of this one
+                h8 w{};
+                if constexpr (OP == kPoly) av = *reinterpret_cast<const h8*>(src + mirror + slot * 8);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) dst[(int64_t)(j + q) * d.kp + i] = v[q];
+                for (int q = 0; q < 8; ++q) {
+                    float z = f * out[(j + q) * T::kOutRow + row];
+                    if constexpr (OP == kPoly) z += g.b * (float)av[q];
+                    w[q] = (half_t)z;
+                }
+                *reinterpret_cast<h8*>(dst + mirror + slot * 8) = w;
             }
         }
+    }
 }
 
 // X <- a X + B X; the last step writes o as bf16, or updates the master and
 // the parameter with it, instead of X.
-template <int LAST>
-__global__ __launch_bounds__(kThreads) void ns_apply_kernel(NsArgs g, int it, int has_lo, MuonArgs ma)
+template <int LAST, int WR, int WC, int MB, int S>
+__global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) void ns_apply_kernel(NsArgs g, int it, int has_lo, MuonArgs ma)
 {
-    __shared__ Stage sp[2], sq[2];
+    using T = Tile<WR, WC, MB, S>;
+    __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
     const GroupDesc& gd = g.groups[g.group];
     if ((int)blockIdx.x >= gd.n_full) return;
     const ProdTile pt = g.list[gd.full0 + blockIdx.x];
@@ -212,49 +386,75 @@ __global__ __launch_bounds__(kThreads) void ns_apply_kernel(NsArgs g, int it, in
     half_t* xo = reinterpret_cast<half_t*>(g.area + d.x[(it & 1) ^ 1]);
     half_t* lo = reinterpret_cast<half_t*>(g.area + d.lo);
     const half_t* bm = reinterpret_cast<const half_t*>(g.area + d.b);
-    f32x4 acc[4][4];
-    product<true>(bm + (int64_t)pt.i * kT * d.kp, d.kp, xi + pt.j * kT, d.np, d.kp, sp, sq, acc);
+    const int kb = d.kp / kB, nb = d.np / kB;
+    f32x4 acc[4 * MB][4];
+    product<T, WR, WC, MB, S, true>(bm, pt.i, kb, kb, xi, pt.j, kb, nb, kb, reinterpret_cast<half_t*>(lds), acc);
     if constexpr (LAST == kNsUpdate) use_device_scalars(ma, nullptr);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int bi = pt.i * kT + (wave >> 1) * 64 + (lane & 15), bj = pt.j * kT + (wave & 1) * 64 + (lane >> 4) * 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    float* out = reinterpret_cast<float*>(lds) + wave * T::kOut;
     const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
     const float fa = g.a * r, fb = r / kNsScale;
+    const int bj = pt.j + wave % WC;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int m = 0; m < MB; ++m) {
+        const int bi = pt.i + (wave / WC) * MB + m;
+        if (bi >= kb || bj >= nb) continue;
+        stage_block<T::kOutRow>(acc + 4 * m, out);
+        const int64_t at = ((int64_t)bi * nb + bj) * kBlock;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int i = bi + 16 * x, j = bj + 16 * y;
-            const int64_t at = (int64_t)i * d.np + j;
-            const h4 xh = *reinterpret_cast<const h4*>(xi + at);
-            h4 xl{};
-            if (has_lo) xl = *reinterpret_cast<const h4*>(lo + at);
-            h4 vh, vl;
+        for (int h = 0; h < 8; ++h) {
+            const int slot = lane + 64 * h, row = slot >> 3, j = ((slot & 7) ^ slot_key(row)) << 3;
+            const h8 xh = *reinterpret_cast<const h8*>(xi + at + slot * 8);
+            h8 xl{};
+            if (has_lo) xl = *reinterpret_cast<const h8*>(lo + at + slot * 8);
+            float z[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float z = fa * ((float)xh[q] + (float)xl[q]) + fb * acc[x][y][q];
-                if constexpr (LAST == kNsMid) {
-                    vh[q] = (half_t)z;
-                    vl[q] = (half_t)(z - (float)vh[q]);
-                } else {
-                    const int row = d.tall ? j + q : i, col = d.tall ? i : j + q;
-                    if (row < d.rows && col < d.cols) {
-                        const float o = z / kNsScale;
-                        if constexpr (LAST == kNsWriteO) {
-                            d.o[(int64_t)row * d.ldo + col] = bf16_rne(o);
-                        } else {
-                            const int64_t p = (int64_t)row * d.ld + col;
-                            const float v = muon_elem(d.master[p], o, ma.lr * d.scale, ma);
-                            d.master[p] = v;
-                            d.param[p] = bf16_rne(v);
-                        }
-                    }
-                }
-            }
+            for (int q = 0; q < 8; ++q)
+                z[q] = fa * ((float)xh[q] + (float)xl[q]) + fb * out[row * T::kOutRow + j + q];
             if constexpr (LAST == kNsMid) {
-                *reinterpret_cast<h4*>(xo + at) = vh;
-                *reinterpret_cast<h4*>(lo + at) = vl;
+                h8 vh, vl;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    vh[q] = (half_t)z[q];
+                    vl[q] = (half_t)(z[q] - (float)vh[q]);
+                }
+                *reinterpret_cast<h8*>(xo + at + slot * 8) = vh;
+                *reinterpret_cast<h8*>(lo + at + slot * 8) = vl;
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) out[row * T::kOutRow + j + q] = z[q] / kNsScale;
             }
         }
+        if constexpr (LAST != kNsMid) {
+            // rows of o: the block's rows, or its columns when u is tall; four
+            // elements a lane
+            wave_sync();
+            const int r0 = (d.tall ? bj : bi) * kB, c0 = (d.tall ? bi : bj) * kB;
+            const float eta = ma.lr * d.scale;
+#pragma unroll 4
+            for (int h = 0; h < 16; ++h) {
+                const int rr = 4 * h + (lane >> 4), cc = 4 * (lane & 15);
+                const int64_t row = r0 + rr, col = c0 + cc;
+                const int64_t left = d.cols - col;
+                const int n = row < d.rows ? (left >= 4 ? 4 : (left > 0 ? (int)left : 0)) : 0;
+                float o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    o[q] = d.tall ? out[(cc + q) * T::kOutRow + rr] : out[rr * T::kOutRow + cc + q];
+                if constexpr (LAST == kNsWriteO) {
+                    store_quad(d.o + row * d.ldo + col, n, o);
+                } else {
+                    const int64_t p = row * d.ld + col;
+                    float v[4];
+                    load_quad(d.master + p, n, v);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = muon_elem(v[q], o[q], eta, ma);
+                    store_quad(d.master + p, n, v);
+                    store_quad(d.param + p, n, v);
+                }
+            }
+        }
+    }
 }
 
 }  // namespace
@@ -267,27 +467,47 @@ hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, int grid, hipStream_t 
     return hipGetLastError();
 }
 
-hipError_t launch_ns_gram(const NsArgs& g, int it, int grid, hipStream_t s)
+#define Z1_TILES(tile, CALL)                                       \
+    do {                                                           \
+        if ((tile) == kTile256) CALL(2, 4, 2, 2);                  \
+        else if ((tile) == kTile192) CALL(3, 3, 1, 3);             \
+        else CALL(2, 2, 1, 2);                                     \
+    } while (0)
+
+hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hipStream_t s)
 {
-    ns_sym_kernel<kGram><<<dim3(grid), dim3(kThreads), 0, s>>>(g, it);
+#define Z1_CALL(WR, WC, MB, S) ns_sym_kernel<kGram, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), 0, s>>>(g, it)
+    Z1_TILES(tile, Z1_CALL);
+#undef Z1_CALL
     return hipGetLastError();
 }
 
-hipError_t launch_ns_poly(const NsArgs& g, int grid, hipStream_t s)
+hipError_t launch_ns_poly(const NsArgs& g, TileShape tile, int grid, hipStream_t s)
 {
-    ns_sym_kernel<kPoly><<<dim3(grid), dim3(kThreads), 0, s>>>(g, 1);
+#define Z1_CALL(WR, WC, MB, S) ns_sym_kernel<kPoly, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), 0, s>>>(g, 1)
+    Z1_TILES(tile, Z1_CALL);
+#undef Z1_CALL
     return hipGetLastError();
 }
 
-hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, int grid,
-                           hipStream_t s)
+hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, TileShape tile,
+                           int grid, hipStream_t s)
 {
     const int has_lo = it > 0 || u_f32 ? 1 : 0;
-    const dim3 gr(grid), bl(kThreads);
-    if (last == kNsMid) ns_apply_kernel<kNsMid><<<gr, bl, 0, s>>>(g, it, has_lo, ma);
-    else if (last == kNsWriteO) ns_apply_kernel<kNsWriteO><<<gr, bl, 0, s>>>(g, it, has_lo, ma);
-    else ns_apply_kernel<kNsUpdate><<<gr, bl, 0, s>>>(g, it, has_lo, ma);
+#define Z1_APPLY(LAST, WR, WC, MB, S) \
+    ns_apply_kernel<LAST, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), 0, s>>>(g, it, has_lo, ma)
+#define Z1_MID(WR, WC, MB, S) Z1_APPLY(kNsMid, WR, WC, MB, S)
+#define Z1_O(WR, WC, MB, S) Z1_APPLY(kNsWriteO, WR, WC, MB, S)
+#define Z1_UPD(WR, WC, MB, S) Z1_APPLY(kNsUpdate, WR, WC, MB, S)
+    if (last == kNsMid) Z1_TILES(tile, Z1_MID);
+    else if (last == kNsWriteO) Z1_TILES(tile, Z1_O);
+    else Z1_TILES(tile, Z1_UPD);
+#undef Z1_UPD
+#undef Z1_O
+#undef Z1_MID
+#undef Z1_APPLY
     return hipGetLastError();
 }
+#undef Z1_TILES
 
 }  // namespace z1
