@@ -516,7 +516,7 @@ typedef struct zero1_matrix {
 #define ZERO1_MUON_MAX_GROUPS 64
 typedef struct zero1_matrix_group {
     int32_t n_sym, n_full, n_blocks;
-    int16_t sym_tile, full_tile;
+    int16_t sym_tile, full_tile, thin, reserved;
 } zero1_matrix_group;
 
 /* A validated list of matrices uploaded by zero1_muon_plan.  Plain data owned
@@ -529,6 +529,7 @@ typedef struct zero1_matrix_plan {
     uint32_t flags;         /* ZERO1_MV_BF16, ZERO1_U_F32                       */
     uint32_t has;           /* which buffers the matrices have                  */
     int32_t device;         /* calls are made with this device current          */
+    int32_t n_dense, dense_tiles;
     zero1_matrix_group groups[ZERO1_MUON_MAX_GROUPS];
 } zero1_matrix_plan;
 

@@ -36,11 +36,13 @@ struct MatDesc {
     int64_t vcols, qpr;
     int32_t vrows;
     int32_t tile0, n_tiles;        // its streaming tiles
+    int32_t split, n_parts;        // thin: columns a part of the gram sum, parts
     int32_t reserved;
-    // byte offsets inside the workspace's group area
+    // byte offsets inside the workspace's group area: X twice, its low halves,
+    // A, B; of a thin matrix fp32 X, the parts' exponents, the parts, P
     int64_t x[2], lo, a, b;
 };
-static_assert(sizeof(MatDesc) == 184, "matrix descriptor layout");
+static_assert(sizeof(MatDesc) == 192, "matrix descriptor layout");
 
 // A streaming tile: quads [512 idx, +512) of matrix `mat`, the first of them
 // quad q0 of row row0.
@@ -54,11 +56,20 @@ struct ProdTile {
 };
 
 // Matrices that are iterated together, and what there is of them in the list
-// of ProdTiles: tiles of A and B (upper triangle), tiles of X, blocks of X.
+// of ProdTiles: tiles of A and B (upper triangle), tiles of X, blocks of X; of
+// thin matrices parts of the gram sum (i: the part, j: its first 64 columns)
+// and X's columns in 64s (j).
 struct GroupDesc {
     int64_t sym0, full0, blocks0;
-    int32_t n_sym, n_full, n_blocks, reserved;
+    int32_t n_sym, n_full, n_blocks;
+    int32_t first;                 // its first matrix
 };
+
+// Matrices with k up to this take the kernels of ns_thin.hip.
+constexpr int kThin = 128;
+constexpr int kThinMaxParts = 32;
+// Growth of the product of a segment's steps (ns_thin.hip).
+constexpr double kThinGrowth = 2048.0;
 
 // Shapes of the products' tiles.
 enum TileShape : int { kTile128 = 0, kTile192 = 1, kTile256 = 2 };
@@ -118,6 +129,14 @@ hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hip
 hipError_t launch_ns_poly(const NsArgs& g, TileShape tile, int grid, hipStream_t s);
 hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, TileShape tile,
                            int grid, hipStream_t s);
+
+// Thin matrices padded to kp (32, 64 or 128) rows; f32: X is read as fp32; mid:
+// from the workspace.
+hipError_t launch_thin_gram(const NsArgs& g, int kp, bool f32, int mid, int grid, hipStream_t s);
+hipError_t launch_thin_poly(const NsArgs& g, int kp, int mid, int steps, double eps, NormRec* norms, int grid,
+                            hipStream_t s);
+hipError_t launch_thin_apply(const NsArgs& g, int kp, bool f32, int mid, NsLast last, const MuonArgs& ma, int grid,
+                             hipStream_t s);
 
 #ifdef __HIPCC__
 // ------------------------------------------------------------------ device

@@ -149,47 +149,76 @@ zero1_status check_hparams(const zero1_muon_hparams* hp)
     return check_scalars(hp);
 }
 
-// The singular values s <= 1 of the normalised matrix go through
-// p(s) = a s + b s^3 + c s^5 a step.  What bounds them bounds every entry of
-// X, A and B, which fp16 holds times 2^12: 3, 9 and 12 leave a third of its
-// range for roundings.
+// What a step does to singular values s in [0, top], on t = s^2: the largest
+// |p(s)| = s |q(t)|, |q(t)| = |a + b t + c t^2| and |b t + c t^2| (B's
+// eigenvalues).
+struct Reach {
+    double p, q, b;
+};
+
+Reach reach(const zero1_muon_hparams* hp, double top)
+{
+    const double a = hp->ns_a, b = hp->ns_b, c = hp->ns_c, tt = top * top;
+    Reach r{0.0, std::fabs(a), 0.0};   // at t = 0
+    auto look = [&](double t) {
+        if (!(t > 0.0 && t <= tt)) return;
+        const double be = b * t + c * t * t, q = a + be;
+        r.p = std::max(r.p, std::sqrt(t) * std::fabs(q));
+        r.q = std::max(r.q, std::fabs(q));
+        r.b = std::max(r.b, std::fabs(be));
+    };
+    look(tt);
+    if (c != 0.0) {
+        look(-b / (2.0 * c));                       // q' = 0
+        const double disc = 9.0 * b * b - 20.0 * a * c;
+        if (disc >= 0.0) {                          // p' = 0
+            look((-3.0 * b + std::sqrt(disc)) / (10.0 * c));
+            look((-3.0 * b - std::sqrt(disc)) / (10.0 * c));
+        }
+    } else if (b != 0.0) {
+        look(-a / (3.0 * b));
+    }
+    return r;
+}
+
+// What bounds the singular values bounds every entry of X, A and B, which fp16
+// holds times 2^12: 3, 9 and 12 leave a third of its range for roundings.
 zero1_status check_iteration(const zero1_muon_hparams* hp)
 {
     if (hp->ns_steps < 1 || hp->ns_steps > kMaxSteps)
         return fail(ZERO1_EINVAL, "ns_steps=%d must be in [1, %d]", hp->ns_steps, kMaxSteps);
     if (!(hp->ns_eps >= 0.0) || std::isinf(hp->ns_eps))
         return fail(ZERO1_EINVAL, "ns_eps=%g must be finite and >= 0", hp->ns_eps);
-    const double a = hp->ns_a, b = hp->ns_b, c = hp->ns_c;
-    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+    if (!std::isfinite(hp->ns_a) || !std::isfinite(hp->ns_b) || !std::isfinite(hp->ns_c))
         return fail(ZERO1_EINVAL, "ns_a, ns_b and ns_c must be finite");
     double top = 1.0;
     for (int it = 0; it < hp->ns_steps; ++it) {
-        // on t = s^2 in [0, top^2]: |b t + c t^2| (B's eigenvalues) and |p(s)|
-        const double tt = top * top;
-        auto beta = [&](double t) { return std::fabs(b * t + c * t * t); };
-        auto poly = [&](double t) { return std::sqrt(t) * std::fabs(a + b * t + c * t * t); };
-        double most_b = beta(tt), most_p = poly(tt);
-        if (c != 0.0) {
-            const double tb = -b / (2.0 * c);
-            if (tb > 0.0 && tb < tt) most_b = std::max(most_b, beta(tb));
-            const double disc = 9.0 * b * b - 20.0 * a * c;
-            if (disc >= 0.0)
-                for (int sgn = -1; sgn <= 1; sgn += 2) {
-                    const double tp = (-3.0 * b + sgn * std::sqrt(disc)) / (10.0 * c);
-                    if (tp > 0.0 && tp < tt) most_p = std::max(most_p, poly(tp));
-                }
-        } else if (b != 0.0) {
-            const double tp = -a / (3.0 * b);
-            if (tp > 0.0 && tp < tt) most_p = std::max(most_p, poly(tp));
-        }
-        if (!(most_b <= 12.0) || !(most_p <= 3.0))
+        const Reach r = reach(hp, top);
+        if (!(r.b <= 12.0) || !(r.p <= 3.0))
             return fail(ZERO1_EINVAL,
                         "ns_a=%g, ns_b=%g, ns_c=%g let singular values reach %g (|b s^2 + c s^4| %g) in step %d; at most 3 "
                         "(12) is supported",
-                        a, b, c, most_p, most_b, it + 1);
-        top = std::max(most_p, 1e-30);
+                        hp->ns_a, hp->ns_b, hp->ns_c, r.p, r.b, it + 1);
+        top = r.p;
     }
     return ZERO1_OK;
+}
+
+// Steps of a thin matrix's iteration, from singular values within `top` on,
+// that are taken as one product: as many as keep what it does to singular
+// values near zero within kThinGrowth.  Moves `top` along.
+int segment_steps(const zero1_muon_hparams* hp, int left, double& top)
+{
+    double growth = 1.0;
+    int m = 0;
+    while (m < left) {
+        const Reach r = reach(hp, top);
+        growth *= std::max(1.0, r.q);
+        if (m > 0 && growth > kThinGrowth) break;
+        top = r.p;
+        ++m;
+    }
+    return m;
 }
 
 MuonArgs muon_args(const zero1_muon_hparams* hp, uint32_t flags)
@@ -323,6 +352,7 @@ struct Host {
     int64_t area = 0;
     uint32_t has = 0;
     int64_t elems = 0;
+    int32_t n_dense = 0, dense_tiles = 0;   // matrices that are not thin (the first ones), their streaming tiles
     size_t off_tiles() const { return round_up(sizeof(MatDesc) * mats.size(), 256); }
     size_t off_groups() const { return off_tiles() + round_up(sizeof(StreamTile) * tiles.size(), 256); }
     size_t off_list() const { return off_groups() + round_up(sizeof(GroupDesc) * groups.size(), 256); }
@@ -394,11 +424,33 @@ zero1_status check_buffers(const zero1_matrix* mats, int n, uint32_t flags)
     return check_blocks(blocks);
 }
 
-int64_t group_bytes(int64_t k, int64_t n)
+// Rows that a thin matrix is padded to; 0: it is not thin.
+int thin_rows(int64_t k) { return k > kThin ? 0 : k > 64 ? 128 : k > 32 ? 64 : 32; }
+
+// Lays out a matrix's iteration buffers from byte `at` on; returns their end.
+int64_t place(MatDesc& d, int64_t at)
 {
-    const int64_t kp = round_up64(k, kPad), np = round_up64(n, kPad);
-    return 2 * (3 * kp * np + 2 * kp * kp);
+    const int thin = thin_rows(d.k);
+    if (thin) {
+        d.kp = thin;
+        d.n_parts = (int32_t)std::min<int64_t>(kThinMaxParts, (d.n + 255) / 256);
+        d.split = (int32_t)round_up64((d.n + d.n_parts - 1) / d.n_parts, kPad);
+        d.n_parts = (d.n + d.split - 1) / d.split;
+        d.x[0] = at;
+        d.lo = d.x[0] + round_up64((int64_t)d.k * d.np * 4, 256);
+        d.a = d.lo + 256;
+        d.b = d.a + (int64_t)d.n_parts * thin * thin * 4;
+        return d.b + (int64_t)2 * thin * thin * 2;
+    }
+    const int64_t x = (int64_t)d.kp * d.np * 2, a = (int64_t)d.kp * d.kp * 2;   // multiples of 8 KiB
+    d.x[0] = at;
+    d.x[1] = at + x;
+    d.lo = at + 2 * x;
+    d.a = at + 3 * x;
+    d.b = d.a + a;
+    return d.b + a;
 }
+static_assert(kThinMaxParts * sizeof(int32_t) <= 256, "exponents of the parts");
 
 // Block rows and columns of X, or of A and B.
 struct Blocks {
@@ -468,10 +520,27 @@ void add_group(Host& h, size_t first, size_t end)
 {
     zero1_matrix_group z;
     std::memset(&z, 0, sizeof z);
-    z.sym_tile = best_tile(h, first, end, true);
-    z.full_tile = best_tile(h, first, end, false);
     GroupDesc g;
     std::memset(&g, 0, sizeof g);
+    g.first = (int32_t)first;
+    z.thin = (int16_t)thin_rows(h.mats[first].k);
+    if (z.thin) {
+        g.sym0 = (int64_t)h.list.size();
+        for (size_t m = first; m < end; ++m)
+            for (int p = 0; p < h.mats[m].n_parts; ++p)
+                h.list.push_back(ProdTile{(int32_t)m, p, p * (h.mats[m].split / kPad), 0});
+        g.n_sym = z.n_sym = (int32_t)(h.list.size() - g.sym0);
+        g.full0 = (int64_t)h.list.size();
+        for (size_t m = first; m < end; ++m)
+            for (int j = 0; j < h.mats[m].np / kPad; ++j) h.list.push_back(ProdTile{(int32_t)m, 0, j, 0});
+        g.n_full = z.n_full = (int32_t)(h.list.size() - g.full0);
+        g.n_blocks = z.n_blocks = (int32_t)(end - first);
+        h.groups.push_back(g);
+        h.shape.push_back(z);
+        return;
+    }
+    z.sym_tile = best_tile(h, first, end, true);
+    z.full_tile = best_tile(h, first, end, false);
     g.sym0 = (int64_t)h.list.size();
     g.n_sym = z.n_sym = add_tiles(h, first, end, kTiles[z.sym_tile].side, true);
     g.full0 = (int64_t)h.list.size();
@@ -480,6 +549,14 @@ void add_group(Host& h, size_t first, size_t end)
     g.n_blocks = z.n_blocks = add_tiles(h, first, end, 1, false);
     h.groups.push_back(g);
     h.shape.push_back(z);
+}
+
+void sides(const zero1_matrix& q, MatDesc& d)
+{
+    d.k = (int32_t)std::min(q.rows, q.cols);
+    d.n = (int32_t)std::max(q.rows, q.cols);
+    d.kp = (int32_t)round_up64(d.k, kPad);
+    d.np = (int32_t)round_up64(d.n, kPad);
 }
 
 zero1_status build(const zero1_matrix* mats, int n, Host& h)
@@ -499,8 +576,14 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         return small(a) != small(b) ? small(a) > small(b) : large(a) > large(b);
     });
     int64_t used = 0, total = 0;
-    for (int i = 0; i < n; ++i) total += group_bytes(small(i), large(i));
-    const int64_t budget = std::max(kGroupBytes, total / (ZERO1_MUON_MAX_GROUPS / 2 - 1));
+    for (int i = 0; i < n; ++i) {
+        MatDesc d;
+        std::memset(&d, 0, sizeof d);
+        sides(mats[i], d);
+        total += place(d, 0);
+    }
+    // two groups in a row hold more than the budget, but for the classes' ends
+    const int64_t budget = std::max(kGroupBytes, total / (ZERO1_MUON_MAX_GROUPS / 2 - 4));
     size_t group_first = 0;
     auto close_group = [&](size_t end) {
         add_group(h, group_first, end);
@@ -525,10 +608,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         d.o = q.o;
         d.scale = q.scale;
         d.tall = q.rows > q.cols ? 1 : 0;
-        d.k = (int32_t)std::min(q.rows, q.cols);
-        d.n = (int32_t)std::max(q.rows, q.cols);
-        d.kp = (int32_t)round_up64(d.k, kPad);
-        d.np = (int32_t)round_up64(d.n, kPad);
+        sides(q, d);
         const bool flat = q.rows == 1 || (d.ld == q.cols && d.ldu == q.cols && d.ldo == q.cols);
         d.vrows = flat ? 1 : (int32_t)q.rows;
         d.vcols = flat ? q.rows * q.cols : q.cols;
@@ -546,14 +626,16 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
             h.tiles.push_back(s);
         }
         if (h.has & kHasU) {   // its place in a group's buffers
-            const int64_t x = round_up64((int64_t)d.kp * d.np * 2, 256), a = round_up64((int64_t)d.kp * d.kp * 2, 256);
-            if (used > 0 && used + 3 * x + 2 * a > budget) close_group(h.mats.size());
-            d.x[0] = used;
-            d.x[1] = used + x;
-            d.lo = used + 2 * x;
-            d.a = used + 3 * x;
-            d.b = d.a + a;
-            used = d.b + a;
+            int64_t to = place(d, used);
+            if (used > 0 && (to > budget || thin_rows(d.k) != thin_rows(h.mats.back().k))) {
+                close_group(h.mats.size());
+                to = place(d, used);
+            }
+            used = to;
+        }
+        if (!thin_rows(d.k)) {
+            ++h.n_dense;
+            h.dense_tiles = (int32_t)h.tiles.size();
         }
         h.mats.push_back(d);
     }
@@ -621,7 +703,7 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
 {
     const double* partials = reinterpret_cast<const double*>(ws);
     NormRec* norms = reinterpret_cast<NormRec*>(ws + ws_norms(plan));
-    Z1_HIP(launch_ns_norms(plan_mats(plan), plan->n_mats, partials, hp->ns_eps, norms, s));
+    if (plan->n_dense > 0) Z1_HIP(launch_ns_norms(plan_mats(plan), plan->n_dense, partials, hp->ns_eps, norms, s));
     const char* tb = static_cast<const char*>(plan->table);
     NsArgs g;
     std::memset(&g, 0, sizeof g);
@@ -637,6 +719,18 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
     const MuonArgs ma = muon_args(hp, flags);
     for (g.group = 0; g.group < plan->n_groups; ++g.group) {
         const zero1_matrix_group& q = plan->groups[g.group];
+        if (q.thin) {
+            double top = 1.0;
+            for (int it = 0; it < hp->ns_steps;) {
+                const int m = segment_steps(hp, hp->ns_steps - it, top), mid = it > 0 ? 1 : 0;
+                const NsLast to = it + m == hp->ns_steps ? last : kNsMid;
+                Z1_HIP(launch_thin_gram(g, q.thin, u_f32 || mid, mid, q.n_sym, s));
+                Z1_HIP(launch_thin_poly(g, q.thin, mid, m, hp->ns_eps, norms, q.n_blocks, s));
+                Z1_HIP(launch_thin_apply(g, q.thin, u_f32 || mid, mid, to, ma, q.n_full, s));
+                it += m;
+            }
+            continue;
+        }
         const TileShape sym = (TileShape)q.sym_tile, full = (TileShape)q.full_tile;
         Z1_HIP(launch_ns_prepare(g, u_f32, q.n_blocks, s));
         for (int it = 0; it < hp->ns_steps; ++it) {
@@ -701,6 +795,8 @@ zero1_status zero1_muon_plan(const zero1_matrix* mats, int n_mats, uint32_t flag
         std::copy(h.shape.begin(), h.shape.end(), p.groups);
         p.flags = flags & kPlanFlags;
         p.has = h.has;
+        p.n_dense = h.n_dense;
+        p.dense_tiles = h.dense_tiles;
         p.device = dev;
         *plan_out = p;
         return ok();
@@ -761,9 +857,11 @@ zero1_status zero1_orthogonalize(const zero1_matrix_plan* plan, const zero1_muon
     if ((st = check_ws(plan, ws, ws_bytes))) return st;
     if ((st = plan_device(plan, cus))) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const Shape sh = stream_shape(plan->n_tiles, cus);
-    Z1_HIP(launch_u_sumsq(plan_mats(plan), plan_tiles(plan), plan->n_tiles, (plan->flags & ZERO1_U_F32) != 0,
-                          static_cast<double*>(ws), sh.grid, sh.split, s));
+    if (plan->n_dense > 0) {
+        const Shape sh = stream_shape(plan->dense_tiles, cus);
+        Z1_HIP(launch_u_sumsq(plan_mats(plan), plan_tiles(plan), plan->dense_tiles, (plan->flags & ZERO1_U_F32) != 0,
+                              static_cast<double*>(ws), sh.grid, sh.split, s));
+    }
     if ((st = iterate(plan, hp, flags, kNsWriteO, static_cast<char*>(ws), s))) return st;
     return finish(s);
 }
@@ -799,8 +897,8 @@ zero1_status zero1_muon_step(const uint16_t* const* grads, int W, int64_t begin,
     if ((st = check_ws(plan, ws, ws_bytes))) return st;
     if ((st = plan_device(plan, cus))) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if ((st = momentum(grads, W, begin, plan, hp, rank_sumsq, n_ranks, flags, info_out, static_cast<double*>(ws), cus,
-                       s)))
+    if ((st = momentum(grads, W, begin, plan, hp, rank_sumsq, n_ranks, flags, info_out,
+                       plan->n_dense > 0 ? static_cast<double*>(ws) : nullptr, cus, s)))
         return st;
     if ((st = iterate(plan, hp, flags, kNsUpdate, static_cast<char*>(ws), s))) return st;
     return finish(s);

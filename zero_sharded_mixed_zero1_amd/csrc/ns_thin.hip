@@ -1,0 +1,528 @@
+// ns_thin.hip -- orthogonalisation of thin matrices (k = min(rows, cols) up to
+// 128) on gfx950, in three launches however many steps there are.
+//
+// A step multiplies X from the left by Q = a I + b A + c A A, a polynomial of
+// A = X X^T, and A becomes Q A Q.  So the steps need X only through A, which is
+// k x k: gram forms A once, poly runs all steps in one workgroup a matrix and
+// keeps the product P = Q_m ... Q_1, apply forms P X.  X is read twice and
+// written once, where the tiles of newton_schulz.hip read and write it every
+// step (and would leave most of the chip idle: k <= 128 is one tile of A).
+//
+// Precision: A's small eigenvalues are squares of X's small singular values, so
+// A, Q and P are held and multiplied as two fp16 halves (22 bits, three MFMAs a
+// product: hi hi, hi lo, lo hi).  An error of 2^-22 in A stays that small
+// beside every singular value that matters: one of 2^-11 or less of the largest
+// only meets b s^2 of 2^-22 beside a.  P grows like a^m on directions X does
+// not have, and its errors with it; so steps are taken in segments whose growth
+// is at most 2^11 (six default steps), with X in fp32 between them.
+//
+// Powers of two carried in fp16: X and A 2^12, Q 2^10, P 2^4 (|A| <= 9,
+// |Q| <= 27, |P| <= 2^11, checked on the host).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "muon.h"
+
+namespace z1 {
+namespace {
+
+using namespace dev;
+
+typedef _Float16 half_t;
+typedef half_t h4 __attribute__((ext_vector_type(4)));
+typedef half_t h8 __attribute__((ext_vector_type(8)));
+
+constexpr float kQScale = 1024.0f, kPScale = 16.0f;
+
+// Where a segment finds X: u, or (mid) the workspace's fp32 X, which carries S.
+template <typename U>
+struct Source {
+    const U* p;
+    int64_t ld;
+    int tall;
+};
+
+template <typename U>
+__device__ __forceinline__ Source<U> source(const NsArgs& g, const MatDesc& d, int mid)
+{
+    if (mid) return Source<U>{reinterpret_cast<const U*>(g.area + d.x[0]), d.np, 0};
+    return Source<U>{static_cast<const U*>(d.u), d.ldu, d.tall};
+}
+
+// Calls f(i, j, n, v): n elements v of X from (i, j) on, along j (or, for a
+// tall source, along i), for the columns [j0, j0 + 64) of X; all kThreads take
+// part.  Elements outside X are zero; (i, j) are inside KP x 64 blocks.
+template <typename U, int KP, typename F>
+__device__ __forceinline__ void for_columns(const Source<U>& s, const MatDesc& d, int j0, F f)
+{
+    if (!s.tall) {
+#pragma unroll 4
+        for (int t = threadIdx.x; t < KP * 16; t += kThreads) {
+            const int i = t >> 4, j = (t & 15) * 4;
+            const int left = d.n - (j0 + j), n = i < d.k ? (left >= 4 ? 4 : (left > 0 ? left : 0)) : 0;
+            float v[4];
+            load_quad(s.p + (int64_t)i * s.ld + j0 + j, n, v);
+            f(i, j, v);
+        }
+    } else {
+        constexpr int Q = KP / 4;
+#pragma unroll 4
+        for (int t = threadIdx.x; t < 64 * Q; t += kThreads) {
+            const int j = t / Q, i = (t % Q) * 4;
+            const int left = d.k - i, n = j0 + j < d.n ? (left >= 4 ? 4 : (left > 0 ? left : 0)) : 0;
+            float v[4];
+            load_quad(s.p + (int64_t)(j0 + j) * s.ld + i, n, v);
+            f(i, j, v);
+        }
+    }
+}
+
+struct HiLo {
+    half_t hi, lo;
+};
+
+__device__ __forceinline__ HiLo split(float x)
+{
+    const half_t h = (half_t)x;
+    return HiLo{h, (half_t)(x - (float)h)};
+}
+
+// ------------------------------------------------------------- gram
+// Partial sums of X X^T over `split` columns of X each, one workgroup a part:
+// G times 2^2e, with the power of two 2^e that brings the part's largest
+// element to 2^13..2^14 (found in a first look at it; exact, so that neither
+// squares of tiny u underflow nor those of huge u overflow).
+template <typename U, int KP>
+__global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
+{
+    constexpr bool LO = sizeof(U) == 4;
+    constexpr int N = KP / 32, ROW = 64 + 8;   // 16 x 16 tiles a wave and side; LDS row
+    __shared__ half_t hi[KP][ROW], lo[LO ? KP : 1][ROW];
+    __shared__ uint32_t top;
+    const GroupDesc& gd = g.groups[g.group];
+    if ((int)blockIdx.x >= gd.n_sym) return;
+    const ProdTile pt = g.list[gd.sym0 + blockIdx.x];
+    const MatDesc& d = g.mats[pt.mat];
+    const Source<U> src = source<U>(g, d, mid);
+    const int c0 = pt.j * 64, c1 = min(d.n, c0 + d.split);
+    int e = 0;
+    if (!mid) {
+        if (threadIdx.x == 0) top = 0;
+        __syncthreads();
+        uint32_t m = 0;
+        for (int j0 = c0; j0 < c1; j0 += 64)
+            for_columns<U, KP>(src, d, j0, [&](int, int, const float (&v)[4]) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(v[q]) & 0x7fffffffu);
+            });
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+        if ((threadIdx.x & 63) == 0) atomicMax(&top, m);   // a maximum of integers: any order
+        __syncthreads();
+        const uint32_t t = top;
+        if (t != 0 && t < 0x7f800000u) e = 13 - ilogbf(__uint_as_float(t));
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wi = (wave >> 1) * (KP / 2), wj = (wave & 1) * (KP / 2);
+    f32x4 acc[N][N];
+#pragma unroll
+    for (int x = 0; x < N; ++x)
+#pragma unroll
+        for (int y = 0; y < N; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
+    for (int j0 = c0; j0 < c1; j0 += 64) {
+        __syncthreads();
+        for_columns<U, KP>(src, d, j0, [&](int i, int j, const float (&v)[4]) {
+            HiLo s[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s[q] = split(ldexpf(v[q], e));
+            if (!src.tall) {
+                *reinterpret_cast<h4*>(&hi[i][j]) = h4{s[0].hi, s[1].hi, s[2].hi, s[3].hi};
+                if constexpr (LO) *reinterpret_cast<h4*>(&lo[i][j]) = h4{s[0].lo, s[1].lo, s[2].lo, s[3].lo};
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    hi[i + q][j] = s[q].hi;
+                    if constexpr (LO) lo[i + q][j] = s[q].lo;
+                }
+            }
+        });
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = 32 * h + 8 * (lane >> 4), r = lane & 15;
+            h8 ph[N], qh[N], pl[N], ql[N];
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                ph[x] = *reinterpret_cast<const h8*>(&hi[wi + 16 * x + r][c]);
+                qh[x] = *reinterpret_cast<const h8*>(&hi[wj + 16 * x + r][c]);
+                if constexpr (LO) {
+                    pl[x] = *reinterpret_cast<const h8*>(&lo[wi + 16 * x + r][c]);
+                    ql[x] = *reinterpret_cast<const h8*>(&lo[wj + 16 * x + r][c]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+#pragma unroll
+                for (int y = 0; y < N; ++y) {
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], ph[x], acc[x][y], 0, 0, 0);
+                    if constexpr (LO) {
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ql[y], ph[x], acc[x][y], 0, 0, 0);
+                        acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], pl[x], acc[x][y], 0, 0, 0);
+                    }
+                }
+        }
+    }
+    float* out = reinterpret_cast<float*>(g.area + d.a) + (int64_t)pt.i * KP * KP;
+#pragma unroll
+    for (int x = 0; x < N; ++x)
+#pragma unroll
+        for (int y = 0; y < N; ++y)
+            *reinterpret_cast<f32x4*>(out + (wi + 16 * x + (lane & 15)) * KP + wj + 16 * y + 4 * (lane >> 4)) = acc[x][y];
+    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[pt.i] = e;
+}
+
+// ------------------------------------------------------------- poly
+// The waves of the poly kernel: RW x CW of them, MI x NI tiles of 16 x 16 each.
+template <int KP>
+struct Poly {
+    static constexpr int RW = KP == 128 ? 4 : 2, CW = 2, MI = KP / 16 / RW, NI = KP / 16 / CW;
+    static constexpr int kThr = 64 * RW * CW, ROW = KP + 8;
+    typedef f32x4 Acc[MI][NI];
+    struct Mat {
+        half_t hi[KP][ROW], lo[KP][ROW];
+    };
+};
+
+// acc = M N, N symmetric.
+template <int KP>
+__device__ __forceinline__ void multiply(const typename Poly<KP>::Mat& M, const typename Poly<KP>::Mat& N,
+                                         typename Poly<KP>::Acc& acc)
+{
+    using T = Poly<KP>;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
+    const int wi = (wave / T::CW) * 16 * T::MI, wj = (wave % T::CW) * 16 * T::NI;
+#pragma unroll
+    for (int x = 0; x < T::MI; ++x)
+#pragma unroll
+        for (int y = 0; y < T::NI; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k0 = 0; k0 < KP; k0 += 32) {
+        const int c = k0 + 8 * (lane >> 4);
+        h8 ph[T::MI], pl[T::MI], qh[T::NI], ql[T::NI];
+#pragma unroll
+        for (int x = 0; x < T::MI; ++x) {
+            ph[x] = *reinterpret_cast<const h8*>(&M.hi[wi + 16 * x + r][c]);
+            pl[x] = *reinterpret_cast<const h8*>(&M.lo[wi + 16 * x + r][c]);
+        }
+#pragma unroll
+        for (int y = 0; y < T::NI; ++y) {
+            qh[y] = *reinterpret_cast<const h8*>(&N.hi[wj + 16 * y + r][c]);
+            ql[y] = *reinterpret_cast<const h8*>(&N.lo[wj + 16 * y + r][c]);
+        }
+#pragma unroll
+        for (int x = 0; x < T::MI; ++x)
+#pragma unroll
+            for (int y = 0; y < T::NI; ++y) {
+                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], ph[x], acc[x][y], 0, 0, 0);
+                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ql[y], ph[x], acc[x][y], 0, 0, 0);
+                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], pl[x], acc[x][y], 0, 0, 0);
+            }
+    }
+}
+
+// f(i, j, v) for the lane's quads of an accumulator: v is row i, columns j..j+3.
+template <int KP, typename A, typename F>
+__device__ __forceinline__ void for_quads(A& acc, F f)
+{
+    using T = Poly<KP>;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wi = (wave / T::CW) * 16 * T::MI + (lane & 15), wj = (wave % T::CW) * 16 * T::NI + 4 * (lane >> 4);
+#pragma unroll
+    for (int x = 0; x < T::MI; ++x)
+#pragma unroll
+        for (int y = 0; y < T::NI; ++y) f(wi + 16 * x, wj + 16 * y, acc[x][y]);
+}
+
+// acc, times f, into LDS (between barriers of the caller's).
+template <int KP>
+__device__ __forceinline__ void store(typename Poly<KP>::Mat& M, typename Poly<KP>::Acc& acc, float f)
+{
+    for_quads<KP>(acc, [&](int i, int j, const f32x4& v) {
+        h4 h, l;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const HiLo s = split(v[q] * f);
+            h[q] = s.hi;
+            l[q] = s.lo;
+        }
+        *reinterpret_cast<h4*>(&M.hi[i][j]) = h;
+        *reinterpret_cast<h4*>(&M.lo[i][j]) = l;
+    });
+}
+
+// One workgroup a matrix: the norm (the trace of the parts' sum is |u|^2), A
+// from the parts, `steps` steps, and P as two fp16 halves.  The norm goes to
+// `norms` for apply: S / (norm + eps) = 2^e r.
+template <int KP>
+__global__ __launch_bounds__(Poly<KP>::kThr) void thin_poly_kernel(NsArgs g, int mid, int steps, double eps,
+                                                                   NormRec* __restrict__ norms)
+{
+    using T = Poly<KP>;
+    __shared__ typename T::Mat A, Q;
+    __shared__ double diag[KP];
+    __shared__ NormRec nr;
+    const GroupDesc& gd = g.groups[g.group];
+    const int mat = gd.first + (int)blockIdx.x;
+    const MatDesc& d = g.mats[mat];
+    const float* part = reinterpret_cast<const float*>(g.area + d.a);
+    const int32_t* exps = reinterpret_cast<const int32_t*>(g.area + d.lo);
+    half_t* pm = reinterpret_cast<half_t*>(g.area + d.b);
+    double f2;   // A is f2 sum of the parts, each divided by its power of two
+    if (!mid) {
+        for (int t = threadIdx.x; t < KP; t += T::kThr) {
+            double tr = 0.0;
+            for (int p = 0; p < d.n_parts; ++p)
+                tr = tr + ldexp((double)part[(int64_t)p * KP * KP + t * KP + t], -2 * exps[p]);
+            diag[t] = tr;
+        }
+        __syncthreads();
+        double tr = 0.0;
+        for (int t = 0; t < KP; ++t) tr = tr + diag[t];
+        const double f = (double)kNsScale / (sqrt(tr) + eps);
+        if (threadIdx.x == 0) {
+            const bool bad = !(f > 0.0) || isinf(f);
+            nr.e = bad ? 0 : ilogb(f);
+            nr.r = bad ? __builtin_nanf("") : (float)ldexp(f, -nr.e);
+            norms[mat] = nr;
+        }
+        __syncthreads();
+        f2 = f * f / kNsScale;
+    } else {
+        if (threadIdx.x == 0) norms[mat] = nr = NormRec{1.0f, 0};
+        __syncthreads();
+        f2 = 1.0 / kNsScale;   // the parts carry S^2, A carries S
+    }
+    if (nr.r != nr.r) {   // u / (norm + eps) holds a NaN: so does all of o, by apply's factor
+        for (int t = threadIdx.x; t < 2 * KP * KP; t += T::kThr) pm[t] = (half_t)0.0f;
+        return;
+    }
+    typename T::Acc acc, tacc, pacc;
+    for_quads<KP>(acc, [&](int, int, f32x4& v) { v = f32x4{0, 0, 0, 0}; });
+#pragma unroll 4
+    for (int p = 0; p < d.n_parts; ++p) {
+        const float w = (float)ldexp(f2, -2 * exps[p]);
+        for_quads<KP>(acc, [&](int i, int j, f32x4& v) {
+            v += w * *reinterpret_cast<const f32x4*>(part + (int64_t)p * KP * KP + i * KP + j);
+        });
+    }
+    store<KP>(A, acc, 1.0f);
+    __syncthreads();
+    const float qa = g.a * kQScale, qb = g.b * (kQScale / kNsScale), qc = g.c * (kQScale / (kNsScale * kNsScale));
+    for (int it = 0; it < steps; ++it) {
+        const bool last = it + 1 == steps;
+        multiply<KP>(A, A, acc);
+        for_quads<KP>(acc, [&](int i, int j, f32x4& v) {
+            const h4 h = *reinterpret_cast<const h4*>(&A.hi[i][j]), l = *reinterpret_cast<const h4*>(&A.lo[i][j]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = qc * v[q] + qb * ((float)h[q] + (float)l[q]) + (i == j + q ? qa : 0.0f);
+        });
+        // (Q is not read after the barrier that ends a step)
+        store<KP>(Q, acc, 1.0f);
+        __syncthreads();
+        if (!last) multiply<KP>(Q, A, tacc);
+        if (it == 0) {
+            for_quads<KP>(acc, [&](int, int, f32x4& v) { v *= kPScale / kQScale; });
+#pragma unroll
+            for (int x = 0; x < T::MI; ++x)
+#pragma unroll
+                for (int y = 0; y < T::NI; ++y) pacc[x][y] = acc[x][y];
+        } else {
+            __syncthreads();   // A has been read by all
+            store<KP>(A, pacc, 1.0f);
+            __syncthreads();
+            multiply<KP>(Q, A, pacc);
+            for_quads<KP>(pacc, [&](int, int, f32x4& v) { v *= 1.0f / kQScale; });
+        }
+        if (!last) {
+            __syncthreads();
+            store<KP>(A, tacc, 1.0f / kQScale);   // T = Q A
+            __syncthreads();
+            multiply<KP>(Q, A, acc);              // A <- Q T
+            __syncthreads();
+            store<KP>(A, acc, 1.0f / kQScale);
+            __syncthreads();
+        }
+    }
+    for_quads<KP>(pacc, [&](int i, int j, const f32x4& v) {
+        h4 h, l;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const HiLo s = split(v[q]);
+            h[q] = s.hi;
+            l[q] = s.lo;
+        }
+        *reinterpret_cast<h4*>(pm + i * KP + j) = h;
+        *reinterpret_cast<h4*>(pm + KP * KP + i * KP + j) = l;
+    });
+}
+
+// ------------------------------------------------------------- apply
+// 64 columns of P X a workgroup.  P comes straight from memory (L2) into the
+// MFMA's registers, X through LDS with its inner dimension (k) along rows.
+template <typename U, int KP, int LAST>
+__global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid, MuonArgs ma)
+{
+    constexpr bool LO = sizeof(U) == 4;
+    constexpr int RW = KP == 32 ? 2 : 4, CW = 4 / RW, MI = KP / 16 / RW, NI = 4 / CW, ROW = KP + 8;
+    __shared__ half_t hi[64][ROW], lo[LO ? 64 : 1][ROW];
+    const GroupDesc& gd = g.groups[g.group];
+    if ((int)blockIdx.x >= gd.n_full) return;
+    const ProdTile pt = g.list[gd.full0 + blockIdx.x];
+    const MatDesc& d = g.mats[pt.mat];
+    const Source<U> src = source<U>(g, d, mid);
+    const NormRec nr = g.norms[pt.mat];
+    const int j0 = pt.j * 64;
+    for_columns<U, KP>(src, d, j0, [&](int i, int j, const float (&v)[4]) {
+        HiLo s[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[q] = split(ldexpf(v[q], nr.e));
+        if (src.tall) {
+            *reinterpret_cast<h4*>(&hi[j][i]) = h4{s[0].hi, s[1].hi, s[2].hi, s[3].hi};
+            if constexpr (LO) *reinterpret_cast<h4*>(&lo[j][i]) = h4{s[0].lo, s[1].lo, s[2].lo, s[3].lo};
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                hi[j + q][i] = s[q].hi;
+                if constexpr (LO) lo[j + q][i] = s[q].lo;
+            }
+        }
+    });
+    __syncthreads();
+    if constexpr (LAST == kNsUpdate) use_device_scalars(ma, nullptr);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
+    const int wi = (wave / CW) * 16 * MI, wj = (wave % CW) * 16 * NI;
+    const half_t* pm = reinterpret_cast<const half_t*>(g.area + d.b);
+    // o's rows are X's columns when u is tall: then the lane's four elements
+    // are to be four neighbouring rows of X
+    const bool along_i = LAST != kNsMid && d.tall;
+    f32x4 acc[MI][NI];
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k0 = 0; k0 < KP; k0 += 32) {
+        const int c = k0 + 8 * (lane >> 4);
+        h8 ph[MI], pl[MI], xh[NI], xl[NI];
+#pragma unroll
+        for (int x = 0; x < MI; ++x) {
+            ph[x] = *reinterpret_cast<const h8*>(pm + (wi + 16 * x + r) * KP + c);
+            pl[x] = *reinterpret_cast<const h8*>(pm + KP * KP + (wi + 16 * x + r) * KP + c);
+        }
+#pragma unroll
+        for (int y = 0; y < NI; ++y) {
+            xh[y] = *reinterpret_cast<const h8*>(&hi[wj + 16 * y + r][c]);
+            if constexpr (LO) xl[y] = *reinterpret_cast<const h8*>(&lo[wj + 16 * y + r][c]);
+        }
+#pragma unroll
+        for (int x = 0; x < MI; ++x)
+#pragma unroll
+            for (int y = 0; y < NI; ++y) {
+                if (along_i) {
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph[x], xh[y], acc[x][y], 0, 0, 0);
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl[x], xh[y], acc[x][y], 0, 0, 0);
+                    if constexpr (LO) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph[x], xl[y], acc[x][y], 0, 0, 0);
+                } else {
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xh[y], ph[x], acc[x][y], 0, 0, 0);
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xh[y], pl[x], acc[x][y], 0, 0, 0);
+                    if constexpr (LO) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xl[y], ph[x], acc[x][y], 0, 0, 0);
+                }
+            }
+    }
+    const float f = nr.r * (LAST == kNsMid ? 1.0f / kPScale : 1.0f / (kPScale * kNsScale));
+    const float eta = ma.lr * d.scale;
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y) {
+            const int four = 4 * (lane >> 4);
+            const int i = wi + 16 * x + (along_i ? four : r), j = j0 + wj + 16 * y + (along_i ? r : four);
+            float o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = acc[x][y][q] * f;
+            if constexpr (LAST == kNsMid) {
+                // (the padding of X's fp32 rows is written, and read as zero)
+                if (i < d.k && j < d.np)
+                    st4(reinterpret_cast<float*>(g.area + d.x[0]) + (int64_t)i * d.np + j, f32x4{o[0], o[1], o[2], o[3]});
+            } else {
+                const int64_t row = along_i ? j : i, col = along_i ? i : j, left = d.cols - col;
+                const int n = row < d.rows ? (left >= 4 ? 4 : (left > 0 ? (int)left : 0)) : 0;
+                if constexpr (LAST == kNsWriteO) {
+                    store_quad(d.o + row * d.ldo + col, n, o);
+                } else {
+                    float v[4];
+                    load_quad(d.master + row * d.ld + col, n, v);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = muon_elem(v[q], o[q], eta, ma);
+                    store_quad(d.master + row * d.ld + col, n, v);
+                    store_quad(d.param + row * d.ld + col, n, v);
+                }
+            }
+        }
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ launchers
+#define Z1_KP(kp, CALL)           \
+    do {                          \
+        if ((kp) == 32) CALL(32);  \
+        else if ((kp) == 64) CALL(64); \
+        else CALL(128);           \
+    } while (0)
+
+hipError_t launch_thin_gram(const NsArgs& g, int kp, bool f32, int mid, int grid, hipStream_t s)
+{
+#define Z1_CALL(KP)                                                                                     \
+    do {                                                                                                \
+        if (f32) thin_gram_kernel<float, KP><<<dim3(grid), dim3(kThreads), 0, s>>>(g, mid);             \
+        else thin_gram_kernel<uint16_t, KP><<<dim3(grid), dim3(kThreads), 0, s>>>(g, mid);              \
+    } while (0)
+    Z1_KP(kp, Z1_CALL);
+#undef Z1_CALL
+    return hipGetLastError();
+}
+
+hipError_t launch_thin_poly(const NsArgs& g, int kp, int mid, int steps, double eps, NormRec* norms, int grid,
+                            hipStream_t s)
+{
+#define Z1_CALL(KP) thin_poly_kernel<KP><<<dim3(grid), dim3(Poly<KP>::kThr), 0, s>>>(g, mid, steps, eps, norms)
+    Z1_KP(kp, Z1_CALL);
+#undef Z1_CALL
+    return hipGetLastError();
+}
+
+hipError_t launch_thin_apply(const NsArgs& g, int kp, bool f32, int mid, NsLast last, const MuonArgs& ma, int grid,
+                             hipStream_t s)
+{
+#define Z1_LAST(U, KP)                                                                                          \
+    do {                                                                                                        \
+        const dim3 gr(grid), bl(kThreads);                                                                      \
+        if (last == kNsMid) thin_apply_kernel<U, KP, kNsMid><<<gr, bl, 0, s>>>(g, mid, ma);                     \
+        else if (last == kNsWriteO) thin_apply_kernel<U, KP, kNsWriteO><<<gr, bl, 0, s>>>(g, mid, ma);          \
+        else thin_apply_kernel<U, KP, kNsUpdate><<<gr, bl, 0, s>>>(g, mid, ma);                                 \
+    } while (0)
+#define Z1_CALL(KP)                         \
+    do {                                    \
+        if (f32) Z1_LAST(float, KP);        \
+        else Z1_LAST(uint16_t, KP);         \
+    } while (0)
+    Z1_KP(kp, Z1_CALL);
+#undef Z1_CALL
+#undef Z1_LAST
+    return hipGetLastError();
+}
+#undef Z1_KP
+
+}  // namespace z1
