@@ -190,52 +190,111 @@ __device__ __forceinline__ float muon_elem(float p, float o, float eta, const Mu
     return (p - eta * o) * a.delta;
 }
 
-// Loads and stores of a quad's n elements; four at once when all are there.
-__device__ __forceinline__ void load_quad(const uint16_t* p, int n, float (&x)[4])
+// A quad: four neighbouring elements of a row, loaded and stored whole.  The
+// last quad of a row that is no multiple of four long begins `skip` elements
+// early, so that it too can be loaded whole; those elements belong to the quad
+// before, and are not stored.  skip = 4: nothing of it is the lane's (it loads
+// from wherever the caller points it).  Rows shorter than four elements have
+// one quad with `skip` negative: -skip elements, one by one.
+__device__ __forceinline__ void widen4(u16x4 v, float (&x)[4])
 {
-    if (n == 4) {
-        const u16x4 v = ld4(p);
-        x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
-    } else {
+    x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
+}
+
+template <bool SHORT>
+__device__ __forceinline__ void load_quad(const uint16_t* p, int skip, float (&x)[4])
+{
+    if constexpr (SHORT) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = j < n ? widen(p[j]) : 0.0f;
+        for (int j = 0; j < 3; ++j) x[j] = j < -skip ? widen(p[j]) : 0.0f;
+        x[3] = 0.0f;
+    } else {
+        widen4(ld4(p), x);
     }
 }
 
-__device__ __forceinline__ void load_quad(const float* p, int n, float (&x)[4])
+template <bool SHORT>
+__device__ __forceinline__ void load_quad(const float* p, int skip, float (&x)[4])
 {
-    if (n == 4) {
+    if constexpr (SHORT) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) x[j] = j < -skip ? p[j] : 0.0f;
+        x[3] = 0.0f;
+    } else {
         const f32x4 v = ld4(p);
         x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = j < n ? p[j] : 0.0f;
     }
 }
 
-// Stores in the array's type; x becomes the values as stored.
-__device__ __forceinline__ void store_quad(uint16_t* p, int n, float (&x)[4])
+// Whether element j of a quad is the lane's.
+template <bool SHORT>
+__device__ __forceinline__ bool owns(int skip, int j)
 {
-    u16x4 v;
-    v.x = bf16_rne(x[0]); v.y = bf16_rne(x[1]); v.z = bf16_rne(x[2]); v.w = bf16_rne(x[3]);
-    x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
-    if (n == 4) {
+    return SHORT ? j < -skip : j >= skip;
+}
+
+// Stores the lane's elements in the array's type; x becomes what was stored.
+template <bool SHORT>
+__device__ __forceinline__ void store_quad(uint16_t* p, int skip, float (&x)[4])
+{
+    const u16x4 v = {bf16_rne(x[0]), bf16_rne(x[1]), bf16_rne(x[2]), bf16_rne(x[3])};
+    widen4(v, x);
+    if (!SHORT && skip == 0) {
         st4(p, v);
     } else {
-        if (n > 0) p[0] = v.x;
-        if (n > 1) p[1] = v.y;
-        if (n > 2) p[2] = v.z;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (owns<SHORT>(skip, j)) p[j] = v[j];
     }
 }
 
-__device__ __forceinline__ void store_quad(float* p, int n, float (&x)[4])
+template <bool SHORT>
+__device__ __forceinline__ void store_quad(float* p, int skip, float (&x)[4])
 {
-    if (n == 4) {
+    if (!SHORT && skip == 0) {
         st4(p, f32x4{x[0], x[1], x[2], x[3]});
     } else {
-        if (n > 0) p[0] = x[0];
-        if (n > 1) p[1] = x[1];
-        if (n > 2) p[2] = x[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (owns<SHORT>(skip, j)) p[j] = x[j];
+    }
+}
+
+// The quad of columns [c, c + 4) of a row of `cols`: where it begins and its
+// skip; nothing of it is the lane's unless `in`.
+struct Span4 {
+    int64_t col;
+    int skip;
+};
+
+template <bool SHORT>
+__device__ __forceinline__ Span4 span4(int64_t c, int64_t cols, bool in)
+{
+    if constexpr (SHORT) return Span4{0, in && c == 0 ? -(int)cols : 0};
+    const int64_t left = cols - c;
+    if (!in || left <= 0) return Span4{0, 4};
+    if (left >= 4) return Span4{c, 0};
+    return Span4{cols - 4, 4 - (int)left};
+}
+
+// Elements c .. c + 3 of a row of `cols` in x, zeros past its end.
+template <bool SHORT, typename T>
+__device__ __forceinline__ void load_padded(const T* row, int64_t c, int64_t cols, bool in, float (&x)[4])
+{
+    const Span4 s = span4<SHORT>(c, cols, in);
+    float v[4];
+    load_quad<SHORT>(row + s.col, s.skip, v);
+    if constexpr (SHORT) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float y = v[j];
+#pragma unroll
+            for (int k = 1; k <= 4; ++k) y = s.skip == k ? (j + k < 4 ? v[(j + k) & 3] : 0.0f) : y;
+            x[j] = y;
+        }
     }
 }
 

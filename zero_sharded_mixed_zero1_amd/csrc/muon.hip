@@ -4,11 +4,12 @@
 //
 // All are HBM-bound (under one flop per byte).  A workgroup takes a tile of
 // 512 quads (2048 elements) of one matrix; lane l handles quads l and 256 + l,
-// so a wave's load covers one contiguous run of a row.  A quad is up to four
+// so a wave's load covers one contiguous run of a row.  A quad is four
 // neighbouring elements of one row: rows may start at any element (odd column
 // counts, blocks cut out of wider matrices), because gfx950's vector loads and
-// stores need no more than the element's alignment, and only the last quad of
-// a row is taken element by element.  Matrices that are contiguous in all
+// stores need no more than the element's alignment.  No load is conditional
+// (the last quad of a row is loaded from a little earlier, a lane past the end
+// loads row 0), so that a tile's loads are all in flight at once.  Matrices that are contiguous in all
 // their arrays are one long row.
 //
 // Arithmetic: one binary32 operation at a time (no contraction), gradients
@@ -40,27 +41,28 @@ __device__ __forceinline__ Walk walk(int64_t n, int split)
     return Walk{lo + b / nx, lo + per < n ? lo + per : n, G / nx};
 }
 
-// A lane's quad: its row and first column, and how many elements it has.
+// A lane's quad (see span4) and its row.  A lane past the matrix's end is given
+// row 0, nothing of which it stores.
 struct Quad {
     int64_t row, col;
-    int n;
+    int skip;
 };
 
+template <bool SHORT>
 __device__ __forceinline__ Quad quad_at(const MatDesc& d, const StreamTile& t, int lane_quad)
 {
-    Quad q;
+    int64_t row = 0, c;
     if (d.vrows == 1) {
-        q.row = 0;
-        q.col = 4 * ((int64_t)t.idx * kQuadsPerTile + lane_quad);
+        c = 4 * ((int64_t)t.idx * kQuadsPerTile + lane_quad);
     } else {   // qpr < 2^30 (cols < 2^31), so 32-bit division
         const uint32_t x = (uint32_t)t.q0 + (uint32_t)lane_quad, per = (uint32_t)d.qpr;
         const uint32_t r = x / per;
-        q.row = (int64_t)t.row0 + r;
-        q.col = 4 * (int64_t)(x - r * per);
+        row = (int64_t)t.row0 + r;
+        c = 4 * (int64_t)(x - r * per);
     }
-    const int64_t left = d.vcols - q.col;
-    q.n = q.row < d.vrows ? (left >= 4 ? 4 : (left > 0 ? (int)left : 0)) : 0;
-    return q;
+    const bool in = row < d.vrows;
+    const Span4 s = span4<SHORT>(c, d.vcols, in);
+    return Quad{in ? row : 0, s.col, s.skip};
 }
 
 // Fixed-order workgroup sum; the total is in thread 0.  `sh` alternates
@@ -75,27 +77,53 @@ __device__ __forceinline__ double tile_sum(double x, double* sh)
 }
 
 // The reduced gradient of the lane's two quads: slices added in rank order,
-// the loads of up to four slices in flight together; then the average.
-__device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at)[2], const int (&n)[2],
-                                             float (&g)[2][4])
+// the loads of up to eight slices in flight together; then the average.
+template <bool SHORT, int N>
+__device__ __forceinline__ void add_slices(const Reduce& r, int w0, const int64_t (&at)[2], const int (&skip)[2],
+                                           float (&g)[2][4])
 {
-    for (int w0 = 0; w0 < r.W; w0 += 4) {
-        float x[4][2][4];
+    if constexpr (SHORT) {
+        for (int w = w0; w < w0 + N; ++w)
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            if (w0 + w < r.W) {
+            for (int h = 0; h < 2; ++h) {
+                float x[4];
+                load_quad<true>(r.gp.p[w] + at[h], skip[h], x);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) load_quad(r.gp.p[w0 + w] + at[h], n[h], x[w][h]);
+                for (int j = 0; j < 4; ++j) g[h][j] = w == 0 ? x[j] : g[h][j] + x[j];
             }
+    } else {
+        u16x4 raw[N][2];
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-            if (w0 + w < r.W) {
+        for (int w = 0; w < N; ++w)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) raw[w][h] = ld4(r.gp.p[w0 + w] + at[h]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) g[h][j] = (w0 + w == 0) ? x[w][h][j] : g[h][j] + x[w][h][j];
+        for (int w = 0; w < N; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[4];
+                widen4(raw[w][h], x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[h][j] = w == 0 && w0 == 0 ? x[j] : g[h][j] + x[j];
             }
     }
+}
+
+template <bool SHORT>
+__device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at)[2], const int (&skip)[2],
+                                             float (&g)[2][4])
+{
+    int w = 0;
+    for (; w + 8 <= r.W; w += 8) add_slices<SHORT, 8>(r, w, at, skip, g);
+    if (w + 4 <= r.W) {
+        add_slices<SHORT, 4>(r, w, at, skip, g);
+        w += 4;
+    }
+    if (w + 2 <= r.W) {
+        add_slices<SHORT, 2>(r, w, at, skip, g);
+        w += 2;
+    }
+    if (w < r.W) add_slices<SHORT, 1>(r, w, at, skip, g);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -106,6 +134,45 @@ __device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at
             if (r.round_bf16) v = widen(bf16_rne(v));
             g[h][j] = v;
         }
+}
+
+// One tile of the momentum; returns the lane's sum of squares of u.
+template <typename M, typename U, bool NORM, bool SHORT>
+__device__ __forceinline__ double momentum_tile(const Reduce& r, const MatDesc& d, const StreamTile& tile, float mu,
+                                                int nesterov, bool clip, float coef)
+{
+    Quad q[2];
+    int64_t at[2], ga[2];
+    int skip[2];
+    float g[2][4], m[2][4], u[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        q[h] = quad_at<SHORT>(d, tile, (int)threadIdx.x + h * kThreads);
+        skip[h] = q[h].skip;
+        at[h] = q[h].row * d.ld + q[h].col;
+        ga[h] = d.shard_offset + at[h];
+        load_quad<SHORT>(static_cast<const M*>(d.m) + at[h], skip[h], m[h]);
+    }
+    reduce_quads<SHORT>(r, ga, skip, g);
+    double acc = 0.0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float gj = clip ? g[h][j] * coef : g[h][j];
+            const float mj = mu * m[h][j] + gj;
+            m[h][j] = mj;
+            u[h][j] = nesterov ? gj + mu * mj : mj;
+        }
+        store_quad<SHORT>(static_cast<M*>(d.m) + at[h], skip[h], m[h]);
+        store_quad<SHORT>(static_cast<U*>(d.u) + (q[h].row * d.ldu + q[h].col), skip[h], u[h]);
+        if constexpr (NORM) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (owns<SHORT>(skip[h], j)) acc = fma((double)u[h][j], (double)u[h][j], acc);
+        }
+    }
+    return acc;
 }
 
 // m = mu m + g; u = g + mu m (Nesterov) or m.  Moves 2W + 2 sizeof(m) +
@@ -140,43 +207,34 @@ __global__ __launch_bounds__(kThreads) void momentum_kernel(Reduce r, const MatD
     for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
         const StreamTile tile = tiles[t];
         const MatDesc& d = mats[tile.mat];
-        Quad q[2];
-        int64_t at[2];
-        int n[2];
-        float g[2][4], m[2][4], u[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            q[h] = quad_at(d, tile, (int)threadIdx.x + h * kThreads);
-            n[h] = q[h].n;
-            at[h] = q[h].row * d.ld + q[h].col;
-            load_quad(static_cast<const M*>(d.m) + at[h], n[h], m[h]);
-        }
-        const int64_t ga[2] = {d.shard_offset + at[0], d.shard_offset + at[1]};
-        reduce_quads(r, ga, n, g);
-        double acc = 0.0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float gj = clip ? g[h][j] * coef : g[h][j];
-                const float mj = ma.mu * m[h][j] + gj;
-                m[h][j] = mj;
-                u[h][j] = nesterov ? gj + ma.mu * mj : mj;
-            }
-            store_quad(static_cast<M*>(d.m) + at[h], n[h], m[h]);
-            store_quad(static_cast<U*>(d.u) + (q[h].row * d.ldu + q[h].col), n[h], u[h]);
-            if constexpr (NORM) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < n[h]) acc = fma((double)u[h][j], (double)u[h][j], acc);
-            }
-        }
+        const double acc = d.vcols >= 4 ? momentum_tile<M, U, NORM, false>(r, d, tile, ma.mu, nesterov, clip, coef)
+                                        : momentum_tile<M, U, NORM, true>(r, d, tile, ma.mu, nesterov, clip, coef);
         if constexpr (NORM) {
             const double b = tile_sum(acc, sums[buf]);
             buf ^= 1;
             if (threadIdx.x == 0) partials[t] = b;
         }
     }
+}
+
+template <typename U, bool SHORT>
+__device__ __forceinline__ double sumsq_tile(const MatDesc& d, const StreamTile& tile)
+{
+    float u[2][4];
+    int skip[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const Quad q = quad_at<SHORT>(d, tile, (int)threadIdx.x + h * kThreads);
+        skip[h] = q.skip;
+        load_quad<SHORT>(static_cast<const U*>(d.u) + (q.row * d.ldu + q.col), q.skip, u[h]);
+    }
+    double acc = 0.0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (owns<SHORT>(skip[h], j)) acc = fma((double)u[h][j], (double)u[h][j], acc);
+    return acc;
 }
 
 template <typename U>
@@ -190,15 +248,7 @@ __global__ __launch_bounds__(kThreads) void u_sumsq_kernel(const MatDesc* __rest
     for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
         const StreamTile tile = tiles[t];
         const MatDesc& d = mats[tile.mat];
-        double acc = 0.0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const Quad q = quad_at(d, tile, (int)threadIdx.x + h * kThreads);
-            float u[4];
-            load_quad(static_cast<const U*>(d.u) + (q.row * d.ldu + q.col), q.n, u);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc = fma((double)u[j], (double)u[j], acc);
-        }
+        const double acc = d.vcols >= 4 ? sumsq_tile<U, false>(d, tile) : sumsq_tile<U, true>(d, tile);
         const double b = tile_sum(acc, sums[buf]);
         buf ^= 1;
         if (threadIdx.x == 0) partials[t] = b;
@@ -214,7 +264,13 @@ __global__ __launch_bounds__(kThreads) void ns_norms_kernel(const MatDesc* __res
     __shared__ double sums[kThreads / 64];
     const MatDesc& d = mats[blockIdx.x];
     double a = 0.0;
-    for (int i = threadIdx.x; i < d.n_tiles; i += kThreads) a = a + partials[d.tile0 + i];
+    for (int i0 = threadIdx.x; i0 < d.n_tiles; i0 += 16 * kThreads) {   // 16 loads in flight
+        double x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = i0 + k * kThreads < d.n_tiles ? partials[d.tile0 + i0 + k * kThreads] : 0.0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) a = a + x[k];
+    }
     const double tot = tile_sum(a, sums);
     if (threadIdx.x == 0) {
         const double f = (double)kNsScale / (sqrt(tot) + eps);
@@ -232,6 +288,29 @@ __global__ __launch_bounds__(kThreads) void ns_norms_kernel(const MatDesc* __res
     }
 }
 
+template <bool SHORT>
+__device__ __forceinline__ void update_tile(const MatDesc& d, const StreamTile& tile, const MuonArgs& ma)
+{
+    const float eta = ma.lr * d.scale;
+    Quad q[2];
+    int64_t at[2];
+    float p[2][4], o[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        q[h] = quad_at<SHORT>(d, tile, (int)threadIdx.x + h * kThreads);
+        at[h] = q[h].row * d.ld + q[h].col;
+        load_quad<SHORT>(d.master + at[h], q[h].skip, p[h]);
+        load_quad<SHORT>(d.o + (q[h].row * d.ldo + q[h].col), q[h].skip, o[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[h][j] = muon_elem(p[h][j], o[h][j], eta, ma);
+        store_quad<SHORT>(d.master + at[h], q[h].skip, p[h]);
+        store_quad<SHORT>(d.param + at[h], q[h].skip, p[h]);
+    }
+}
+
 // p = (p - eta o) delta, the bf16 parameter from the new p: 12 bytes an element.
 __global__ __launch_bounds__(kThreads) void muon_update_kernel(const MatDesc* __restrict__ mats,
                                                                const StreamTile* __restrict__ tiles, int n_tiles,
@@ -242,24 +321,8 @@ __global__ __launch_bounds__(kThreads) void muon_update_kernel(const MatDesc* __
     for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
         const StreamTile tile = tiles[t];
         const MatDesc& d = mats[tile.mat];
-        const float eta = ma.lr * d.scale;
-        Quad q[2];
-        int64_t at[2];
-        float p[2][4], o[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            q[h] = quad_at(d, tile, (int)threadIdx.x + h * kThreads);
-            at[h] = q[h].row * d.ld + q[h].col;
-            load_quad(d.master + at[h], q[h].n, p[h]);
-            load_quad(d.o + (q[h].row * d.ldo + q[h].col), q[h].n, o[h]);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[h][j] = muon_elem(p[h][j], o[h][j], eta, ma);
-            store_quad(d.master + at[h], q[h].n, p[h]);
-            store_quad(d.param + at[h], q[h].n, p[h]);
-        }
+        if (d.vcols >= 4) update_tile<false>(d, tile, ma);
+        else update_tile<true>(d, tile, ma);
     }
 }
 

@@ -433,7 +433,7 @@ int64_t place(MatDesc& d, int64_t at)
     const int thin = thin_rows(d.k);
     if (thin) {
         d.kp = thin;
-        d.n_parts = (int32_t)std::min<int64_t>(kThinMaxParts, (d.n + 255) / 256);
+        d.n_parts = (int32_t)std::min<int64_t>(kThinMaxParts, (d.n + 127) / 128);
         d.split = (int32_t)round_up64((d.n + d.n_parts - 1) / d.n_parts, kPad);
         d.n_parts = (d.n + d.split - 1) / d.split;
         d.x[0] = at;

@@ -65,8 +65,6 @@ __device__ __forceinline__ int64_t elem_at(int i, int j, int cb)
     return ((int64_t)(i >> 6) * cb + (j >> 6)) * kBlock + r * kB + (((c >> 3) ^ slot_key(r)) << 3) + (c & 7);
 }
 
-__device__ __forceinline__ float to_f32(uint16_t h) { return widen(h); }
-__device__ __forceinline__ float to_f32(float x) { return x; }
 
 // ------------------------------------------------------------- prepare
 // Xs = 2^e u as hi (and lo where u is fp32: a bf16 u fits hi exactly), u
@@ -85,14 +83,22 @@ __global__ __launch_bounds__(kThreads) void ns_prepare_kernel(NsArgs g)
     const int i0 = pt.i * kB, j0 = pt.j * kB;
     // rows of u are rows of X, or columns when u is tall
     const int a0 = d.tall ? j0 : i0, b0 = d.tall ? i0 : j0;
-    const int c = threadIdx.x & 63, r0 = threadIdx.x >> 6;
-#pragma unroll 4
-    for (int r = r0; r < kB; r += 4) {
-        const bool in = a0 + r < d.rows && b0 + c < d.cols;
-        const float x = in ? ldexpf(to_f32(u[(int64_t)(a0 + r) * d.ldu + b0 + c]), e) : 0.0f;
-        if (d.tall) sh[c][r] = x;
-        else sh[r][c] = x;
+    float v[4][4];
+    const int c = 4 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {   // (rows and columns are more than kThin here)
+        const int64_t row = a0 + r0 + 16 * h;
+        const bool in = row < d.rows;
+        load_padded<false>(u + (in ? row : 0) * d.ldu, b0 + c, d.cols, in, v[h]);
     }
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float x = ldexpf(v[h][q], e);
+            if (d.tall) sh[c + q][r0 + 16 * h] = x;
+            else sh[r0 + 16 * h][c + q] = x;
+        }
     __syncthreads();
     const int64_t at = ((int64_t)pt.i * (d.np / kB) + pt.j) * kBlock;
     half_t* hi = reinterpret_cast<half_t*>(g.area + d.x[0]) + at;
@@ -371,6 +377,53 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
     }
 }
 
+// The end of the last step for one block of o, staged in `out`: o as bf16, or
+// the update of the master and the parameter with it.  Rows of o are the
+// block's rows, or its columns when u is tall; four elements a lane, the loads
+// of eight quads in flight.
+template <int LAST, int ROW>
+__device__ __forceinline__ void finish_block(const MatDesc& d, const float* out, int bi, int bj, const MuonArgs& ma)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t r0 = (int64_t)(d.tall ? bj : bi) * kB, c0 = (int64_t)(d.tall ? bi : bj) * kB;
+    const float eta = ma.lr * d.scale;
+    const int c = 4 * (lane & 15), rl = lane >> 4;
+    const Span4 s = span4<false>(c0 + c, d.cols, true);
+#pragma unroll
+    for (int h0 = 0; h0 < 16; h0 += 8) {
+        int64_t row[8];
+        int skip[8];
+        float v[8][4];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            const int64_t r = r0 + 4 * (h0 + h) + rl;
+            const bool in = r < d.rows;
+            row[h] = in ? r : 0;
+            skip[h] = in ? s.skip : 4;
+            if constexpr (LAST == kNsUpdate) load_quad<false>(d.master + row[h] * d.ld + s.col, skip[h], v[h]);
+        }
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            const int rr = 4 * (h0 + h) + rl;
+            float o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int cc = (int)(s.col - c0) + q;   // (before the block where the quad begins early: not stored)
+                const int k = cc < 0 || cc > kB - 1 ? 0 : cc;
+                o[q] = d.tall ? out[k * ROW + rr] : out[rr * ROW + k];
+            }
+            if constexpr (LAST == kNsWriteO) {
+                store_quad<false>(d.o + row[h] * d.ldo + s.col, skip[h], o);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[h][q] = muon_elem(v[h][q], o[q], eta, ma);
+                store_quad<false>(d.master + row[h] * d.ld + s.col, skip[h], v[h]);
+                store_quad<false>(d.param + row[h] * d.ld + s.col, skip[h], v[h]);
+            }
+        }
+    }
+}
+
 // X <- a X + B X; the last step writes o as bf16, or updates the master and
 // the parameter with it, instead of X.
 template <int LAST, int WR, int WC, int MB, int S>
@@ -426,33 +479,8 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
             }
         }
         if constexpr (LAST != kNsMid) {
-            // rows of o: the block's rows, or its columns when u is tall; four
-            // elements a lane
             wave_sync();
-            const int r0 = (d.tall ? bj : bi) * kB, c0 = (d.tall ? bi : bj) * kB;
-            const float eta = ma.lr * d.scale;
-#pragma unroll 4
-            for (int h = 0; h < 16; ++h) {
-                const int rr = 4 * h + (lane >> 4), cc = 4 * (lane & 15);
-                const int64_t row = r0 + rr, col = c0 + cc;
-                const int64_t left = d.cols - col;
-                const int n = row < d.rows ? (left >= 4 ? 4 : (left > 0 ? (int)left : 0)) : 0;
-                float o[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    o[q] = d.tall ? out[(cc + q) * T::kOutRow + rr] : out[rr * T::kOutRow + cc + q];
-                if constexpr (LAST == kNsWriteO) {
-                    store_quad(d.o + row * d.ldo + col, n, o);
-                } else {
-                    const int64_t p = row * d.ld + col;
-                    float v[4];
-                    load_quad(d.master + p, n, v);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = muon_elem(v[q], o[q], eta, ma);
-                    store_quad(d.master + p, n, v);
-                    store_quad(d.param + p, n, v);
-                }
-            }
+            finish_block<LAST, T::kOutRow>(d, out, bi, bj, ma);
         }
     }
 }

@@ -34,48 +34,59 @@ typedef half_t h8 __attribute__((ext_vector_type(8)));
 
 constexpr float kQScale = 1024.0f, kPScale = 16.0f;
 
-// Where a segment finds X: u, or (mid) the workspace's fp32 X, which carries S.
+// Where a segment finds X: u, or (mid) the workspace's fp32 X, which carries S
+// and is zero in its padding.
 template <typename U>
 struct Source {
     const U* p;
-    int64_t ld;
+    int64_t ld, rows, cols;
     int tall;
 };
 
 template <typename U>
 __device__ __forceinline__ Source<U> source(const NsArgs& g, const MatDesc& d, int mid)
 {
-    if (mid) return Source<U>{reinterpret_cast<const U*>(g.area + d.x[0]), d.np, 0};
-    return Source<U>{static_cast<const U*>(d.u), d.ldu, d.tall};
+    if (mid) return Source<U>{reinterpret_cast<const U*>(g.area + d.x[0]), d.np, d.k, d.np, 0};
+    return Source<U>{static_cast<const U*>(d.u), d.ldu, d.rows, d.cols, d.tall};
 }
 
-// Calls f(i, j, n, v): n elements v of X from (i, j) on, along j (or, for a
-// tall source, along i), for the columns [j0, j0 + 64) of X; all kThreads take
-// part.  Elements outside X are zero; (i, j) are inside KP x 64 blocks.
-template <typename U, int KP, typename F>
-__device__ __forceinline__ void for_columns(const Source<U>& s, const MatDesc& d, int j0, F f)
-{
-    if (!s.tall) {
-#pragma unroll 4
-        for (int t = threadIdx.x; t < KP * 16; t += kThreads) {
-            const int i = t >> 4, j = (t & 15) * 4;
-            const int left = d.n - (j0 + j), n = i < d.k ? (left >= 4 ? 4 : (left > 0 ? left : 0)) : 0;
-            float v[4];
-            load_quad(s.p + (int64_t)i * s.ld + j0 + j, n, v);
-            f(i, j, v);
-        }
-    } else {
-        constexpr int Q = KP / 4;
-#pragma unroll 4
-        for (int t = threadIdx.x; t < 64 * Q; t += kThreads) {
-            const int j = t / Q, i = (t % Q) * 4;
-            const int left = d.k - i, n = j0 + j < d.n ? (left >= 4 ? 4 : (left > 0 ? left : 0)) : 0;
-            float v[4];
-            load_quad(s.p + (int64_t)(j0 + j) * s.ld + i, n, v);
-            f(i, j, v);
+// A workgroup's share of KP x C of X, columns [j0, j0 + C): a quad a lane and
+// round, along j (wide) or along i (tall), zeros outside X.
+template <int KP, int C>
+struct Chunk {
+    static constexpr int kRounds = KP * C / 4 / kThreads;
+    float v[kRounds][4];
+
+    static __device__ __forceinline__ int at_i(int tall, int h)
+    {
+        const int t = threadIdx.x + h * kThreads;
+        return tall ? (t % (KP / 4)) * 4 : t / (C / 4);
+    }
+    static __device__ __forceinline__ int at_j(int tall, int h)
+    {
+        const int t = threadIdx.x + h * kThreads;
+        return tall ? t / (KP / 4) : (t % (C / 4)) * 4;
+    }
+
+    template <bool SHORT, typename U>
+    __device__ __forceinline__ void load_rows(const Source<U>& s, int64_t j0)
+    {
+#pragma unroll
+        for (int h = 0; h < kRounds; ++h) {
+            const int64_t i = at_i(s.tall, h), j = j0 + at_j(s.tall, h);
+            const int64_t row = s.tall ? j : i, col = s.tall ? i : j;
+            const bool in = row < s.rows;
+            load_padded<SHORT>(s.p + (in ? row : 0) * s.ld, col, s.cols, in, v[h]);
         }
     }
-}
+
+    template <typename U>
+    __device__ __forceinline__ void load(const Source<U>& s, int64_t j0)
+    {
+        if (s.cols >= 4) load_rows<false>(s, j0);
+        else load_rows<true>(s, j0);
+    }
+};
 
 struct HiLo {
     half_t hi, lo;
@@ -88,15 +99,18 @@ __device__ __forceinline__ HiLo split(float x)
 }
 
 // ------------------------------------------------------------- gram
-// Partial sums of X X^T over `split` columns of X each, one workgroup a part:
-// G times 2^2e, with the power of two 2^e that brings the part's largest
-// element to 2^13..2^14 (found in a first look at it; exact, so that neither
-// squares of tiny u underflow nor those of huge u overflow).
+// Partial sums of X X^T over `split` columns of X each, one workgroup a part,
+// 64 columns at a time: G times 2^2e, with the power of two 2^e that brings the
+// largest element so far to 2^13..2^14 (exact, so that neither squares of tiny
+// u underflow nor those of huge u overflow); when a larger one comes, the sum
+// is scaled down to it.  The next 64 columns are loaded while these are
+// multiplied.
 template <typename U, int KP>
 __global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
 {
     constexpr bool LO = sizeof(U) == 4;
     constexpr int N = KP / 32, ROW = 64 + 8;   // 16 x 16 tiles a wave and side; LDS row
+    typedef Chunk<KP, 64> C;
     __shared__ half_t hi[KP][ROW], lo[LO ? KP : 1][ROW];
     __shared__ uint32_t top;
     const GroupDesc& gd = g.groups[g.group];
@@ -104,24 +118,7 @@ __global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
     const ProdTile pt = g.list[gd.sym0 + blockIdx.x];
     const MatDesc& d = g.mats[pt.mat];
     const Source<U> src = source<U>(g, d, mid);
-    const int c0 = pt.j * 64, c1 = min(d.n, c0 + d.split);
-    int e = 0;
-    if (!mid) {
-        if (threadIdx.x == 0) top = 0;
-        __syncthreads();
-        uint32_t m = 0;
-        for (int j0 = c0; j0 < c1; j0 += 64)
-            for_columns<U, KP>(src, d, j0, [&](int, int, const float (&v)[4]) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(v[q]) & 0x7fffffffu);
-            });
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-        if ((threadIdx.x & 63) == 0) atomicMax(&top, m);   // a maximum of integers: any order
-        __syncthreads();
-        const uint32_t t = top;
-        if (t != 0 && t < 0x7f800000u) e = 13 - ilogbf(__uint_as_float(t));
-    }
+    const int64_t c0 = (int64_t)pt.j * 64, c1 = min((int64_t)d.n, c0 + d.split);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wi = (wave >> 1) * (KP / 2), wj = (wave & 1) * (KP / 2);
     f32x4 acc[N][N];
@@ -129,12 +126,41 @@ __global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
     for (int x = 0; x < N; ++x)
 #pragma unroll
         for (int y = 0; y < N; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
-    for (int j0 = c0; j0 < c1; j0 += 64) {
-        __syncthreads();
-        for_columns<U, KP>(src, d, j0, [&](int i, int j, const float (&v)[4]) {
+    if (threadIdx.x == 0) top = 0;
+    int e = mid ? 0 : 1000;   // 1000: nothing but zeros so far
+    C x;
+    x.load(src, c0);
+    for (int64_t j0 = c0; j0 < c1; j0 += 64) {
+        __syncthreads();   // top is set; hi and lo have been read
+        if (!mid) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int h = 0; h < C::kRounds; ++h)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m = max(m, __float_as_uint(x.v[h][q]) & 0x7fffffffu);
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+            if (lane == 0) atomicMax(&top, m);   // a maximum of integers: any order
+            __syncthreads();
+            const uint32_t t = top;
+            // (an infinity or a NaN makes the sum one, at any scale)
+            const int en = t == 0 ? 1000 : t < 0x7f800000u ? 13 - ilogbf(__uint_as_float(t)) : min(e, 0);
+            if (en != e && e != 1000) {
+                const float f = ldexpf(1.0f, max(2 * (en - e), -200));
+#pragma unroll
+                for (int a = 0; a < N; ++a)
+#pragma unroll
+                    for (int b = 0; b < N; ++b) acc[a][b] *= f;
+            }
+            e = en;
+        }
+        const int ex = e == 1000 ? 0 : e;
+#pragma unroll
+        for (int h = 0; h < C::kRounds; ++h) {
+            const int i = C::at_i(src.tall, h), j = C::at_j(src.tall, h);
             HiLo s[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) s[q] = split(ldexpf(v[q], e));
+            for (int q = 0; q < 4; ++q) s[q] = split(ldexpf(x.v[h][q], ex));
             if (!src.tall) {
                 *reinterpret_cast<h4*>(&hi[i][j]) = h4{s[0].hi, s[1].hi, s[2].hi, s[3].hi};
                 if constexpr (LO) *reinterpret_cast<h4*>(&lo[i][j]) = h4{s[0].lo, s[1].lo, s[2].lo, s[3].lo};
@@ -145,40 +171,41 @@ __global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
                     if constexpr (LO) lo[i + q][j] = s[q].lo;
                 }
             }
-        });
+        }
         __syncthreads();
+        if (j0 + 64 < c1) x.load(src, j0 + 64);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c = 32 * h + 8 * (lane >> 4), r = lane & 15;
             h8 ph[N], qh[N], pl[N], ql[N];
 #pragma unroll
-            for (int x = 0; x < N; ++x) {
-                ph[x] = *reinterpret_cast<const h8*>(&hi[wi + 16 * x + r][c]);
-                qh[x] = *reinterpret_cast<const h8*>(&hi[wj + 16 * x + r][c]);
+            for (int a = 0; a < N; ++a) {
+                ph[a] = *reinterpret_cast<const h8*>(&hi[wi + 16 * a + r][c]);
+                qh[a] = *reinterpret_cast<const h8*>(&hi[wj + 16 * a + r][c]);
                 if constexpr (LO) {
-                    pl[x] = *reinterpret_cast<const h8*>(&lo[wi + 16 * x + r][c]);
-                    ql[x] = *reinterpret_cast<const h8*>(&lo[wj + 16 * x + r][c]);
+                    pl[a] = *reinterpret_cast<const h8*>(&lo[wi + 16 * a + r][c]);
+                    ql[a] = *reinterpret_cast<const h8*>(&lo[wj + 16 * a + r][c]);
                 }
             }
 #pragma unroll
-            for (int x = 0; x < N; ++x)
+            for (int a = 0; a < N; ++a)
 #pragma unroll
-                for (int y = 0; y < N; ++y) {
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], ph[x], acc[x][y], 0, 0, 0);
+                for (int b = 0; b < N; ++b) {
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[b], ph[a], acc[a][b], 0, 0, 0);
                     if constexpr (LO) {
-                        acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ql[y], ph[x], acc[x][y], 0, 0, 0);
-                        acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], pl[x], acc[x][y], 0, 0, 0);
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ql[b], ph[a], acc[a][b], 0, 0, 0);
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[b], pl[a], acc[a][b], 0, 0, 0);
                     }
                 }
         }
     }
     float* out = reinterpret_cast<float*>(g.area + d.a) + (int64_t)pt.i * KP * KP;
 #pragma unroll
-    for (int x = 0; x < N; ++x)
+    for (int a = 0; a < N; ++a)
 #pragma unroll
-        for (int y = 0; y < N; ++y)
-            *reinterpret_cast<f32x4*>(out + (wi + 16 * x + (lane & 15)) * KP + wj + 16 * y + 4 * (lane >> 4)) = acc[x][y];
-    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[pt.i] = e;
+        for (int b = 0; b < N; ++b)
+            *reinterpret_cast<f32x4*>(out + (wi + 16 * a + (lane & 15)) * KP + wj + 16 * b + 4 * (lane >> 4)) = acc[a][b];
+    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[pt.i] = e == 1000 ? 0 : e;
 }
 
 // ------------------------------------------------------------- poly
@@ -193,7 +220,8 @@ struct Poly {
     };
 };
 
-// acc = M N, N symmetric.
+// acc = M N, N symmetric.  The operands of the next 32 of the inner dimension
+// are read while these are multiplied.
 template <int KP>
 __device__ __forceinline__ void multiply(const typename Poly<KP>::Mat& M, const typename Poly<KP>::Mat& N,
                                          typename Poly<KP>::Acc& acc)
@@ -228,6 +256,15 @@ __device__ __forceinline__ void multiply(const typename Poly<KP>::Mat& M, const 
                 acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], pl[x], acc[x][y], 0, 0, 0);
             }
     }
+    constexpr int kReads = 2 * (T::MI + T::NI), kMfma = 3 * T::MI * T::NI, kEach = kMfma / kReads > 0 ? kMfma / kReads : 1;
+    __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+#pragma unroll
+    for (int k0 = 32; k0 < KP; k0 += 32)
+#pragma unroll
+        for (int i = 0; i < kReads; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
 }
 
 // f(i, j, v) for the lane's quads of an accumulator: v is row i, columns j..j+3.
@@ -368,6 +405,67 @@ __global__ __launch_bounds__(Poly<KP>::kThr) void thin_poly_kernel(NsArgs g, int
 }
 
 // ------------------------------------------------------------- apply
+// o, or the update with it, from a wave's accumulators: rows i0.. and columns
+// j0.. of X; a lane holds four neighbouring columns, or rows (along_i).
+template <int LAST, bool SHORT, int MI, int NI>
+__device__ __forceinline__ void thin_finish(const MatDesc& d, const f32x4 (&acc)[MI][NI], float f, int i0, int64_t j0,
+                                            bool along_i, const MuonArgs& ma)
+{
+    const int lane = threadIdx.x & 63, r = lane & 15, four = 4 * (lane >> 4);
+    const float eta = ma.lr * d.scale;
+    float v[MI][NI][4];
+    int64_t row[MI][NI], col[MI][NI];
+    int skip[MI][NI], shift[MI][NI];
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y) {
+            const int64_t i = i0 + 16 * x + (along_i ? four : r), j = j0 + 16 * y + (along_i ? r : four);
+            const int64_t rr = along_i ? j : i, cc = along_i ? i : j;
+            const bool in = rr < d.rows;
+            row[x][y] = in ? rr : 0;
+            // the lane's elements are columns cc .. cc + 3 of o; those past its
+            // end are dropped one by one (no lane holds the ones before cc)
+            const int64_t left = d.cols - cc;
+            skip[x][y] = !in || left <= 0 ? 0 : left >= 4 ? 4 : (int)left;
+            col[x][y] = skip[x][y] == 4 ? cc : SHORT ? 0 : (skip[x][y] ? d.cols - 4 : 0);
+            shift[x][y] = (int)(cc - col[x][y]);
+            if constexpr (LAST == kNsUpdate)
+                load_quad<SHORT>(d.master + row[x][y] * d.ld + col[x][y], SHORT ? -skip[x][y] : 0, v[x][y]);
+        }
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+        for (int y = 0; y < NI; ++y) {
+            const int n = skip[x][y];
+            float o[4], p[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = acc[x][y][q] * f;
+            if constexpr (LAST == kNsUpdate) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {   // the master's element for o[q]
+                    float y4 = v[x][y][q];
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) y4 = shift[x][y] == k ? v[x][y][(q + k) & 3] : y4;
+                    p[q] = muon_elem(y4, o[q], eta, ma);
+                }
+            }
+            const int64_t at = row[x][y] * (LAST == kNsUpdate ? d.ld : d.ldo) + col[x][y] + (n < 4 ? shift[x][y] : 0);
+            if constexpr (LAST == kNsUpdate) {
+                if (n == 4) {
+                    store_quad<false>(d.master + at, 0, p);
+                    store_quad<false>(d.param + at, 0, p);
+                } else if (n > 0) {
+                    store_quad<true>(d.master + at, -n, p);
+                    store_quad<true>(d.param + at, -n, p);
+                }
+            } else {
+                if (n == 4) store_quad<false>(d.o + at, 0, o);
+                else if (n > 0) store_quad<true>(d.o + at, -n, o);
+            }
+        }
+}
+
 // 64 columns of P X a workgroup.  P comes straight from memory (L2) into the
 // MFMA's registers, X through LDS with its inner dimension (k) along rows.
 template <typename U, int KP, int LAST>
@@ -382,11 +480,27 @@ __global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid,
     const MatDesc& d = g.mats[pt.mat];
     const Source<U> src = source<U>(g, d, mid);
     const NormRec nr = g.norms[pt.mat];
-    const int j0 = pt.j * 64;
-    for_columns<U, KP>(src, d, j0, [&](int i, int j, const float (&v)[4]) {
+    const int64_t j0 = (int64_t)pt.j * 64;
+    Chunk<KP, 64> xs;
+    xs.load(src, j0);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
+    const int wi = (wave / CW) * 16 * MI, wj = (wave % CW) * 16 * NI;
+    const half_t* pm = reinterpret_cast<const half_t*>(g.area + d.b);
+    h8 ph[KP / 32][MI], pl[KP / 32][MI];
+#pragma unroll
+    for (int k = 0; k < KP / 32; ++k)
+#pragma unroll
+        for (int x = 0; x < MI; ++x) {
+            const half_t* at = pm + (wi + 16 * x + r) * KP + 32 * k + 8 * (lane >> 4);
+            ph[k][x] = *reinterpret_cast<const h8*>(at);
+            pl[k][x] = *reinterpret_cast<const h8*>(at + KP * KP);
+        }
+#pragma unroll
+    for (int h = 0; h < Chunk<KP, 64>::kRounds; ++h) {
+        const int i = Chunk<KP, 64>::at_i(src.tall, h), j = Chunk<KP, 64>::at_j(src.tall, h);
         HiLo s[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] = split(ldexpf(v[q], nr.e));
+        for (int q = 0; q < 4; ++q) s[q] = split(ldexpf(xs.v[h][q], nr.e));
         if (src.tall) {
             *reinterpret_cast<h4*>(&hi[j][i]) = h4{s[0].hi, s[1].hi, s[2].hi, s[3].hi};
             if constexpr (LO) *reinterpret_cast<h4*>(&lo[j][i]) = h4{s[0].lo, s[1].lo, s[2].lo, s[3].lo};
@@ -397,12 +511,9 @@ __global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid,
                 if constexpr (LO) lo[j + q][i] = s[q].lo;
             }
         }
-    });
+    }
     __syncthreads();
     if constexpr (LAST == kNsUpdate) use_device_scalars(ma, nullptr);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
-    const int wi = (wave / CW) * 16 * MI, wj = (wave % CW) * 16 * NI;
-    const half_t* pm = reinterpret_cast<const half_t*>(g.area + d.b);
     // o's rows are X's columns when u is tall: then the lane's four elements
     // are to be four neighbouring rows of X
     const bool along_i = LAST != kNsMid && d.tall;
@@ -412,64 +523,42 @@ __global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid,
 #pragma unroll
         for (int y = 0; y < NI; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int k0 = 0; k0 < KP; k0 += 32) {
-        const int c = k0 + 8 * (lane >> 4);
-        h8 ph[MI], pl[MI], xh[NI], xl[NI];
-#pragma unroll
-        for (int x = 0; x < MI; ++x) {
-            ph[x] = *reinterpret_cast<const h8*>(pm + (wi + 16 * x + r) * KP + c);
-            pl[x] = *reinterpret_cast<const h8*>(pm + KP * KP + (wi + 16 * x + r) * KP + c);
-        }
+    for (int k = 0; k < KP / 32; ++k) {
+        const int c = 32 * k + 8 * (lane >> 4);
+        h8 xh[NI], xl[NI];
 #pragma unroll
         for (int y = 0; y < NI; ++y) {
             xh[y] = *reinterpret_cast<const h8*>(&hi[wj + 16 * y + r][c]);
             if constexpr (LO) xl[y] = *reinterpret_cast<const h8*>(&lo[wj + 16 * y + r][c]);
         }
+        auto add = [&](f32x4& a, h8 p, h8 v) {
+            a = along_i ? __builtin_amdgcn_mfma_f32_16x16x32_f16(p, v, a, 0, 0, 0)
+                        : __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p, a, 0, 0, 0);
+        };
 #pragma unroll
         for (int x = 0; x < MI; ++x)
 #pragma unroll
             for (int y = 0; y < NI; ++y) {
-                if (along_i) {
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph[x], xh[y], acc[x][y], 0, 0, 0);
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl[x], xh[y], acc[x][y], 0, 0, 0);
-                    if constexpr (LO) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph[x], xl[y], acc[x][y], 0, 0, 0);
-                } else {
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xh[y], ph[x], acc[x][y], 0, 0, 0);
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xh[y], pl[x], acc[x][y], 0, 0, 0);
-                    if constexpr (LO) acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xl[y], ph[x], acc[x][y], 0, 0, 0);
-                }
+                add(acc[x][y], ph[k][x], xh[y]);
+                add(acc[x][y], pl[k][x], xh[y]);
+                if constexpr (LO) add(acc[x][y], ph[k][x], xl[y]);
             }
     }
     const float f = nr.r * (LAST == kNsMid ? 1.0f / kPScale : 1.0f / (kPScale * kNsScale));
-    const float eta = ma.lr * d.scale;
+    if constexpr (LAST == kNsMid) {
 #pragma unroll
-    for (int x = 0; x < MI; ++x)
+        for (int x = 0; x < MI; ++x)
 #pragma unroll
-        for (int y = 0; y < NI; ++y) {
-            const int four = 4 * (lane >> 4);
-            const int i = wi + 16 * x + (along_i ? four : r), j = j0 + wj + 16 * y + (along_i ? r : four);
-            float o[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] = acc[x][y][q] * f;
-            if constexpr (LAST == kNsMid) {
-                // (the padding of X's fp32 rows is written, and read as zero)
-                if (i < d.k && j < d.np)
-                    st4(reinterpret_cast<float*>(g.area + d.x[0]) + (int64_t)i * d.np + j, f32x4{o[0], o[1], o[2], o[3]});
-            } else {
-                const int64_t row = along_i ? j : i, col = along_i ? i : j, left = d.cols - col;
-                const int n = row < d.rows ? (left >= 4 ? 4 : (left > 0 ? (int)left : 0)) : 0;
-                if constexpr (LAST == kNsWriteO) {
-                    store_quad(d.o + row * d.ldo + col, n, o);
-                } else {
-                    float v[4];
-                    load_quad(d.master + row * d.ld + col, n, v);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = muon_elem(v[q], o[q], eta, ma);
-                    store_quad(d.master + row * d.ld + col, n, v);
-                    store_quad(d.param + row * d.ld + col, n, v);
-                }
+            for (int y = 0; y < NI; ++y) {
+                // (np is a multiple of 64: the row has room, its padding gets zeros)
+                const int i = wi + 16 * x + r;
+                const int64_t j = j0 + wj + 16 * y + 4 * (lane >> 4);
+                if (i < d.k) st4(reinterpret_cast<float*>(g.area + d.x[0]) + i * (int64_t)d.np + j, acc[x][y] * f);
             }
-        }
+    } else {
+        if (d.cols >= 4) thin_finish<LAST, false>(d, acc, f, wi, j0 + wj, along_i, ma);
+        else thin_finish<LAST, true>(d, acc, f, wi, j0 + wj, along_i, ma);
+    }
 }
 
 }  // namespace
