@@ -515,8 +515,9 @@ typedef struct zero1_matrix {
  * shapes. */
 #define ZERO1_MUON_MAX_GROUPS 64
 typedef struct zero1_matrix_group {
-    int32_t n_sym, n_full, n_blocks;
-    int16_t sym_tile, full_tile, thin, reserved;
+    int64_t sym0, full0, blocks0;
+    int32_t n_sym, n_full, n_blocks, first;
+    int16_t sym_tile, full_tile, thin, parts, one, reserved[3];
 } zero1_matrix_group;
 
 /* A validated list of matrices uploaded by zero1_muon_plan.  Plain data owned
@@ -524,7 +525,7 @@ typedef struct zero1_matrix_group {
 typedef struct zero1_matrix_plan {
     void* table;
     int64_t elems;          /* sum of rows * cols                               */
-    int64_t off_tiles, off_groups, off_list, area_bytes;
+    int64_t off_tiles, off_list, area_bytes;
     int32_t n_mats, n_tiles, n_groups;
     uint32_t flags;         /* ZERO1_MV_BF16, ZERO1_U_F32                       */
     uint32_t has;           /* which buffers the matrices have                  */

@@ -94,13 +94,14 @@ class Matrix(ctypes.Structure):
 
 
 class MatrixGroup(ctypes.Structure):
-    _fields_ = [("n_sym", ctypes.c_int32), ("n_full", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+    _fields_ = [("sym0", i64), ("full0", i64), ("blocks0", i64), ("n_sym", ctypes.c_int32),
+                ("n_full", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("first", ctypes.c_int32),
                 ("sym_tile", ctypes.c_int16), ("full_tile", ctypes.c_int16), ("thin", ctypes.c_int16),
-                ("reserved", ctypes.c_int16)]
+                ("parts", ctypes.c_int16), ("one", ctypes.c_int16), ("reserved", ctypes.c_int16 * 3)]
 
 
 class MatrixPlan(ctypes.Structure):
-    _fields_ = [("table", P), ("elems", i64), ("off_tiles", i64), ("off_groups", i64), ("off_list", i64),
+    _fields_ = [("table", P), ("elems", i64), ("off_tiles", i64), ("off_list", i64),
                 ("area_bytes", i64), ("n_mats", ctypes.c_int32), ("n_tiles", ctypes.c_int32),
                 ("n_groups", ctypes.c_int32), ("flags", ctypes.c_uint32), ("has", ctypes.c_uint32),
                 ("device", ctypes.c_int32), ("n_dense", ctypes.c_int32), ("dense_tiles", ctypes.c_int32),

@@ -55,21 +55,13 @@ struct ProdTile {
     int32_t mat, i, j, reserved;
 };
 
-// Matrices that are iterated together, and what there is of them in the list
-// of ProdTiles: tiles of A and B (upper triangle), tiles of X, blocks of X; of
-// thin matrices parts of the gram sum (i: the part, j: its first 64 columns)
-// and X's columns in 64s (j).
-struct GroupDesc {
-    int64_t sym0, full0, blocks0;
-    int32_t n_sym, n_full, n_blocks;
-    int32_t first;                 // its first matrix
-};
-
 // Matrices with k up to this take the kernels of ns_thin.hip.
 constexpr int kThin = 128;
 constexpr int kThinMaxParts = 32;
-// Growth of the product of a segment's steps (ns_thin.hip).
-constexpr double kThinGrowth = 2048.0;
+constexpr int kThinOne = 256;      // n up to this: one workgroup does all of a matrix of k <= 64
+// How much a segment's steps before its last may grow small singular values
+// (ns_thin.hip).
+constexpr double kThinGrowth = 160.0;
 
 // Shapes of the products' tiles.
 enum TileShape : int { kTile128 = 0, kTile192 = 1, kTile256 = 2 };
@@ -104,9 +96,10 @@ struct MuonClip {
 
 struct NsArgs {
     const MatDesc* mats;
-    const GroupDesc* groups;
-    const ProdTile* list;
-    int group;
+    const ProdTile* sym;           // a group's tiles of A and B, of X, blocks of X; of thin matrices
+    const ProdTile* full;          // parts of the gram sum (i: the part, j: its first 64 columns), X's
+    const ProdTile* blocks;        // columns in 64s (j), none
+    int first;                     // the group's first matrix
     char* area;                    // the workspace's group area
     const NormRec* norms;
     float a, b, c;
@@ -135,6 +128,12 @@ hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, con
 hipError_t launch_thin_gram(const NsArgs& g, int kp, bool f32, int mid, int grid, hipStream_t s);
 hipError_t launch_thin_poly(const NsArgs& g, int kp, int mid, int steps, double eps, NormRec* norms, int grid,
                             hipStream_t s);
+// The parts' sum, where there is more than one.
+hipError_t launch_thin_sum(const NsArgs& g, int kp, int n_mats, hipStream_t s);
+// A group of matrices of one part and k <= 64, in one launch (from u, all
+// steps in one segment).
+hipError_t launch_thin_one(const NsArgs& g, int kp, bool f32, int steps, double eps, NormRec* norms, NsLast last,
+                           const MuonArgs& ma, int n_mats, hipStream_t s);
 hipError_t launch_thin_apply(const NsArgs& g, int kp, bool f32, int mid, NsLast last, const MuonArgs& ma, int grid,
                              hipStream_t s);
 

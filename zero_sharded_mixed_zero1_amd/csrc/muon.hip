@@ -65,42 +65,48 @@ __device__ __forceinline__ Quad quad_at(const MatDesc& d, const StreamTile& t, i
     return Quad{in ? row : 0, s.col, s.skip};
 }
 
-// Fixed-order workgroup sum; the total is in thread 0.  `sh` alternates
-// between two buffers from tile to tile, so one barrier a tile is enough.
-__device__ __forceinline__ double tile_sum(double x, double* sh)
+// Fixed-order workgroup sums of N tiles at once, one number a wave in `sh` at
+// the end.  `sh` alternates between two buffers, so one barrier a round is
+// enough.
+template <int N>
+__device__ __forceinline__ void tile_sums(double (&x)[N], double (*sh)[kThreads / 64])
 {
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) x[k] += __shfl_xor(x[k], off, 64);
+        if ((threadIdx.x & 63) == 0) sh[k][threadIdx.x >> 6] = x[k];
+    }
     __syncthreads();
-    return ((sh[0] + sh[1]) + sh[2]) + sh[3];
 }
 
-// The reduced gradient of the lane's two quads: slices added in rank order,
-// the loads of up to eight slices in flight together; then the average.
-template <bool SHORT, int N>
-__device__ __forceinline__ void add_slices(const Reduce& r, int w0, const int64_t (&at)[2], const int (&skip)[2],
-                                           float (&g)[2][4])
+__device__ __forceinline__ double four(const double (&s)[kThreads / 64]) { return ((s[0] + s[1]) + s[2]) + s[3]; }
+
+// The reduced gradient of the lane's Q quads: slices added in rank order, the
+// loads of N slices in flight together; then the average.
+template <bool SHORT, int N, int Q>
+__device__ __forceinline__ void add_slices(const Reduce& r, int w0, const int64_t (&at)[Q], const int (&skip)[Q],
+                                           float (&g)[Q][4])
 {
     if constexpr (SHORT) {
         for (int w = w0; w < w0 + N; ++w)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < Q; ++h) {
                 float x[4];
                 load_quad<true>(r.gp.p[w] + at[h], skip[h], x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) g[h][j] = w == 0 ? x[j] : g[h][j] + x[j];
             }
     } else {
-        u16x4 raw[N][2];
+        u16x4 raw[N][Q];
 #pragma unroll
         for (int w = 0; w < N; ++w)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) raw[w][h] = ld4(r.gp.p[w0 + w] + at[h]);
+            for (int h = 0; h < Q; ++h) raw[w][h] = ld4(r.gp.p[w0 + w] + at[h]);
 #pragma unroll
         for (int w = 0; w < N; ++w)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < Q; ++h) {
                 float x[4];
                 widen4(raw[w][h], x);
 #pragma unroll
@@ -109,15 +115,17 @@ __device__ __forceinline__ void add_slices(const Reduce& r, int w0, const int64_
     }
 }
 
-template <bool SHORT>
-__device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at)[2], const int (&skip)[2],
-                                             float (&g)[2][4])
+template <bool SHORT, bool FEW, int Q>
+__device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at)[Q], const int (&skip)[Q],
+                                             float (&g)[Q][4])
 {
     int w = 0;
-    for (; w + 8 <= r.W; w += 8) add_slices<SHORT, 8>(r, w, at, skip, g);
-    if (w + 4 <= r.W) {
-        add_slices<SHORT, 4>(r, w, at, skip, g);
-        w += 4;
+    if constexpr (!FEW) {
+        for (; w + 8 <= r.W; w += 8) add_slices<SHORT, 8>(r, w, at, skip, g);
+        if (w + 4 <= r.W) {
+            add_slices<SHORT, 4>(r, w, at, skip, g);
+            w += 4;
+        }
     }
     if (w + 2 <= r.W) {
         add_slices<SHORT, 2>(r, w, at, skip, g);
@@ -125,7 +133,7 @@ __device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at
     }
     if (w < r.W) add_slices<SHORT, 1>(r, w, at, skip, g);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < Q; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float v = g[h][j];
@@ -136,55 +144,68 @@ __device__ __forceinline__ void reduce_quads(const Reduce& r, const int64_t (&at
         }
 }
 
-// One tile of the momentum; returns the lane's sum of squares of u.
-template <typename M, typename U, bool NORM, bool SHORT>
-__device__ __forceinline__ double momentum_tile(const Reduce& r, const MatDesc& d, const StreamTile& tile, float mu,
-                                                int nesterov, bool clip, float coef)
+struct MomentumArgs {
+    float mu;
+    int nesterov;
+    bool clip;
+    float coef;
+};
+
+// N tiles of the momentum together (d: their matrices); acc: the lane's sum of
+// squares of u in each.
+template <typename M, typename U, bool NORM, bool SHORT, bool FEW, int N>
+__device__ __forceinline__ void momentum_tiles(const Reduce& r, const MatDesc* const (&d)[N], const StreamTile (&tile)[N],
+                                               const MomentumArgs& a, double (&acc)[N])
 {
-    Quad q[2];
-    int64_t at[2], ga[2];
-    int skip[2];
-    float g[2][4], m[2][4], u[2][4];
+    constexpr int Q = 2 * N;
+    int64_t at[Q], ga[Q], ua[Q];
+    int skip[Q];
+    float g[Q][4], m[Q][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        q[h] = quad_at<SHORT>(d, tile, (int)threadIdx.x + h * kThreads);
-        skip[h] = q[h].skip;
-        at[h] = q[h].row * d.ld + q[h].col;
-        ga[h] = d.shard_offset + at[h];
-        load_quad<SHORT>(static_cast<const M*>(d.m) + at[h], skip[h], m[h]);
+    for (int h = 0; h < Q; ++h) {
+        const MatDesc& e = *d[h / 2];
+        const Quad q = quad_at<SHORT>(e, tile[h / 2], (int)threadIdx.x + (h & 1) * kThreads);
+        skip[h] = q.skip;
+        at[h] = q.row * e.ld + q.col;
+        ua[h] = q.row * e.ldu + q.col;
+        ga[h] = e.shard_offset + at[h];
+        load_quad<SHORT>(static_cast<const M*>(e.m) + at[h], skip[h], m[h]);
     }
-    reduce_quads<SHORT>(r, ga, skip, g);
-    double acc = 0.0;
+    reduce_quads<SHORT, FEW>(r, ga, skip, g);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < Q; ++h) {
+        const MatDesc& e = *d[h / 2];
+        float u[4];
+        if ((h & 1) == 0) acc[h / 2] = 0.0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float gj = clip ? g[h][j] * coef : g[h][j];
-            const float mj = mu * m[h][j] + gj;
+            const float gj = a.clip ? g[h][j] * a.coef : g[h][j];
+            const float mj = a.mu * m[h][j] + gj;
             m[h][j] = mj;
-            u[h][j] = nesterov ? gj + mu * mj : mj;
+            u[j] = a.nesterov ? gj + a.mu * mj : mj;
         }
-        store_quad<SHORT>(static_cast<M*>(d.m) + at[h], skip[h], m[h]);
-        store_quad<SHORT>(static_cast<U*>(d.u) + (q[h].row * d.ldu + q[h].col), skip[h], u[h]);
+        store_quad<SHORT>(static_cast<M*>(e.m) + at[h], skip[h], m[h]);
+        store_quad<SHORT>(static_cast<U*>(e.u) + ua[h], skip[h], u);
         if constexpr (NORM) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (owns<SHORT>(skip[h], j)) acc = fma((double)u[h][j], (double)u[h][j], acc);
+                if (owns<SHORT>(skip[h], j)) acc[h / 2] = fma((double)u[j], (double)u[j], acc[h / 2]);
         }
     }
-    return acc;
 }
 
 // m = mu m + g; u = g + mu m (Nesterov) or m.  Moves 2W + 2 sizeof(m) +
-// sizeof(u) bytes an element.
-template <typename M, typename U, bool NORM>
+// sizeof(u) bytes an element.  FEW: one or two slices, whose tiles are taken two
+// at a time (a tile of them alone is too little in flight).
+template <typename M, typename U, bool NORM, bool FEW>
 __global__ __launch_bounds__(kThreads) void momentum_kernel(Reduce r, const MatDesc* __restrict__ mats,
                                                             const StreamTile* __restrict__ tiles, int n_tiles,
                                                             int nesterov, MuonArgs ma, MuonClip mc,
                                                             double* __restrict__ partials, int split)
 {
     __shared__ NormInfo ni;
-    __shared__ double sums[2][kThreads / 64];
+    constexpr int N = FEW ? 2 : 1;
+    __shared__ double sums[2][N][kThreads / 64];
     use_device_scalars(ma, &mc.max_norm);
     bool clip = false;
     float coef = 1.0f;
@@ -202,56 +223,86 @@ __global__ __launch_bounds__(kThreads) void momentum_kernel(Reduce r, const MatD
         clip = ni.clip != 0;
         coef = ni.clip_coef;
     }
+    const MomentumArgs a{ma.mu, nesterov, clip, coef};
     const Walk wk = walk(n_tiles, split);
     int buf = 0;
-    for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
-        const StreamTile tile = tiles[t];
-        const MatDesc& d = mats[tile.mat];
-        const double acc = d.vcols >= 4 ? momentum_tile<M, U, NORM, false>(r, d, tile, ma.mu, nesterov, clip, coef)
-                                        : momentum_tile<M, U, NORM, true>(r, d, tile, ma.mu, nesterov, clip, coef);
+    for (int64_t t = wk.lo; t < wk.hi; t += N * wk.step) {
+        StreamTile tile[N];
+        const MatDesc* d[N];
+        bool one = false, shorts = false;   // the second tile is missing; rows shorter than a quad
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int64_t tk = t + k * wk.step;
+            one = one || tk >= wk.hi;
+            tile[k] = tiles[tk < wk.hi ? tk : t];
+            d[k] = mats + tile[k].mat;
+            shorts = shorts || d[k]->vcols < 4;
+        }
+        double acc[N];
+        if (N > 1 && (one || shorts)) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (t + k * wk.step >= wk.hi) break;
+                const MatDesc* dk[1] = {d[k]};
+                const StreamTile tk[1] = {tile[k]};
+                double ak[1];
+                if (d[k]->vcols < 4) momentum_tiles<M, U, NORM, true, FEW, 1>(r, dk, tk, a, ak);
+                else momentum_tiles<M, U, NORM, false, FEW, 1>(r, dk, tk, a, ak);
+                acc[k] = ak[0];
+            }
+        } else if (shorts) {
+            momentum_tiles<M, U, NORM, true, FEW, N>(r, d, tile, a, acc);
+        } else {
+            momentum_tiles<M, U, NORM, false, FEW, N>(r, d, tile, a, acc);
+        }
         if constexpr (NORM) {
-            const double b = tile_sum(acc, sums[buf]);
+            tile_sums<N>(acc, sums[buf]);
+            if (threadIdx.x < N && t + threadIdx.x * wk.step < wk.hi)
+                partials[t + threadIdx.x * wk.step] = four(sums[buf][threadIdx.x]);
             buf ^= 1;
-            if (threadIdx.x == 0) partials[t] = b;
         }
     }
 }
 
-template <typename U, bool SHORT>
-__device__ __forceinline__ double sumsq_tile(const MatDesc& d, const StreamTile& tile)
-{
-    float u[2][4];
-    int skip[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const Quad q = quad_at<SHORT>(d, tile, (int)threadIdx.x + h * kThreads);
-        skip[h] = q.skip;
-        load_quad<SHORT>(static_cast<const U*>(d.u) + (q.row * d.ldu + q.col), q.skip, u[h]);
-    }
-    double acc = 0.0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (owns<SHORT>(skip[h], j)) acc = fma((double)u[h][j], (double)u[h][j], acc);
-    return acc;
-}
-
+// Four tiles a round, so that 8 quads a lane are in flight.
 template <typename U>
 __global__ __launch_bounds__(kThreads) void u_sumsq_kernel(const MatDesc* __restrict__ mats,
                                                            const StreamTile* __restrict__ tiles, int n_tiles,
                                                            double* __restrict__ partials, int split)
 {
-    __shared__ double sums[2][kThreads / 64];
+    constexpr int N = 4;
+    __shared__ double sums[2][N][kThreads / 64];
     const Walk wk = walk(n_tiles, split);
     int buf = 0;
-    for (int64_t t = wk.lo; t < wk.hi; t += wk.step) {
-        const StreamTile tile = tiles[t];
-        const MatDesc& d = mats[tile.mat];
-        const double acc = d.vcols >= 4 ? sumsq_tile<U, false>(d, tile) : sumsq_tile<U, true>(d, tile);
-        const double b = tile_sum(acc, sums[buf]);
+    for (int64_t t = wk.lo; t < wk.hi; t += N * wk.step) {
+        float u[N][2][4];
+        int skip[N][2];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {   // (these matrices are not thin: no row is short)
+            const int64_t tk = t + k * wk.step;
+            const StreamTile tile = tiles[tk < wk.hi ? tk : t];
+            const MatDesc& d = mats[tile.mat];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const Quad q = quad_at<false>(d, tile, (int)threadIdx.x + h * kThreads);
+                skip[k][h] = q.skip;
+                load_quad<false>(static_cast<const U*>(d.u) + (q.row * d.ldu + q.col), q.skip, u[k][h]);
+            }
+        }
+        double acc[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            acc[k] = 0.0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (owns<false>(skip[k][h], j)) acc[k] = fma((double)u[k][h][j], (double)u[k][h][j], acc[k]);
+        }
+        tile_sums<N>(acc, sums[buf]);
+        if (threadIdx.x < N && t + threadIdx.x * wk.step < wk.hi)
+            partials[t + threadIdx.x * wk.step] = four(sums[buf][threadIdx.x]);
         buf ^= 1;
-        if (threadIdx.x == 0) partials[t] = b;
     }
 }
 
@@ -261,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void ns_norms_kernel(const MatDesc* __res
                                                             const double* __restrict__ partials, double eps,
                                                             NormRec* __restrict__ norms)
 {
-    __shared__ double sums[kThreads / 64];
+    __shared__ double sums[1][kThreads / 64];
     const MatDesc& d = mats[blockIdx.x];
     double a = 0.0;
     for (int i0 = threadIdx.x; i0 < d.n_tiles; i0 += 16 * kThreads) {   // 16 loads in flight
@@ -271,8 +322,10 @@ __global__ __launch_bounds__(kThreads) void ns_norms_kernel(const MatDesc* __res
 #pragma unroll
         for (int k = 0; k < 16; ++k) a = a + x[k];
     }
-    const double tot = tile_sum(a, sums);
+    double x[1] = {a};
+    tile_sums<1>(x, sums);
     if (threadIdx.x == 0) {
+        const double tot = four(sums[0]);
         const double f = (double)kNsScale / (sqrt(tot) + eps);
         NormRec n;
         // a norm that is infinite, NaN, or zero with eps = 0: u / (norm + eps)
@@ -333,13 +386,18 @@ hipError_t launch_momentum(const Reduce& r, const MatDesc* mats, const StreamTil
                            bool u_f32, bool nesterov, const MuonArgs& ma, const MuonClip& mc, double* partials,
                            int nblocks, int split, hipStream_t s)
 {
-#define Z1_MOM(M, U, N)                                                                                          \
-    momentum_kernel<M, U, N><<<dim3(nblocks), dim3(kThreads), 0, s>>>(r, mats, tiles, n_tiles, nesterov ? 1 : 0, \
-                                                                      ma, mc, partials, split)
-#define Z1_MOM_N(M, U)                  \
-    do {                                \
-        if (partials) Z1_MOM(M, U, true); \
-        else Z1_MOM(M, U, false);       \
+    const int nv = nesterov ? 1 : 0;
+#define Z1_MOM(M, U, N, F) \
+    momentum_kernel<M, U, N, F><<<dim3(nblocks), dim3(kThreads), 0, s>>>(r, mats, tiles, n_tiles, nv, ma, mc, partials, split)
+#define Z1_MOM_N(M, U)                                     \
+    do {                                                   \
+        if (r.W <= 2) {                                    \
+            if (partials) Z1_MOM(M, U, true, true);        \
+            else Z1_MOM(M, U, false, true);                \
+        } else {                                           \
+            if (partials) Z1_MOM(M, U, true, false);       \
+            else Z1_MOM(M, U, false, false);               \
+        }                                                  \
     } while (0)
     if (m_bf16) {
         if (u_f32) Z1_MOM_N(uint16_t, float);

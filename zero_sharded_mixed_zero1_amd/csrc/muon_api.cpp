@@ -205,19 +205,18 @@ zero1_status check_iteration(const zero1_muon_hparams* hp)
 }
 
 // Steps of a thin matrix's iteration, from singular values within `top` on,
-// that are taken as one product: as many as keep what it does to singular
-// values near zero within kThinGrowth.  Moves `top` along.
+// that are taken as one product: as many as keep what the steps before the last
+// do to singular values near zero within kThinGrowth.  Moves `top` along.
 int segment_steps(const zero1_muon_hparams* hp, int left, double& top)
 {
     double growth = 1.0;
     int m = 0;
-    while (m < left) {
+    do {
         const Reach r = reach(hp, top);
         growth *= std::max(1.0, r.q);
-        if (m > 0 && growth > kThinGrowth) break;
         top = r.p;
         ++m;
-    }
+    } while (m < left && growth <= kThinGrowth);
     return m;
 }
 
@@ -346,16 +345,14 @@ double tile_time(const TileCost& c, double tiles, int inner)
 struct Host {
     std::vector<MatDesc> mats;
     std::vector<StreamTile> tiles;
-    std::vector<GroupDesc> groups;
     std::vector<ProdTile> list;
-    std::vector<zero1_matrix_group> shape;
+    std::vector<zero1_matrix_group> groups;
     int64_t area = 0;
     uint32_t has = 0;
     int64_t elems = 0;
     int32_t n_dense = 0, dense_tiles = 0;   // matrices that are not thin (the first ones), their streaming tiles
     size_t off_tiles() const { return round_up(sizeof(MatDesc) * mats.size(), 256); }
-    size_t off_groups() const { return off_tiles() + round_up(sizeof(StreamTile) * tiles.size(), 256); }
-    size_t off_list() const { return off_groups() + round_up(sizeof(GroupDesc) * groups.size(), 256); }
+    size_t off_list() const { return off_tiles() + round_up(sizeof(StreamTile) * tiles.size(), 256); }
     size_t bytes() const { return off_list() + sizeof(ProdTile) * list.size(); }
 };
 
@@ -433,7 +430,7 @@ int64_t place(MatDesc& d, int64_t at)
     const int thin = thin_rows(d.k);
     if (thin) {
         d.kp = thin;
-        d.n_parts = (int32_t)std::min<int64_t>(kThinMaxParts, (d.n + 127) / 128);
+        d.n_parts = thin <= 64 && d.n <= kThinOne ? 1 : (int32_t)std::min<int64_t>(kThinMaxParts, (d.n + 127) / 128);
         d.split = (int32_t)round_up64((d.n + d.n_parts - 1) / d.n_parts, kPad);
         d.n_parts = (d.n + d.split - 1) / d.split;
         d.x[0] = at;
@@ -450,7 +447,7 @@ int64_t place(MatDesc& d, int64_t at)
     d.b = d.a + a;
     return d.b + a;
 }
-static_assert(kThinMaxParts * sizeof(int32_t) <= 256, "exponents of the parts");
+static_assert((kThinMaxParts + 1) * sizeof(int32_t) <= 256, "exponents of the parts and of their sum");
 
 // Block rows and columns of X, or of A and B.
 struct Blocks {
@@ -518,37 +515,37 @@ int16_t best_tile(const Host& h, size_t first, size_t end, bool sym)
 
 void add_group(Host& h, size_t first, size_t end)
 {
-    zero1_matrix_group z;
-    std::memset(&z, 0, sizeof z);
-    GroupDesc g;
+    zero1_matrix_group g;
     std::memset(&g, 0, sizeof g);
     g.first = (int32_t)first;
-    z.thin = (int16_t)thin_rows(h.mats[first].k);
-    if (z.thin) {
-        g.sym0 = (int64_t)h.list.size();
-        for (size_t m = first; m < end; ++m)
-            for (int p = 0; p < h.mats[m].n_parts; ++p)
-                h.list.push_back(ProdTile{(int32_t)m, p, p * (h.mats[m].split / kPad), 0});
-        g.n_sym = z.n_sym = (int32_t)(h.list.size() - g.sym0);
-        g.full0 = (int64_t)h.list.size();
+    g.thin = (int16_t)thin_rows(h.mats[first].k);
+    auto here = [&h] { return (int64_t)h.list.size(); };
+    g.sym0 = here();
+    if (g.thin) {
+        bool one = g.thin <= 64;
+        for (size_t m = first; m < end; ++m) {
+            const MatDesc& d = h.mats[m];
+            one = one && d.n <= kThinOne;
+            g.parts = std::max(g.parts, (int16_t)d.n_parts);
+            for (int p = 0; p < d.n_parts; ++p) h.list.push_back(ProdTile{(int32_t)m, p, p * (d.split / kPad), 0});
+        }
+        g.one = one ? 1 : 0;
+        g.n_sym = (int32_t)(here() - g.sym0);
+        g.full0 = here();
         for (size_t m = first; m < end; ++m)
             for (int j = 0; j < h.mats[m].np / kPad; ++j) h.list.push_back(ProdTile{(int32_t)m, 0, j, 0});
-        g.n_full = z.n_full = (int32_t)(h.list.size() - g.full0);
-        g.n_blocks = z.n_blocks = (int32_t)(end - first);
-        h.groups.push_back(g);
-        h.shape.push_back(z);
-        return;
+        g.n_full = (int32_t)(here() - g.full0);
+        g.n_blocks = (int32_t)(end - first);
+    } else {
+        g.sym_tile = best_tile(h, first, end, true);
+        g.full_tile = best_tile(h, first, end, false);
+        g.n_sym = add_tiles(h, first, end, kTiles[g.sym_tile].side, true);
+        g.full0 = here();
+        g.n_full = add_tiles(h, first, end, kTiles[g.full_tile].side, false);
+        g.blocks0 = here();
+        g.n_blocks = add_tiles(h, first, end, 1, false);
     }
-    z.sym_tile = best_tile(h, first, end, true);
-    z.full_tile = best_tile(h, first, end, false);
-    g.sym0 = (int64_t)h.list.size();
-    g.n_sym = z.n_sym = add_tiles(h, first, end, kTiles[z.sym_tile].side, true);
-    g.full0 = (int64_t)h.list.size();
-    g.n_full = z.n_full = add_tiles(h, first, end, kTiles[z.full_tile].side, false);
-    g.blocks0 = (int64_t)h.list.size();
-    g.n_blocks = z.n_blocks = add_tiles(h, first, end, 1, false);
     h.groups.push_back(g);
-    h.shape.push_back(z);
 }
 
 void sides(const zero1_matrix& q, MatDesc& d)
@@ -708,8 +705,7 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
     NsArgs g;
     std::memset(&g, 0, sizeof g);
     g.mats = plan_mats(plan);
-    g.groups = reinterpret_cast<const GroupDesc*>(tb + plan->off_groups);
-    g.list = reinterpret_cast<const ProdTile*>(tb + plan->off_list);
+    const ProdTile* list = reinterpret_cast<const ProdTile*>(tb + plan->off_list);
     g.area = ws + ws_area(plan);
     g.norms = norms;
     g.a = (float)hp->ns_a;
@@ -717,16 +713,25 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
     g.c = (float)hp->ns_c;
     const bool u_f32 = (plan->flags & ZERO1_U_F32) != 0;
     const MuonArgs ma = muon_args(hp, flags);
-    for (g.group = 0; g.group < plan->n_groups; ++g.group) {
-        const zero1_matrix_group& q = plan->groups[g.group];
+    for (int i = 0; i < plan->n_groups; ++i) {
+        const zero1_matrix_group& q = plan->groups[i];
+        g.first = q.first;
+        g.sym = list + q.sym0;
+        g.full = list + q.full0;
+        g.blocks = list + q.blocks0;
         if (q.thin) {
             double top = 1.0;
             for (int it = 0; it < hp->ns_steps;) {
                 const int m = segment_steps(hp, hp->ns_steps - it, top), mid = it > 0 ? 1 : 0;
                 const NsLast to = it + m == hp->ns_steps ? last : kNsMid;
-                Z1_HIP(launch_thin_gram(g, q.thin, u_f32 || mid, mid, q.n_sym, s));
-                Z1_HIP(launch_thin_poly(g, q.thin, mid, m, hp->ns_eps, norms, q.n_blocks, s));
-                Z1_HIP(launch_thin_apply(g, q.thin, u_f32 || mid, mid, to, ma, q.n_full, s));
+                if (q.one && !mid && to != kNsMid) {
+                    Z1_HIP(launch_thin_one(g, q.thin, u_f32, m, hp->ns_eps, norms, to, ma, q.n_blocks, s));
+                } else {
+                    Z1_HIP(launch_thin_gram(g, q.thin, u_f32 || mid, mid, q.n_sym, s));
+                    if (q.parts > 1) Z1_HIP(launch_thin_sum(g, q.thin, q.n_blocks, s));
+                    Z1_HIP(launch_thin_poly(g, q.thin, mid, m, hp->ns_eps, norms, q.n_blocks, s));
+                    Z1_HIP(launch_thin_apply(g, q.thin, u_f32 || mid, mid, to, ma, q.n_full, s));
+                }
                 it += m;
             }
             continue;
@@ -776,23 +781,19 @@ zero1_status zero1_muon_plan(const zero1_matrix* mats, int n_mats, uint32_t flag
         std::vector<char> host(need, 0);
         std::memcpy(host.data(), h.mats.data(), sizeof(MatDesc) * h.mats.size());
         std::memcpy(host.data() + h.off_tiles(), h.tiles.data(), sizeof(StreamTile) * h.tiles.size());
-        if (!h.groups.empty()) {
-            std::memcpy(host.data() + h.off_groups(), h.groups.data(), sizeof(GroupDesc) * h.groups.size());
-            std::memcpy(host.data() + h.off_list(), h.list.data(), sizeof(ProdTile) * h.list.size());
-        }
+        if (!h.list.empty()) std::memcpy(host.data() + h.off_list(), h.list.data(), sizeof(ProdTile) * h.list.size());
         Z1_HIP(hipMemcpy(table, host.data(), need, hipMemcpyHostToDevice));
         zero1_matrix_plan p;
         std::memset(&p, 0, sizeof p);
         p.table = table;
         p.elems = h.elems;
         p.off_tiles = (int64_t)h.off_tiles();
-        p.off_groups = (int64_t)h.off_groups();
         p.off_list = (int64_t)h.off_list();
         p.area_bytes = h.area;
         p.n_mats = n_mats;
         p.n_tiles = (int32_t)h.tiles.size();
         p.n_groups = (int32_t)h.groups.size();
-        std::copy(h.shape.begin(), h.shape.end(), p.groups);
+        std::copy(h.groups.begin(), h.groups.end(), p.groups);
         p.flags = flags & kPlanFlags;
         p.has = h.has;
         p.n_dense = h.n_dense;

@@ -74,9 +74,7 @@ __global__ __launch_bounds__(kThreads) void ns_prepare_kernel(NsArgs g)
 {
     constexpr bool LO = sizeof(U) == 4;
     __shared__ float sh[kB][kB + 1];
-    const GroupDesc& gd = g.groups[g.group];
-    if ((int)blockIdx.x >= gd.n_blocks) return;
-    const ProdTile pt = g.list[gd.blocks0 + blockIdx.x];
+    const ProdTile pt = g.blocks[blockIdx.x];
     const MatDesc& d = g.mats[pt.mat];
     const int e = g.norms[pt.mat].e;
     const U* u = static_cast<const U*>(d.u);
@@ -328,9 +326,7 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
 {
     using T = Tile<WR, WC, MB, S>;
     __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
-    const GroupDesc& gd = g.groups[g.group];
-    if ((int)blockIdx.x >= gd.n_sym) return;
-    const ProdTile pt = g.list[gd.sym0 + blockIdx.x];
+    const ProdTile pt = g.sym[blockIdx.x];
     const MatDesc& d = g.mats[pt.mat];
     const half_t* src = reinterpret_cast<const half_t*>(g.area + (OP == kGram ? d.x[it & 1] : d.a));
     half_t* dst = reinterpret_cast<half_t*>(g.area + (OP == kGram ? d.a : d.b));
@@ -431,9 +427,7 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
 {
     using T = Tile<WR, WC, MB, S>;
     __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
-    const GroupDesc& gd = g.groups[g.group];
-    if ((int)blockIdx.x >= gd.n_full) return;
-    const ProdTile pt = g.list[gd.full0 + blockIdx.x];
+    const ProdTile pt = g.full[blockIdx.x];
     const MatDesc& d = g.mats[pt.mat];
     const half_t* xi = reinterpret_cast<const half_t*>(g.area + d.x[it & 1]);
     half_t* xo = reinterpret_cast<half_t*>(g.area + d.x[(it & 1) ^ 1]);

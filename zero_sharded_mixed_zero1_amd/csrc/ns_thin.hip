@@ -1,5 +1,5 @@
 // ns_thin.hip -- orthogonalisation of thin matrices (k = min(rows, cols) up to
-// 128) on gfx950, in three launches however many steps there are.
+// 128) on gfx950, in one to four launches however many steps there are.
 //
 // A step multiplies X from the left by Q = a I + b A + c A A, a polynomial of
 // A = X X^T, and A becomes Q A Q.  So the steps need X only through A, which is
@@ -8,16 +8,20 @@
 // written once, where the tiles of newton_schulz.hip read and write it every
 // step (and would leave most of the chip idle: k <= 128 is one tile of A).
 //
-// Precision: A's small eigenvalues are squares of X's small singular values, so
-// A, Q and P are held and multiplied as two fp16 halves (22 bits, three MFMAs a
-// product: hi hi, hi lo, lo hi).  An error of 2^-22 in A stays that small
-// beside every singular value that matters: one of 2^-11 or less of the largest
-// only meets b s^2 of 2^-22 beside a.  P grows like a^m on directions X does
-// not have, and its errors with it; so steps are taken in segments whose growth
-// is at most 2^11 (six default steps), with X in fp32 between them.
+// Precision: A, B = b A + c A A, T = A Q and P are held in fp32 and multiplied
+// as two fp16 halves (22 bits; hi hi, hi lo and lo hi).  What A is off from the
+// true P X X^T P^T is multiplied by Q on both sides, so on directions that X
+// hardly has it grows by a^2 a step, from 2^-22 of the largest eigenvalue to
+// 5e-3 of it in the four steps before the fifth, where b A stands beside a.  So
+// steps are taken in segments whose A has grown by at most 160^2 (five default
+// steps), with X in fp32 between them and A formed anew.  (All steps at once: a
+// sixth step is off by 0.1 to 0.7 %, an eighth by more.)  The products keep the
+// order of their factors: taking Q A Q as Q Q A, or reading P or T transposed,
+// is the same only for factors that commute exactly, and is off by up to 9e-3
+// after five steps, where this is off by up to 2e-4.
 //
-// Powers of two carried in fp16: X and A 2^12, Q 2^10, P 2^4 (|A| <= 9,
-// |Q| <= 27, |P| <= 2^11, checked on the host).
+// Powers of two carried in fp16: X and A 2^12, B 2^10, P 2^3 (|A| <= 9,
+// |B| <= 12, |P| <= 160 * 27, checked on the host).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -31,8 +35,9 @@ using namespace dev;
 typedef _Float16 half_t;
 typedef half_t h4 __attribute__((ext_vector_type(4)));
 typedef half_t h8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
 
-constexpr float kQScale = 1024.0f, kPScale = 16.0f;
+constexpr float kQScale = 1024.0f, kPScale = 8.0f;
 
 // Where a segment finds X: u, or (mid) the workspace's fp32 X, which carries S
 // and is zero in its padding.
@@ -106,19 +111,15 @@ __device__ __forceinline__ HiLo split(float x)
 // is scaled down to it.  The next 64 columns are loaded while these are
 // multiplied.
 template <typename U, int KP>
-__global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
+__device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int part, int64_t c0, int mid)
 {
     constexpr bool LO = sizeof(U) == 4;
     constexpr int N = KP / 32, ROW = 64 + 8;   // 16 x 16 tiles a wave and side; LDS row
     typedef Chunk<KP, 64> C;
     __shared__ half_t hi[KP][ROW], lo[LO ? KP : 1][ROW];
     __shared__ uint32_t top;
-    const GroupDesc& gd = g.groups[g.group];
-    if ((int)blockIdx.x >= gd.n_sym) return;
-    const ProdTile pt = g.list[gd.sym0 + blockIdx.x];
-    const MatDesc& d = g.mats[pt.mat];
     const Source<U> src = source<U>(g, d, mid);
-    const int64_t c0 = (int64_t)pt.j * 64, c1 = min((int64_t)d.n, c0 + d.split);
+    const int64_t c1 = min((int64_t)d.n, c0 + d.split);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wi = (wave >> 1) * (KP / 2), wj = (wave & 1) * (KP / 2);
     f32x4 acc[N][N];
@@ -199,30 +200,64 @@ __global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
                 }
         }
     }
-    float* out = reinterpret_cast<float*>(g.area + d.a) + (int64_t)pt.i * KP * KP;
+    float* out = reinterpret_cast<float*>(g.area + d.a) + (int64_t)part * KP * KP;
 #pragma unroll
     for (int a = 0; a < N; ++a)
 #pragma unroll
         for (int b = 0; b < N; ++b)
             *reinterpret_cast<f32x4*>(out + (wi + 16 * a + (lane & 15)) * KP + wj + 16 * b + 4 * (lane >> 4)) = acc[a][b];
-    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[pt.i] = e == 1000 ? 0 : e;
+    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[part] = e == 1000 ? 0 : e;
+}
+
+template <typename U, int KP>
+__global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
+{
+    const ProdTile pt = g.sym[blockIdx.x];
+    thin_gram<U, KP>(g, g.mats[pt.mat], pt.i, (int64_t)pt.j * 64, mid);
+}
+
+// Slot of the sum's exponent among the parts'.
+constexpr int kSumExp = kThinMaxParts;
+
+// The parts' sum into part 0, with the least of their exponents: a quad a lane,
+// KP * KP / 4 lanes a matrix (one workgroup alone would read 64 KiB a part at
+// k = 128: 2 to 3 us each).
+template <int KP>
+__global__ __launch_bounds__(kThreads) void thin_sum_kernel(NsArgs g)
+{
+    constexpr int kPer = KP * KP / 4 / kThreads;   // workgroups a matrix
+    const MatDesc& d = g.mats[g.first + (int)blockIdx.x / kPer];
+    const int quad = ((int)blockIdx.x % kPer) * kThreads + threadIdx.x;
+    f32x4* part = reinterpret_cast<f32x4*>(g.area + d.a) + quad;
+    int32_t* exps = reinterpret_cast<int32_t*>(g.area + d.lo);
+    int least = exps[0];
+    for (int n = 1; n < d.n_parts; ++n) least = min(least, exps[n]);
+    f32x4 sum = f32x4{0, 0, 0, 0};
+#pragma unroll 8
+    for (int n = 0; n < d.n_parts; ++n)
+        sum += ldexpf(1.0f, max(2 * (least - exps[n]), -200)) * part[(int64_t)n * (KP * KP / 4)];
+    *part = sum;
+    if (quad == 0) exps[kSumExp] = least;
 }
 
 // ------------------------------------------------------------- poly
 // The waves of the poly kernel: RW x CW of them, MI x NI tiles of 16 x 16 each.
+// kOwnP: P has LDS of its own.
 template <int KP>
 struct Poly {
     static constexpr int RW = KP == 128 ? 4 : 2, CW = 2, MI = KP / 16 / RW, NI = KP / 16 / CW;
-    static constexpr int kThr = 64 * RW * CW, ROW = KP + 8;
+    // rows are 32 bytes more than a multiple of 128: neither eight lanes along
+    // eight rows nor sixteen down four rows meet in a bank
+    static constexpr int kThr = 64 * RW * CW, ROW = KP + 16;
+    static constexpr bool kOwnP = KP < 128;
     typedef f32x4 Acc[MI][NI];
-    struct Mat {
-        half_t hi[KP][ROW], lo[KP][ROW];
-    };
+    typedef half_t Mat[2][KP][ROW];   // high and low halves
 };
 
-// acc = M N, N symmetric.  The operands of the next 32 of the inner dimension
-// are read while these are multiplied.
-template <int KP>
+// acc = M N, or M N^T (NT), without the product of the low halves.  N is read
+// along its rows for M N^T and down its columns for M N.  The operands of the
+// next 32 of the inner dimension are read while these are multiplied.
+template <int KP, bool NT>
 __device__ __forceinline__ void multiply(const typename Poly<KP>::Mat& M, const typename Poly<KP>::Mat& N,
                                          typename Poly<KP>::Acc& acc)
 {
@@ -236,27 +271,36 @@ __device__ __forceinline__ void multiply(const typename Poly<KP>::Mat& M, const 
 #pragma unroll
     for (int k0 = 0; k0 < KP; k0 += 32) {
         const int c = k0 + 8 * (lane >> 4);
-        h8 ph[T::MI], pl[T::MI], qh[T::NI], ql[T::NI];
+        h8 p[2][T::MI], q[2][T::NI];
 #pragma unroll
-        for (int x = 0; x < T::MI; ++x) {
-            ph[x] = *reinterpret_cast<const h8*>(&M.hi[wi + 16 * x + r][c]);
-            pl[x] = *reinterpret_cast<const h8*>(&M.lo[wi + 16 * x + r][c]);
-        }
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int y = 0; y < T::NI; ++y) {
-            qh[y] = *reinterpret_cast<const h8*>(&N.hi[wj + 16 * y + r][c]);
-            ql[y] = *reinterpret_cast<const h8*>(&N.lo[wj + 16 * y + r][c]);
-        }
-#pragma unroll
-        for (int x = 0; x < T::MI; ++x)
+            for (int x = 0; x < T::MI; ++x) p[h][x] = *reinterpret_cast<const h8*>(&M[h][wi + 16 * x + r][c]);
 #pragma unroll
             for (int y = 0; y < T::NI; ++y) {
-                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], ph[x], acc[x][y], 0, 0, 0);
-                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ql[y], ph[x], acc[x][y], 0, 0, 0);
-                acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qh[y], pl[x], acc[x][y], 0, 0, 0);
+                if constexpr (NT) {
+                    q[h][y] = *reinterpret_cast<const h8*>(&N[h][wj + 16 * y + r][c]);
+                } else {
+                    typedef __attribute__((address_space(3))) s4 lds_s4;
+                    union { s4 s[2]; h8 v; } both;
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+                        both.s[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_s4*)&N[h][c + 4 * z + (r >> 2)][wj + 16 * y + 4 * (r & 3)]);
+                    q[h][y] = both.v;
+                }
             }
+        }
+#pragma unroll
+        for (int ab = 0; ab < 3; ++ab)   // hi hi, hi lo, lo hi
+#pragma unroll
+            for (int x = 0; x < T::MI; ++x)
+#pragma unroll
+                for (int y = 0; y < T::NI; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[ab & 1][y], p[ab >> 1][x], acc[x][y], 0, 0, 0);
     }
-    constexpr int kReads = 2 * (T::MI + T::NI), kMfma = 3 * T::MI * T::NI, kEach = kMfma / kReads > 0 ? kMfma / kReads : 1;
+    constexpr int kReads = 2 * (T::MI + (NT ? 1 : 2) * T::NI), kMfma = 3 * T::MI * T::NI;
+    constexpr int kEach = kMfma / kReads > 0 ? kMfma / kReads : 1;
     __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
 #pragma unroll
     for (int k0 = 32; k0 < KP; k0 += 32)
@@ -267,9 +311,10 @@ __device__ __forceinline__ void multiply(const typename Poly<KP>::Mat& M, const 
         }
 }
 
-// f(i, j, v) for the lane's quads of an accumulator: v is row i, columns j..j+3.
-template <int KP, typename A, typename F>
-__device__ __forceinline__ void for_quads(A& acc, F f)
+// f(x, y, i, j) for the lane's quads of an accumulator: [x][y] is row i,
+// columns j..j+3.
+template <int KP, typename F>
+__device__ __forceinline__ void for_quads(F f)
 {
     using T = Poly<KP>;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -277,53 +322,45 @@ __device__ __forceinline__ void for_quads(A& acc, F f)
 #pragma unroll
     for (int x = 0; x < T::MI; ++x)
 #pragma unroll
-        for (int y = 0; y < T::NI; ++y) f(wi + 16 * x, wj + 16 * y, acc[x][y]);
+        for (int y = 0; y < T::NI; ++y) f(x, y, wi + 16 * x, wj + 16 * y);
 }
 
-// acc, times f, into LDS (between barriers of the caller's).
+// A quad as two halves to M[..][i][j..j+3].
 template <int KP>
-__device__ __forceinline__ void store(typename Poly<KP>::Mat& M, typename Poly<KP>::Acc& acc, float f)
+__device__ __forceinline__ void put(typename Poly<KP>::Mat& M, int i, int j, const f32x4& v)
 {
-    for_quads<KP>(acc, [&](int i, int j, const f32x4& v) {
-        h4 h, l;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const HiLo s = split(v[q] * f);
-            h[q] = s.hi;
-            l[q] = s.lo;
-        }
-        *reinterpret_cast<h4*>(&M.hi[i][j]) = h;
-        *reinterpret_cast<h4*>(&M.lo[i][j]) = l;
-    });
+    const h4 hi = __builtin_convertvector(v, h4);
+    *reinterpret_cast<h4*>(&M[0][i][j]) = hi;
+    *reinterpret_cast<h4*>(&M[1][i][j]) = __builtin_convertvector(v - __builtin_convertvector(hi, f32x4), h4);
 }
 
-// One workgroup a matrix: the norm (the trace of the parts' sum is |u|^2), A
-// from the parts, `steps` steps, and P as two fp16 halves.  The norm goes to
+// One workgroup a matrix: the norm (the trace of the sum is |u|^2), A from the
+// sum, `steps` steps, and P as two fp16 halves.  The norm goes to
 // `norms` for apply: S / (norm + eps) = 2^e r.
+//
+// A step multiplies by Q = a I + B: T = A Q = a A + A B, A <- Q T = a T + B T,
+// P <- Q P = a P + B P, with A, T and P in registers (fp32) for the a-terms and
+// in LDS as two halves for the products.
+// Bound by the chain of products: at k = 128 each is 3072 cycles of MFMA and as
+// many of LDS reads on its one CU (9 us a step), at 64 mostly latency (2.5 us).
 template <int KP>
-__global__ __launch_bounds__(Poly<KP>::kThr) void thin_poly_kernel(NsArgs g, int mid, int steps, double eps,
-                                                                   NormRec* __restrict__ norms)
+__device__ __forceinline__ NormRec thin_poly(const NsArgs& g, const MatDesc& d, int mat, int mid, int steps, double eps,
+                                             NormRec* norms)
 {
     using T = Poly<KP>;
-    __shared__ typename T::Mat A, Q;
+    __shared__ typename T::Mat A, B;
+    __shared__ typename Poly<T::kOwnP ? KP : 16>::Mat own_p;   // (unused, and left out, where P shares A's)
     __shared__ double diag[KP];
     __shared__ NormRec nr;
-    const GroupDesc& gd = g.groups[g.group];
-    const int mat = gd.first + (int)blockIdx.x;
-    const MatDesc& d = g.mats[mat];
     const float* part = reinterpret_cast<const float*>(g.area + d.a);
-    const int32_t* exps = reinterpret_cast<const int32_t*>(g.area + d.lo);
+    const int ex = -2 * reinterpret_cast<const int32_t*>(g.area + d.lo)[d.n_parts > 1 ? kSumExp : 0];
     half_t* pm = reinterpret_cast<half_t*>(g.area + d.b);
-    double f2;   // A is f2 sum of the parts, each divided by its power of two
+    double f2;   // A is f2 times the sum, divided by its power of two
     if (!mid) {
-        for (int t = threadIdx.x; t < KP; t += T::kThr) {
-            double tr = 0.0;
-            for (int p = 0; p < d.n_parts; ++p)
-                tr = tr + ldexp((double)part[(int64_t)p * KP * KP + t * KP + t], -2 * exps[p]);
-            diag[t] = tr;
-        }
+        for (int t = threadIdx.x; t < KP; t += T::kThr) diag[t] = ldexp((double)part[t * KP + t], ex);
         __syncthreads();
         double tr = 0.0;
+#pragma unroll 8
         for (int t = 0; t < KP; ++t) tr = tr + diag[t];
         const double f = (double)kNsScale / (sqrt(tr) + eps);
         if (threadIdx.x == 0) {
@@ -341,67 +378,80 @@ __global__ __launch_bounds__(Poly<KP>::kThr) void thin_poly_kernel(NsArgs g, int
     }
     if (nr.r != nr.r) {   // u / (norm + eps) holds a NaN: so does all of o, by apply's factor
         for (int t = threadIdx.x; t < 2 * KP * KP; t += T::kThr) pm[t] = (half_t)0.0f;
-        return;
+        return nr;
     }
-    typename T::Acc acc, tacc, pacc;
-    for_quads<KP>(acc, [&](int, int, f32x4& v) { v = f32x4{0, 0, 0, 0}; });
-#pragma unroll 4
-    for (int p = 0; p < d.n_parts; ++p) {
-        const float w = (float)ldexp(f2, -2 * exps[p]);
-        for_quads<KP>(acc, [&](int i, int j, f32x4& v) {
-            v += w * *reinterpret_cast<const f32x4*>(part + (int64_t)p * KP * KP + i * KP + j);
-        });
-    }
-    store<KP>(A, acc, 1.0f);
+    typename T::Acc acc, a, t, p;
+    const float w = (float)ldexp(f2, ex);
+    for_quads<KP>([&](int x, int y, int i, int j) { a[x][y] = w * *reinterpret_cast<const f32x4*>(part + i * KP + j); });
+    for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(A, i, j, a[x][y]); });
     __syncthreads();
-    const float qa = g.a * kQScale, qb = g.b * (kQScale / kNsScale), qc = g.c * (kQScale / (kNsScale * kNsScale));
+    const float qb = g.b * (kQScale / kNsScale), qc = g.c * (kQScale / (kNsScale * kNsScale)), inv = 1.0f / kQScale;
     for (int it = 0; it < steps; ++it) {
         const bool last = it + 1 == steps;
-        multiply<KP>(A, A, acc);
-        for_quads<KP>(acc, [&](int i, int j, f32x4& v) {
-            const h4 h = *reinterpret_cast<const h4*>(&A.hi[i][j]), l = *reinterpret_cast<const h4*>(&A.lo[i][j]);
+        multiply<KP, true>(A, A, acc);
+        for_quads<KP>([&](int x, int y, int i, int j) {
+            const f32x4 v = qc * acc[x][y] + qb * a[x][y];
+            put<KP>(B, i, j, v);
+            if (it == 0) {   // P = a I + B
+                p[x][y] = (kPScale * inv) * v;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                v[q] = qc * v[q] + qb * ((float)h[q] + (float)l[q]) + (i == j + q ? qa : 0.0f);
+                for (int q = 0; q < 4; ++q) p[x][y][q] += i == j + q ? g.a * kPScale : 0.0f;
+            }
         });
-        // (Q is not read after the barrier that ends a step)
-        store<KP>(Q, acc, 1.0f);
         __syncthreads();
-        if (!last) multiply<KP>(Q, A, tacc);
-        if (it == 0) {
-            for_quads<KP>(acc, [&](int, int, f32x4& v) { v *= kPScale / kQScale; });
-#pragma unroll
-            for (int x = 0; x < T::MI; ++x)
-#pragma unroll
-                for (int y = 0; y < T::NI; ++y) pacc[x][y] = acc[x][y];
+        if (!last) {
+            multiply<KP, true>(A, B, acc);
+            for_quads<KP>([&](int x, int y, int, int) { t[x][y] = g.a * a[x][y] + inv * acc[x][y]; });
+        }
+        if constexpr (T::kOwnP) {
+            if (it > 0) {
+                multiply<KP, false>(B, own_p, acc);
+                for_quads<KP>([&](int x, int y, int, int) { p[x][y] = g.a * p[x][y] + inv * acc[x][y]; });
+            }
+            if (!last) {
+                __syncthreads();
+                for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(own_p, i, j, p[x][y]); });
+            }
         } else {
-            __syncthreads();   // A has been read by all
-            store<KP>(A, pacc, 1.0f);
-            __syncthreads();
-            multiply<KP>(Q, A, pacc);
-            for_quads<KP>(pacc, [&](int, int, f32x4& v) { v *= 1.0f / kQScale; });
+            if (it > 0) {
+                __syncthreads();
+                for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(A, i, j, p[x][y]); });
+                __syncthreads();
+                multiply<KP, false>(B, A, acc);
+                for_quads<KP>([&](int x, int y, int, int) { p[x][y] = g.a * p[x][y] + inv * acc[x][y]; });
+            }
+            if (!last) __syncthreads();
         }
         if (!last) {
+            for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(A, i, j, t[x][y]); });
             __syncthreads();
-            store<KP>(A, tacc, 1.0f / kQScale);   // T = Q A
+            multiply<KP, false>(B, A, acc);
+            for_quads<KP>([&](int x, int y, int, int) { a[x][y] = g.a * t[x][y] + inv * acc[x][y]; });
             __syncthreads();
-            multiply<KP>(Q, A, acc);              // A <- Q T
-            __syncthreads();
-            store<KP>(A, acc, 1.0f / kQScale);
+            for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(A, i, j, a[x][y]); });
             __syncthreads();
         }
     }
-    for_quads<KP>(pacc, [&](int i, int j, const f32x4& v) {
+    for_quads<KP>([&](int x, int y, int i, int j) {
         h4 h, l;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const HiLo s = split(v[q]);
+            const HiLo s = split(p[x][y][q]);
             h[q] = s.hi;
             l[q] = s.lo;
         }
         *reinterpret_cast<h4*>(pm + i * KP + j) = h;
         *reinterpret_cast<h4*>(pm + KP * KP + i * KP + j) = l;
     });
+    return nr;
+}
+
+template <int KP>
+__global__ __launch_bounds__(Poly<KP>::kThr) void thin_poly_kernel(NsArgs g, int mid, int steps, double eps,
+                                                                   NormRec* norms)
+{
+    const int mat = g.first + (int)blockIdx.x;
+    thin_poly<KP>(g, g.mats[mat], mat, mid, steps, eps, norms);
 }
 
 // ------------------------------------------------------------- apply
@@ -469,18 +519,13 @@ __device__ __forceinline__ void thin_finish(const MatDesc& d, const f32x4 (&acc)
 // 64 columns of P X a workgroup.  P comes straight from memory (L2) into the
 // MFMA's registers, X through LDS with its inner dimension (k) along rows.
 template <typename U, int KP, int LAST>
-__global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid, MuonArgs ma)
+__device__ __forceinline__ void thin_apply(const NsArgs& g, const MatDesc& d, NormRec nr, int64_t j0, int mid,
+                                           const MuonArgs& ma)
 {
     constexpr bool LO = sizeof(U) == 4;
     constexpr int RW = KP == 32 ? 2 : 4, CW = 4 / RW, MI = KP / 16 / RW, NI = 4 / CW, ROW = KP + 8;
     __shared__ half_t hi[64][ROW], lo[LO ? 64 : 1][ROW];
-    const GroupDesc& gd = g.groups[g.group];
-    if ((int)blockIdx.x >= gd.n_full) return;
-    const ProdTile pt = g.list[gd.full0 + blockIdx.x];
-    const MatDesc& d = g.mats[pt.mat];
     const Source<U> src = source<U>(g, d, mid);
-    const NormRec nr = g.norms[pt.mat];
-    const int64_t j0 = (int64_t)pt.j * 64;
     Chunk<KP, 64> xs;
     xs.load(src, j0);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15;
@@ -513,7 +558,6 @@ __global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid,
         }
     }
     __syncthreads();
-    if constexpr (LAST == kNsUpdate) use_device_scalars(ma, nullptr);
     // o's rows are X's columns when u is tall: then the lane's four elements
     // are to be four neighbouring rows of X
     const bool along_i = LAST != kNsMid && d.tall;
@@ -561,6 +605,34 @@ __global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid,
     }
 }
 
+template <typename U, int KP, int LAST>
+__global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid, MuonArgs ma)
+{
+    if constexpr (LAST == kNsUpdate) use_device_scalars(ma, nullptr);
+    const ProdTile pt = g.full[blockIdx.x];
+    thin_apply<U, KP, LAST>(g, g.mats[pt.mat], g.norms[pt.mat], (int64_t)pt.j * 64, mid, ma);
+}
+
+// All three for a matrix of one part, where a launch costs more than the work:
+// 64 x 64 takes 16 us this way and 24 in three.  What passes between them goes
+// through memory as it does there (the workgroup's own L1).
+template <typename U, int KP, int LAST>
+__global__ __launch_bounds__(kThreads) void thin_one_kernel(NsArgs g, int steps, double eps, NormRec* norms, MuonArgs ma)
+{
+    static_assert(Poly<KP>::kThr == kThreads, "one workgroup shape");
+    if constexpr (LAST == kNsUpdate) use_device_scalars(ma, nullptr);
+    const int mat = g.first + (int)blockIdx.x;
+    const MatDesc& d = g.mats[mat];
+    thin_gram<U, KP>(g, d, 0, 0, 0);
+    __syncthreads();
+    const NormRec nr = thin_poly<KP>(g, d, mat, 0, steps, eps, norms);
+    __syncthreads();
+    for (int64_t j0 = 0; j0 < d.n; j0 += 64) {
+        thin_apply<U, KP, LAST>(g, d, nr, j0, 0, ma);
+        __syncthreads();
+    }
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ launchers
@@ -589,6 +661,35 @@ hipError_t launch_thin_poly(const NsArgs& g, int kp, int mid, int steps, double 
 #define Z1_CALL(KP) thin_poly_kernel<KP><<<dim3(grid), dim3(Poly<KP>::kThr), 0, s>>>(g, mid, steps, eps, norms)
     Z1_KP(kp, Z1_CALL);
 #undef Z1_CALL
+    return hipGetLastError();
+}
+
+hipError_t launch_thin_sum(const NsArgs& g, int kp, int n_mats, hipStream_t s)
+{
+#define Z1_CALL(KP) thin_sum_kernel<KP><<<dim3(n_mats * (KP * KP / 4 / kThreads)), dim3(kThreads), 0, s>>>(g)
+    Z1_KP(kp, Z1_CALL);
+#undef Z1_CALL
+    return hipGetLastError();
+}
+
+hipError_t launch_thin_one(const NsArgs& g, int kp, bool f32, int steps, double eps, NormRec* norms, NsLast last,
+                           const MuonArgs& ma, int n_mats, hipStream_t s)
+{
+#define Z1_ONE(U, KP, LAST) thin_one_kernel<U, KP, LAST><<<dim3(n_mats), dim3(kThreads), 0, s>>>(g, steps, eps, norms, ma)
+#define Z1_TYPE(KP, LAST)                      \
+    do {                                       \
+        if (f32) Z1_ONE(float, KP, LAST);      \
+        else Z1_ONE(uint16_t, KP, LAST);       \
+    } while (0)
+    if (kp == 32) {
+        if (last == kNsWriteO) Z1_TYPE(32, kNsWriteO);
+        else Z1_TYPE(32, kNsUpdate);
+    } else {
+        if (last == kNsWriteO) Z1_TYPE(64, kNsWriteO);
+        else Z1_TYPE(64, kNsUpdate);
+    }
+#undef Z1_TYPE
+#undef Z1_ONE
     return hipGetLastError();
 }
 
