@@ -65,6 +65,31 @@ __device__ __forceinline__ Quad quad_at(const MatDesc& d, const StreamTile& t, i
     return Quad{in ? row : 0, s.col, s.skip};
 }
 
+// x plus the x of another lane, as the data-parallel primitive CTRL picks it
+// (zero where it picks none or the row is masked out).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double x)
+{
+    const long long b = __double_as_longlong(x);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xf, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, true);
+    return x + __longlong_as_double(((long long)hi << 32) | (unsigned)lo);
+}
+
+// The sum over a wave, in lane 63, in a fixed order: within rows of 16 lanes,
+// then across the rows.  (Six exchanges through LDS take twelve of its
+// instructions a tile and bound a pass over bf16.)
+__device__ __forceinline__ double wave_sum(double x)
+{
+    x = dpp_add<0x111, 0xf>(x);   // row_shr 1, 2, 4, 8
+    x = dpp_add<0x112, 0xf>(x);
+    x = dpp_add<0x114, 0xf>(x);
+    x = dpp_add<0x118, 0xf>(x);
+    x = dpp_add<0x142, 0xa>(x);   // row_bcast 15: rows 0, 2 into 1, 3
+    x = dpp_add<0x143, 0xc>(x);   // row_bcast 31: rows 0-1 into 2-3
+    return x;
+}
+
 // Fixed-order workgroup sums of N tiles at once, one number a wave in `sh` at
 // the end.  `sh` alternates between two buffers, so one barrier a round is
 // enough.
@@ -73,9 +98,8 @@ __device__ __forceinline__ void tile_sums(double (&x)[N], double (*sh)[kThreads 
 {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) x[k] += __shfl_xor(x[k], off, 64);
-        if ((threadIdx.x & 63) == 0) sh[k][threadIdx.x >> 6] = x[k];
+        x[k] = wave_sum(x[k]);
+        if ((threadIdx.x & 63) == 63) sh[k][threadIdx.x >> 6] = x[k];
     }
     __syncthreads();
 }

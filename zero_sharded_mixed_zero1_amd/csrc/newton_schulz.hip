@@ -331,10 +331,10 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
     const half_t* src = reinterpret_cast<const half_t*>(g.area + (OP == kGram ? d.x[it & 1] : d.a));
     half_t* dst = reinterpret_cast<half_t*>(g.area + (OP == kGram ? d.a : d.b));
     const int kb = d.kp / kB, inner = OP == kGram ? d.np / kB : kb;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     f32x4 acc[4 * MB][4];
     product<T, WR, WC, MB, S, false>(src, pt.i, kb, inner, src, pt.j, kb, inner, inner, reinterpret_cast<half_t*>(lds),
                                   acc);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     float* out = reinterpret_cast<float*>(lds) + wave * T::kOut;
     const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
     const float f = OP == kGram ? r * r / kNsScale : g.c / kNsScale;

@@ -85,11 +85,28 @@ struct Chunk {
         }
     }
 
+    // (no quad of these columns crosses the end of a row)
+    template <typename U>
+    __device__ __forceinline__ void load_whole(const Source<U>& s, int64_t j0)
+    {
+#pragma unroll
+        for (int h = 0; h < kRounds; ++h) {
+            const int64_t i = at_i(s.tall, h), j = j0 + at_j(s.tall, h);
+            const int64_t row = s.tall ? j : i, col = s.tall ? i : j;
+            const bool in = row < s.rows && col < s.cols;
+            float x[4];
+            load_quad<false>(s.p + (in ? row * s.ld + col : 0), 0, x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[h][q] = in ? x[q] : 0.0f;
+        }
+    }
+
     template <typename U>
     __device__ __forceinline__ void load(const Source<U>& s, int64_t j0)
     {
-        if (s.cols >= 4) load_rows<false>(s, j0);
-        else load_rows<true>(s, j0);
+        if (s.cols < 4) load_rows<true>(s, j0);
+        else if ((s.cols & 3) == 0 || (!s.tall && j0 + C <= s.cols)) load_whole(s, j0);
+        else load_rows<false>(s, j0);
     }
 };
 
