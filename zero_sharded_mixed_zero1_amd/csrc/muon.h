@@ -151,11 +151,18 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef u16x4 u16x4u __attribute__((aligned(2)));
 typedef f32x4 f32x4u __attribute__((aligned(4)));
 
+template <bool KEEP = false>
 __device__ __forceinline__ u16x4 ld4(const uint16_t* p)
 {
-    return __builtin_nontemporal_load((gptr<const u16x4u>)p);
+    if constexpr (KEEP) return *(gptr<const u16x4u>)p;
+    else return __builtin_nontemporal_load((gptr<const u16x4u>)p);
 }
-__device__ __forceinline__ f32x4 ld4(const float* p) { return __builtin_nontemporal_load((gptr<const f32x4u>)p); }
+template <bool KEEP = false>
+__device__ __forceinline__ f32x4 ld4(const float* p)
+{
+    if constexpr (KEEP) return *(gptr<const f32x4u>)p;
+    else return __builtin_nontemporal_load((gptr<const f32x4u>)p);
+}
 __device__ __forceinline__ void st4(uint16_t* p, u16x4 v) { __builtin_nontemporal_store(v, (gptr<u16x4u>)p); }
 __device__ __forceinline__ void st4(float* p, f32x4 v) { __builtin_nontemporal_store(v, (gptr<f32x4u>)p); }
 
@@ -200,7 +207,7 @@ __device__ __forceinline__ void widen4(u16x4 v, float (&x)[4])
     x[0] = widen(v.x); x[1] = widen(v.y); x[2] = widen(v.z); x[3] = widen(v.w);
 }
 
-template <bool SHORT>
+template <bool SHORT, bool KEEP = false>
 __device__ __forceinline__ void load_quad(const uint16_t* p, int skip, float (&x)[4])
 {
     if constexpr (SHORT) {
@@ -208,11 +215,11 @@ __device__ __forceinline__ void load_quad(const uint16_t* p, int skip, float (&x
         for (int j = 0; j < 3; ++j) x[j] = j < -skip ? widen(p[j]) : 0.0f;
         x[3] = 0.0f;
     } else {
-        widen4(ld4(p), x);
+        widen4(ld4<KEEP>(p), x);
     }
 }
 
-template <bool SHORT>
+template <bool SHORT, bool KEEP = false>
 __device__ __forceinline__ void load_quad(const float* p, int skip, float (&x)[4])
 {
     if constexpr (SHORT) {
@@ -220,7 +227,7 @@ __device__ __forceinline__ void load_quad(const float* p, int skip, float (&x)[4
         for (int j = 0; j < 3; ++j) x[j] = j < -skip ? p[j] : 0.0f;
         x[3] = 0.0f;
     } else {
-        const f32x4 v = ld4(p);
+        const f32x4 v = ld4<KEEP>(p);
         x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
     }
 }
@@ -282,7 +289,7 @@ __device__ __forceinline__ void load_padded(const T* row, int64_t c, int64_t col
 {
     const Span4 s = span4<SHORT>(c, cols, in);
     float v[4];
-    load_quad<SHORT>(row + s.col, s.skip, v);
+    load_quad<SHORT, true>(row + s.col, s.skip, v);
     if constexpr (SHORT) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = v[j];

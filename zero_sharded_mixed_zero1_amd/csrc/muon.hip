@@ -310,7 +310,7 @@ __global__ __launch_bounds__(kThreads) void u_sumsq_kernel(const MatDesc* __rest
             for (int h = 0; h < 2; ++h) {
                 const Quad q = quad_at<false>(d, tile, (int)threadIdx.x + h * kThreads);
                 skip[k][h] = q.skip;
-                load_quad<false>(static_cast<const U*>(d.u) + (q.row * d.ldu + q.col), q.skip, u[k][h]);
+                load_quad<false, true>(static_cast<const U*>(d.u) + (q.row * d.ldu + q.col), q.skip, u[k][h]);
             }
         }
         double acc[N];

@@ -321,17 +321,18 @@ constexpr int64_t kGroupBytes = (int64_t)512 << 20;
 // dimension `one` where a tile has the chip to itself and `all` where every
 // slot holds one (the chip's clock falls with the load).  Measured on MI355X:
 //   matrix        product (inner)  128 x 128   192 x 192   256 x 256
-//   4096 x 11008  gram (11008)        262 us      201 us      229 us
-//                 apply (4096)        384         428         362
+//   4096 x 11008  gram (11008)        257 us      202 us      232 us
+//                 poly (4096)         101          84          97
+//                 apply (4096)        361         419         346
 //   1111 x 2501   gram (2501)          29          47          60   (3 matrices)
-//                 apply (1111)         40          34          41
-//   768 x 768     gram (768)           14          23          29   (12 matrices)
+//                 apply (1111)         37          33          40
+//   768 x 768     gram (768)           14          22          29   (12 matrices)
 struct TileCost {
     int side;       // blocks
     int slots;      // tiles the chip holds at once
     double start, one, all;
 };
-constexpr TileCost kTiles[3] = {{2, 512, 6.0, 0.44, 0.98}, {3, 256, 9.0, 0.87, 1.15}, {4, 256, 11.0, 1.10, 1.72}};
+constexpr TileCost kTiles[3] = {{2, 512, 6.0, 0.44, 0.95}, {3, 256, 11.0, 0.87, 1.10}, {4, 256, 14.0, 1.08, 1.60}};
 constexpr int kXcds = 8;
 
 double tile_time(const TileCost& c, double tiles, int inner)

@@ -317,12 +317,20 @@ __device__ __forceinline__ void stage_block(const f32x4 (*acc)[4], float* out)
     wave_sync();
 }
 
+// A lane's slots (16 bytes) of a block, all in flight.
+__device__ __forceinline__ void load_slots(const half_t* block, h8 (&v)[8])
+{
+#pragma unroll
+    for (int h = 0; h < 8; ++h) v[h] = *reinterpret_cast<const h8*>(block + ((threadIdx.x & 63) + 64 * h) * 8);
+}
+
 enum Op : int { kGram = 0, kPoly = 1 };
 
 // A = X X^T or B = b A + c A A: the blocks of the upper triangle, each stored
 // with its mirror image.
 template <int OP, int WR, int WC, int MB, int S>
-__global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) void ns_sym_kernel(NsArgs g, int it)
+__global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks))
+void ns_sym_kernel(NsArgs g, int it)
 {
     using T = Tile<WR, WC, MB, S>;
     __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
@@ -331,10 +339,10 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
     const half_t* src = reinterpret_cast<const half_t*>(g.area + (OP == kGram ? d.x[it & 1] : d.a));
     half_t* dst = reinterpret_cast<half_t*>(g.area + (OP == kGram ? d.a : d.b));
     const int kb = d.kp / kB, inner = OP == kGram ? d.np / kB : kb;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     f32x4 acc[4 * MB][4];
     product<T, WR, WC, MB, S, false>(src, pt.i, kb, inner, src, pt.j, kb, inner, inner, reinterpret_cast<half_t*>(lds),
-                                  acc);
+                                     acc);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     float* out = reinterpret_cast<float*>(lds) + wave * T::kOut;
     const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
     const float f = OP == kGram ? r * r / kNsScale : g.c / kNsScale;
@@ -343,32 +351,30 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
     for (int m = 0; m < MB; ++m) {
         const int bi = pt.i + (wave / WC) * MB + m;
         if (bi > bj || bi >= kb || bj >= kb) continue;   // below the diagonal, or past the end
-        stage_block<T::kOutRow>(acc + 4 * m, out);
         const int64_t at = ((int64_t)bi * kb + bj) * kBlock, mirror = ((int64_t)bj * kb + bi) * kBlock;
+        h8 av[8], aw[8];
+        if constexpr (OP == kPoly) {
+            load_slots(src + at, av);
+            load_slots(src + mirror, aw);
+        }
+        stage_block<T::kOutRow>(acc + 4 * m, out);
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
             const int slot = lane + 64 * h, row = slot >> 3, j = ((slot & 7) ^ slot_key(row)) << 3;
-            h8 av{}, v;
-            if constexpr (OP == kPoly) av = *reinterpret_cast<const h8*>(src + at + slot * 8);
+            h8 v, w;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                float z = f * out[row * T::kOutRow + j + q];
-                if constexpr (OP == kPoly) z += g.b * (float)av[q];
+                // row `row` of the block (bj, bi) is column `row` of this one
+                float z = f * out[row * T::kOutRow + j + q], y = f * out[(j + q) * T::kOutRow + row];
+                if constexpr (OP == kPoly) {
+                    z += g.b * (float)av[h][q];
+                    y += g.b * (float)aw[h][q];
+                }
                 v[q] = (half_t)z;
+                w[q] = (half_t)y;
             }
             *reinterpret_cast<h8*>(dst + at + slot * 8) = v;
-            if (bi != bj) {
-                // the block (bj, bi): row `row` of it is column `row` of this one
-                h8 w{};
-                if constexpr (OP == kPoly) av = *reinterpret_cast<const h8*>(src + mirror + slot * 8);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float z = f * out[(j + q) * T::kOutRow + row];
-                    if constexpr (OP == kPoly) z += g.b * (float)av[q];
-                    w[q] = (half_t)z;
-                }
-                *reinterpret_cast<h8*>(dst + mirror + slot * 8) = w;
-            }
+            if (bi != bj) *reinterpret_cast<h8*>(dst + mirror + slot * 8) = w;
         }
     }
 }
@@ -423,7 +429,8 @@ __device__ __forceinline__ void finish_block(const MatDesc& d, const float* out,
 // X <- a X + B X; the last step writes o as bf16, or updates the master and
 // the parameter with it, instead of X.
 template <int LAST, int WR, int WC, int MB, int S>
-__global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) void ns_apply_kernel(NsArgs g, int it, int has_lo, MuonArgs ma)
+__global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks))
+void ns_apply_kernel(NsArgs g, int it, int has_lo, MuonArgs ma)
 {
     using T = Tile<WR, WC, MB, S>;
     __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
@@ -446,18 +453,18 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks)) vo
     for (int m = 0; m < MB; ++m) {
         const int bi = pt.i + (wave / WC) * MB + m;
         if (bi >= kb || bj >= nb) continue;
-        stage_block<T::kOutRow>(acc + 4 * m, out);
         const int64_t at = ((int64_t)bi * nb + bj) * kBlock;
+        h8 xh[8], xl[8] = {};
+        load_slots(xi + at, xh);
+        if (has_lo) load_slots(lo + at, xl);
+        stage_block<T::kOutRow>(acc + 4 * m, out);
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
             const int slot = lane + 64 * h, row = slot >> 3, j = ((slot & 7) ^ slot_key(row)) << 3;
-            const h8 xh = *reinterpret_cast<const h8*>(xi + at + slot * 8);
-            h8 xl{};
-            if (has_lo) xl = *reinterpret_cast<const h8*>(lo + at + slot * 8);
             float z[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                z[q] = fa * ((float)xh[q] + (float)xl[q]) + fb * out[row * T::kOutRow + j + q];
+                z[q] = fa * ((float)xh[h][q] + (float)xl[h][q]) + fb * out[row * T::kOutRow + j + q];
             if constexpr (LAST == kNsMid) {
                 h8 vh, vl;
 #pragma unroll
@@ -489,11 +496,11 @@ hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, int grid, hipStream_t 
     return hipGetLastError();
 }
 
-#define Z1_TILES(tile, CALL)                                       \
-    do {                                                           \
-        if ((tile) == kTile256) CALL(2, 4, 2, 2);                  \
-        else if ((tile) == kTile192) CALL(3, 3, 1, 3);             \
-        else CALL(2, 2, 1, 2);                                     \
+#define Z1_TILES(tile, CALL)                              \
+    do {                                                  \
+        if ((tile) == kTile256) CALL(2, 4, 2, 2);         \
+        else if ((tile) == kTile192) CALL(3, 3, 1, 3);    \
+        else CALL(2, 2, 1, 2);                            \
     } while (0)
 
 hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hipStream_t s)
