@@ -578,3 +578,307 @@ def test_column_blocks_of_one_parameter(env):
         room = 6 * 2.0 ** -24 * (np.linalg.norm(master[:, blk]) + eta * size) + eta * bound
         assert np.linalg.norm(dm.cpu().numpy()[:, blk] - want) <= room
     assert_bf16_equal(to_np_u16(par), ref.bf16(dm.cpu().numpy()), "param")
+
+
+# ------------------------------------------------------------------ o before its rounding
+class Steps:
+    """Matrices u (fp32, each entry the exact sum of two bf16 slices) whose o
+    muon_step leaves in the master unrounded: momentum and master are zero, lr
+    and scale 1, so m = u = g and p = 0 - o."""
+
+    def __init__(self, env, us, u_f32):
+        torch, dev = self.torch, self.dev = env
+        self.hi = [ref.bf16(u.astype(np.float32)).reshape(u.shape) for u in us]
+        self.u = [ref.widen(h).reshape(h.shape) for h in self.hi]
+        parts = [self.hi]
+        if u_f32:
+            lo = [ref.bf16(u.astype(np.float32) - w).reshape(u.shape) for u, w in zip(us, self.u)]
+            self.u = [w + ref.widen(x).reshape(x.shape) for w, x in zip(self.u, lo)]
+            parts.append(lo)
+        self.grads = [to_dev_u16(torch, np.concatenate([h.ravel() for h in p]), dev) for p in parts]
+        self.bufs, mats, at = [], [], 0
+        for u in us:
+            b = dict(param=torch.zeros(u.shape, dtype=torch.int16, device=dev), master=torch.zeros(u.shape, device=dev),
+                     m=torch.zeros(u.shape, device=dev),
+                     u=torch.zeros(u.shape, dtype=torch.float32 if u_f32 else torch.int16, device=dev))
+            self.bufs.append(b)
+            mats.append(z.matrix(*u.shape, shard_offset=at, **b))
+            at += u.size
+        self.table = ws_tensor(torch, z.muon_table_bytes(mats), dev)
+        self.plan = z.muon_plan(mats, self.table, flags=z.U_F32 if u_f32 else 0)
+        self.ws = ws_tensor(torch, z.muon_workspace_bytes(self.plan), dev)
+
+    def o(self, steps, coef=(ref.A, ref.B, ref.C), eps=1e-7):
+        for b in self.bufs:
+            b["master"].zero_()
+            b["m"].zero_()
+        self.ws.fill_(0xFF)
+        hp = dict(lr=1.0, momentum=0.5, weight_decay=0.0, ns_steps=steps, ns_a=coef[0], ns_b=coef[1], ns_c=coef[2],
+                  ns_eps=eps)
+        z.muon_step(self.grads, 0, self.plan, hp, flags=z.NO_NESTEROV | z.SUM_ONLY, ws=self.ws)
+        self.torch.cuda.synchronize()
+        return [-b["master"].cpu().numpy().astype(np.float64) for b in self.bufs]
+
+
+def spectrum(rng, shape, kind):
+    r, c = shape
+    k = min(shape)
+    if kind == "gauss":
+        return rng.standard_normal(shape) * 1e-3
+    U, _ = np.linalg.qr(rng.standard_normal((r, k)))
+    V, _ = np.linalg.qr(rng.standard_normal((c, k)))
+    s = np.arange(1, k + 1.0)
+    return (U * (s ** -1 if kind == "power" else np.where(s <= 4, 1.0, 1e-3))) @ V.T
+
+
+EDGE_SHAPES = [(32, 200), (33, 200), (200, 33), (64, 255), (64, 256), (64, 257), (257, 64), (65, 65), (128, 300), (300, 128),
+               (128, 128), (129, 300), (3, 1000), (1000, 3), (1, 700), (700, 2), (20, 5000), (5000, 100), (127, 4200)]
+
+
+@pytest.mark.parametrize("u_f32", [False, True])
+@pytest.mark.parametrize("kind", ["gauss", "power", "low"])
+def test_o_before_rounding(env, kind, u_f32):
+    """Around every size where the path changes (32, 64 and 128 rows; 256
+    columns; one part of the gram sum or several; one segment of steps or two):
+    within the first-order bound without the last rounding, and where the
+    smaller side is at most 128 within the header's 0.05 % of a segment of
+    five default steps."""
+    rng = np.random.default_rng(77)
+    t = Steps(env, [spectrum(rng, s, kind) for s in EDGE_SHAPES], u_f32)
+    for steps in (1, 2, 5, 8):
+        for got, u in zip(t.o(steps), t.u):
+            exact = ref.iterate64(u, steps)
+            bound, size = ref.iterate_bound(u, steps)
+            off = np.linalg.norm(got - exact)
+            what = (u.shape, steps, off / size)
+            assert off <= (bound - ref.BF16 * size) / (1 + ref.BF16), what
+            if min(u.shape) <= 128 and steps <= 5:
+                assert off <= 5e-4 * size, what
+
+
+@pytest.mark.parametrize("coef,steps", [((1.5, -0.5, 0.0), 20), ((1.5, -0.5, 0.0), 64), ((1.875, -1.25, 0.375), 16)])
+def test_many_steps_converge(env, coef, steps):
+    """Coefficients that converge (p(1) = 1, p'(1) = 0): after enough steps every
+    singular value is 1 whatever the roundings before, so o is U V^T.  What stays
+    are the last steps' own roundings, which the bound counts."""
+    rng = np.random.default_rng(5)
+    us = [spectrum(rng, s, "gauss") for s in [(20, 90), (90, 20), (60, 300), (100, 700), (150, 400)]]
+    t = Steps(env, us, True)
+    for got, u in zip(t.o(steps, coef), t.u):
+        exact = ref.iterate64(u, steps, coef)
+        bound, size = ref.iterate_bound(u, steps, coef)
+        off = np.linalg.norm(got - exact)
+        assert off <= (bound - ref.BF16 * size) / (1 + ref.BF16), (u.shape, off / size, bound / size)
+
+
+def test_zero_matrices_and_tiny_eps(env):
+    """0 / (0 + eps) is zero for every eps > 0, however small, on every path."""
+    shapes = [(5, 9), (50, 60), (40, 700), (100, 300), (150, 200)]
+    t = Steps(env, [np.zeros(s) for s in shapes], True)
+    for eps in (1e-7, 1e-20, 1e-200, 1e-308):
+        for o in t.o(5, eps=eps):
+            assert (o == 0.0).all(), (eps, o.shape)
+    for o in t.o(5, eps=0.0):
+        assert np.isnan(o).all(), o.shape
+
+
+def test_plan_of_every_path_equals_each_alone(env):
+    """Dense matrices and thin ones of every class in one plan: each has the bits
+    that it has in a plan of its own."""
+    rng = np.random.default_rng(8)
+    us = [spectrum(rng, s, "gauss") for s in EDGE_SHAPES + [(400, 500), (260, 1300)]]
+    for u_f32 in (False, True):
+        t = Steps(env, us, u_f32)
+        assert t.plan.n_groups >= 4 and t.plan.n_dense == 3
+        for steps in (5, 7):
+            together = t.o(steps)
+            for i, u in enumerate(us):
+                alone = Steps(env, [u], u_f32).o(steps)[0]
+                assert np.array_equal(alone, together[i]), (u.shape, steps)
+
+
+# ------------------------------------------------------------------ the ends of the range
+@pytest.mark.parametrize("W", [16, 127, 128])
+def test_momentum_of_many_slices(env, W):
+    torch, dev = env
+    t = Mats(env, [(33, 130), (7, 2), (40, 300)], W=W, pad=1, skew=1, seed=W)
+    z.muon_momentum(t.grads, 0, t.plan, HP)
+    torch.cuda.synchronize()
+    for i in range(3):
+        m, u = ref.momentum32(t.g(i), t.m0[i], HP["momentum"])
+        assert_f32_equal(t.get("m", i), m, f"m {i}")
+        assert_bf16_equal(t.get("u", i), ref.bf16(u), f"u {i}")
+
+
+def test_rows_shorter_than_four(env):
+    """Tall matrices of one to three columns, contiguous and cut out of wider
+    rows: every call on them."""
+    torch, dev = env
+    shapes = [(3000, 1), (1000, 2), (2049, 3), (5, 3)]
+    for pad, W in ((0, 2), (2, 2), (1, 3), (5, 9)):
+        t = Mats(env, shapes, W=W, pad=pad, pad_u=pad, pad_o=2 * pad, skew=1)
+        ws = t.workspace()
+        z.muon_momentum(t.grads, 0, t.plan, HP)
+        z.orthogonalize(t.plan, HP, ws=ws)
+        z.muon_update(t.plan, HP)
+        torch.cuda.synchronize()
+        for i, s in enumerate(shapes):
+            m, u = ref.momentum32(t.g(i), t.m0[i], HP["momentum"])
+            assert_f32_equal(t.get("m", i), m, f"m {s}")
+            assert_bf16_equal(t.get("u", i), ref.bf16(u), f"u {s}")
+            t.u0[i] = ref.widen(ref.bf16(u)).reshape(s)
+            check_o(t, i)
+            o = ref.widen(t.get("o", i)).reshape(s)
+            p = ref.update32(t.master0[i], o, HP["lr"], HP["weight_decay"], t.scale[i])
+            assert_f32_equal(t.get("master", i), p, f"master {s}")
+            assert_bf16_equal(t.get("param", i), ref.bf16(p), f"param {s}")
+        b = Mats(env, shapes, W=W, pad=pad, pad_u=pad, skew=1, with_o=False)
+        z.muon_step(b.grads, 0, b.plan, HP, ws=b.workspace())
+        torch.cuda.synchronize()
+        for i in range(len(shapes)):
+            check_step(b, i, b.master0[i], b.m0[i])
+
+
+@pytest.mark.parametrize("W", [2, 3])
+def test_more_tiles_than_workgroups(env, W):
+    """A plan of more than 8192 tiles, which the workgroups walk in one part per
+    XCD: an odd matrix, a flat one and short rows, bit for bit (the fp32
+    operations of the contract, one torch operation each)."""
+    torch, dev = env
+    gen = torch.Generator(device=dev).manual_seed(3)
+    shapes, pads = [(3001, 5003), (1024, 2048), (40001, 3)], [2, 0, 1]
+    total = sum(r * (c + p) for (r, c), p in zip(shapes, pads))
+    grads = [(torch.randn(total, generator=gen, device=dev) * 1e-2).bfloat16() for _ in range(W)]
+    mats, state, at = [], [], 0
+    for (r, c), p in zip(shapes, pads):
+        ld = c + p
+        def arr(dtype):
+            return (torch.randn(r, ld, generator=gen, device=dev) * 1e-2).to(dtype)
+        b = dict(param=arr(torch.bfloat16), master=arr(torch.float32), m=arr(torch.float32), u=arr(torch.bfloat16),
+                 o=arr(torch.bfloat16))
+        state.append((at, c, ld, b, {k: v.clone() for k, v in b.items()}))
+        mats.append(z.matrix(r, c, ld=ld, ldu=ld, ldo=ld, shard_offset=at, scale=0.5, **b))
+        at += r * ld
+    table = ws_tensor(torch, z.muon_table_bytes(mats), dev)
+    plan = z.muon_plan(mats, table)
+    assert plan.n_tiles > 8192
+    z.muon_momentum(grads, 0, plan, HP)
+    z.muon_update(plan, HP)
+    torch.cuda.synchronize()
+    mu = torch.tensor(HP["momentum"], dtype=torch.float32, device=dev)
+    eta = torch.tensor(float(np.float32(HP["lr"]) * np.float32(0.5)), dtype=torch.float32, device=dev)
+    delta = torch.tensor(1.0 - HP["lr"] * HP["weight_decay"], dtype=torch.float32, device=dev)
+    for at, c, ld, b, old in state:
+        n = b["m"].shape[0] * ld
+        g = grads[0][at:at + n].float()
+        for w in range(1, W):
+            g = g + grads[w][at:at + n].float()
+        g = (g / torch.tensor(float(W), device=dev)).reshape(-1, ld)   # (a true division)
+        m = mu * old["m"] + g
+        u = g + mu * m
+        p = (old["master"] - eta * old["o"].float()) * delta
+        for name, want in (("m", m), ("u", u.bfloat16()), ("master", p), ("param", p.bfloat16())):
+            assert torch.equal(b[name][:, :c], want[:, :c]), (name, c)
+            assert torch.equal(b[name][:, c:], old[name][:, c:]), (name, c, "beside the columns")
+
+
+@pytest.mark.parametrize("rows,cols,ld", [(5, 200, (1 << 30) + 1), (140, 130, (1 << 25) + 3), (300, 60, (1 << 24) + 5)])
+def test_offsets_past_32_bits(env, rows, cols, ld):
+    """Rows so far apart that the last ones lie past 2^32 elements of every
+    array, gradients at a `begin` beyond that as well."""
+    torch, dev = env
+    n = (rows - 1) * ld + cols
+    assert n > 1 << 32
+    rng = np.random.default_rng(2)
+    begin = 7
+    def strided(dtype, values):
+        flat = torch.empty(n + begin, dtype=dtype, device=dev)
+        view = torch.as_strided(flat, (rows, cols), (ld, 1), begin)
+        view.copy_(torch.from_numpy(values))
+        return flat, view
+    G = synth.bf16(rows * cols, synth.grad_key(4, 1, 0), 0, 1e-2, 1).reshape(rows, cols)
+    m0 = rng.standard_normal((rows, cols)).astype(np.float32) * np.float32(1e-2)
+    p0 = rng.standard_normal((rows, cols)).astype(np.float32) * np.float32(2e-2)
+    zero = np.zeros((rows, cols), np.int16)
+    g, _ = strided(torch.int16, G.view(np.int16))
+    m, mv = strided(torch.float32, m0)
+    p, pv = strided(torch.float32, p0)
+    bufs = {k: strided(torch.int16, zero) for k in ("param", "u", "o")}
+    def plan_of(**kw):
+        mats = [z.matrix(rows, cols, ld=ld, ldu=ld, ldo=ld, scale=0.3, param=bufs["param"][0][begin:], master=p[begin:],
+                         m=m[begin:], u=bufs["u"][0][begin:], **kw)]
+        table = ws_tensor(torch, z.muon_table_bytes(mats), dev)
+        plan = z.muon_plan(mats, table)
+        return plan, table, ws_tensor(torch, z.muon_workspace_bytes(plan), dev)
+    plan, table, ws = plan_of(o=bufs["o"][0][begin:])
+    z.muon_momentum([g], begin, plan, HP)
+    z.orthogonalize(plan, HP, ws=ws)
+    z.muon_update(plan, HP)
+    torch.cuda.synchronize()
+    me, ue = ref.momentum32(ref.widen(G).reshape(rows, cols), m0, HP["momentum"])
+    assert_f32_equal(mv.cpu().numpy(), me, "m")
+    u = bufs["u"][1].cpu().numpy().view(np.uint16)
+    assert_bf16_equal(u, ref.bf16(ue), "u")
+    u = ref.widen(u).reshape(rows, cols)
+    o = ref.widen(bufs["o"][1].cpu().numpy().view(np.uint16)).reshape(rows, cols)
+    bound, size = ref.iterate_bound(u)
+    exact = ref.iterate64(u)
+    assert np.linalg.norm(o - exact) <= bound
+    pe = ref.update32(p0, o, HP["lr"], HP["weight_decay"], 0.3)
+    assert_f32_equal(pv.cpu().numpy(), pe, "master")
+    assert_bf16_equal(bufs["param"][1].cpu().numpy().view(np.uint16), ref.bf16(pe), "param")
+    # the step in one call, from the first state
+    mv.copy_(torch.from_numpy(m0))
+    pv.copy_(torch.from_numpy(p0))
+    z.muon_step([g], begin, plan, HP, ws=ws)
+    torch.cuda.synchronize()
+    assert_f32_equal(mv.cpu().numpy(), me, "m of the step")
+    eta, delta = HP["lr"] * 0.3, 1 - HP["lr"] * HP["weight_decay"]
+    want = (p0.astype(np.float64) - eta * exact) * delta
+    # eta's own rounding is one of the six counted
+    room = 6 * 2.0 ** -24 * (np.linalg.norm(p0) + eta * size) + eta * bound
+    assert np.linalg.norm(pv.cpu().numpy() - want) <= room
+    del plan, table, ws, g, m, mv, p, pv, bufs
+    torch.cuda.empty_cache()
+
+
+def test_captured_clip_reads_its_device_scalars(env):
+    """A captured step that clips by the max_norm of its device scalars, the sum
+    of squares formed by the library's own reduction in the same graph: every
+    replay equals the eager step with that max_norm."""
+    torch, dev = env
+    shapes = [(130, 300), (40, 64)]
+    a, b = Mats(env, shapes, W=2, seed=51), Mats(env, shapes, W=2, seed=51)
+    wa, wb = a.workspace(), b.workspace()
+    n = a.G[0].size
+    sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
+    rws = ws_tensor(torch, z.workspace_bytes(n, 2), dev)
+    z.shard_reduce(b.grads, 0, n, sumsq_out=sumsq, ws=rws)
+    torch.cuda.synchronize()
+    norm = math.sqrt(float(sumsq[0]))
+    scal = torch.zeros(6, dtype=torch.int32, device=dev)
+    def set_scalars(hp):
+        scal.copy_(torch.from_numpy(np.frombuffer(bytes(z.muon_scalars_derive(hp)), np.int32).copy()))
+    first = dict(HP, max_norm=0.5 * norm)
+    set_scalars(first)
+    for t, ws in ((a, wa), (b, wb)):
+        z.muon_step(t.grads, 0, t.plan, first, rank_sumsq=sumsq, n_ranks=1, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        z.shard_reduce(a.grads, 0, n, sumsq_out=sumsq, ws=rws)
+        z.muon_step(a.grads, 0, a.plan, dict(device_scalars=scal), rank_sumsq=sumsq, n_ranks=1, ws=wa)
+    results = []
+    for f in (0.25, 2.0, 0.75):
+        hp = dict(HP, max_norm=f * norm)
+        set_scalars(hp)
+        g.replay()
+        torch.cuda.synchronize()
+        z.muon_step(b.grads, 0, b.plan, hp, rank_sumsq=sumsq, n_ranks=1, ws=wb)
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert_f32_equal(a.get("master", i), b.get("master", i), f"master, {f}")
+            assert_f32_equal(a.get("m", i), b.get("m", i), f"m, {f}")
+            assert_bf16_equal(a.get("u", i), b.get("u", i), f"u, {f}")
+        results.append(a.get("u", 0).copy())
+    assert not np.array_equal(results[0], results[1])

@@ -259,3 +259,26 @@ def test_header_documents_every_muon_flag():
     src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "zero1.h")).read()
     for name, bit in (("U_F32", z.U_F32), ("NO_NESTEROV", z.NO_NESTEROV)):
         assert f"#define ZERO1_{name}" in src and hex(bit) + "u" in src
+
+
+def test_clip_arguments_refused():
+    g, p = [FAKE], _plan()
+    for call in (lambda **kw: z.muon_momentum(g, 0, p, _hp(), stream=0, **kw),
+                 lambda **kw: z.muon_step(g, 0, p, _hp(), ws=FAKE, ws_bytes=1 << 30, stream=0, **kw)):
+        assert "n_ranks=0" in _einval(lambda: call(rank_sumsq=FAKE))
+        assert "info_out" in _einval(lambda: call(info_out=FAKE, n_ranks=1))
+
+
+def test_sizes_out_of_reach_refused():
+    """What no memory holds is refused, not laid out: spans past 2^44 elements,
+    more tiles or blocks than a plan or a launch takes."""
+    def tb(*mats):
+        return lambda: z.muon_table_bytes(list(mats))
+    u = dict(u=FAKE, param=None, master=None, m=None, o=None)
+    assert "2^44" in _einval(tb(_mat(1 << 20, 3, ld=1 << 30)))
+    assert "2^44" in _einval(tb(_mat(1 << 20, 3, ldo=1 << 30)))
+    assert "too many elements" in _einval(tb(_mat(32768, (1 << 23))))
+    assert "iterated together" in _einval(tb(_mat(1, (1 << 29), **u)))
+    assert z.muon_table_bytes([_mat(1, 1 << 28, **u)]) > 0
+    # (there is nothing to iterate without u)
+    assert z.muon_table_bytes([_mat(1, 1 << 29, u=None)]) > 0

@@ -96,9 +96,10 @@ struct MuonClip {
 
 struct NsArgs {
     const MatDesc* mats;
-    const ProdTile* sym;           // a group's tiles of A and B, of X, blocks of X; of thin matrices
-    const ProdTile* full;          // parts of the gram sum (i: the part, j: its first 64 columns), X's
-    const ProdTile* blocks;        // columns in 64s (j), none
+    const ProdTile* sym;           // tiles of A and B; of thin matrices the parts of the gram sum
+                                   // (i: the part, j: its first 64 columns)
+    const ProdTile* full;          // tiles of X; of thin matrices X's columns in 64s (j)
+    const ProdTile* blocks;        // blocks of X; of thin matrices none
     int first;                     // the group's first matrix
     char* area;                    // the workspace's group area
     const NormRec* norms;
@@ -165,6 +166,19 @@ __device__ __forceinline__ f32x4 ld4(const float* p)
 }
 __device__ __forceinline__ void st4(uint16_t* p, u16x4 v) { __builtin_nontemporal_store(v, (gptr<u16x4u>)p); }
 __device__ __forceinline__ void st4(float* p, f32x4 v) { __builtin_nontemporal_store(v, (gptr<f32x4u>)p); }
+
+// What the iteration starts with, from the sum of squares of u.  A zero matrix
+// stays one at any scale, but for eps = 0: then, and when the norm is infinite or
+// NaN, u / (norm + eps) holds a NaN and the iteration spreads it over the whole
+// matrix.  (No other norm leaves the exponents: the least is 2^-149.)
+__device__ __forceinline__ NormRec norm_rec(double sumsq, double eps)
+{
+    if (sumsq == 0.0 && eps > 0.0) return NormRec{1.0f, 0};
+    const double f = (double)kNsScale / (sqrt(sumsq) + eps);
+    if (!(f > 0.0) || isinf(f)) return NormRec{__builtin_nanf(""), 0};
+    const int e = ilogb(f);
+    return NormRec{(float)ldexp(f, -e), e};
+}
 
 __device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 

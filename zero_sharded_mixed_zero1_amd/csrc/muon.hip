@@ -9,8 +9,8 @@
 // counts, blocks cut out of wider matrices), because gfx950's vector loads and
 // stores need no more than the element's alignment.  No load is conditional
 // (the last quad of a row is loaded from a little earlier, a lane past the end
-// loads row 0), so that a tile's loads are all in flight at once.  Matrices that are contiguous in all
-// their arrays are one long row.
+// loads row 0), so that a tile's loads are all in flight at once.  Matrices that
+// are contiguous in all their arrays are one long row.
 //
 // Arithmetic: one binary32 operation at a time (no contraction), gradients
 // summed in rank order as the reduce of the AdamW step does; sums of squares
@@ -349,19 +349,7 @@ __global__ __launch_bounds__(kThreads) void ns_norms_kernel(const MatDesc* __res
     double x[1] = {a};
     tile_sums<1>(x, sums);
     if (threadIdx.x == 0) {
-        const double tot = four(sums[0]);
-        const double f = (double)kNsScale / (sqrt(tot) + eps);
-        NormRec n;
-        // a norm that is infinite, NaN, or zero with eps = 0: u / (norm + eps)
-        // holds a NaN, and the iteration spreads it over the whole matrix
-        if (!(f > 0.0) || isinf(f)) {
-            n.r = __builtin_nanf("");
-            n.e = 0;
-        } else {
-            n.e = ilogb(f);
-            n.r = (float)ldexp(f, -n.e);
-        }
-        norms[blockIdx.x] = n;
+        norms[blockIdx.x] = norm_rec(four(sums[0]), eps);
     }
 }
 

@@ -14,6 +14,7 @@
 #include <cstring>
 #include <exception>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "../../include/zero1.h"
@@ -106,6 +107,8 @@ constexpr uint32_t kMuonFlags = ZERO1_SUM_ONLY | ZERO1_MV_BF16 | ZERO1_RECOMPUTE
 constexpr int64_t kMaxSide = ((int64_t)1 << 31) - 256;   // rows, cols
 constexpr int64_t kMaxInner = 32768;                     // the smaller of the two
 constexpr int kMaxSteps = 64;
+constexpr int64_t kMaxTiles = (int64_t)1 << 26;          // streaming tiles of a plan: 2^37 elements
+constexpr int64_t kMaxGrid = (((int64_t)1 << 32) - 1) / 576;  // workgroups a launch: fewer than 2^32 threads
 
 enum Has : uint32_t { kHasMaster = 1, kHasM = 2, kHasU = 4, kHasO = 8 };
 
@@ -259,6 +262,13 @@ zero1_status check_grads(const uint16_t* const* grads, int W, int64_t begin, uin
     return ZERO1_OK;
 }
 
+zero1_status check_clip(const double* rank_sumsq, int n_ranks, const zero1_norm_info* info_out)
+{
+    if (rank_sumsq && n_ranks < 1) return fail(ZERO1_EINVAL, "n_ranks=%d must be >= 1", n_ranks);
+    if (info_out && !rank_sumsq) return fail(ZERO1_EINVAL, "info_out needs rank_sumsq");
+    return ZERO1_OK;
+}
+
 // ------------------------------------------------------------------ overlap
 // rows x cols elements of `esize` bytes with a row stride of ld elements.
 struct Block {
@@ -359,7 +369,7 @@ struct Host {
 
 uint32_t buffers_of(const zero1_matrix& q)
 {
-    return (q.master ? kHasMaster : 0) | (q.m ? kHasM : 0) | (q.u ? kHasU : 0) | (q.o ? kHasO : 0);
+    return (q.master ? +kHasMaster : 0u) | (q.m ? +kHasM : 0u) | (q.u ? +kHasU : 0u) | (q.o ? +kHasO : 0u);
 }
 
 // What the sizes of a plan's parts depend on.
@@ -377,6 +387,10 @@ zero1_status check_shape(const zero1_matrix& q, int i, uint32_t has0)
         if (strides[k] != 0 && (strides[k] < q.cols || strides[k] > kMaxSide))
             return fail(ZERO1_EINVAL, "matrix %d: %s=%lld must be 0 or in [cols=%lld, %lld]", i, names[k],
                         (long long)strides[k], (long long)q.cols, (long long)kMaxSide);
+    for (int k = 0; k < 3; ++k)
+        if ((q.rows - 1) * std::max(strides[k], q.cols) + q.cols > ((int64_t)1 << 44))
+            return fail(ZERO1_EINVAL, "matrix %d: %lld rows of %s=%lld span more than 2^44 elements", i,
+                        (long long)q.rows, names[k], (long long)std::max(strides[k], q.cols));
     const uint32_t has = buffers_of(q);
     if (!has) return fail(ZERO1_EINVAL, "matrix %d has no buffer", i);
     if (i > 0 && has != has0)
@@ -514,8 +528,14 @@ int16_t best_tile(const Host& h, size_t first, size_t end, bool sym)
     return best;
 }
 
-void add_group(Host& h, size_t first, size_t end)
+zero1_status add_group(Host& h, size_t first, size_t end)
 {
+    int64_t most = 0;   // 64 x 64 blocks, or 64 columns of thin matrices: no list of the group is longer
+    for (size_t m = first; m < end; ++m)
+        most += (int64_t)(h.mats[m].np / kPad) * (thin_rows(h.mats[m].k) ? 1 : h.mats[m].kp / kPad);
+    if (most > kMaxGrid)
+        return fail(ZERO1_EINVAL, "matrices of %lld blocks are iterated together, at most %lld can be",
+                    (long long)most, (long long)kMaxGrid);
     zero1_matrix_group g;
     std::memset(&g, 0, sizeof g);
     g.first = (int32_t)first;
@@ -547,6 +567,7 @@ void add_group(Host& h, size_t first, size_t end)
         g.n_blocks = add_tiles(h, first, end, 1, false);
     }
     h.groups.push_back(g);
+    return ZERO1_OK;
 }
 
 void sides(const zero1_matrix& q, MatDesc& d)
@@ -584,10 +605,9 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
     const int64_t budget = std::max(kGroupBytes, total / (ZERO1_MUON_MAX_GROUPS / 2 - 4));
     size_t group_first = 0;
     auto close_group = [&](size_t end) {
-        add_group(h, group_first, end);
         h.area = std::max(h.area, used);
-        group_first = end;
         used = 0;
+        return add_group(h, std::exchange(group_first, end), end);
     };
     for (int k = 0; k < n; ++k) {
         const zero1_matrix& q = mats[order[k]];
@@ -612,7 +632,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         d.vcols = flat ? q.rows * q.cols : q.cols;
         d.qpr = (d.vcols + 3) / 4;
         const int64_t quads = d.vrows * d.qpr, nt = (quads + kQuadsPerTile - 1) / kQuadsPerTile;
-        if ((int64_t)h.tiles.size() + nt > INT32_MAX) return fail(ZERO1_EINVAL, "too many elements in one plan");
+        if ((int64_t)h.tiles.size() + nt > kMaxTiles) return fail(ZERO1_EINVAL, "too many elements in one plan");
         d.tile0 = (int32_t)h.tiles.size();
         d.n_tiles = (int32_t)nt;
         for (int64_t t = 0; t < nt; ++t) {
@@ -626,7 +646,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         if (h.has & kHasU) {   // its place in a group's buffers
             int64_t to = place(d, used);
             if (used > 0 && (to > budget || thin_rows(d.k) != thin_rows(h.mats.back().k))) {
-                close_group(h.mats.size());
+                if (zero1_status st = close_group(h.mats.size())) return st;
                 to = place(d, used);
             }
             used = to;
@@ -638,8 +658,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         h.mats.push_back(d);
     }
     if (h.has & kHasU) {
-        close_group(h.mats.size());
-        if ((int64_t)h.list.size() > INT32_MAX) return fail(ZERO1_EINVAL, "too many tiles in one plan");
+        if (zero1_status st = close_group(h.mats.size())) return st;
         if (h.groups.size() > ZERO1_MUON_MAX_GROUPS) return fail(ZERO1_EINVAL, "too many groups in one plan");
     }
     return ZERO1_OK;
@@ -677,14 +696,10 @@ Shape stream_shape(int n_tiles, int cus)
     return Shape{cus * 8 / 8 * 8, 8};
 }
 
-zero1_status momentum(const uint16_t* const* grads, int W, int64_t begin, const zero1_matrix_plan* plan,
-                      const zero1_muon_hparams* hp, const double* rank_sumsq, int n_ranks, uint32_t flags,
-                      zero1_norm_info* info_out, double* partials, int cus, hipStream_t s)
+zero1_status momentum(const Reduce& r, const zero1_matrix_plan* plan, const zero1_muon_hparams* hp,
+                      const double* rank_sumsq, int n_ranks, uint32_t flags, zero1_norm_info* info_out,
+                      double* partials, int cus, hipStream_t s)
 {
-    Reduce r;
-    if (zero1_status st = check_grads(grads, W, begin, flags, r)) return st;
-    if (rank_sumsq && n_ranks < 1) return fail(ZERO1_EINVAL, "n_ranks=%d must be >= 1", n_ranks);
-    if (info_out && !rank_sumsq) return fail(ZERO1_EINVAL, "info_out needs rank_sumsq");
     const MuonClip mc{rank_sumsq, n_ranks, hp->max_norm, (flags & ZERO1_CLIP_EPS) ? 1 : 0,
                       reinterpret_cast<NormInfo*>(info_out)};
     const Shape sh = stream_shape(plan->n_tiles, cus);
@@ -841,9 +856,10 @@ zero1_status zero1_muon_momentum(const uint16_t* const* grads, int W, int64_t be
     if ((st = check_hparams(hp))) return st;
     Reduce r;
     if ((st = check_grads(grads, W, begin, flags, r))) return st;
+    if ((st = check_clip(rank_sumsq, n_ranks, info_out))) return st;
     if ((st = plan_device(plan, cus))) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if ((st = momentum(grads, W, begin, plan, hp, rank_sumsq, n_ranks, flags, info_out, nullptr, cus, s))) return st;
+    if ((st = momentum(r, plan, hp, rank_sumsq, n_ranks, flags, info_out, nullptr, cus, s))) return st;
     return finish(s);
 }
 
@@ -896,10 +912,11 @@ zero1_status zero1_muon_step(const uint16_t* const* grads, int W, int64_t begin,
     if ((st = check_iteration(hp))) return st;
     Reduce r;
     if ((st = check_grads(grads, W, begin, flags, r))) return st;
+    if ((st = check_clip(rank_sumsq, n_ranks, info_out))) return st;
     if ((st = check_ws(plan, ws, ws_bytes))) return st;
     if ((st = plan_device(plan, cus))) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if ((st = momentum(grads, W, begin, plan, hp, rank_sumsq, n_ranks, flags, info_out,
+    if ((st = momentum(r, plan, hp, rank_sumsq, n_ranks, flags, info_out,
                        plan->n_dense > 0 ? static_cast<double*>(ws) : nullptr, cus, s)))
         return st;
     if ((st = iterate(plan, hp, flags, kNsUpdate, static_cast<char*>(ws), s))) return st;

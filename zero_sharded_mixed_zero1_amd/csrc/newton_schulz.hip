@@ -38,7 +38,6 @@ namespace {
 using namespace dev;
 
 typedef _Float16 half_t;
-typedef half_t h4 __attribute__((ext_vector_type(4)));
 typedef half_t h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
@@ -57,14 +56,6 @@ __device__ __forceinline__ int slot_key(int r)
     const int v = r >> 1;
     return ((v >> 1) & 1) | ((v & 1) << 1) | (v & 4);
 }
-
-// Element (i, j) of a matrix of `cb` blocks a row.
-__device__ __forceinline__ int64_t elem_at(int i, int j, int cb)
-{
-    const int r = i & (kB - 1), c = j & (kB - 1);
-    return ((int64_t)(i >> 6) * cb + (j >> 6)) * kBlock + r * kB + (((c >> 3) ^ slot_key(r)) << 3) + (c & 7);
-}
-
 
 // ------------------------------------------------------------- prepare
 // Xs = 2^e u as hi (and lo where u is fp32: a bf16 u fits hi exactly), u

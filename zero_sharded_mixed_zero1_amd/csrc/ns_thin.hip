@@ -380,14 +380,9 @@ __device__ __forceinline__ NormRec thin_poly(const NsArgs& g, const MatDesc& d, 
 #pragma unroll 8
         for (int t = 0; t < KP; ++t) tr = tr + diag[t];
         const double f = (double)kNsScale / (sqrt(tr) + eps);
-        if (threadIdx.x == 0) {
-            const bool bad = !(f > 0.0) || isinf(f);
-            nr.e = bad ? 0 : ilogb(f);
-            nr.r = bad ? __builtin_nanf("") : (float)ldexp(f, -nr.e);
-            norms[mat] = nr;
-        }
+        if (threadIdx.x == 0) norms[mat] = nr = norm_rec(tr, eps);
         __syncthreads();
-        f2 = f * f / kNsScale;
+        f2 = tr > 0.0 ? f * f / kNsScale : 0.0;
     } else {
         if (threadIdx.x == 0) norms[mat] = nr = NormRec{1.0f, 0};
         __syncthreads();
