@@ -530,7 +530,7 @@ typedef struct zero1_matrix_plan {
     uint32_t flags;         /* ZERO1_MV_BF16, ZERO1_U_F32                       */
     uint32_t has;           /* which buffers the matrices have                  */
     int32_t device;         /* calls are made with this device current          */
-    int32_t n_dense, dense_tiles;
+    int32_t n_dense, dense_tiles, dense_most, reserved;
     zero1_matrix_group groups[ZERO1_MUON_MAX_GROUPS];
 } zero1_matrix_plan;
 

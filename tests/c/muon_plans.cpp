@@ -56,6 +56,7 @@ int set_error(int st, const char* msg) { g_error = msg; return st; }
 static const zero1_matrix_plan* g_plan;
 static std::vector<std::string> g_log;   // launches by name
 static char *g_ws, *g_ws_end;
+static bool g_norms_first;               // norms have a launch of their own
 
 static void in_table(const void* p, size_t bytes, size_t total)
 {
@@ -103,9 +104,11 @@ hipError_t launch_muon_update(const MatDesc*, const StreamTile*, int n_tiles, co
     REQUIRE(n_tiles == g_plan->n_tiles && nblocks % split == 0);
     return launched("update", nblocks, kThreads);
 }
-hipError_t launch_ns_prepare(const NsArgs& g, bool, int grid, hipStream_t)
+hipError_t launch_ns_prepare(const NsArgs& g, bool, const double* partials, double, NormRec* norms, int grid, hipStream_t)
 {
     group_args(g);
+    REQUIRE(norms == g.norms && (partials == nullptr) == g_norms_first);
+    REQUIRE(!partials || (char*)partials == g_ws);
     in_table(g.blocks, sizeof(ProdTile) * grid, g_table_bytes);
     return launched("prepare", grid, kThreads);
 }
@@ -215,6 +218,9 @@ static void check_table(const zero1_matrix_plan& p, const std::vector<zero1_matr
         if (d.k > kThin) REQUIRE(++dense == m + 1);   // those that are not thin come first
     }
     REQUIRE(a == b && next == p.n_tiles && dense == p.n_dense);
+    int most = 0;
+    for (int m = 0; m < dense; ++m) most = std::max(most, mats[m].n_tiles);
+    REQUIRE(p.dense_most == most);
     REQUIRE(p.dense_tiles == (dense ? mats[dense - 1].tile0 + mats[dense - 1].n_tiles : 0));
     if (!mats[0].u) {
         REQUIRE(p.n_groups == 0);
@@ -276,7 +282,7 @@ static void check_table(const zero1_matrix_plan& p, const std::vector<zero1_matr
 static std::vector<std::string> expected(const zero1_matrix_plan& p, int steps, int segments)
 {
     std::vector<std::string> e;
-    if (p.n_dense) e.push_back("norms");
+    if (p.dense_most > kNormTiles) e.push_back("norms");
     for (int gi = 0; gi < p.n_groups; ++gi) {
         const zero1_matrix_group& g = p.groups[gi];
         if (g.thin && g.one && segments == 1) {
@@ -306,6 +312,7 @@ int main()
     auto pick = [&](int64_t lo, int64_t hi) { return lo + (int64_t)(rng() % (uint64_t)(hi - lo + 1)); };
     const int64_t edges[] = {1, 2, 3, 4, 31, 32, 33, 63, 64, 65, 127, 128, 129, 192, 255, 256, 257, 511, 513};
     int64_t widest = 0;
+    int large = 0;
     for (g_case = 0; g_case < 400; ++g_case) {
         const int n = (int)pick(1, g_case % 10 == 0 ? 60 : 8);
         const bool no_u = g_case % 13 == 5;
@@ -345,6 +352,8 @@ int main()
         REQUIRE(zero1_muon_plan(mats.data(), n, flags, table, need, &plan) == ZERO1_OK);
         g_plan = &plan;
         g_table_bytes = need;
+        g_norms_first = plan.dense_most > kNormTiles;
+        large += g_norms_first;
         check_table(plan, mats);
 
         g_ws = reinterpret_cast<char*>((uintptr_t)1 << 41);   // (nothing touches it here)
@@ -387,7 +396,7 @@ int main()
         }
         std::free(table);
     }
-    REQUIRE(widest >= 1 << 20);
+    REQUIRE(widest >= 1 << 20 && large >= 10);
     std::printf("all ok\n");
     return 0;
 }

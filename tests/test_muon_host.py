@@ -50,13 +50,13 @@ def _valid(mats, flags=0):
 
 def test_table_bytes_and_layout():
     # 192 bytes a matrix; streaming tiles of 512 quads (16 bytes each); of
-    # a thin matrix a part of the gram sum and 64 columns
-    assert z.muon_table_bytes([_mat()]) == 256 + 256 + 16 * (1 + 1)
-    assert z.muon_table_bytes([_mat(100, 1000)]) == 256 + -(-49 * 16 // 256) * 256 + 16 * (8 + 16)
+    # a thin matrix a part of the gram sum and 64 columns (32 bytes each)
+    assert z.muon_table_bytes([_mat()]) == 256 + 256 + 32 * (1 + 1)
+    assert z.muon_table_bytes([_mat(100, 1000)]) == 256 + -(-49 * 16 // 256) * 256 + 32 * (8 + 16)
     # of others product tiles of 128 x 128: A's upper triangle, X; X's blocks of
-    # 64 x 64 (16 bytes each)
+    # 64 x 64 (32 bytes each)
     # 300 x 700: 3 x 6 tiles of X, 6 of A's 3 x 3, 5 x 11 blocks; 52500 quads
-    assert z.muon_table_bytes([_mat(300, 700)]) == 256 + -(-103 * 16 // 256) * 256 + 16 * (6 + 18 + 55)
+    assert z.muon_table_bytes([_mat(300, 700)]) == 256 + -(-103 * 16 // 256) * 256 + 32 * (6 + 18 + 55)
     # without u there is nothing to iterate
     assert z.muon_table_bytes([_mat(u=None)]) == 256 + 256
     # a tall matrix has the tiles of its transpose

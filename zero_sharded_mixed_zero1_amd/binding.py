@@ -105,6 +105,7 @@ class MatrixPlan(ctypes.Structure):
                 ("area_bytes", i64), ("n_mats", ctypes.c_int32), ("n_tiles", ctypes.c_int32),
                 ("n_groups", ctypes.c_int32), ("flags", ctypes.c_uint32), ("has", ctypes.c_uint32),
                 ("device", ctypes.c_int32), ("n_dense", ctypes.c_int32), ("dense_tiles", ctypes.c_int32),
+                ("dense_most", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("groups", MatrixGroup * 64)]
 
 

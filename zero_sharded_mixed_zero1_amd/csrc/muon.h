@@ -14,6 +14,7 @@ namespace z1 {
 // Streaming kernels (momentum, update, sum of squares): a workgroup's tile is
 // 512 quads, a quad being up to four neighbouring elements of one row.
 constexpr int kQuadsPerTile = 512;
+constexpr int kSumsqTiles = 4;     // tiles that a workgroup of the sum of squares takes at once
 // Side of the square blocks that X, A and B are laid out in and padded to.
 constexpr int kPad = 64;
 // Power of two that X, A and B carry in fp16 (see newton_schulz.hip).
@@ -38,8 +39,9 @@ struct MatDesc {
     int32_t tile0, n_tiles;        // its streaming tiles
     int32_t split, n_parts;        // thin: columns a part of the gram sum, parts
     int32_t reserved;
-    // byte offsets inside the workspace's group area: X twice, its low halves,
-    // A, B; of a thin matrix fp32 X, the parts' exponents, the parts, P
+    // byte offsets inside the workspace's group area: X (twice, its low halves,
+    // A and B follow, see Buffers); of a thin matrix fp32 X, the parts'
+    // exponents, the parts, P
     int64_t x[2], lo, a, b;
 };
 static_assert(sizeof(MatDesc) == 192, "matrix descriptor layout");
@@ -51,17 +53,40 @@ struct StreamTile {
 };
 
 // A tile of one matrix's product: its first block row i and block column j.
+// With what of the matrix the products need beside it (`at`: d.x[0]; kb, nb:
+// blocks of kp and np), so that a workgroup knows its addresses after one load
+// from memory, not two in a row: 0.4 us of the 13.8 that a gram of 768 x 768 took.
 struct ProdTile {
-    int32_t mat, i, j, reserved;
+    int64_t at;
+    int32_t mat, i, j, kb, nb, reserved;
 };
+static_assert(sizeof(ProdTile) == 32, "tile layout");
 
 // Matrices with k up to this take the kernels of ns_thin.hip.
 constexpr int kThin = 128;
 constexpr int kThinMaxParts = 32;
 constexpr int kThinOne = 256;      // n up to this: one workgroup does all of a matrix of k <= 64
+// The iteration's buffers of a matrix that is not thin: byte offsets of X (two
+// copies), its low halves, A and B.
+struct Buffers {
+    int64_t x0, x1, lo, a, b, end;
+};
+
+inline __host__ __device__ Buffers buffers(int64_t at, uint32_t kb, uint32_t nb)
+{   // (numbers of blocks fit 32 bits, and 32-bit products stay in scalar registers)
+    const int64_t x = (int64_t)(kb * nb) * (2 * kPad * kPad), a = (int64_t)(kb * kb) * (2 * kPad * kPad);
+    return Buffers{at, at + x, at + 2 * x, at + 3 * x, at + 3 * x + a, at + 3 * x + 2 * a};
+}
+
 // How much a segment's steps before its last may grow small singular values
 // (ns_thin.hip).
 constexpr double kThinGrowth = 160.0;
+
+// Matrices of at most this many streaming tiles: every workgroup of prepare forms
+// its matrix's norm from their partial sums; for larger ones a launch before it
+// does.  Prepare alone and both: 288 tiles 9.2 and 10.4 us, 1357 tiles 11.3 and
+// 13.1, 2048 tiles 9.2 and 12.2, 4096 tiles 12.0 and 12.2.
+constexpr int kNormTiles = 2048;
 
 // Shapes of the products' tiles.
 enum TileShape : int { kTile128 = 0, kTile192 = 1, kTile256 = 2 };
@@ -118,7 +143,9 @@ hipError_t launch_ns_norms(const MatDesc* mats, int n_mats, const double* partia
 hipError_t launch_muon_update(const MatDesc* mats, const StreamTile* tiles, int n_tiles, const MuonArgs& ma,
                               int nblocks, int split, hipStream_t s);
 
-hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, int grid, hipStream_t s);
+// partials: the norms are formed here too (else launch_ns_norms has).
+hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, const double* partials, double eps, NormRec* norms, int grid,
+                             hipStream_t s);
 hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hipStream_t s);
 hipError_t launch_ns_poly(const NsArgs& g, TileShape tile, int grid, hipStream_t s);
 hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, TileShape tile,
@@ -178,6 +205,65 @@ __device__ __forceinline__ NormRec norm_rec(double sumsq, double eps)
     if (!(f > 0.0) || isinf(f)) return NormRec{__builtin_nanf(""), 0};
     const int e = ilogb(f);
     return NormRec{(float)ldexp(f, -e), e};
+}
+
+// x plus the x of another lane, as the data-parallel primitive CTRL picks it
+// (zero where it picks none or the row is masked out).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double x)
+{
+    const long long b = __double_as_longlong(x);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xf, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, true);
+    return x + __longlong_as_double(((long long)hi << 32) | (unsigned)lo);
+}
+
+// The sum over a wave, in lane 63, in a fixed order: within rows of 16 lanes,
+// then across the rows.  (Six exchanges through LDS take twelve of its
+// instructions a tile and bound a pass over bf16.)
+__device__ __forceinline__ double wave_sum(double x)
+{
+    x = dpp_add<0x111, 0xf>(x);   // row_shr 1, 2, 4, 8
+    x = dpp_add<0x112, 0xf>(x);
+    x = dpp_add<0x114, 0xf>(x);
+    x = dpp_add<0x118, 0xf>(x);
+    x = dpp_add<0x142, 0xa>(x);   // row_bcast 15: rows 0, 2 into 1, 3
+    x = dpp_add<0x143, 0xc>(x);   // row_bcast 31: rows 0-1 into 2-3
+    return x;
+}
+
+// Fixed-order workgroup sums of N tiles at once, one number a wave in `sh` at
+// the end.  `sh` alternates between two buffers, so one barrier a round is
+// enough.
+template <int N>
+__device__ __forceinline__ void tile_sums(double (&x)[N], double (*sh)[kThreads / 64])
+{
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        x[k] = wave_sum(x[k]);
+        if ((threadIdx.x & 63) == 63) sh[k][threadIdx.x >> 6] = x[k];
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ double four(const double (&s)[kThreads / 64]) { return ((s[0] + s[1]) + s[2]) + s[3]; }
+
+// The start of a matrix's iteration from its streaming tiles' partial sums, added
+// in a fixed order by a workgroup of kThreads; all of it gets the result.
+__device__ __forceinline__ NormRec matrix_norm(const MatDesc& d, const double* __restrict__ partials, double eps,
+                                               double (*sums)[kThreads / 64])
+{
+    double a = 0.0;
+    for (int i0 = threadIdx.x; i0 < d.n_tiles; i0 += 16 * kThreads) {   // 16 loads in flight
+        double x[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = i0 + k * kThreads < d.n_tiles ? partials[d.tile0 + i0 + k * kThreads] : 0.0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) a = a + x[k];
+    }
+    double x[1] = {a};
+    tile_sums<1>(x, sums);
+    return norm_rec(four(sums[0]), eps);
 }
 
 __device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }

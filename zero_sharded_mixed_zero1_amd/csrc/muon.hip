@@ -65,47 +65,6 @@ __device__ __forceinline__ Quad quad_at(const MatDesc& d, const StreamTile& t, i
     return Quad{in ? row : 0, s.col, s.skip};
 }
 
-// x plus the x of another lane, as the data-parallel primitive CTRL picks it
-// (zero where it picks none or the row is masked out).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double dpp_add(double x)
-{
-    const long long b = __double_as_longlong(x);
-    const int lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xf, true);
-    const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, true);
-    return x + __longlong_as_double(((long long)hi << 32) | (unsigned)lo);
-}
-
-// The sum over a wave, in lane 63, in a fixed order: within rows of 16 lanes,
-// then across the rows.  (Six exchanges through LDS take twelve of its
-// instructions a tile and bound a pass over bf16.)
-__device__ __forceinline__ double wave_sum(double x)
-{
-    x = dpp_add<0x111, 0xf>(x);   // row_shr 1, 2, 4, 8
-    x = dpp_add<0x112, 0xf>(x);
-    x = dpp_add<0x114, 0xf>(x);
-    x = dpp_add<0x118, 0xf>(x);
-    x = dpp_add<0x142, 0xa>(x);   // row_bcast 15: rows 0, 2 into 1, 3
-    x = dpp_add<0x143, 0xc>(x);   // row_bcast 31: rows 0-1 into 2-3
-    return x;
-}
-
-// Fixed-order workgroup sums of N tiles at once, one number a wave in `sh` at
-// the end.  `sh` alternates between two buffers, so one barrier a round is
-// enough.
-template <int N>
-__device__ __forceinline__ void tile_sums(double (&x)[N], double (*sh)[kThreads / 64])
-{
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        x[k] = wave_sum(x[k]);
-        if ((threadIdx.x & 63) == 63) sh[k][threadIdx.x >> 6] = x[k];
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ double four(const double (&s)[kThreads / 64]) { return ((s[0] + s[1]) + s[2]) + s[3]; }
-
 // The reduced gradient of the lane's Q quads: slices added in rank order, the
 // loads of N slices in flight together; then the average.
 template <bool SHORT, int N, int Q>
@@ -294,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void u_sumsq_kernel(const MatDesc* __rest
                                                            const StreamTile* __restrict__ tiles, int n_tiles,
                                                            double* __restrict__ partials, int split)
 {
-    constexpr int N = 4;
+    constexpr int N = kSumsqTiles;
     __shared__ double sums[2][N][kThreads / 64];
     const Walk wk = walk(n_tiles, split);
     int buf = 0;
@@ -330,27 +289,14 @@ __global__ __launch_bounds__(kThreads) void u_sumsq_kernel(const MatDesc* __rest
     }
 }
 
-// One workgroup a matrix: the norm from its tiles' partials in a fixed order,
-// and the scale the iteration starts with.
+// One workgroup a matrix.
 __global__ __launch_bounds__(kThreads) void ns_norms_kernel(const MatDesc* __restrict__ mats,
                                                             const double* __restrict__ partials, double eps,
                                                             NormRec* __restrict__ norms)
 {
     __shared__ double sums[1][kThreads / 64];
-    const MatDesc& d = mats[blockIdx.x];
-    double a = 0.0;
-    for (int i0 = threadIdx.x; i0 < d.n_tiles; i0 += 16 * kThreads) {   // 16 loads in flight
-        double x[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = i0 + k * kThreads < d.n_tiles ? partials[d.tile0 + i0 + k * kThreads] : 0.0;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) a = a + x[k];
-    }
-    double x[1] = {a};
-    tile_sums<1>(x, sums);
-    if (threadIdx.x == 0) {
-        norms[blockIdx.x] = norm_rec(four(sums[0]), eps);
-    }
+    const NormRec n = matrix_norm(mats[blockIdx.x], partials, eps, sums);
+    if (threadIdx.x == 0) norms[blockIdx.x] = n;
 }
 
 template <bool SHORT>

@@ -362,6 +362,7 @@ struct Host {
     uint32_t has = 0;
     int64_t elems = 0;
     int32_t n_dense = 0, dense_tiles = 0;   // matrices that are not thin (the first ones), their streaming tiles
+    int32_t dense_most = 0;                 // and the most of one
     size_t off_tiles() const { return round_up(sizeof(MatDesc) * mats.size(), 256); }
     size_t off_list() const { return off_tiles() + round_up(sizeof(StreamTile) * tiles.size(), 256); }
     size_t bytes() const { return off_list() + sizeof(ProdTile) * list.size(); }
@@ -454,13 +455,13 @@ int64_t place(MatDesc& d, int64_t at)
         d.b = d.a + (int64_t)d.n_parts * thin * thin * 4;
         return d.b + (int64_t)2 * thin * thin * 2;
     }
-    const int64_t x = (int64_t)d.kp * d.np * 2, a = (int64_t)d.kp * d.kp * 2;   // multiples of 8 KiB
-    d.x[0] = at;
-    d.x[1] = at + x;
-    d.lo = at + 2 * x;
-    d.a = at + 3 * x;
-    d.b = d.a + a;
-    return d.b + a;
+    const Buffers b = buffers(at, (uint32_t)(d.kp / kPad), (uint32_t)(d.np / kPad));   // multiples of 8 KiB
+    d.x[0] = b.x0;
+    d.x[1] = b.x1;
+    d.lo = b.lo;
+    d.a = b.a;
+    d.b = b.b;
+    return b.end;
 }
 static_assert((kThinMaxParts + 1) * sizeof(int32_t) <= 256, "exponents of the parts and of their sum");
 
@@ -470,6 +471,12 @@ struct Blocks {
 };
 
 Blocks blocks_of(const MatDesc& d, bool sym) { return Blocks{d.kp / kPad, (sym ? d.kp : d.np) / kPad}; }
+
+ProdTile tile_of(const Host& h, size_t m, int i, int j)
+{
+    const MatDesc& d = h.mats[m];
+    return ProdTile{d.x[0], (int32_t)m, i, j, d.kp / kPad, d.np / kPad, 0};
+}
 
 // Appends a group's tiles of `side` blocks: all of X, or (sym) those of A and B
 // that reach above the diagonal.  Workgroup b runs on XCD b % 8, which has an
@@ -489,7 +496,7 @@ int32_t add_tiles(Host& h, size_t first, size_t end, int side, bool sym)
             for (int js = 0; js < b.cols; js += strip)
                 for (int i = 0; i < b.rows; i += side)
                     for (int j = js; j < std::min(js + strip, b.cols); j += side)
-                        if (!sym || j >= i) seq.push_back(ProdTile{(int32_t)e, i, j, 0});
+                        if (!sym || j >= i) seq.push_back(tile_of(h, e, i, j));
         }
         const size_t base = h.list.size() - start;
         h.list.resize(h.list.size() + seq.size());
@@ -548,13 +555,13 @@ zero1_status add_group(Host& h, size_t first, size_t end)
             const MatDesc& d = h.mats[m];
             one = one && d.n <= kThinOne;
             g.parts = std::max(g.parts, (int16_t)d.n_parts);
-            for (int p = 0; p < d.n_parts; ++p) h.list.push_back(ProdTile{(int32_t)m, p, p * (d.split / kPad), 0});
+            for (int p = 0; p < d.n_parts; ++p) h.list.push_back(tile_of(h, m, p, p * (d.split / kPad)));
         }
         g.one = one ? 1 : 0;
         g.n_sym = (int32_t)(here() - g.sym0);
         g.full0 = here();
         for (size_t m = first; m < end; ++m)
-            for (int j = 0; j < h.mats[m].np / kPad; ++j) h.list.push_back(ProdTile{(int32_t)m, 0, j, 0});
+            for (int j = 0; j < h.mats[m].np / kPad; ++j) h.list.push_back(tile_of(h, m, 0, j));
         g.n_full = (int32_t)(here() - g.full0);
         g.n_blocks = (int32_t)(end - first);
     } else {
@@ -654,6 +661,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         if (!thin_rows(d.k)) {
             ++h.n_dense;
             h.dense_tiles = (int32_t)h.tiles.size();
+            h.dense_most = std::max(h.dense_most, d.n_tiles);
         }
         h.mats.push_back(d);
     }
@@ -716,7 +724,8 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
 {
     const double* partials = reinterpret_cast<const double*>(ws);
     NormRec* norms = reinterpret_cast<NormRec*>(ws + ws_norms(plan));
-    if (plan->n_dense > 0) Z1_HIP(launch_ns_norms(plan_mats(plan), plan->n_dense, partials, hp->ns_eps, norms, s));
+    const bool norms_first = plan->dense_most > kNormTiles;
+    if (norms_first) Z1_HIP(launch_ns_norms(plan_mats(plan), plan->n_dense, partials, hp->ns_eps, norms, s));
     const char* tb = static_cast<const char*>(plan->table);
     NsArgs g;
     std::memset(&g, 0, sizeof g);
@@ -753,7 +762,7 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
             continue;
         }
         const TileShape sym = (TileShape)q.sym_tile, full = (TileShape)q.full_tile;
-        Z1_HIP(launch_ns_prepare(g, u_f32, q.n_blocks, s));
+        Z1_HIP(launch_ns_prepare(g, u_f32, norms_first ? nullptr : partials, hp->ns_eps, norms, q.n_blocks, s));
         for (int it = 0; it < hp->ns_steps; ++it) {
             Z1_HIP(launch_ns_gram(g, it, sym, q.n_sym, s));
             Z1_HIP(launch_ns_poly(g, sym, q.n_sym, s));
@@ -814,6 +823,7 @@ zero1_status zero1_muon_plan(const zero1_matrix* mats, int n_mats, uint32_t flag
         p.has = h.has;
         p.n_dense = h.n_dense;
         p.dense_tiles = h.dense_tiles;
+        p.dense_most = h.dense_most;
         p.device = dev;
         *plan_out = p;
         return ok();
@@ -876,7 +886,8 @@ zero1_status zero1_orthogonalize(const zero1_matrix_plan* plan, const zero1_muon
     if ((st = plan_device(plan, cus))) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (plan->n_dense > 0) {
-        const Shape sh = stream_shape(plan->dense_tiles, cus);
+        Shape sh = stream_shape(plan->dense_tiles, cus);
+        if (sh.split == 1) sh.grid = (sh.grid + kSumsqTiles - 1) / kSumsqTiles;
         Z1_HIP(launch_u_sumsq(plan_mats(plan), plan_tiles(plan), plan->dense_tiles, (plan->flags & ZERO1_U_F32) != 0,
                               static_cast<double*>(ws), sh.grid, sh.split, s));
     }

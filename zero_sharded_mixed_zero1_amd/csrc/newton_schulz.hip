@@ -38,6 +38,7 @@ namespace {
 using namespace dev;
 
 typedef _Float16 half_t;
+typedef half_t h4 __attribute__((ext_vector_type(4)));
 typedef half_t h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
@@ -60,14 +61,17 @@ __device__ __forceinline__ int slot_key(int r)
 // ------------------------------------------------------------- prepare
 // Xs = 2^e u as hi (and lo where u is fp32: a bf16 u fits hi exactly), u
 // transposed if tall, zeros in the padding.  One workgroup a block.
+// Given `partials`, each workgroup forms its matrix's norm from them itself, and
+// the first one stores it for the products.
 template <typename U>
-__global__ __launch_bounds__(kThreads) void ns_prepare_kernel(NsArgs g)
+__global__ __launch_bounds__(kThreads) void ns_prepare_kernel(NsArgs g, const double* partials, double eps,
+                                                              NormRec* norms)
 {
     constexpr bool LO = sizeof(U) == 4;
     __shared__ float sh[kB][kB + 1];
+    __shared__ double sums[1][kThreads / 64];
     const ProdTile pt = g.blocks[blockIdx.x];
     const MatDesc& d = g.mats[pt.mat];
-    const int e = g.norms[pt.mat].e;
     const U* u = static_cast<const U*>(d.u);
     const int i0 = pt.i * kB, j0 = pt.j * kB;
     // rows of u are rows of X, or columns when u is tall
@@ -80,6 +84,14 @@ __global__ __launch_bounds__(kThreads) void ns_prepare_kernel(NsArgs g)
         const bool in = row < d.rows;
         load_padded<false>(u + (in ? row : 0) * d.ldu, b0 + c, d.cols, in, v[h]);
     }
+    int e;
+    if (partials) {
+        const NormRec n = matrix_norm(d, partials, eps, sums);
+        e = n.e;
+        if (pt.i == 0 && pt.j == 0 && threadIdx.x == 0) norms[pt.mat] = n;
+    } else {
+        e = norms[pt.mat].e;
+    }
 #pragma unroll
     for (int h = 0; h < 4; ++h)
 #pragma unroll
@@ -89,9 +101,10 @@ __global__ __launch_bounds__(kThreads) void ns_prepare_kernel(NsArgs g)
             else sh[r0 + 16 * h][c + q] = x;
         }
     __syncthreads();
-    const int64_t at = ((int64_t)pt.i * (d.np / kB) + pt.j) * kBlock;
-    half_t* hi = reinterpret_cast<half_t*>(g.area + d.x[0]) + at;
-    half_t* lo = reinterpret_cast<half_t*>(g.area + d.lo) + at;
+    const Buffers buf = buffers(pt.at, pt.kb, pt.nb);
+    const int64_t at = ((int64_t)pt.i * pt.nb + pt.j) * kBlock;
+    half_t* hi = reinterpret_cast<half_t*>(g.area + buf.x0) + at;
+    half_t* lo = reinterpret_cast<half_t*>(g.area + buf.lo) + at;
 #pragma unroll
     for (int h = 0; h < kBlock / 8 / kThreads; ++h) {
         const int slot = threadIdx.x + h * kThreads, r = slot >> 3, j = ((slot & 7) ^ slot_key(r)) << 3;
@@ -121,13 +134,16 @@ struct Tile {
     static constexpr int kStage = kBlocks * kBlock;            // elements of a stage
     static constexpr int kLoads = (kBlocks * 8 + kWaves - 1) / kWaves;   // 1 KiB loads a wave issues a stage
     static constexpr bool kEven = kBlocks * 8 % kWaves == 0;
-    // the epilogue's staging of one block a wave, rows padded by 16 bytes
-    static constexpr int kOutRow = kB + 4;
-    static constexpr int kOut = kB * kOutRow;                  // floats a wave
-    static constexpr size_t kStages = (size_t)S * kStage * 2, kOuts = (size_t)kWaves * kOut * 4;
+    static constexpr size_t kStages = (size_t)S * kStage * 2, kOuts = (size_t)kWaves * kBlock * 4;
     static constexpr size_t kLds = kStages > kOuts ? kStages : kOuts;
     static_assert(kLds <= 160 * 1024, "LDS of a CU");
-    static constexpr int kMinBlocks = kLds <= 80 * 1024 ? 2 : 1;   // workgroups a CU holds
+    // Waves a SIMD that registers are left for (not what LDS allows: with half of
+    // LDS to itself a kernel of four waves would be given 512 registers, half of
+    // them behind copies).  LDS is dynamic for the same reason.
+    static constexpr int kMinBlocks = kThr == 256 ? 2 : 1;
+    // registers left for the epilogue's operands while the product runs (256 a
+    // lane at two waves a SIMD; three leave 168)
+    static constexpr bool kAhead = MB == 1 && kWaves <= 4;
 };
 
 // One wave copies 1 KiB from memory to LDS: lane l its 16 bytes at base +
@@ -149,14 +165,32 @@ __device__ __forceinline__ void stage_wait()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Reads a block in LDS down its columns: a lane gets column c0 + (lane & 15), rows
+// r0 + 8 (lane >> 4) and the next seven.  (It gives the address of 8 bytes: of row
+// ((lane & 15) >> 2) of a group of four, a quarter of the 16 columns.)
+__device__ __forceinline__ h8 columns(const half_t* block, int r0, int c0)
+{
+    typedef __attribute__((address_space(3))) s4 lds_s4;
+    const int lane = threadIdx.x & 63;
+    union { s4 s[2]; h8 v; } both;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+        const int r = r0 + 8 * (lane >> 4) + ((lane & 15) >> 2) + 4 * z, c = c0 + 4 * (lane & 3);
+        const half_t* a = block + r * kB + (((c >> 3) ^ slot_key(r)) << 3) + (c & 7);
+        both.s[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)a);
+    }
+    return both.v;
+}
+
 // P: block row p0 of a matrix of `pc` blocks a row and `pr` block rows, read
 // along its rows; Q: block row q0 of one of `qr` by `qc` likewise, or, with QT,
 // block column q0, read down its columns.  `steps` blocks of the inner
 // dimension.  Tiles past the last block row or column repeat it (their results
-// are not stored).
-template <typename T, int WR, int WC, int MB, int S, bool QT>
+// are not stored).  `ahead` runs when the last stage has arrived: the loads that
+// it issues delay none of the product's.
+template <typename T, int WR, int WC, int MB, int S, bool QT, typename F>
 __device__ __forceinline__ void product(const half_t* P, int p0, int pr, int pc, const half_t* Q, int q0, int qr,
-                                        int qc, int steps, half_t* sh, f32x4 (&acc)[4 * MB][4])
+                                        int qc, int steps, half_t* sh, f32x4 (&acc)[4 * MB][4], F ahead)
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wi = wave / WC, wj = wave % WC;
@@ -199,9 +233,6 @@ __device__ __forceinline__ void product(const half_t* P, int p0, int pr, int pc,
     // the second half of the inner block); rows 16 apart have the same key
     const int row = lane & 15, key = slot_key(row);
     const int off[2] = {row * kB + (((lane >> 4) ^ key) << 3), row * kB + (((4 + (lane >> 4)) ^ key) << 3)};
-    // down columns: the lane's row inside a group of 4, and its 8 bytes of the
-    // group's 32
-    const int trow = 8 * (lane >> 4) + ((lane & 15) >> 2), tq = lane & 3;
     struct Frag {
         h8 p[4 * MB], q[4];
     };
@@ -214,16 +245,7 @@ __device__ __forceinline__ void product(const half_t* P, int p0, int pr, int pc,
             if constexpr (!QT) {
                 f.q[y] = *reinterpret_cast<const h8*>(sq + y * 16 * kB + off[h]);
             } else {
-                // columns 16 y + 4 tq.. of rows 32 h + trow and 4 below
-                typedef __attribute__((address_space(3))) s4 lds_s4;
-                union { s4 s[2]; h8 v; } both;
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int r = 32 * h + trow + 4 * z, c = 16 * y + 4 * tq;
-                    const half_t* a = sq + r * kB + (((c >> 3) ^ slot_key(r)) << 3) + (c & 7);
-                    both.s[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)a);
-                }
-                f.q[y] = both.v;
+                f.q[y] = columns(sq, 32 * h, 16 * y);
             }
         }
 #pragma unroll
@@ -275,6 +297,7 @@ __device__ __forceinline__ void product(const half_t* P, int p0, int pr, int pc,
                 issue(put);
                 put = next(put);
             }
+            if (t + 2 == steps) ahead();
             get = next(get);
         }
         // (the last round reads the last stage again: the loop stays one block)
@@ -294,8 +317,45 @@ __device__ __forceinline__ void wave_sync()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// One 64 x 64 block of the wave's accumulators into its staging area.
-template <int ROW>
+// Where a wave's fp32 copy of a block in LDS holds (row, col): its quads of four
+// columns are XORed with a key that takes 16 values over 16 rows (a wave writes
+// quads of 16 rows at once), other ones in the next rows (it reads quads of four
+// rows), and pairs over columns (for a tall u): the first two meet in no bank,
+// the third in two.
+__device__ __forceinline__ int spot(int row, int col)
+{
+    const int key = (((row ^ (row >> 3)) & 7) << 1) | (row & 1);
+    return row * kB + (((col >> 2) ^ key) << 2) + (col & 3);
+}
+
+// Where a block holds the quads of a lane's accumulators: row 16 x + (lane & 15),
+// columns 16 y + 4 (lane >> 4).
+__device__ __forceinline__ int quad(int x, int y)
+{
+    const int lane = threadIdx.x & 63, row = lane & 15;   // (rows 16 apart have the same key)
+    return (16 * x + row) * kB + (((2 * y + (lane >> 5)) ^ slot_key(row)) << 3) + ((lane >> 4) & 1) * 4;
+}
+
+// All of a lane's quads of a block, in flight.
+__device__ __forceinline__ void load_quads(const half_t* block, h4 (&v)[4][4])
+{
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[x][y] = *reinterpret_cast<const h4*>(block + quad(x, y));
+}
+
+// A block that the wave has put together in LDS to memory, whole slots.
+__device__ __forceinline__ void store_block(half_t* block, const half_t* lds)
+{
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+        const int at = ((threadIdx.x & 63) + 64 * h) * 8;
+        *reinterpret_cast<h8*>(block + at) = *reinterpret_cast<const h8*>(lds + at);
+    }
+}
+
+// One 64 x 64 block of the wave's accumulators into its part of LDS, in fp32.
 __device__ __forceinline__ void stage_block(const f32x4 (*acc)[4], float* out)
 {
     const int lane = threadIdx.x & 63;
@@ -304,11 +364,11 @@ __device__ __forceinline__ void stage_block(const f32x4 (*acc)[4], float* out)
     for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<f32x4*>(out + (16 * x + (lane & 15)) * ROW + 16 * y + 4 * (lane >> 4)) = acc[x][y];
+            *reinterpret_cast<f32x4*>(out + spot(16 * x + (lane & 15), 16 * y + 4 * (lane >> 4))) = acc[x][y];
     wave_sync();
 }
 
-// A lane's slots (16 bytes) of a block, all in flight.
+// A lane's slots of a block, all in flight.
 __device__ __forceinline__ void load_slots(const half_t* block, h8 (&v)[8])
 {
 #pragma unroll
@@ -324,49 +384,59 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks))
 void ns_sym_kernel(NsArgs g, int it)
 {
     using T = Tile<WR, WC, MB, S>;
-    __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
     const ProdTile pt = g.sym[blockIdx.x];
-    const MatDesc& d = g.mats[pt.mat];
-    const half_t* src = reinterpret_cast<const half_t*>(g.area + (OP == kGram ? d.x[it & 1] : d.a));
-    half_t* dst = reinterpret_cast<half_t*>(g.area + (OP == kGram ? d.a : d.b));
-    const int kb = d.kp / kB, inner = OP == kGram ? d.np / kB : kb;
+    const Buffers buf = buffers(pt.at, pt.kb, pt.nb);
+    const half_t* src = reinterpret_cast<const half_t*>(g.area + (OP == kGram ? (it & 1 ? buf.x1 : buf.x0) : buf.a));
+    half_t* dst = reinterpret_cast<half_t*>(g.area + (OP == kGram ? buf.a : buf.b));
+    const int kb = pt.kb, inner = OP == kGram ? pt.nb : kb;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int bj = pt.j + wave % WC;
+    const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
+    const int lane_row = lane & 15, key = slot_key(lane_row);   // (rows 16 apart have the same key)
+    h4 av[4][4];
+    auto operands = [&](int bi) {   // A of the epilogue's block (bi, bj)
+        if (OP == kPoly && bi <= bj && bj < kb) {
+            const half_t* a = src + ((int64_t)bi * kb + bj) * kBlock;
+            load_quads(a, av);
+        }
+    };
     f32x4 acc[4 * MB][4];
     product<T, WR, WC, MB, S, false>(src, pt.i, kb, inner, src, pt.j, kb, inner, inner, reinterpret_cast<half_t*>(lds),
-                                     acc);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    float* out = reinterpret_cast<float*>(lds) + wave * T::kOut;
-    const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
+                                     acc, [&] { if constexpr (T::kAhead) operands(pt.i + wave / WC); });
+    half_t* out = reinterpret_cast<half_t*>(lds) + wave * kBlock;
     const float f = OP == kGram ? r * r / kNsScale : g.c / kNsScale;
-    const int bj = pt.j + wave % WC;
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
         const int bi = pt.i + (wave / WC) * MB + m;
         if (bi > bj || bi >= kb || bj >= kb) continue;   // below the diagonal, or past the end
-        const int64_t at = ((int64_t)bi * kb + bj) * kBlock, mirror = ((int64_t)bj * kb + bi) * kBlock;
-        h8 av[8], aw[8];
-        if constexpr (OP == kPoly) {
-            load_slots(src + at, av);
-            load_slots(src + mirror, aw);
-        }
-        stage_block<T::kOutRow>(acc + 4 * m, out);
+        if constexpr (!T::kAhead) operands(bi);
+        half_t* at = dst + ((int64_t)bi * kb + bj) * kBlock;
+        half_t* mirror = dst + ((int64_t)bj * kb + bi) * kBlock;
+        wave_sync();
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            const int slot = lane + 64 * h, row = slot >> 3, j = ((slot & 7) ^ slot_key(row)) << 3;
-            h8 v, w;
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                // row `row` of the block (bj, bi) is column `row` of this one
-                float z = f * out[row * T::kOutRow + j + q], y = f * out[(j + q) * T::kOutRow + row];
+            for (int y = 0; y < 4; ++y) {
+                f32x4 z = f * acc[4 * m + x][y];
                 if constexpr (OP == kPoly) {
-                    z += g.b * (float)av[h][q];
-                    y += g.b * (float)aw[h][q];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) z[q] = fmaf(g.b, (float)av[x][y][q], z[q]);
                 }
-                v[q] = (half_t)z;
-                w[q] = (half_t)y;
+                *reinterpret_cast<h4*>(out + quad(x, y)) = __builtin_convertvector(z, h4);
             }
-            *reinterpret_cast<h8*>(dst + at + slot * 8) = v;
-            if (bi != bj) *reinterpret_cast<h8*>(dst + mirror + slot * 8) = w;
-        }
+        wave_sync();
+        store_block(at, out);
+        if (bi == bj) continue;
+        // the mirror image: a lane gets column 16 y + lane_row, rows 32 h + 8 (lane >> 4)
+        // and the next seven, as one slot (A is its own transpose bit for bit, so
+        // b A needs no other block)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<h8*>(mirror + (16 * y + lane_row) * kB + (((4 * h + (lane >> 4)) ^ key) << 3)) =
+                    columns(out, 32 * h, 16 * y);
     }
 }
 
@@ -374,7 +444,7 @@ void ns_sym_kernel(NsArgs g, int it)
 // the update of the master and the parameter with it.  Rows of o are the
 // block's rows, or its columns when u is tall; four elements a lane, the loads
 // of eight quads in flight.
-template <int LAST, int ROW>
+template <int LAST>
 __device__ __forceinline__ void finish_block(const MatDesc& d, const float* out, int bi, int bj, const MuonArgs& ma)
 {
     const int lane = threadIdx.x & 63;
@@ -384,34 +454,44 @@ __device__ __forceinline__ void finish_block(const MatDesc& d, const float* out,
     const Span4 s = span4<false>(c0 + c, d.cols, true);
 #pragma unroll
     for (int h0 = 0; h0 < 16; h0 += 8) {
-        int64_t row[8];
-        int skip[8];
+        auto row_of = [&](int h) { return r0 + 4 * (h0 + h) + rl; };
         float v[8][4];
+        if constexpr (LAST == kNsUpdate) {
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-            const int64_t r = r0 + 4 * (h0 + h) + rl;
-            const bool in = r < d.rows;
-            row[h] = in ? r : 0;
-            skip[h] = in ? s.skip : 4;
-            if constexpr (LAST == kNsUpdate) load_quad<false>(d.master + row[h] * d.ld + s.col, skip[h], v[h]);
+            for (int h = 0; h < 8; ++h) {
+                const int64_t r = row_of(h);
+                load_quad<false>(d.master + (r < d.rows ? r : 0) * d.ld + s.col, 0, v[h]);
+            }
         }
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
             const int rr = 4 * (h0 + h) + rl;
-            float o[4];
+            const int64_t row = row_of(h);
+            if (row >= d.rows) continue;
+            // columns c .. c + 3 of o; a quad that begins `skip` elements early holds
+            // column c there
+            float w[4], o[4];
+            if (d.tall) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = out[spot(c + q, rr)];
+            } else {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(out + spot(rr, c));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = x[q];
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int cc = (int)(s.col - c0) + q;   // (before the block where the quad begins early: not stored)
-                const int k = cc < 0 || cc > kB - 1 ? 0 : cc;
-                o[q] = d.tall ? out[k * ROW + rr] : out[rr * ROW + k];
+                o[q] = w[q];
+#pragma unroll
+                for (int k = 1; k <= q; ++k) o[q] = s.skip == k ? w[q - k] : o[q];
             }
             if constexpr (LAST == kNsWriteO) {
-                store_quad<false>(d.o + row[h] * d.ldo + s.col, skip[h], o);
+                store_quad<false>(d.o + row * d.ldo + s.col, s.skip, o);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[h][q] = muon_elem(v[h][q], o[q], eta, ma);
-                store_quad<false>(d.master + row[h] * d.ld + s.col, skip[h], v[h]);
-                store_quad<false>(d.param + row[h] * d.ld + s.col, skip[h], v[h]);
+                store_quad<false>(d.master + row * d.ld + s.col, s.skip, v[h]);
+                store_quad<false>(d.param + row * d.ld + s.col, s.skip, v[h]);
             }
         }
     }
@@ -424,55 +504,74 @@ __global__ __launch_bounds__(64 * WR * WC, (Tile<WR, WC, MB, S>::kMinBlocks))
 void ns_apply_kernel(NsArgs g, int it, int has_lo, MuonArgs ma)
 {
     using T = Tile<WR, WC, MB, S>;
-    __shared__ __attribute__((aligned(1024))) char lds[T::kLds];
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
     const ProdTile pt = g.full[blockIdx.x];
-    const MatDesc& d = g.mats[pt.mat];
-    const half_t* xi = reinterpret_cast<const half_t*>(g.area + d.x[it & 1]);
-    half_t* xo = reinterpret_cast<half_t*>(g.area + d.x[(it & 1) ^ 1]);
-    half_t* lo = reinterpret_cast<half_t*>(g.area + d.lo);
-    const half_t* bm = reinterpret_cast<const half_t*>(g.area + d.b);
-    const int kb = d.kp / kB, nb = d.np / kB;
-    f32x4 acc[4 * MB][4];
-    product<T, WR, WC, MB, S, true>(bm, pt.i, kb, kb, xi, pt.j, kb, nb, kb, reinterpret_cast<half_t*>(lds), acc);
+    const Buffers buf = buffers(pt.at, pt.kb, pt.nb);
+    const half_t* xi = reinterpret_cast<const half_t*>(g.area + (it & 1 ? buf.x1 : buf.x0));
+    half_t* xo = reinterpret_cast<half_t*>(g.area + (it & 1 ? buf.x0 : buf.x1));
+    half_t* lo = reinterpret_cast<half_t*>(g.area + buf.lo);
+    const half_t* bm = reinterpret_cast<const half_t*>(g.area + buf.b);
+    const int kb = pt.kb, nb = pt.nb;
+    MatDesc d;
+    if constexpr (LAST != kNsMid) d = g.mats[pt.mat];
     if constexpr (LAST == kNsUpdate) use_device_scalars(ma, nullptr);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    float* out = reinterpret_cast<float*>(lds) + wave * T::kOut;
-    const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
-    const float fa = g.a * r, fb = r / kNsScale;
     const int bj = pt.j + wave % WC;
+    const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
+    h8 xh[8], xl[8] = {};
+    auto operands = [&](int bi) {   // of the epilogue's block (bi, bj)
+        if (bi < kb && bj < nb) {
+            const int64_t at = ((int64_t)bi * nb + bj) * kBlock;
+            load_slots(xi + at, xh);
+            if (has_lo) load_slots(lo + at, xl);
+        }
+    };
+    f32x4 acc[4 * MB][4];
+    product<T, WR, WC, MB, S, true>(bm, pt.i, kb, kb, xi, pt.j, kb, nb, kb, reinterpret_cast<half_t*>(lds), acc,
+                                    [&] { if constexpr (T::kAhead) operands(pt.i + wave / WC); });
+    float* out = reinterpret_cast<float*>(lds) + wave * kBlock;
+    const float scale = LAST == kNsMid ? 1.0f : 1.0f / kNsScale;
+    const float fa = g.a * r * scale, fb = r / kNsScale * scale;
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
         const int bi = pt.i + (wave / WC) * MB + m;
         if (bi >= kb || bj >= nb) continue;
         const int64_t at = ((int64_t)bi * nb + bj) * kBlock;
-        h8 xh[8], xl[8] = {};
-        load_slots(xi + at, xh);
-        if (has_lo) load_slots(lo + at, xl);
-        stage_block<T::kOutRow>(acc + 4 * m, out);
+        if constexpr (!T::kAhead) operands(bi);
+        stage_block(acc + 4 * m, out);
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
             const int slot = lane + 64 * h, row = slot >> 3, j = ((slot & 7) ^ slot_key(row)) << 3;
-            float z[8];
+            f32x4* const x[2] = {reinterpret_cast<f32x4*>(out + spot(row, j)), reinterpret_cast<f32x4*>(out + spot(row, j + 4))};
+            h8 vh, vl;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                z[q] = fa * ((float)xh[h][q] + (float)xl[h][q]) + fb * out[row * T::kOutRow + j + q];
-            if constexpr (LAST == kNsMid) {
-                h8 vh, vl;
+            for (int e = 0; e < 2; ++e) {
+                f32x4 z = *x[e];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    vh[q] = (half_t)z[q];
-                    vl[q] = (half_t)(z[q] - (float)vh[q]);
+                for (int q = 0; q < 4; ++q)
+                    z[q] = fmaf(fb, z[q], fmaf(fa, (float)xh[h][4 * e + q], fa * (float)xl[h][4 * e + q]));
+                if constexpr (LAST == kNsMid) {
+                    const h4 hi = __builtin_convertvector(z, h4);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) z[q] = fmaf(-1.0f, (float)hi[q], z[q]);
+                    const h4 rest = __builtin_convertvector(z, h4);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        vh[4 * e + q] = hi[q];
+                        vl[4 * e + q] = rest[q];
+                    }
+                } else {
+                    *x[e] = z;
                 }
+            }
+            if constexpr (LAST == kNsMid) {
                 *reinterpret_cast<h8*>(xo + at + slot * 8) = vh;
                 *reinterpret_cast<h8*>(lo + at + slot * 8) = vl;
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) out[row * T::kOutRow + j + q] = z[q] / kNsScale;
             }
         }
         if constexpr (LAST != kNsMid) {
             wave_sync();
-            finish_block<LAST, T::kOutRow>(d, out, bi, bj, ma);
+            finish_block<LAST>(d, out, bi, bj, ma);
         }
     }
 }
@@ -480,12 +579,15 @@ void ns_apply_kernel(NsArgs g, int it, int has_lo, MuonArgs ma)
 }  // namespace
 
 // ------------------------------------------------------------------ launchers
-hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, int grid, hipStream_t s)
+hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, const double* partials, double eps, NormRec* norms, int grid,
+                             hipStream_t s)
 {
-    if (u_f32) ns_prepare_kernel<float><<<dim3(grid), dim3(kThreads), 0, s>>>(g);
-    else ns_prepare_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, s>>>(g);
+    if (u_f32) ns_prepare_kernel<float><<<dim3(grid), dim3(kThreads), 0, s>>>(g, partials, eps, norms);
+    else ns_prepare_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, s>>>(g, partials, eps, norms);
     return hipGetLastError();
 }
+
+constexpr int kFewTiles = 256;   // as many as CUs
 
 #define Z1_TILES(tile, CALL)                              \
     do {                                                  \
@@ -496,15 +598,21 @@ hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, int grid, hipStream_t 
 
 hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hipStream_t s)
 {
-#define Z1_CALL(WR, WC, MB, S) ns_sym_kernel<kGram, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), 0, s>>>(g, it)
-    Z1_TILES(tile, Z1_CALL);
+#define Z1_CALL(WR, WC, MB, S) ns_sym_kernel<kGram, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), Tile<WR, WC, MB, S>::kLds, s>>>(g, it)
+    // Where no CU has two tiles, LDS has room for two stages more, whose loads
+    // then cover the first touch of X by the chip.  Two against four: 3 of 1111 x
+    // 2501 27.2 and 24.8 us, 1000 x 1000 12.3 and 11.7, 12 of 768 x 768 12.3 both,
+    // 192 x 192 4.2 and 4.4; poly and apply, whose operands are smaller, lose by it
+    // (13.1 and 13.4; 13.9 and 14.3).
+    if (tile == kTile128 && grid <= kFewTiles) Z1_CALL(2, 2, 1, 4);
+    else Z1_TILES(tile, Z1_CALL);
 #undef Z1_CALL
     return hipGetLastError();
 }
 
 hipError_t launch_ns_poly(const NsArgs& g, TileShape tile, int grid, hipStream_t s)
 {
-#define Z1_CALL(WR, WC, MB, S) ns_sym_kernel<kPoly, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), 0, s>>>(g, 1)
+#define Z1_CALL(WR, WC, MB, S) ns_sym_kernel<kPoly, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), Tile<WR, WC, MB, S>::kLds, s>>>(g, 1)
     Z1_TILES(tile, Z1_CALL);
 #undef Z1_CALL
     return hipGetLastError();
@@ -515,7 +623,7 @@ hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, con
 {
     const int has_lo = it > 0 || u_f32 ? 1 : 0;
 #define Z1_APPLY(LAST, WR, WC, MB, S) \
-    ns_apply_kernel<LAST, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), 0, s>>>(g, it, has_lo, ma)
+    ns_apply_kernel<LAST, WR, WC, MB, S><<<dim3(grid), dim3(64 * WR * WC), Tile<WR, WC, MB, S>::kLds, s>>>(g, it, has_lo, ma)
 #define Z1_MID(WR, WC, MB, S) Z1_APPLY(kNsMid, WR, WC, MB, S)
 #define Z1_O(WR, WC, MB, S) Z1_APPLY(kNsWriteO, WR, WC, MB, S)
 #define Z1_UPD(WR, WC, MB, S) Z1_APPLY(kNsUpdate, WR, WC, MB, S)
