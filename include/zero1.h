@@ -391,7 +391,8 @@ zero1_status zero1_mta_step_static(const uint16_t* const* grads, int W, int64_t 
  * and zero1_mta_update, the sum of squares of zero1_grad_norm, the partials
  * sum of zero1_partials_sum (and of an empty zero1_shard_reduce /
  * zero1_grad_norm).  The request is dropped when that call returns, whether
- * or not it launched anything; a later request replaces an earlier one.
+ * or not it launched anything; a later request replaces an earlier one.  The
+ * Muon calls neither take it nor drop it.
  *
  * The events are created and owned by the caller (hipEventCreate, timing
  * enabled, on the device the step runs on) and must outlive the kernel.
@@ -479,11 +480,13 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
  * Arithmetic: momentum and update, like the AdamW step, one binary32 operation
  * at a time (eta = fp32(lr) * scale is one of them).  The norm is fp64.  The
  * products multiply fp16 operands on the matrix cores and add in fp32; X is
- * held as two fp16 halves (22 bits), A and B as one.  o is within about 0.2 %
- * (2-norm) of the iteration in 64 bits before its rounding to bf16; for single
- * rows and other matrices of few singular values within about 0.5 %.  Results
- * do not depend on the other matrices of the plan, and a rerun gives the same
- * bits.
+ * held as two fp16 halves (22 bits), A and B as one, and as two where the
+ * smaller side is at most 128.  Before its rounding to bf16 o is within (2-norm,
+ * default coefficients) 0.05 % of the iteration in 64 bits in up to five steps
+ * where the smaller side is at most 128, else within about 0.15 % in five steps
+ * and 0.3 % in eight.  An entry of a u that is small beside eps is off by up to
+ * 2^-37 of its matrix's scale besides.  Results do not depend on the other
+ * matrices of the plan, and a rerun gives the same bits.
  * Non-finite values: a matrix whose u holds an infinity or a NaN gets NaN in
  * the whole of its o (as the formulas give); the other matrices do not. */
 
@@ -511,8 +514,9 @@ typedef struct zero1_matrix {
     int64_t ldo;            /* row stride of o                                  */
 } zero1_matrix;
 
-/* Matrices of a plan that are iterated together: their launches' sizes and tile
- * shapes. */
+/* Matrices of a plan that are iterated together: the launches' lists (where they
+ * begin in the table and how long they are), tile shapes and kernels.  Set by
+ * zero1_muon_plan; callers only keep them. */
 #define ZERO1_MUON_MAX_GROUPS 64
 typedef struct zero1_matrix_group {
     int64_t sym0, full0, blocks0;
@@ -565,7 +569,10 @@ zero1_status zero1_muon_scalars_derive(const zero1_muon_hparams* hp, zero1_muon_
  * zero1_muon_plan: validates the matrices (sizes, strides, no two buffers
  *   sharing an element; blocks of columns of one array are told apart by their
  *   common stride) and copies the table into `table` (device, 256-byte
- *   aligned).  Synchronous, once per list.  `flags`: ZERO1_MV_BF16, ZERO1_U_F32.
+ *   aligned).  Synchronous, once per list.  `flags`: ZERO1_MV_BF16, ZERO1_U_F32;
+ *   they hold for every call with the plan, whatever these calls' flags say.
+ *   Up to 2^37 elements a plan; two calls that overlap on the device need
+ *   workspaces of their own, and so do two captured graphs.
  * zero1_muon_workspace_bytes: workspace of zero1_orthogonalize and
  *   zero1_muon_step (256-byte aligned): the iteration's buffers of one group of
  *   matrices at a time (about 512 MiB, or one matrix where it needs more) and

@@ -20,6 +20,9 @@
 // is the same only for factors that commute exactly, and is off by up to 9e-3
 // after five steps, where this is off by up to 2e-4.
 //
+// Measured, five steps: 64 x 64 20.5 us (one launch); 24 of 100 x 1000 80 us: gram
+// 15, the parts' sum 5, poly 51, apply 14.
+//
 // Powers of two carried in fp16: X and A 2^12, B 2^10, P 2^3 (|A| <= 9,
 // |B| <= 12, |P| <= 160 * 27, checked on the host).
 #include <hip/hip_runtime.h>
@@ -626,7 +629,7 @@ __global__ __launch_bounds__(kThreads) void thin_apply_kernel(NsArgs g, int mid,
 }
 
 // All three for a matrix of one part, where a launch costs more than the work:
-// 64 x 64 takes 16 us this way and 24 in three.  What passes between them goes
+// 64 x 64 takes 20.5 us this way and 25 in three launches.  What passes between them goes
 // through memory as it does there (the workgroup's own L1).
 template <typename U, int KP, int LAST>
 __global__ __launch_bounds__(kThreads) void thin_one_kernel(NsArgs g, int steps, double eps, NormRec* norms, MuonArgs ma)
