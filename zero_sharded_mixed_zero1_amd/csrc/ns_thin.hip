@@ -20,8 +20,8 @@
 // is the same only for factors that commute exactly, and is off by up to 9e-3
 // after five steps, where this is off by up to 2e-4.
 //
-// Measured, five steps: 64 x 64 20.5 us (one launch); 24 of 100 x 1000 80 us: gram
-// 15, the parts' sum 5, poly 51, apply 14.
+// Measured, five steps: 64 x 64 20.5 us (one launch); 24 of 100 x 1000 79 us: gram
+// 14, the parts' sum 5, poly 51, apply 13.
 //
 // Powers of two carried in fp16: X and A 2^12, B 2^10, P 2^3 (|A| <= 9,
 // |B| <= 12, |P| <= 160 * 27, checked on the host).
@@ -88,17 +88,23 @@ struct Chunk {
         }
     }
 
-    // (no quad of these columns crosses the end of a row)
+    // (no quad of these columns crosses the end of a row; a lane's quads are of one
+    // column and of rows a constant apart)
     template <typename U>
     __device__ __forceinline__ void load_whole(const Source<U>& s, int64_t j0)
     {
+        const int64_t i = at_i(s.tall, 0), j = j0 + at_j(s.tall, 0);
+        const int64_t row = s.tall ? j : i, col = s.tall ? i : j;
+        const int64_t step = s.tall ? kThreads / (KP / 4) : kThreads / (C / 4);
+        const int64_t left = col < s.cols ? s.rows - row : 0;   // rows from the lane's first on
+        const U* p = s.p + row * s.ld + col;
+        const int64_t apart = step * s.ld;
 #pragma unroll
         for (int h = 0; h < kRounds; ++h) {
-            const int64_t i = at_i(s.tall, h), j = j0 + at_j(s.tall, h);
-            const int64_t row = s.tall ? j : i, col = s.tall ? i : j;
-            const bool in = row < s.rows && col < s.cols;
+            const bool in = h * step < left;
             float x[4];
-            load_quad<false>(s.p + (in ? row * s.ld + col : 0), 0, x);
+            load_quad<false>(in ? p : s.p, 0, x);
+            p += apart;
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[h][q] = in ? x[q] : 0.0f;
         }
@@ -220,12 +226,16 @@ __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int
                 }
         }
     }
+    // (one of several parts: the tiles on and above the diagonal, thin_sum mirrors
+    // the sum; writing them all took 1.3 us more of 24 matrices of 100 x 1000)
     float* out = reinterpret_cast<float*>(g.area + d.a) + (int64_t)part * KP * KP;
 #pragma unroll
     for (int a = 0; a < N; ++a)
 #pragma unroll
         for (int b = 0; b < N; ++b)
-            *reinterpret_cast<f32x4*>(out + (wi + 16 * a + (lane & 15)) * KP + wj + 16 * b + 4 * (lane >> 4)) = acc[a][b];
+            if (d.n_parts == 1 || wi + 16 * a <= wj + 16 * b)
+                *reinterpret_cast<f32x4*>(out + (wi + 16 * a + (lane & 15)) * KP + wj + 16 * b + 4 * (lane >> 4)) =
+                    acc[a][b];
     if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[part] = e == 1000 ? 0 : e;
 }
 
@@ -241,13 +251,15 @@ constexpr int kSumExp = kThinMaxParts;
 
 // The parts' sum into part 0, with the least of their exponents: a quad a lane,
 // KP * KP / 4 lanes a matrix (one workgroup alone would read 64 KiB a part at
-// k = 128: 2 to 3 us each).
+// k = 128: 2 to 3 us each).  Tiles of 16 x 16 above the diagonal are stored with
+// their mirror images.
 template <int KP>
 __global__ __launch_bounds__(kThreads) void thin_sum_kernel(NsArgs g)
 {
     constexpr int kPer = KP * KP / 4 / kThreads;   // workgroups a matrix
     const MatDesc& d = g.mats[g.first + (int)blockIdx.x / kPer];
-    const int quad = ((int)blockIdx.x % kPer) * kThreads + threadIdx.x;
+    const int quad = ((int)blockIdx.x % kPer) * kThreads + threadIdx.x, i = quad / (KP / 4), j = quad % (KP / 4) * 4;
+    if (d.n_parts == 1 || i / 16 > j / 16) return;
     f32x4* part = reinterpret_cast<f32x4*>(g.area + d.a) + quad;
     int32_t* exps = reinterpret_cast<int32_t*>(g.area + d.lo);
     int least = exps[0];
@@ -257,6 +269,11 @@ __global__ __launch_bounds__(kThreads) void thin_sum_kernel(NsArgs g)
     for (int n = 0; n < d.n_parts; ++n)
         sum += ldexpf(1.0f, max(2 * (least - exps[n]), -200)) * part[(int64_t)n * (KP * KP / 4)];
     *part = sum;
+    if (i / 16 < j / 16) {
+        float* mirror = reinterpret_cast<float*>(g.area + d.a) + j * KP + i;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mirror[q * KP] = sum[q];
+    }
     if (quad == 0) exps[kSumExp] = least;
 }
 
@@ -345,13 +362,25 @@ __device__ __forceinline__ void for_quads(F f)
         for (int y = 0; y < T::NI; ++y) f(x, y, wi + 16 * x, wj + 16 * y);
 }
 
+// a x + b y.
+__device__ __forceinline__ f32x4 axby(float a, const f32x4& x, float b, const f32x4& y)
+{
+    f32x4 z;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) z[q] = fmaf(a, x[q], b * y[q]);
+    return z;
+}
+
 // A quad as two halves to M[..][i][j..j+3].
 template <int KP>
 __device__ __forceinline__ void put(typename Poly<KP>::Mat& M, int i, int j, const f32x4& v)
 {
     const h4 hi = __builtin_convertvector(v, h4);
+    f32x4 rest;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) rest[q] = fmaf(-1.0f, (float)hi[q], v[q]);   // (one instruction an element)
     *reinterpret_cast<h4*>(&M[0][i][j]) = hi;
-    *reinterpret_cast<h4*>(&M[1][i][j]) = __builtin_convertvector(v - __builtin_convertvector(hi, f32x4), h4);
+    *reinterpret_cast<h4*>(&M[1][i][j]) = __builtin_convertvector(rest, h4);
 }
 
 // One workgroup a matrix: the norm (the trace of the sum is |u|^2), A from the
@@ -405,7 +434,7 @@ __device__ __forceinline__ NormRec thin_poly(const NsArgs& g, const MatDesc& d, 
         const bool last = it + 1 == steps;
         multiply<KP, true>(A, A, acc);
         for_quads<KP>([&](int x, int y, int i, int j) {
-            const f32x4 v = qc * acc[x][y] + qb * a[x][y];
+            const f32x4 v = axby(qc, acc[x][y], qb, a[x][y]);
             put<KP>(B, i, j, v);
             if (it == 0) {   // P = a I + B
                 p[x][y] = (kPScale * inv) * v;
@@ -416,12 +445,12 @@ __device__ __forceinline__ NormRec thin_poly(const NsArgs& g, const MatDesc& d, 
         __syncthreads();
         if (!last) {
             multiply<KP, true>(A, B, acc);
-            for_quads<KP>([&](int x, int y, int, int) { t[x][y] = g.a * a[x][y] + inv * acc[x][y]; });
+            for_quads<KP>([&](int x, int y, int, int) { t[x][y] = axby(g.a, a[x][y], inv, acc[x][y]); });
         }
         if constexpr (T::kOwnP) {
             if (it > 0) {
                 multiply<KP, false>(B, own_p, acc);
-                for_quads<KP>([&](int x, int y, int, int) { p[x][y] = g.a * p[x][y] + inv * acc[x][y]; });
+                for_quads<KP>([&](int x, int y, int, int) { p[x][y] = axby(g.a, p[x][y], inv, acc[x][y]); });
             }
             if (!last) {
                 __syncthreads();
@@ -433,7 +462,7 @@ __device__ __forceinline__ NormRec thin_poly(const NsArgs& g, const MatDesc& d, 
                 for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(A, i, j, p[x][y]); });
                 __syncthreads();
                 multiply<KP, false>(B, A, acc);
-                for_quads<KP>([&](int x, int y, int, int) { p[x][y] = g.a * p[x][y] + inv * acc[x][y]; });
+                for_quads<KP>([&](int x, int y, int, int) { p[x][y] = axby(g.a, p[x][y], inv, acc[x][y]); });
             }
             if (!last) __syncthreads();
         }
@@ -441,7 +470,7 @@ __device__ __forceinline__ NormRec thin_poly(const NsArgs& g, const MatDesc& d, 
             for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(A, i, j, t[x][y]); });
             __syncthreads();
             multiply<KP, false>(B, A, acc);
-            for_quads<KP>([&](int x, int y, int, int) { a[x][y] = g.a * t[x][y] + inv * acc[x][y]; });
+            for_quads<KP>([&](int x, int y, int, int) { a[x][y] = axby(g.a, t[x][y], inv, acc[x][y]); });
             __syncthreads();
             for_quads<KP>([&](int x, int y, int i, int j) { put<KP>(A, i, j, a[x][y]); });
             __syncthreads();
