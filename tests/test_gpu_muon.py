@@ -882,3 +882,86 @@ def test_captured_clip_reads_its_device_scalars(env):
             assert_bf16_equal(a.get("u", i), b.get("u", i), f"u, {f}")
         results.append(a.get("u", 0).copy())
     assert not np.array_equal(results[0], results[1])
+
+
+@pytest.mark.parametrize("rows,cols,count,tiles", [(4090, 4101, 1, (1, 1)), (5103, 5003, 1, (2, 2)), (4099, 2051, 3, (0, 2)),
+                                                   (1111, 2501, 3, (0, 1))])
+def test_every_tile_shape(env, rows, cols, count, tiles):
+    """Sizes that take the larger tiles of the products, ragged against all of them,
+    cut out of wider arrays: the iteration in 64 bits (on the GPU for its size),
+    o's neighbours untouched, a captured replay the same bits, and the update in
+    the last product's epilogue."""
+    torch, dev = env
+    gen = torch.Generator(device=dev).manual_seed(7)
+    ld, ldo = cols + 3, cols + 5
+    u = torch.zeros(count, rows, ld, dtype=torch.bfloat16, device=dev)
+    o = torch.full((count, rows, ldo), 7.0, dtype=torch.bfloat16, device=dev)
+    for k in range(count):
+        low = torch.randn(rows, 8, generator=gen, device=dev) @ torch.randn(8, cols, generator=gen, device=dev)
+        u[k, :, :cols] = ((3 * low + torch.randn(rows, cols, generator=gen, device=dev)) * 1e-3).bfloat16()
+    mats = [z.matrix(rows, cols, u=u[k], ldu=ld, o=o[k], ldo=ldo) for k in range(count)]
+    table = ws_tensor(torch, z.muon_table_bytes(mats), dev)
+    plan = z.muon_plan(mats, table)
+    assert (plan.groups[0].sym_tile, plan.groups[0].full_tile) == tiles and plan.n_groups == 1
+    ws = ws_tensor(torch, z.muon_workspace_bytes(plan), dev)
+    ws.fill_(0xFF)
+    z.orthogonalize(plan, HP, ws=ws)
+    torch.cuda.synchronize()
+    assert (o[:, :, cols:] == 7.0).all()
+    exact = []
+    for k in range(count):
+        x = u[k, :, :cols].double()
+        x = x / (torch.linalg.vector_norm(x) + 1e-7)
+        for _ in range(5):
+            if rows <= cols:
+                s = x @ x.T
+                x = ref.A * x + (ref.B * s + ref.C * (s @ s)) @ x
+            else:
+                s = x.T @ x
+                x = ref.A * x + x @ (ref.B * s + ref.C * (s @ s))
+        off, size = (float(torch.linalg.vector_norm(v)) for v in (o[k, :, :cols].double() - x, x))
+        assert off <= math.hypot(3e-3, ref.BF16) * size, (k, off / size)
+        exact.append(x)
+    first = o.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        z.orthogonalize(plan, HP, ws=ws)
+    for _ in range(2):
+        o.zero_()
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o[:, :, :cols], first[:, :, :cols])
+    # the step: u = g of one slice, so that its o is the same but for the rounding
+    mom, master = torch.zeros(count, rows, ld, device=dev), torch.zeros(count, rows, ld, device=dev)
+    param = torch.full((count, rows, ld), 7.0, dtype=torch.bfloat16, device=dev)
+    u2 = torch.zeros_like(u)
+    mats = [z.matrix(rows, cols, ld=ld, shard_offset=k * rows * ld, param=param[k], master=master[k], m=mom[k], u=u2[k],
+                     ldu=ld) for k in range(count)]
+    table2 = ws_tensor(torch, z.muon_table_bytes(mats), dev)
+    plan2 = z.muon_plan(mats, table2)
+    z.muon_step([u], 0, plan2, dict(lr=1.0, momentum=0.5, weight_decay=0.0), flags=z.NO_NESTEROV, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(u2, u)
+    assert (param[:, :, cols:] == 7.0).all() and (master[:, :, cols:] == 0).all()
+    assert torch.equal(param[:, :, :cols], master[:, :, :cols].bfloat16())
+    for k in range(count):
+        off = float(torch.linalg.vector_norm(-master[k, :, :cols].double() - exact[k]))
+        assert off <= 3e-3 * float(torch.linalg.vector_norm(exact[k])), k
+        # and is what orthogonalize rounds
+        assert torch.equal((-master[k, :, :cols]).bfloat16(), first[k, :, :cols])
+
+
+@pytest.mark.parametrize("steps", [1, 5, 7])
+def test_in_place_on_every_path(env, steps):
+    """o in place of u: thin matrices of one part and of several, in one segment of
+    steps and in two, wide and tall, and others."""
+    torch, dev = env
+    shapes = [(30, 40), (64, 250), (250, 64), (100, 1001), (1001, 100), (3, 700), (200, 600), (601, 203)]
+    a = Mats(env, shapes, pad_u=3, skew=1)
+    b = Mats(env, shapes, pad_u=3, skew=1, in_place=True)
+    for t in (a, b):
+        z.orthogonalize(t.plan, dict(HP, ns_steps=steps), ws=t.workspace())
+    torch.cuda.synchronize()
+    for i in range(len(shapes)):
+        assert_bf16_equal(b.get("o", i), a.get("o", i), f"in place {shapes[i]}")

@@ -390,7 +390,7 @@ __device__ __forceinline__ void put(typename Poly<KP>::Mat& M, int i, int j, con
 // A step multiplies by Q = a I + B: T = A Q = a A + A B, A <- Q T = a T + B T,
 // P <- Q P = a P + B P, with A, T and P in registers (fp32) for the a-terms and
 // in LDS as two halves for the products.
-// Bound by the chain of products: at k = 128 each is 3072 cycles of MFMA and as
+// Bound by the chain of products: at k = 128 each takes 3100 cycles of MFMA and as
 // many of LDS reads on its one CU (9 us a step), at 64 mostly latency (2.5 us).
 template <int KP>
 __device__ __forceinline__ NormRec thin_poly(const NsArgs& g, const MatDesc& d, int mat, int mid, int steps, double eps,
