@@ -519,9 +519,9 @@ typedef struct zero1_matrix {
  * zero1_muon_plan; callers only keep them. */
 #define ZERO1_MUON_MAX_GROUPS 64
 typedef struct zero1_matrix_group {
-    int64_t sym0, full0, blocks0;
-    int32_t n_sym, n_full, n_blocks, first;
-    int16_t sym_tile, full_tile, thin, parts, one, reserved[3];
+    int64_t sym0, full0, blocks0, gram0;
+    int32_t n_sym, n_full, n_blocks, first, n_gram, reserved0;
+    int16_t sym_tile, full_tile, thin, parts, one, split, reserved[2];
 } zero1_matrix_group;
 
 /* A validated list of matrices uploaded by zero1_muon_plan.  Plain data owned

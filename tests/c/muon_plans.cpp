@@ -30,6 +30,7 @@ using namespace z1;
     } while (0)
 
 static int g_case = 0;
+static int splits = 0;   // groups of split grams seen
 
 // ------------------------------------------------------------------ stand-ins
 extern "C" {
@@ -117,6 +118,12 @@ hipError_t launch_ns_gram(const NsArgs& g, int, TileShape, int grid, hipStream_t
     group_args(g);
     in_table(g.sym, sizeof(ProdTile) * grid, g_table_bytes);
     return launched("gram", grid, 576);
+}
+hipError_t launch_ns_gram_split(const NsArgs& g, int, int grid, hipStream_t)
+{
+    group_args(g);
+    in_table(g.gram, sizeof(ProdTile) * grid, g_table_bytes);
+    return launched("gram split", grid, 256);
 }
 hipError_t launch_ns_poly(const NsArgs& g, TileShape, int grid, hipStream_t)
 {
@@ -256,6 +263,7 @@ static void check_table(const zero1_matrix_plan& p, const std::vector<zero1_matr
                 used.push_back({d.b, d.b + 2 * (int64_t)d.kp * d.kp * 2});
             } else {
                 REQUIRE(d.k > kThin && d.kp % kPad == 0 && d.kp >= d.k && d.np >= d.n);
+                REQUIRE(g.split == (d.kp / kPad <= kSplitRows && d.np / kPad >= kSplitInner));
                 used.push_back({d.x[0], d.x[0] + x});
                 used.push_back({d.x[1], d.x[1] + x});
                 used.push_back({d.lo, d.lo + x});
@@ -274,6 +282,8 @@ static void check_table(const zero1_matrix_plan& p, const std::vector<zero1_matr
             check_tiles(p, mats, list, g, end, g.sym0, g.n_sym, g.sym_tile + 2, true);
             check_tiles(p, mats, list, g, end, g.full0, g.n_full, g.full_tile + 2, false);
             check_tiles(p, mats, list, g, end, g.blocks0, g.n_blocks, 1, false);
+            if (g.split) check_tiles(p, mats, list, g, end, g.gram0, g.n_gram, 1, true);
+            splits += g.split;
         }
     }
 }
@@ -297,7 +307,7 @@ static std::vector<std::string> expected(const zero1_matrix_plan& p, int steps, 
         } else {
             e.push_back("prepare");
             for (int s = 0; s < steps; ++s) {
-                e.push_back("gram");
+                e.push_back(g.split ? "gram split" : "gram");
                 e.push_back("poly");
                 e.push_back(s + 1 == steps ? "last" : "apply");
             }
@@ -396,7 +406,7 @@ int main()
         }
         std::free(table);
     }
-    REQUIRE(widest >= 1 << 20 && large >= 10);
+    REQUIRE(widest >= 1 << 20 && large >= 10 && splits >= 10);
     std::printf("all ok\n");
     return 0;
 }

@@ -965,3 +965,24 @@ def test_in_place_on_every_path(env, steps):
     torch.cuda.synchronize()
     for i in range(len(shapes)):
         assert_bf16_equal(b.get("o", i), a.get("o", i), f"in place {shapes[i]}")
+
+
+@pytest.mark.parametrize("u_f32", [False, True])
+def test_split_gram(env, u_f32):
+    """Matrices whose gram's inner dimension is split between waves (few block rows,
+    a long other side, any remainder of it by four), around both ends of the rule:
+    within the bound before the last rounding, and the same bits in a plan of its
+    own."""
+    rng = np.random.default_rng(21)
+    shapes = [(129, 1024), (140, 1030), (1100, 200), (300, 1217), (512, 961), (511, 960), (513, 1000), (1345, 321)]
+    us = [spectrum(rng, s, k) for s, k in zip(shapes, ["gauss", "power", "low", "gauss", "power", "gauss", "gauss", "low"])]
+    t = Steps(env, us, u_f32)
+    assert sum(t.plan.groups[i].split for i in range(t.plan.n_groups)) == 1 and t.plan.n_groups == 2
+    for steps in (1, 5):
+        together = t.o(steps)
+        for i, u in enumerate(t.u):
+            exact = ref.iterate64(u, steps)
+            bound, size = ref.iterate_bound(u, steps)
+            off = np.linalg.norm(together[i] - exact)
+            assert off <= (bound - ref.BF16 * size) / (1 + ref.BF16), (shapes[i], steps, off / size)
+            assert np.array_equal(Steps(env, [us[i]], u_f32).o(steps)[0], together[i]), (shapes[i], steps)

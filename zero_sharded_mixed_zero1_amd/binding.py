@@ -94,10 +94,12 @@ class Matrix(ctypes.Structure):
 
 
 class MatrixGroup(ctypes.Structure):
-    _fields_ = [("sym0", i64), ("full0", i64), ("blocks0", i64), ("n_sym", ctypes.c_int32),
-                ("n_full", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("first", ctypes.c_int32),
+    _fields_ = [("sym0", i64), ("full0", i64), ("blocks0", i64), ("gram0", i64),
+                ("n_sym", ctypes.c_int32), ("n_full", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+                ("first", ctypes.c_int32), ("n_gram", ctypes.c_int32), ("reserved0", ctypes.c_int32),
                 ("sym_tile", ctypes.c_int16), ("full_tile", ctypes.c_int16), ("thin", ctypes.c_int16),
-                ("parts", ctypes.c_int16), ("one", ctypes.c_int16), ("reserved", ctypes.c_int16 * 3)]
+                ("parts", ctypes.c_int16), ("one", ctypes.c_int16), ("split", ctypes.c_int16),
+                ("reserved", ctypes.c_int16 * 2)]
 
 
 class MatrixPlan(ctypes.Structure):

@@ -88,6 +88,15 @@ constexpr double kThinGrowth = 160.0;
 // 13.1, 2048 tiles 9.2 and 12.2, 4096 tiles 12.0 and 12.2.
 constexpr int kNormTiles = 2048;
 
+// A = X X^T of few block rows and a long inner dimension (blocks): each 64 x 64
+// block is a workgroup's, whose four waves take every fourth inner block.  By the
+// matrix alone, so that its sums are in one order whatever else is in the plan.
+// Against 128 x 128 tiles: 2 of 4050 x 209 13.6 us and 33.1, 1 of 512 x 4096 13.6
+// and 33.6, 6 of 500 x 2000 9.8 and 19.4, 12 of 512 x 2048 17.6 and 20.4; where
+// such tiles fill the chip it is even or behind: 24 of 384 x 1152 13.9 and 13.6,
+// 64 of 320 x 2048 39.0 and 37.3, 40 of 512 x 2048 62 and 43 (a step takes 158).
+constexpr int kSplitRows = 8, kSplitInner = 16;
+
 // Shapes of the products' tiles.
 enum TileShape : int { kTile128 = 0, kTile192 = 1, kTile256 = 2 };
 
@@ -125,6 +134,7 @@ struct NsArgs {
                                    // (i: the part, j: its first 64 columns)
     const ProdTile* full;          // tiles of X; of thin matrices X's columns in 64s (j)
     const ProdTile* blocks;        // blocks of X; of thin matrices none
+    const ProdTile* gram;          // blocks of A, where the gram is split (kSplitRows)
     int first;                     // the group's first matrix
     char* area;                    // the workspace's group area
     const NormRec* norms;
@@ -147,6 +157,7 @@ hipError_t launch_muon_update(const MatDesc* mats, const StreamTile* tiles, int 
 hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, const double* partials, double eps, NormRec* norms, int grid,
                              hipStream_t s);
 hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hipStream_t s);
+hipError_t launch_ns_gram_split(const NsArgs& g, int it, int grid, hipStream_t s);
 hipError_t launch_ns_poly(const NsArgs& g, TileShape tile, int grid, hipStream_t s);
 hipError_t launch_ns_apply(const NsArgs& g, int it, bool u_f32, NsLast last, const MuonArgs& ma, TileShape tile,
                            int grid, hipStream_t s);

@@ -473,6 +473,12 @@ struct Blocks {
 
 Blocks blocks_of(const MatDesc& d, bool sym) { return Blocks{d.kp / kPad, (sym ? d.kp : d.np) / kPad}; }
 
+// 0: the gram is a product like the others; 1: split (kSplitRows); by the matrix alone.
+int16_t split_gram(int64_t k, int64_t n)
+{
+    return k > kThin && (k + kPad - 1) / kPad <= kSplitRows && (n + kPad - 1) / kPad >= kSplitInner ? 1 : 0;
+}
+
 ProdTile tile_of(const Host& h, size_t m, int i, int j)
 {
     const MatDesc& d = h.mats[m];
@@ -573,6 +579,9 @@ zero1_status add_group(Host& h, size_t first, size_t end)
         g.n_full = add_tiles(h, first, end, kTiles[g.full_tile].side, false);
         g.blocks0 = here();
         g.n_blocks = add_tiles(h, first, end, 1, false);
+        g.split = split_gram(h.mats[first].k, h.mats[first].n);
+        g.gram0 = here();
+        if (g.split) g.n_gram = add_tiles(h, first, end, 1, true);
     }
     h.groups.push_back(g);
     return ZERO1_OK;
@@ -596,10 +605,14 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         h.elems += mats[i].rows * mats[i].cols;
         order[i] = i;
     }
-    // largest products first: the tiles that run longest are dispatched first
+    // largest products first: the tiles that run longest are dispatched first;
+    // those of a split gram behind the others, thin ones last
     auto small = [&](int i) { return std::min(mats[i].rows, mats[i].cols); };
     auto large = [&](int i) { return std::max(mats[i].rows, mats[i].cols); };
+    auto kind = [&](int i) { return small(i) <= kThin ? 2 : (int)split_gram(small(i), large(i)); };
     std::stable_sort(order.begin(), order.end(), [&](int a, int b) {
+        const int ca = kind(a), cb = kind(b);
+        if (ca != cb) return ca < cb;
         return small(a) != small(b) ? small(a) > small(b) : large(a) > large(b);
     });
     int64_t used = 0, total = 0;
@@ -653,7 +666,8 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
         }
         if (h.has & kHasU) {   // its place in a group's buffers
             int64_t to = place(d, used);
-            if (used > 0 && (to > budget || thin_rows(d.k) != thin_rows(h.mats.back().k))) {
+            if (used > 0 && (to > budget || thin_rows(d.k) != thin_rows(h.mats.back().k) ||
+                             split_gram(d.k, d.n) != split_gram(h.mats.back().k, h.mats.back().n))) {
                 if (zero1_status st = close_group(h.mats.size())) return st;
                 to = place(d, used);
             }
@@ -745,6 +759,7 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
         g.sym = list + q.sym0;
         g.full = list + q.full0;
         g.blocks = list + q.blocks0;
+        g.gram = list + q.gram0;
         if (q.thin) {
             double top = 1.0;
             for (int it = 0; it < hp->ns_steps;) {
@@ -765,7 +780,8 @@ zero1_status iterate(const zero1_matrix_plan* plan, const zero1_muon_hparams* hp
         const TileShape sym = (TileShape)q.sym_tile, full = (TileShape)q.full_tile;
         Z1_HIP(launch_ns_prepare(g, u_f32, norms_first ? nullptr : partials, hp->ns_eps, norms, q.n_blocks, s));
         for (int it = 0; it < hp->ns_steps; ++it) {
-            Z1_HIP(launch_ns_gram(g, it, sym, q.n_sym, s));
+            if (q.split) Z1_HIP(launch_ns_gram_split(g, it, q.n_gram, s));
+            else Z1_HIP(launch_ns_gram(g, it, sym, q.n_sym, s));
             Z1_HIP(launch_ns_poly(g, sym, q.n_sym, s));
             Z1_HIP(launch_ns_apply(g, it, u_f32, it + 1 == hp->ns_steps ? last : kNsMid, ma, full, q.n_full, s));
         }

@@ -448,6 +448,98 @@ void ns_sym_kernel(NsArgs g, int it)
     }
 }
 
+// A = X X^T of matrices of few block rows: a 64 x 64 block a workgroup, each wave
+// every fourth inner block through two stages of its own (nothing to wait for but
+// its own loads), the four sums joined in LDS in a fixed order.  A tile's workgroup
+// walks the inner dimension at 0.5 us a block however few there are, here it walks
+// a quarter: 2 of 4050 x 209 take 13.6 us (6 tiles of 128 x 128: 33.1).
+constexpr size_t kSplitLds = (size_t)4 * 2 * 2 * kBlock * 2;
+
+__global__ __launch_bounds__(256, 2) void ns_gram_split_kernel(NsArgs g, int it)
+{
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    constexpr int kLoads = 16;
+    const ProdTile pt = g.gram[blockIdx.x];
+    const Buffers buf = buffers(pt.at, pt.kb, pt.nb);
+    const half_t* src = reinterpret_cast<const half_t*>(g.area + (it & 1 ? buf.x1 : buf.x0));
+    half_t* dst = reinterpret_cast<half_t*>(g.area + buf.a);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const float r = it == 0 ? g.norms[pt.mat].r : 1.0f;
+    half_t* sh = reinterpret_cast<half_t*>(lds) + wave * (4 * kBlock);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) half_t*)sh;
+    const half_t* row[2] = {src + ((int64_t)pt.i * pt.nb + wave) * kBlock, src + ((int64_t)pt.j * pt.nb + wave) * kBlock};
+    const int count = (pt.nb - wave + 3) / 4;
+    auto issue = [&](int b) {
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+            load_1k(row[l >> 3] + (l & 7) * 512, lane * 16, lds0 + (b * 2 * kBlock + l * 512) * 2);
+        row[0] += 4 * kBlock;
+        row[1] += 4 * kBlock;
+    };
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
+    const int lane_row = lane & 15, key = slot_key(lane_row);
+    const int off[2] = {lane_row * kB + (((lane >> 4) ^ key) << 3), lane_row * kB + (((4 + (lane >> 4)) ^ key) << 3)};
+    if (count > 0) issue(0);
+    if (count > 1) issue(1);
+    for (int t = 0; t < count; ++t) {
+        if (t + 1 < count) stage_wait<kLoads>();   // the next stage may be under way
+        else stage_wait<0>();
+        const half_t* s = sh + (t & 1) * (2 * kBlock);
+        h8 p[2][4], q[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                p[h][x] = *reinterpret_cast<const h8*>(s + x * 16 * kB + off[h]);
+                q[h][x] = *reinterpret_cast<const h8*>(s + kBlock + x * 16 * kB + off[h]);
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before it is loaded over
+        if (t + 2 < count) issue(t & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[h][y], p[h][x], acc[x][y], 0, 0, 0);
+    }
+    __syncthreads();
+    f32x4* join = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) join[((wave * 4 + x) * 4 + y) * 64 + lane] = acc[x][y];
+    __syncthreads();
+    // each wave finishes rows 16 wave .. 16 wave + 15
+    half_t* out = reinterpret_cast<half_t*>(lds) + 4 * 2 * kBlock;   // behind the four sums
+    const float f = r * r / kNsScale;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        f32x4 z = join[((0 * 4 + wave) * 4 + y) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) z += join[((w * 4 + wave) * 4 + y) * 64 + lane];
+        *reinterpret_cast<h4*>(out + quad(wave, y)) = __builtin_convertvector(f * z, h4);
+    }
+    __syncthreads();
+    half_t* at = dst + ((int64_t)pt.i * pt.kb + pt.j) * kBlock;
+    half_t* mirror = dst + ((int64_t)pt.j * pt.kb + pt.i) * kBlock;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int slot = (threadIdx.x + 256 * h) * 8;
+        *reinterpret_cast<h8*>(at + slot) = *reinterpret_cast<const h8*>(out + slot);
+    }
+    if (pt.i != pt.j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<h8*>(mirror + (16 * wave + lane_row) * kB + (((4 * h + (lane >> 4)) ^ key) << 3)) =
+                columns(out, 32 * h, 16 * wave);
+    }
+}
+
 // The end of the last step for one block of o, staged in `out`: o as bf16, or
 // the update of the master and the parameter with it.  Rows of o are the
 // block's rows, or its columns when u is tall; four elements a lane, the loads
@@ -615,6 +707,12 @@ hipError_t launch_ns_gram(const NsArgs& g, int it, TileShape tile, int grid, hip
     if (tile == kTile128 && grid <= kFewTiles) Z1_CALL(2, 2, 1, 4);
     else Z1_TILES(tile, Z1_CALL);
 #undef Z1_CALL
+    return hipGetLastError();
+}
+
+hipError_t launch_ns_gram_split(const NsArgs& g, int it, int grid, hipStream_t s)
+{
+    ns_gram_split_kernel<<<dim3(grid), dim3(256), kSplitLds, s>>>(g, it);
     return hipGetLastError();
 }
 
