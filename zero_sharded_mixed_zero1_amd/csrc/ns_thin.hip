@@ -130,6 +130,11 @@ __device__ __forceinline__ HiLo split(float x)
 }
 
 // ------------------------------------------------------------- gram
+// The exponent of a sum of nothing but zeros: above every other, so that the least
+// of several parts' exponents is that of a part which holds something (zeros are
+// zeros at any exponent).
+constexpr int kZeros = 1000;
+
 // Partial sums of X X^T over `split` columns of X each, one workgroup a part,
 // 64 columns at a time: G times 2^2e, with the power of two 2^e that brings the
 // largest element so far to 2^13..2^14 (exact, so that neither squares of tiny
@@ -154,7 +159,7 @@ __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int
 #pragma unroll
         for (int y = 0; y < N; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
     if (threadIdx.x == 0) top = 0;
-    int e = mid ? 0 : 1000;   // 1000: nothing but zeros so far
+    int e = mid ? 0 : kZeros;
     C x;
     x.load(src, c0);
     for (int64_t j0 = c0; j0 < c1; j0 += 64) {
@@ -171,8 +176,8 @@ __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int
             __syncthreads();
             const uint32_t t = top;
             // (an infinity or a NaN makes the sum one, at any scale)
-            const int en = t == 0 ? 1000 : t < 0x7f800000u ? 13 - ilogbf(__uint_as_float(t)) : min(e, 0);
-            if (en != e && e != 1000) {
+            const int en = t == 0 ? kZeros : t < 0x7f800000u ? 13 - ilogbf(__uint_as_float(t)) : min(e, 0);
+            if (en != e && e != kZeros) {
                 const float f = ldexpf(1.0f, max(2 * (en - e), -200));
 #pragma unroll
                 for (int a = 0; a < N; ++a)
@@ -181,7 +186,7 @@ __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int
             }
             e = en;
         }
-        const int ex = e == 1000 ? 0 : e;
+        const int ex = e == kZeros ? 0 : e;
 #pragma unroll
         for (int h = 0; h < C::kRounds; ++h) {
             const int i = C::at_i(src.tall, h), j = C::at_j(src.tall, h);
@@ -236,7 +241,7 @@ __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int
             if (d.n_parts == 1 || wi + 16 * a <= wj + 16 * b)
                 *reinterpret_cast<f32x4*>(out + (wi + 16 * a + (lane & 15)) * KP + wj + 16 * b + 4 * (lane >> 4)) =
                     acc[a][b];
-    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[part] = e == 1000 ? 0 : e;
+    if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[part] = e;
 }
 
 template <typename U, int KP>
