@@ -478,7 +478,10 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
  * Types: gradients bf16; m fp32 (bf16 with ZERO1_MV_BF16); u bf16 (fp32 with
  * ZERO1_U_F32); o bf16; master fp32; param bf16.
  * Arithmetic: momentum and update, like the AdamW step, one binary32 operation
- * at a time (eta = fp32(lr) * scale is one of them).  The norm is fp64.  The
+ * at a time (eta = fp32(lr) * scale is one of them).  The norm is a sum of
+ * squares in fp64; of a matrix whose smaller side is at most 128 it is the trace
+ * of A, summed in fp32 in runs of 8192 columns of 32 parts: off by at most about
+ * 2^-14 of it, whatever the other side (an fp32 u; half of that a bf16 one).  The
  * products multiply fp16 operands on the matrix cores and add in fp32; X is
  * held as two fp16 halves (22 bits), A and B as one, and as two where the
  * smaller side is at most 128.  Before its rounding to bf16 o is within (2-norm,

@@ -6,7 +6,9 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
+import zero_sharded_mixed_zero1_amd as z
 from tests import muon_ref as ref
+from tests.gpu_util import ws_tensor
 from tests.test_gpu_muon import Steps, env  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +37,65 @@ def test_parts_of_the_gram_sum_that_hold_only_zeros(env, u_f32, size):  # noqa: 
     # nothing but zeros in every part
     for got in Steps(env, [np.zeros((100, 1000)), np.zeros((1000, 20))], u_f32).o(5, eps=1e-6 * size):
         assert (got == 0.0).all()
+
+
+def one_step(env, shape, value, u_f32):  # noqa: F811
+    """muon_step on a matrix of equal elements with coefficients (1, 0, 0): the
+    master it leaves is -u / |u|."""
+    torch, dev = env
+    g = torch.full(shape, value, dtype=torch.bfloat16, device=dev)
+    b = dict(param=torch.zeros_like(g), master=torch.zeros(shape, device=dev), m=torch.zeros(shape, device=dev),
+             u=torch.zeros(shape, dtype=torch.float32 if u_f32 else torch.bfloat16, device=dev))
+    mats = [z.matrix(*shape, **b)]
+    table = ws_tensor(torch, z.muon_table_bytes(mats), dev)
+    plan = z.muon_plan(mats, table, flags=z.U_F32 if u_f32 else 0)
+    ws = ws_tensor(torch, z.muon_workspace_bytes(plan), dev)
+    ws.fill_(0xFF)
+    hp = dict(lr=1.0, momentum=0.5, weight_decay=0.0, ns_steps=1, ns_a=1.0, ns_b=0.0, ns_c=0.0, ns_eps=0.0)
+    z.muon_step([g], 0, plan, hp, flags=z.NO_NESTEROV, ws=ws)
+    torch.cuda.synchronize()
+    return b["master"]
+
+
+@pytest.mark.parametrize("value", [1.2578125, 1.40625, 1.7109375])
+@pytest.mark.parametrize("shape,u_f32", [((1, 1 << 26), False), ((3, 1 << 22), False), ((1 << 22, 3), True),
+                                         ((100, 1 << 20), False), ((1, 300001), True)])
+def test_norm_of_long_matrices(env, shape, u_f32, value):  # noqa: F811
+    """The norm of a thin matrix is summed in fp32: parts in runs of at most 8192
+    columns, a part's runs, then the parts.  The matrix cores round once every 8
+    products (an fp32 u: three products of its halves), every addition by at most
+    2^-24 of the sum so far; the norm is off by half of what its square is.  Equal
+    elements are the worst: all roundings of a binade have the same sign.  o's own
+    arithmetic (r, two halves of X, the product with r) adds at most 8 * 2^-24."""
+    torch, _ = env
+    p = one_step(env, shape, value, u_f32)
+    n = max(shape)
+    runs = -(-n // 32 // 8192)
+    room = ((1024 * (3 if u_f32 else 1) + runs + 31) / 2 + 8) * 2.0 ** -24
+    want = 1.0 / float(np.sqrt(float(shape[0]) * shape[1]))
+    lo, hi = float(-p.max()), float(-p.min())
+    assert want * (1 - room) <= lo <= hi <= want * (1 + room), (lo / want - 1, hi / want - 1, room)
+
+
+@pytest.mark.parametrize("u_f32", [False, True])
+def test_long_matrices_of_uneven_size(env, u_f32):  # noqa: F811
+    """Parts of several runs whose sizes rise and fall by 2^100, with zeros between:
+    the runs before are scaled to the largest so far."""
+    rng = np.random.default_rng(12)
+    n = 32 * 8192 * 3 + 777
+    j = np.arange(n)
+    us = []
+    for sign in (1, -1):
+        u = rng.standard_normal((2, n)) * 2.0 ** (sign * 50 * np.cos(j / 9000.0))
+        u[:, (j // 8192) % 4 == 1] = 0.0
+        us.append(u)
+    us.append(np.where(j < n - 5000, 0.0, 1e-25) * rng.standard_normal((2, n)))
+    us.append(rng.standard_normal((n, 2)) * 1e-3)
+    t = Steps(env, us, u_f32)
+    for got, u in zip(t.o(5, eps=0.0), t.u):
+        exact = ref.iterate64(u, 5, eps=0.0)
+        assert np.linalg.norm(got - exact) <= 5e-4 * np.linalg.norm(exact), u.shape
+    us[0][1, n - 3], us[1][0, 5] = np.inf, np.nan
+    with np.errstate(invalid="ignore"):     # (the second slice of an infinity is a NaN)
+        got = Steps(env, us, u_f32).o(5, eps=0.0)
+    assert np.isnan(got[0]).all() and np.isnan(got[1]).all() and np.isfinite(got[2]).all() and np.isfinite(got[3]).all()

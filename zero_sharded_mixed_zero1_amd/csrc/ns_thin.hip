@@ -141,6 +141,16 @@ constexpr int kZeros = 1000;
 // u underflow nor those of huge u overflow); when a larger one comes, the sum
 // is scaled down to it.  The next 64 columns are loaded while these are
 // multiplied.
+//
+// The matrix cores round the sum after every 8 products, each time by up to 2^-24
+// of it and, where all are alike, to the same side: a norm of 2^26 equal elements
+// was off by 1.1e-3 when each part was one chain of fp32 additions.  So the
+// registers go into the part's sum in memory every kRun times 64 columns (2^-14 of
+// the sum in a run, 2^-24 a run); a part of up to 8192 columns does so at its end
+// only.  What one chain takes: 1 of 64 x 200000 in bf16 225 us (230), 128 x 200000
+// 393 (384), 400 of 64 x 1000 142 (141).
+constexpr int kRun = 128;
+
 template <typename U, int KP>
 __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int part, int64_t c0, int mid)
 {
@@ -159,9 +169,12 @@ __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int
 #pragma unroll
         for (int y = 0; y < N; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
     if (threadIdx.x == 0) top = 0;
-    int e = mid ? 0 : kZeros;
+    int e = mid ? 0 : kZeros, kept = kZeros;   // kept: the exponent of the sum in memory, of the runs before
+    float* out = reinterpret_cast<float*>(g.area + d.a) + (int64_t)part * KP * KP;
     C x;
     x.load(src, c0);
+    int left = kRun;     // of 64 columns, until the registers go to memory
+    bool more = false;
     for (int64_t j0 = c0; j0 < c1; j0 += 64) {
         __syncthreads();   // top is set; hi and lo have been read
         if (!mid) {
@@ -230,22 +243,33 @@ __device__ __forceinline__ void thin_gram(const NsArgs& g, const MatDesc& d, int
                     }
                 }
         }
+        if (__builtin_expect(j0 + 64 >= c1 || --left == 0, 0)) {
+            // (one of several parts: the tiles on and above the diagonal, thin_sum mirrors
+            // the sum; writing them all took 1.3 us more of 24 matrices of 100 x 1000)
+            const float f = ldexpf(1.0f, max(2 * (e - kept), -200));
+#pragma unroll
+            for (int a = 0; a < N; ++a)
+#pragma unroll
+                for (int b = 0; b < N; ++b)
+                    if (d.n_parts == 1 || wi + 16 * a <= wj + 16 * b) {
+                        f32x4* at = reinterpret_cast<f32x4*>(out + (wi + 16 * a + (lane & 15)) * KP + wj + 16 * b +
+                                                             4 * (lane >> 4));
+                        if (more) acc[a][b] += f * *at;
+                        *at = acc[a][b];
+                        acc[a][b] = f32x4{0, 0, 0, 0};
+                    }
+            kept = e;
+            left = kRun;
+            more = true;
+        }
     }
-    // (one of several parts: the tiles on and above the diagonal, thin_sum mirrors
-    // the sum; writing them all took 1.3 us more of 24 matrices of 100 x 1000)
-    float* out = reinterpret_cast<float*>(g.area + d.a) + (int64_t)part * KP * KP;
-#pragma unroll
-    for (int a = 0; a < N; ++a)
-#pragma unroll
-        for (int b = 0; b < N; ++b)
-            if (d.n_parts == 1 || wi + 16 * a <= wj + 16 * b)
-                *reinterpret_cast<f32x4*>(out + (wi + 16 * a + (lane & 15)) * KP + wj + 16 * b + 4 * (lane >> 4)) =
-                    acc[a][b];
     if (threadIdx.x == 0) reinterpret_cast<int32_t*>(g.area + d.lo)[part] = e;
 }
 
+// (two waves a SIMD, which leaves 256 registers: without it the sums go back and
+// forth between a lane's two kinds of them, 1 of 64 x 200000, fp32 u, 341 us, 303 with)
 template <typename U, int KP>
-__global__ __launch_bounds__(kThreads) void thin_gram_kernel(NsArgs g, int mid)
+__global__ __launch_bounds__(kThreads, 2) void thin_gram_kernel(NsArgs g, int mid)
 {
     const ProdTile pt = g.sym[blockIdx.x];
     thin_gram<U, KP>(g, g.mats[pt.mat], pt.i, (int64_t)pt.j * 64, mid);
