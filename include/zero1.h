@@ -481,15 +481,17 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
  * at a time (eta = fp32(lr) * scale is one of them).  The norm is a sum of
  * squares in fp64; of a matrix whose smaller side is at most 128 it is the trace
  * of A, summed in fp32 in runs of 8192 columns of 32 parts: off by at most about
- * 2^-14 of it, whatever the other side (an fp32 u; half of that a bf16 one).  The
- * products multiply fp16 operands on the matrix cores and add in fp32; X is
- * held as two fp16 halves (22 bits), A and B as one, and as two where the
- * smaller side is at most 128.  Before its rounding to bf16 o is within (2-norm,
- * default coefficients) 0.05 % of the iteration in 64 bits in up to five steps
- * where the smaller side is at most 128, else within about 0.15 % in five steps
- * and 0.3 % in eight.  An entry of a u that is small beside eps is off by up to
- * 2^-37 of its matrix's scale besides.  Results do not depend on the other
- * matrices of the plan, and a rerun gives the same bits.
+ * 2^-13 of it up to 2^28 columns.  The products multiply fp16 operands on the
+ * matrix cores and add in fp32; X is held as two fp16 halves (22 bits) but enters
+ * its products by the high one (11 bits), A and B are one half, and all are two
+ * where the smaller side is at most 128.  Before its rounding to bf16 o is within
+ * (2-norm, default coefficients, whatever the singular values) 0.15 % of
+ * the iteration in 64 bits in up to five steps and 0.25 % in eight where the smaller
+ * side is at most 128, else within 0.4 % and 1.3 %: equal singular values, and two
+ * strong ones over a tenth, are the worst found; of a few strong directions over
+ * noise it is 0.04 to 0.2 % in five steps.  An entry of a u that is small beside
+ * eps is off by up to 2^-37 of its matrix's scale besides.  Results do not depend
+ * on the other matrices of the plan, and a rerun gives the same bits.
  * Non-finite values: a matrix whose u holds an infinity or a NaN gets NaN in
  * the whole of its o (as the formulas give); the other matrices do not. */
 

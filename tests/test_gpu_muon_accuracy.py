@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 
 import zero_sharded_mixed_zero1_amd as z
+from tests import muon_formats as fmt
 from tests import muon_ref as ref
 from tests.gpu_util import ws_tensor
 from tests.test_gpu_muon import Steps, env  # noqa: F401  (a fixture)
@@ -99,3 +100,41 @@ def test_long_matrices_of_uneven_size(env, u_f32):  # noqa: F811
     with np.errstate(invalid="ignore"):     # (the second slice of an infinity is a NaN)
         got = Steps(env, us, u_f32).o(5, eps=0.0)
     assert np.isnan(got[0]).all() and np.isnan(got[1]).all() and np.isfinite(got[2]).all() and np.isfinite(got[3]).all()
+
+
+DENSE = [(129, 129), (400, 130), (150, 200), (256, 512), (200, 1217), (1100, 300), (513, 700)]
+THIN = [(5, 300), (30, 40), (65, 65), (64, 255), (300, 100), (128, 128), (100, 1001), (127, 2100)]
+
+
+@pytest.mark.parametrize("u_f32", [False, True])
+@pytest.mark.parametrize("kind", fmt.KINDS)
+def test_o_is_as_exact_as_stated(env, kind, u_f32):  # noqa: F811
+    """Within the header's figures of the iteration in 64 bits, on every path.
+
+    Of matrices that are not thin the formats' roundings (muon_formats.dense) explain
+    it in up to five steps, but for the fp32 sums.  Where these differ by their order,
+    an entry of A, B or X within 2^-24 sqrt(n) of a border of fp16's steps (2^-11) is
+    rounded to the other side, one in some hundred, by a step of which the others are
+    off by 1/sqrt(12) in the mean square: a third more at most.  And X itself is off
+    by the sums of B X (k/8 additions, each rounding by at most 2^-24 of a partial
+    sum, |b s^2 + c s^4| < 3 of X; of either sign, so their squares add) and by the
+    epilogue's own operations (a X and the last sum, within 8 * 2^-24 of X).  Like
+    every rounding of X that is a direction X did not have, which the steps after it
+    multiply by a = 3.44 each; X is within 1.8 times o in size.  In eight steps this
+    alone may reach 2 %, so there the stated figure is all that is asked."""
+    rng = np.random.default_rng(41)
+    t = Steps(env, [fmt.spectrum(rng, s, kind) for s in DENSE + THIN], u_f32)
+    worst = {}
+    for steps in (1, 5, 6, 8):
+        for got, u in zip(t.o(steps), t.u):
+            exact = ref.iterate64(u, steps)
+            size = np.linalg.norm(exact)
+            off = np.linalg.norm(got - exact) / size
+            assert off <= fmt.stated(u.shape, steps), (u.shape, steps, off)
+            if min(u.shape) > 128 and steps <= 5:
+                formats = np.linalg.norm(fmt.dense(u, steps) - exact) / size
+                sums = 1.8 * 2.0 ** -24 * (3 * np.sqrt(min(u.shape) / 8) + 8) * sum(ref.A ** j for j in range(steps))
+                assert off <= 4 / 3 * formats + sums, (u.shape, steps, off, formats, sums)
+            key = (min(u.shape) <= 128, steps)
+            worst[key] = max(worst.get(key, 0.0), off)
+    print(kind, "fp32" if u_f32 else "bf16", {("thin " if k[0] else "dense ") + str(k[1]): f"{v:.2e}" for k, v in worst.items()})

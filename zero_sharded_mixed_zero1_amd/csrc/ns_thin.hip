@@ -18,7 +18,8 @@
 // sixth step is off by 0.1 to 0.7 %, an eighth by more.)  The products keep the
 // order of their factors: taking Q A Q as Q Q A, or reading P or T transposed,
 // is the same only for factors that commute exactly, and is off by up to 9e-3
-// after five steps, where this is off by up to 2e-4.
+// after five steps, where this is off by up to 2e-4 (2-norm, singular values 1/i);
+// the worst spectrum found, five decades of them, by 9e-4, in eight steps by 2e-3.
 //
 // Measured, five steps: 64 x 64 20.5 us (one launch); 24 of 100 x 1000 79 us: gram
 // 14, the parts' sum 5, poly 51, apply 13.
