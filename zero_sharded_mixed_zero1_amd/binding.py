@@ -480,9 +480,10 @@ def _muon_hp(hp) -> MuonHParams:
 
 
 def muon_scalars_derive(hp) -> MuonScalars:
-    """The per-step scalars the Muon calls derive from hp (zero1_muon_scalars_derive)."""
+    """The per-step scalars the Muon calls derive from hp (zero1_muon_scalars_derive);
+    its device_scalars is ignored."""
     out = MuonScalars()
-    h = _muon_hp(hp)
+    h = _muon_hp(hp if isinstance(hp, MuonHParams) else {k: v for k, v in hp.items() if k != "device_scalars"})
     _check(lib().zero1_muon_scalars_derive(ctypes.byref(h), ctypes.byref(out)))
     return out
 
