@@ -449,7 +449,7 @@ int64_t place(MatDesc& d, int64_t at)
         d.kp = thin;
         d.n_parts = thin <= 64 && d.n <= kThinOne ? 1 : (int32_t)std::min<int64_t>(kThinMaxParts, (d.n + 127) / 128);
         d.split = (int32_t)round_up64((d.n + d.n_parts - 1) / d.n_parts, kPad);
-        d.n_parts = (d.n + d.split - 1) / d.split;
+        d.n_parts = (int32_t)(((int64_t)d.n + d.split - 1) / d.split);
         d.x[0] = at;
         d.lo = d.x[0] + round_up64((int64_t)d.k * d.np * 4, 256);
         d.a = d.lo + 256;
@@ -603,6 +603,7 @@ zero1_status build(const zero1_matrix* mats, int n, Host& h)
     for (int i = 0; i < n; ++i) {
         if (zero1_status st = check_shape(mats[i], i, h.has)) return st;
         h.elems += mats[i].rows * mats[i].cols;
+        if (h.elems > kMaxTiles * 4 * kQuadsPerTile) return fail(ZERO1_EINVAL, "too many elements in one plan");
         order[i] = i;
     }
     // largest products first: the tiles that run longest are dispatched first;
