@@ -461,7 +461,12 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
 
 /* ---------------------------------------------------------------- Muon
  * The Muon step on weight matrices that this rank owns whole (the embedding,
- * the head, gains and biases take the AdamW step above).  Per matrix, with g
+ * the head, gains and biases take the AdamW step above; its plan tiles one
+ * contiguous run of the shard, so the matrices lie before or behind the run, or
+ * between two runs with a plan and a `begin` each, and the shard is cut at
+ * tensors' borders.  The entry of rank_sumsq is the sum of all runs' sums of
+ * squares: zero1_mta_reduce for AdamW's, zero1_shard_reduce for the matrices',
+ * zero1_partials_sum).  Per matrix, with g
  * the replicas' reduced gradient:
  *   1. momentum       m = mu m + g;  u = g + mu m                (zero1_muon_momentum)
  *   2. orthogonalise  X = u / (||u||_F + eps);  ns_steps times
