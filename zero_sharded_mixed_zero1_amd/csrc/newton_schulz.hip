@@ -157,7 +157,9 @@ struct Tile {
 
 // One wave copies 1 KiB from memory to LDS: lane l its 16 bytes at base +
 // 16 l, to lds + 16 l.  No register receives the data; whoever reads it waits
-// (stage_wait) first.
+// (stage_wait) first.  The compiler does not know that m0 is written (it reserves
+// m0 and takes no such clobber), so nothing else in this file's kernels may use it:
+// a test reads their assembly for that.
 __device__ __forceinline__ void load_1k(const half_t* base, uint32_t lane_off, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
