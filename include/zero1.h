@@ -269,7 +269,8 @@ zero1_status zero1_adamw_step(const float* g, const uint16_t* const* grads,
  *   [0, shard_len) exactly, in any order; no two buffers overlap), cuts them
  *   into chunks and copies the table into `table` (device, 256-byte aligned,
  *   table_bytes long).  Synchronous: call once per tensor-list layout and
- *   reuse the plan for every step.  `flags` may hold ZERO1_MV_BF16.
+ *   reuse the plan for every step.  Not ordered behind work queued on any
+ *   stream: nothing queued may still use the table's memory.  `flags` may hold ZERO1_MV_BF16.
  * zero1_mta_workspace_bytes: step workspace for this plan and W.
  * zero1_mta_reduce: steps 1-2 for this rank: reduces the shard's gradient
  *   slices (grads, W, begin as for zero1_shard_reduce) and writes this rank's
@@ -579,7 +580,8 @@ zero1_status zero1_muon_scalars_derive(const zero1_muon_hparams* hp, zero1_muon_
  * zero1_muon_plan: validates the matrices (sizes, strides, no two buffers
  *   sharing an element; blocks of columns of one array are told apart by their
  *   common stride) and copies the table into `table` (device, 256-byte
- *   aligned).  Synchronous, once per list.  `flags`: ZERO1_MV_BF16, ZERO1_U_F32;
+ *   aligned).  Synchronous, once per list; not ordered behind work queued on any
+ *   stream, so nothing queued may still use that memory.  `flags`: ZERO1_MV_BF16, ZERO1_U_F32;
  *   they hold for every call with the plan, whatever these calls' flags say.
  *   Up to 2^37 elements a plan; two calls that overlap on the device need
  *   workspaces of their own, and so do two captured graphs.

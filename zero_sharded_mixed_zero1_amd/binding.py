@@ -261,6 +261,16 @@ def _ws(ws, ws_bytes):
     return _addr(ws), (ws_bytes if ws_bytes is not None else _nbytes(ws))
 
 
+def _table(table, table_bytes):
+    """A plan's table, into which the plan call copies at once: a tensor may be
+    memory that kernels queued on its device's current stream still write (torch
+    reuses freed memory in stream order), so these end first."""
+    if getattr(table, "is_cuda", False):
+        import torch
+        torch.cuda.current_stream(table.device).synchronize()
+    return _ws(table, table_bytes)
+
+
 def _hp(hp) -> HParams:
     """From an HParams, or a dict with lr, beta1, beta2, eps, weight_decay,
     max_norm, step and optionally device_scalars (a device address or tensor
@@ -347,7 +357,7 @@ def mta_plan(pieces, table, table_bytes=None, flags: int = 0) -> Plan:
     """pieces: Piece structs or tuples (numel, shard_offset, param_bf16, master, m, v)."""
     arr = _pieces(pieces)
     plan = Plan()
-    t, tb = _ws(table, table_bytes)
+    t, tb = _table(table, table_bytes)
     _check(lib().zero1_mta_plan(arr, len(arr), flags, t, tb, ctypes.byref(plan)))
     return plan
 
@@ -500,7 +510,7 @@ def muon_plan(mats, table, table_bytes=None, flags: int = 0) -> MatrixPlan:
     """mats: Matrix structs (see matrix())."""
     arr = _matrices(mats)
     plan = MatrixPlan()
-    t, tb = _ws(table, table_bytes)
+    t, tb = _table(table, table_bytes)
     _check(lib().zero1_muon_plan(arr, len(arr), flags, t, tb, ctypes.byref(plan)))
     return plan
 
