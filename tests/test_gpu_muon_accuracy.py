@@ -138,3 +138,43 @@ def test_o_is_as_exact_as_stated(env, kind, u_f32):  # noqa: F811
             key = (min(u.shape) <= 128, steps)
             worst[key] = max(worst.get(key, 0.0), off)
     print(kind, "fp32" if u_f32 else "bf16", {("thin " if k[0] else "dense ") + str(k[1]): f"{v:.2e}" for k, v in worst.items()})
+
+
+@pytest.mark.parametrize("u_f32", [False, True])
+@pytest.mark.parametrize("shape", [(130, 170), (300, 1100), (2200, 2100)])
+def test_ends_of_the_range_of_matrices_that_are_not_thin(env, shape, u_f32):  # noqa: F811
+    """Sizes whose squares fp32 does not hold, zeros, infinities and NaNs, on the
+    paths of k > 128 (a gram of tiles and a split one; norms in prepare and in a
+    launch of their own): a NaN takes its own matrix only."""
+    torch, dev = env
+    rng = np.random.default_rng(19)
+    base = rng.standard_normal(shape).astype(np.float32)
+    us = [base, base * np.float32(1e36), base * np.float32(1e-36), np.zeros_like(base), base.copy(), base.copy(), base]
+    us[4][-1, -1], us[5][0, 7] = np.inf, np.nan
+    if shape[0] > 2000:
+        us = us[1:6]
+    bf = [torch.from_numpy(ref.bf16(u).reshape(shape).view(np.int16)).to(dev).view(torch.bfloat16) for u in us]
+    u = [x.float() if u_f32 else x for x in bf]
+    o = [torch.full(shape, 7.0, dtype=torch.bfloat16, device=dev) for _ in us]
+    mats = [z.matrix(*shape, u=a, o=b) for a, b in zip(u, o)]
+    table = ws_tensor(torch, z.muon_table_bytes(mats), dev)
+    plan = z.muon_plan(mats, table, flags=z.U_F32 if u_f32 else 0)
+    ws = ws_tensor(torch, z.muon_workspace_bytes(plan), dev)
+    ws.fill_(0xFF)
+    z.orthogonalize(plan, dict(lr=0.0, momentum=0.0, weight_decay=0.0, ns_eps=0.0), ws=ws)
+    torch.cuda.synchronize()
+    for a, b in zip(u, o):
+        x = a.double()
+        if not bool((x != 0).any()) or not bool(torch.isfinite(x).all()):     # 0 / 0; the formulas' NaN
+            assert bool(torch.isnan(b).all())
+            continue
+        x = x / torch.linalg.vector_norm(x)
+        x = x.T.contiguous() if shape[0] > shape[1] else x
+        for _ in range(5):
+            s = x @ x.T
+            x = ref.A * x + (ref.B * s + ref.C * (s @ s)) @ x
+        x = x.T if shape[0] > shape[1] else x
+        off = float(torch.linalg.vector_norm(b.double() - x) / torch.linalg.vector_norm(x))
+        assert off <= fmt.stated(shape, 5) + ref.BF16, off      # (and the rounding to bf16)
+    if shape[0] < 2000:
+        assert torch.equal(o[0], o[-1])
