@@ -554,7 +554,7 @@ typedef struct zero1_muon_hparams {
     double lr;              /* >= 0                                             */
     double momentum;        /* in [0, 1)                                        */
     double weight_decay;    /* >= 0                                             */
-    double max_norm;        /* > 0; read where rank_sumsq is given              */
+    double max_norm;        /* > 0 (+inf too); clips where rank_sumsq is given  */
     double ns_a, ns_b, ns_c;/* coefficients, e.g. 3.4445, -4.7750, 2.0315       */
     double ns_eps;          /* >= 0, added to the norm, e.g. 1e-7               */
     int32_t ns_steps;       /* 1..64, e.g. 5                                    */
@@ -584,20 +584,24 @@ zero1_status zero1_muon_scalars_derive(const zero1_muon_hparams* hp, zero1_muon_
  *   stream, so nothing queued may still use that memory.  `flags`: ZERO1_MV_BF16, ZERO1_U_F32;
  *   they hold for every call with the plan, whatever these calls' flags say.
  *   Up to 2^37 elements a plan; two calls that overlap on the device need
- *   workspaces of their own, and so do two captured graphs.
+ *   matrices (and so plans) and workspaces of their own, and so do two captured
+ *   graphs.
  * zero1_muon_workspace_bytes: workspace of zero1_orthogonalize and
  *   zero1_muon_step (256-byte aligned): the iteration's buffers of one group of
  *   matrices at a time (about 512 MiB, or one matrix where it needs more) and
  *   the norms.  Every byte is written before it is read.
  * zero1_muon_momentum: grads, W, begin as for zero1_shard_reduce: element (i, j)
  *   of a matrix has its gradients at grads[w][begin + shard_offset + i*ld + j].
+ *   The gradients must not overlap the plan's buffers.
  *   flags: ZERO1_SUM_ONLY, ZERO1_G_BF16, ZERO1_CLIP_EPS, ZERO1_NO_NESTEROV.
  *   rank_sumsq: n_ranks doubles as for zero1_adamw_step (g is clipped by the
  *   global norm and info_out written), or NULL: no clipping (info_out NULL).
  * zero1_orthogonalize: o from u.  ZERO1_EINVAL for coefficients that let
  *   singular values grow beyond 3 or B's eigenvalues beyond 12 (the range of
  *   the fp16 operands).
- * zero1_muon_update: flags: ZERO1_DECAY_FIRST (p = p*decay - lr scale o).
+ * zero1_muon_update: flags: ZERO1_DECAY_FIRST (p = p*decay - lr scale o, the
+ *   order in which Muon is usually given; without it the decay also takes lr *
+ *   weight_decay of the update, as in this library's AdamW).
  * zero1_muon_step: the three together; o is not rounded to bf16 on its way to
  *   the update and not written; u is. */
 size_t zero1_muon_table_bytes(const zero1_matrix* mats, int n_mats);

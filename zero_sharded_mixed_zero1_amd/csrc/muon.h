@@ -39,9 +39,9 @@ struct MatDesc {
     int32_t tile0, n_tiles;        // its streaming tiles
     int32_t split, n_parts;        // thin: columns a part of the gram sum, parts
     int32_t reserved;
-    // byte offsets inside the workspace's group area: X (twice, its low halves,
-    // A and B follow, see Buffers); of a thin matrix fp32 X, the parts'
-    // exponents, the parts, P
+    // byte offsets inside the workspace's group area: of a thin matrix fp32 X, the
+    // parts' exponents, the parts, P; of others X (twice), its low halves, A and B,
+    // which the kernels form from x[0] (Buffers): the plans' test reads them here
     int64_t x[2], lo, a, b;
 };
 static_assert(sizeof(MatDesc) == 192, "matrix descriptor layout");

@@ -329,8 +329,10 @@ constexpr int64_t kGroupBytes = (int64_t)512 << 20;
 // Tile shapes (by TileShape) and what they take, in us: `start` a round of
 // tiles for its first loads and its epilogue, then for every 64 of the inner
 // dimension `one` where a tile has the chip to itself and `all` where every
-// slot holds one (the chip's clock falls with the load).  Measured on MI355X in
-// one session (shorter epilogues have taken 1 to 2 us off every entry since):
+// slot holds one (the chip's clock falls with the load).  For the whole chip of 256
+// CUs: on a part of it the results are the same and the choice may be slower.
+// Measured on MI355X in one session (shorter epilogues have taken 1 to 2 us off
+// every entry since):
 //   matrix        product (inner)  128 x 128   192 x 192   256 x 256
 //   4096 x 11008  gram (11008)        257 us      202 us      232 us
 //                 poly (4096)         101          84          97

@@ -690,7 +690,7 @@ hipError_t launch_ns_prepare(const NsArgs& g, bool u_f32, const double* partials
     return hipGetLastError();
 }
 
-constexpr int kFewTiles = 256;   // as many as CUs
+constexpr int kFewTiles = 256;   // as many as the whole chip has CUs
 
 #define Z1_TILES(tile, CALL)                              \
     do {                                                  \

@@ -1,5 +1,5 @@
 // ns_thin.hip -- orthogonalisation of thin matrices (k = min(rows, cols) up to
-// 128) on gfx950, in one to four launches however many steps there are.
+// 128) on gfx950, in one to four launches a segment of steps (five default ones).
 //
 // A step multiplies X from the left by Q = a I + b A + c A A, a polynomial of
 // A = X X^T, and A becomes Q A Q.  So the steps need X only through A, which is
