@@ -93,9 +93,10 @@ def test_long_matrices_of_uneven_size(env, u_f32):  # noqa: F811
     us.append(np.where(j < n - 5000, 0.0, 1e-25) * rng.standard_normal((2, n)))
     us.append(rng.standard_normal((n, 2)) * 1e-3)
     t = Steps(env, us, u_f32)
-    for got, u in zip(t.o(5, eps=0.0), t.u):
-        exact = ref.iterate64(u, 5, eps=0.0)
-        assert np.linalg.norm(got - exact) <= 5e-4 * np.linalg.norm(exact), u.shape
+    for steps in (5, 8):        # (eight: a second segment, whose X comes from the workspace)
+        for got, u in zip(t.o(steps, eps=0.0), t.u):
+            exact = ref.iterate64(u, steps, eps=0.0)
+            assert np.linalg.norm(got - exact) <= fmt.stated(u.shape, steps) * np.linalg.norm(exact), (u.shape, steps)
     us[0][1, n - 3], us[1][0, 5] = np.inf, np.nan
     with np.errstate(invalid="ignore"):     # (the second slice of an infinity is a NaN)
         got = Steps(env, us, u_f32).o(5, eps=0.0)
