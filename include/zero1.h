@@ -13,6 +13,7 @@
  *   5. bf16      the forward-pass parameter is the nearest-even bf16 of the
  *                new master                                          (3-5: zero1_adamw_step)
  *   1-5 fused over a ragged per-tensor list: zero1_mta_plan + zero1_mta_step.
+ * The moments may be held in 8 bits (ZERO1_MV_8BIT, zero1_state8_encode).
  * Beside AdamW, for weight matrices that a rank owns whole: the Muon step
  * (momentum, orthogonalisation by Newton-Schulz products, update), at the end
  * of this header.
@@ -96,6 +97,13 @@ typedef enum zero1_status {
                                     re-reading the slices), else RECOMPUTE_G.     */
 /* 0x10u is unused (rejected as an unknown flag). */
 
+/* m and v are stored in 8 bits: each buffer is one of zero1_state8_bytes(numel)
+ * bytes, 16-byte aligned (the layout and the rounding: zero1_state8_encode); zero
+ * bytes before the first step.  Exclusive with ZERO1_MV_BF16.  A step takes 2W + 18
+ * bytes a parameter of a W = 1..4 step's 2W + 30 with fp32 moments, and the state is
+ * 6 bytes of 12. */
+#define ZERO1_MV_8BIT      0x2000u
+
 /* Compatibility variants (not the pages' step; off by default):
  *   ZERO1_DECAY_FIRST  decay the master before the Adam update, the order
  *                      "并行训练" ("一张卡上装了什么：混合精度与 AdamW") attributes to
@@ -165,8 +173,8 @@ typedef struct zero1_piece {
     int64_t shard_offset;   /* position of its first element inside the shard   */
     uint16_t* param_bf16;   /* numel bf16, written                              */
     float* master;          /* numel fp32, read and written                     */
-    void* m;                /* numel fp32 (bf16 with ZERO1_MV_BF16), r/w        */
-    void* v;                /* numel fp32 (bf16 with ZERO1_MV_BF16), r/w        */
+    void* m;                /* numel fp32 (bf16 with ZERO1_MV_BF16, or an 8-bit */
+    void* v;                /* buffer with ZERO1_MV_8BIT), read and written     */
 } zero1_piece;
 
 /* A validated piece list uploaded into device memory by zero1_mta_plan.
@@ -177,7 +185,7 @@ typedef struct zero1_plan {
     int32_t n_pieces;
     int32_t n_chunks;
     int32_t chunk_elems;    /* elements per chunk (pieces are cut into chunks)  */
-    uint32_t flags;         /* ZERO1_MV_BF16 as given to zero1_mta_plan          */
+    uint32_t flags;         /* ZERO1_MV_BF16, ZERO1_MV_8BIT as given to zero1_mta_plan */
     int32_t aligned;        /* 1 when every piece allows 16-byte vector access  */
     int32_t reserved;
 } zero1_plan;
@@ -236,13 +244,14 @@ zero1_status zero1_grad_norm(const float* g, int64_t len, double* sumsq_out,
  *               grads/W/begin (same arithmetic as zero1_shard_reduce).
  *   grads,W,begin  as for zero1_shard_reduce; ignored when g != NULL.
  *   master      len fp32, updated in place.
- *   m, v        len fp32 (or bf16 with ZERO1_MV_BF16), updated in place;
+ *   m, v        len fp32 (or bf16 with ZERO1_MV_BF16, or 8-bit buffers with
+ *               ZERO1_MV_8BIT), updated in place;
  *               zero before the first step.
  *   param_bf16  len bf16 outputs: nearest-even bf16 of the new master.
  *   hp          (host) hyper-parameters; hp->step is t (or hp->device_scalars).
  *   rank_sumsq  n_ranks doubles: every rank's partial sum of squares (this
  *               rank's included), added in rank order for the global norm.
- *   flags       ZERO1_MV_BF16; ZERO1_SUM_ONLY and ZERO1_G_BF16 (with g == NULL);
+ *   flags       ZERO1_MV_BF16, ZERO1_MV_8BIT; ZERO1_SUM_ONLY and ZERO1_G_BF16 (with g == NULL);
  *               ZERO1_DECAY_FIRST, ZERO1_CLIP_EPS (compatibility variants).
  *   info_out    one zero1_norm_info (device) or NULL; written even when len == 0.
  * Needs no workspace: every workgroup forms the norm from rank_sumsq itself.
@@ -270,7 +279,8 @@ zero1_status zero1_adamw_step(const float* g, const uint16_t* const* grads,
  *   into chunks and copies the table into `table` (device, 256-byte aligned,
  *   table_bytes long).  Synchronous: call once per tensor-list layout and
  *   reuse the plan for every step.  Not ordered behind work queued on any
- *   stream: nothing queued may still use the table's memory.  `flags` may hold ZERO1_MV_BF16.
+ *   stream: nothing queued may still use the table's memory.  `flags` may hold ZERO1_MV_BF16
+ *   or ZERO1_MV_8BIT.
  * zero1_mta_workspace_bytes: step workspace for this plan and W.
  * zero1_mta_reduce: steps 1-2 for this rank: reduces the shard's gradient
  *   slices (grads, W, begin as for zero1_shard_reduce) and writes this rank's
@@ -289,7 +299,7 @@ zero1_status zero1_adamw_step(const float* g, const uint16_t* const* grads,
  *   flags: ZERO1_STORE_G or ZERO1_RECOMPUTE_G (neither:
  *   the library picks, see zero1_mta_design), ZERO1_SUM_ONLY and the
  *   compatibility variants ZERO1_DECAY_FIRST, ZERO1_CLIP_EPS, ZERO1_G_BF16
- *   (ZERO1_MV_BF16 comes from the plan).
+ *   (ZERO1_MV_BF16 and ZERO1_MV_8BIT come from the plan).
  * Every design gives bit-identical master, m, v and params for the same
  * clip coefficient; this rank's fp64 partial depends on the launch shape
  * only in its last bits (different fixed summation trees). */
@@ -424,7 +434,8 @@ zero1_status zero1_time_next_launch(void* start_event, void* stop_event);
  * each (grad_offset = 0, grad_elems = S for buffers that hold only the shard;
  * the shard's begin and N for full replicas); the flat bf16 parameter buffer
  * of param_elems elements with the shard starting at param_offset; flags:
- * ZERO1_MV_BF16 (2-byte m, v) and the design (ZERO1_STORE_G, ZERO1_RECOMPUTE_G,
+ * ZERO1_MV_BF16 (2-byte m, v) or ZERO1_MV_8BIT (one 8-bit buffer of shard_len
+ * elements each) and the design (ZERO1_STORE_G, ZERO1_RECOMPUTE_G,
  * or neither for the one zero1_mta_step picks); capacity: the largest arena
  * the caller can allocate.
  *
@@ -459,6 +470,51 @@ typedef struct zero1_arena_layout {
 #define ZERO1_ARENA_SPACING ((size_t)40 << 30)   /* preferred spacing D */
 
 zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout* out);
+
+/* ---------------------------------------------------------------- 8-bit moments
+ * Moments held in 8 bits take the same step (ZERO1_MV_8BIT): the codes are
+ * widened to fp32, the fp32 step runs on them, the master takes the unrounded m
+ * and v, and these are rounded back.
+ *
+ * Layout of a buffer of n elements (zero1_state8_bytes(n) bytes): n codes, one a
+ * byte; from the next multiple of 16 on, one 32-bit word for each block of 256
+ * consecutive elements (the last may be short).  Blocks count from the piece's first
+ * element.  Bits 0-7 of a word are an exponent byte b (0 only in a block never written), bits 8-31
+ * count the block's roundings.  A code is e4m3 (OCP: sign, 4 bits of exponent, 3
+ * of mantissa) and stands for e4m3(code) * 2^(b-127): of m the value, of v the
+ * square root r (v = r * r in fp32).  b brings the block's largest finite
+ * magnitude into [2^7, 2^8) (b >= 1).  A value that is infinite or NaN is held as
+ * NaN; magnitudes over 240 * 2^120 (3e38) as that, and roots over 240 * 2^56.
+ * A buffer of zero bytes is all zeros.  Buffers are plain data: copy them to save
+ * and restore a state exactly.
+ *
+ * Rounding.  The step rounds a magnitude x, in units of its code's step, to
+ * floor(x + u / 65536), with u 16 random bits: right on average, so that changes far
+ * below a step add up over the steps instead of being lost each time.  A root that is
+ * not zero is held as at least the smallest step.  u are the low (m) and high
+ * (r) halves of mix(mix(mix(s) + c) + j): s the low 32 bits of the block's
+ * first element's place in the shard, c the count in the word of m's block, j the element's
+ * place in its block, all modulo 2^32, with mix(x): x = (x ^ x >> 16) *
+ * 0x6A09E667; x = (x ^ x >> 15) * 0xBB67AE85; x ^ x >> 16.  A step adds 1 to both
+ * words' counts (modulo 2^24).  The same state and gradients give the same bits,
+ * eager or replayed.
+ * Held in 8 bits a value is off by up to 1/8 of itself after a step (at most a code's
+ * distance), 1/16 after zero1_state8_encode, down to 2^-13 of the block's largest; below
+ * that by up to 2^-16 of the largest.
+ *
+ * zero1_state8_bytes: bytes of a buffer of n elements (0 for n <= 0).
+ * zero1_state8_encode: x (n fp32, or bf16 with ZERO1_MV_BF16; any alignment of
+ *   its element) to codes, to the nearest, ties to even, and counts of 0.
+ *   which: ZERO1_STATE_M, or ZERO1_STATE_V for x >= 0 held by its root (a
+ *   negative x: NaN).
+ * zero1_state8_decode: what the buffer stands for, to fp32 (exact but for
+ *   the square's rounding) or bf16 (nearest even) with ZERO1_MV_BF16. */
+#define ZERO1_STATE_M 0
+#define ZERO1_STATE_V 1
+
+size_t zero1_state8_bytes(int64_t n);
+zero1_status zero1_state8_encode(const void* x, int64_t n, void* state, int which, uint32_t flags, void* stream);
+zero1_status zero1_state8_decode(const void* state, int64_t n, void* x, int which, uint32_t flags, void* stream);
 
 /* ---------------------------------------------------------------- Muon
  * The Muon step on weight matrices that this rank owns whole (the embedding,

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 from dataclasses import dataclass, field
 
-from .binding import MV_BF16, ArenaLayout, arena_plan
+from .binding import MV_8BIT, MV_BF16, ArenaLayout, arena_plan, state8_bytes
 
 ALIGN = 2 << 20   # the planner's offsets assume a 2 MiB-aligned base
 
@@ -20,7 +20,8 @@ class Arena:
     base: int                  # offset of that base inside `storage`
     ws: object                 # uint8 [layout.ws_bytes]: the step's workspace
     master: object             # float32 [shard_len]
-    m: object                  # float32 [shard_len], or int16 holding bf16 with MV_BF16
+    m: object                  # float32 [shard_len], or int16 holding bf16 with MV_BF16,
+                               # or uint8 [state8_bytes(shard_len)] with MV_8BIT
     v: object                  # likewise
     params: object             # int16 [param_elems]: the flat bf16 parameter buffer
     grads: list = field(default_factory=list)   # W x int16 [grad_elems]: the gradient buffers
@@ -34,7 +35,7 @@ def arena_tensors(shard_len: int, W: int, grad_elems: int, grad_offset: int, par
     The arguments are zero1_arena_plan's: shard_len elements in the shard, W
     gradient buffers of grad_elems bf16 elements with the shard at grad_offset,
     a parameter buffer of param_elems bf16 elements with the shard at
-    param_offset, flags MV_BF16 and the design (STORE_G, RECOMPUTE_G, or
+    param_offset, flags MV_BF16 or MV_8BIT and the design (STORE_G, RECOMPUTE_G, or
     neither for the one zero1_mta_step picks: pass the same flags to the step).
     capacity: the largest arena to allocate; by default the device's free
     memory less `reserve` bytes.  The views are uninitialised.
@@ -55,7 +56,8 @@ def arena_tensors(shard_len: int, W: int, grad_elems: int, grad_offset: int, par
         nbytes = n * torch.empty((), dtype=dt).element_size()
         return storage[base + off:base + off + nbytes].view(dt)
 
-    mvdt = torch.int16 if flags & MV_BF16 else torch.float32
+    mvdt = torch.uint8 if flags & MV_8BIT else torch.int16 if flags & MV_BF16 else torch.float32
+    mvn = state8_bytes(shard_len) if flags & MV_8BIT else shard_len
     return Arena(storage, L, base, view(L.ws, L.ws_bytes, torch.uint8), view(L.master, shard_len, torch.float32),
-                 view(L.m, shard_len, mvdt), view(L.v, shard_len, mvdt), view(L.params, param_elems, torch.int16),
+                 view(L.m, mvn, mvdt), view(L.v, mvn, mvdt), view(L.params, param_elems, torch.int16),
                  [view(L.grads[w], grad_elems, torch.int16) for w in range(W)])

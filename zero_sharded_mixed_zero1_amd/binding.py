@@ -24,6 +24,8 @@ CLIP_EPS = 0x40
 G_BF16 = 0x80
 U_F32 = 0x200
 NO_NESTEROV = 0x400
+MV_8BIT = 0x2000
+STATE_M, STATE_V = 0, 1
 MAX_W = 128
 STATIC_MAX_G_ELEMS = 16777216
 # the layout of the structures below and the signatures set in lib(); a
@@ -190,6 +192,12 @@ def lib():
         L.zero1_step_scalars_derive.restype = i32
         L.zero1_arena_plan.argtypes = [ctypes.POINTER(ArenaRequest), ctypes.POINTER(ArenaLayout)]
         L.zero1_arena_plan.restype = i32
+        L.zero1_state8_bytes.argtypes = [i64]
+        L.zero1_state8_bytes.restype = szt
+        L.zero1_state8_encode.argtypes = [P, i64, P, i32, u32, P]
+        L.zero1_state8_encode.restype = i32
+        L.zero1_state8_decode.argtypes = [P, i64, P, i32, u32, P]
+        L.zero1_state8_decode.restype = i32
         L.zero1_time_next_launch.argtypes = [P, P]
         L.zero1_time_next_launch.restype = i32
         L.zero1_muon_scalars_derive.argtypes = [ctypes.POINTER(MuonHParams), ctypes.POINTER(MuonScalars)]
@@ -430,6 +438,22 @@ def arena_plan(shard_len: int, W: int, grad_elems: int, grad_offset: int, param_
     out = ArenaLayout()
     _check(lib().zero1_arena_plan(ctypes.byref(req), ctypes.byref(out)))
     return out
+
+
+# ------------------------------------------------------------------ 8-bit moments
+def state8_bytes(n: int) -> int:
+    """Bytes of one moment of n elements in 8 bits (zero1_state8_bytes)."""
+    return lib().zero1_state8_bytes(n)
+
+
+def state8_encode(x, n: int, state, which: int, flags: int = 0, stream=None):
+    """n values of fp32 (bf16 with MV_BF16) into an 8-bit buffer; which: STATE_M or STATE_V."""
+    _check(lib().zero1_state8_encode(_addr(x), n, _addr(state), which, flags, _stream(stream)))
+
+
+def state8_decode(state, n: int, x, which: int, flags: int = 0, stream=None):
+    """What an 8-bit buffer of n elements stands for, as fp32 (bf16 with MV_BF16)."""
+    _check(lib().zero1_state8_decode(_addr(state), n, _addr(x), which, flags, _stream(stream)))
 
 
 def _event(e) -> int:

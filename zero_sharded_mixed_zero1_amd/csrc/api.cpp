@@ -18,6 +18,7 @@
 
 #include "../../include/zero1.h"
 #include "internal.h"
+#include "state8.h"
 
 using namespace z1;
 
@@ -214,7 +215,7 @@ zero1_status check_grads(const uint16_t* const* grads, int W, int64_t begin, int
 }
 
 constexpr uint32_t kAllFlags = ZERO1_SUM_ONLY | ZERO1_MV_BF16 | ZERO1_RECOMPUTE_G | ZERO1_STORE_G |
-                               ZERO1_DECAY_FIRST | ZERO1_CLIP_EPS | ZERO1_G_BF16;
+                               ZERO1_DECAY_FIRST | ZERO1_CLIP_EPS | ZERO1_G_BF16 | ZERO1_MV_8BIT;
 
 zero1_status check_flags(uint32_t flags, uint32_t allowed, const char* fn)
 {
@@ -222,6 +223,18 @@ zero1_status check_flags(uint32_t flags, uint32_t allowed, const char* fn)
     if (flags & ~allowed) return fail(ZERO1_EINVAL, "%s: flags 0x%x do not apply here", fn, flags & ~allowed);
     return ZERO1_OK;
 }
+
+// How the flags say m and v are stored.
+MvKind mv_kind(uint32_t flags) { return flags & ZERO1_MV_8BIT ? kMv8 : flags & ZERO1_MV_BF16 ? kMvBf16 : kMvF32; }
+
+zero1_status check_mv(uint32_t flags, const char* fn)
+{
+    if ((flags & ZERO1_MV_BF16) && (flags & ZERO1_MV_8BIT))
+        return fail(ZERO1_EINVAL, "%s: ZERO1_MV_BF16 and ZERO1_MV_8BIT are exclusive", fn);
+    return ZERO1_OK;
+}
+
+size_t mv_bytes(MvKind mv, int64_t n) { return mv == kMv8 ? state8_size(n) : (size_t)n * (mv == kMvBf16 ? 2 : 4); }
 
 zero1_status check_hparam_values(const zero1_hparams* hp);
 
@@ -421,7 +434,8 @@ zero1_status zero1_adamw_step(const float* g, const uint16_t* const* grads, int 
     if (len < 0) return fail(ZERO1_EINVAL, "len=%lld is negative", (long long)len);
     if (n_ranks < 1) return fail(ZERO1_EINVAL, "n_ranks=%d must be >= 1", n_ranks);
     if (!rank_sumsq) return fail(ZERO1_EINVAL, "rank_sumsq is NULL");
-    const bool mv_bf16 = (flags & ZERO1_MV_BF16) != 0;
+    if ((st = check_mv(flags, "zero1_adamw_step"))) return st;
+    const MvKind mv = mv_kind(flags);
     Reduce r;
     std::memset(&r, 0, sizeof r);
     bool vec = true;
@@ -432,13 +446,15 @@ zero1_status zero1_adamw_step(const float* g, const uint16_t* const* grads, int 
     }
     if (len > 0 && (!master || !m || !v || !param_bf16))
         return fail(ZERO1_EINVAL, "master, m, v and param_bf16 must be non-NULL");
-    const size_t mvb = mv_bf16 ? 2 : 4;
+    if (mv == kMv8 && len > 0 && (!aligned16(m) || !aligned16(v)))
+        return fail(ZERO1_EINVAL, "8-bit m and v must be 16-byte aligned");
+    const size_t mvn = mv_bytes(mv, len);
     if (!aligned16(master) || !aligned16(m) || !aligned16(v) || !aligned16(param_bf16)) vec = false;
     if (len > 0) {
         std::vector<Range> rg = {
             {(uintptr_t)master, (uintptr_t)master + 4 * (size_t)len, "master", 0},
-            {(uintptr_t)m, (uintptr_t)m + mvb * (size_t)len, "m", 0},
-            {(uintptr_t)v, (uintptr_t)v + mvb * (size_t)len, "v", 0},
+            {(uintptr_t)m, (uintptr_t)m + mvn, "m", 0},
+            {(uintptr_t)v, (uintptr_t)v + mvn, "v", 0},
             {(uintptr_t)param_bf16, (uintptr_t)param_bf16 + 2 * (size_t)len, "param_bf16", 0}};
         if (g) rg.push_back({(uintptr_t)g, (uintptr_t)g + 4 * (size_t)len, "g", 0});
         if ((st = check_disjoint(rg))) return st;
@@ -450,7 +466,7 @@ zero1_status zero1_adamw_step(const float* g, const uint16_t* const* grads, int 
     const Scal sc = scalars(hp, flags);
     const Shape sh = update_shape(tiles(len, vec), d);
     const int nb = sh.grid;
-    Z1_HIP(launch_adamw_flat(g, r, len, vec, mv_bf16, master, m, v, param_bf16, sc, rank_sumsq, n_ranks,
+    Z1_HIP(launch_adamw_flat(g, r, len, vec, mv, master, m, v, param_bf16, sc, rank_sumsq, n_ranks,
                              hp->max_norm, (flags & ZERO1_CLIP_EPS) ? 1 : 0,
                              reinterpret_cast<NormInfo*>(info_out), nb, sh.split, s));
     return finish(s);
@@ -476,7 +492,8 @@ zero1_status zero1_mta_plan(const zero1_piece* pieces, int n_pieces, uint32_t fl
     if (zero1_status fs = check_flags(flags, kAllFlags, "zero1_mta_plan")) return fs;
     if (!plan_out) return fail(ZERO1_EINVAL, "plan_out is NULL");
     if (!pieces || n_pieces < 1) return fail(ZERO1_EINVAL, "need at least one piece");
-    const bool mv_bf16 = (flags & ZERO1_MV_BF16) != 0;
+    if (zero1_status ms = check_mv(flags, "zero1_mta_plan")) return ms;
+    const MvKind mv = mv_kind(flags);
     std::vector<int> order(n_pieces);
     for (int i = 0; i < n_pieces; ++i) {
         const zero1_piece& p = pieces[i];
@@ -496,17 +513,18 @@ zero1_status zero1_mta_plan(const zero1_piece* pieces, int n_pieces, uint32_t fl
                         order[k], (long long)p.shard_offset, (long long)pos);
         pos += p.numel;
     }
-    const size_t mvb = mv_bf16 ? 2 : 4;
     std::vector<Range> rg;
     rg.reserve(4 * (size_t)n_pieces);
     bool aligned = true;
     for (int i = 0; i < n_pieces; ++i) {
         const zero1_piece& p = pieces[i];
-        const size_t n = (size_t)p.numel;
+        const size_t n = (size_t)p.numel, mvn = mv_bytes(mv, p.numel);
+        if (mv == kMv8 && (!aligned16(p.m) || !aligned16(p.v)))
+            return fail(ZERO1_EINVAL, "piece %d: 8-bit m and v must be 16-byte aligned", i);
         rg.push_back({(uintptr_t)p.param_bf16, (uintptr_t)p.param_bf16 + 2 * n, "param_bf16", i});
         rg.push_back({(uintptr_t)p.master, (uintptr_t)p.master + 4 * n, "master", i});
-        rg.push_back({(uintptr_t)p.m, (uintptr_t)p.m + mvb * n, "m", i});
-        rg.push_back({(uintptr_t)p.v, (uintptr_t)p.v + mvb * n, "v", i});
+        rg.push_back({(uintptr_t)p.m, (uintptr_t)p.m + mvn, "m", i});
+        rg.push_back({(uintptr_t)p.v, (uintptr_t)p.v + mvn, "v", i});
         if (p.shard_offset % kVec || !aligned16(p.param_bf16) || !aligned16(p.master) || !aligned16(p.m) ||
             !aligned16(p.v))
             aligned = false;
@@ -541,7 +559,7 @@ zero1_status zero1_mta_plan(const zero1_piece* pieces, int n_pieces, uint32_t fl
     plan_out->n_pieces = n_pieces;
     plan_out->n_chunks = (int32_t)nc;
     plan_out->chunk_elems = (int32_t)chunk;
-    plan_out->flags = flags & ZERO1_MV_BF16;
+    plan_out->flags = flags & (ZERO1_MV_BF16 | ZERO1_MV_8BIT);
     plan_out->aligned = aligned ? 1 : 0;
     plan_out->reserved = 0;
     return ok();
@@ -661,7 +679,7 @@ zero1_status zero1_mta_update(const uint16_t* const* grads, int W, int64_t begin
     const ChunkDesc* cd = reinterpret_cast<const ChunkDesc*>(tb + round_up(sizeof(PieceDesc) * plan->n_pieces, 256));
     const Shape sh = update_shape(plan->n_chunks, d);
     const int nb = sh.grid;
-    Z1_HIP(launch_adamw_mta(w.g, r, pd, cd, plan->n_chunks, vec, (plan->flags & ZERO1_MV_BF16) != 0, scalars(hp, flags),
+    Z1_HIP(launch_adamw_mta(w.g, r, pd, cd, plan->n_chunks, vec, mv_kind(plan->flags), scalars(hp, flags),
                             rank_sumsq, n_ranks, hp->max_norm, (flags & ZERO1_CLIP_EPS) ? 1 : 0,
                             reinterpret_cast<NormInfo*>(info_out), nb, sh.split, s));
     return finish(s);
@@ -720,6 +738,51 @@ zero1_status zero1_step_scalars_derive(const zero1_hparams* hp, zero1_step_scala
     return ok();
 }
 
+// ------------------------------------------------------------------ 8-bit moments
+size_t zero1_state8_bytes(int64_t n) { return state8_size(n); }
+
+// Shared checks of the two conversions.
+static zero1_status state8_common(const char* fn, const void* x, int64_t n, const void* state, int which, uint32_t flags,
+                                  DevInfo& d)
+{
+    if (zero1_status fs = check_flags(flags, kAllFlags, fn)) return fs;
+    if (n < 0 || n > (int64_t)1 << 40) return fail(ZERO1_EINVAL, "%s: n=%lld must be in [0, 2^40]", fn, (long long)n);
+    if (which != ZERO1_STATE_M && which != ZERO1_STATE_V)
+        return fail(ZERO1_EINVAL, "%s: which=%d must be ZERO1_STATE_M or ZERO1_STATE_V", fn, which);
+    if (n > 0) {
+        if (!x || !state) return fail(ZERO1_EINVAL, "%s: NULL buffer", fn);
+        const size_t xb = flags & ZERO1_MV_BF16 ? 2 : 4;
+        if (reinterpret_cast<uintptr_t>(x) % xb) return fail(ZERO1_EINVAL, "%s: x must be aligned to its elements", fn);
+        if (!aligned16(state)) return fail(ZERO1_EINVAL, "%s: the 8-bit buffer must be 16-byte aligned", fn);
+        std::vector<Range> rg = {{(uintptr_t)x, (uintptr_t)x + xb * (size_t)n, "x", 0},
+                                 {(uintptr_t)state, (uintptr_t)state + state8_size(n), "state", 0}};
+        if (zero1_status st = check_disjoint(rg)) return st;
+    }
+    return current_device(d);
+}
+
+zero1_status zero1_state8_encode(const void* x, int64_t n, void* state, int which, uint32_t flags, void* stream)
+{
+    DevInfo d;
+    if (zero1_status st = state8_common("zero1_state8_encode", x, n, state, which, flags, d)) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (n > 0)
+        Z1_HIP(launch_state8_encode(x, n, flags & ZERO1_MV_BF16, which == ZERO1_STATE_V, state,
+                                    grid_for(tiles(n, true), d, kReducePerCu), s));
+    return finish(s);
+}
+
+zero1_status zero1_state8_decode(const void* state, int64_t n, void* x, int which, uint32_t flags, void* stream)
+{
+    DevInfo d;
+    if (zero1_status st = state8_common("zero1_state8_decode", x, n, state, which, flags, d)) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (n > 0)
+        Z1_HIP(launch_state8_decode(state, n, flags & ZERO1_MV_BF16, which == ZERO1_STATE_V, x,
+                                    grid_for(tiles(n, true), d, kReducePerCu), s));
+    return finish(s);
+}
+
 zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout* out)
 {
     if (!req || !out) return fail(ZERO1_EINVAL, "request or layout is NULL");
@@ -738,7 +801,8 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
     const size_t unit = (size_t)2 << 20;
     const size_t S = (size_t)q.shard_len;
     const bool store_g = use_store_g(q.flags, q.W);
-    const size_t mvb = (q.flags & ZERO1_MV_BF16) ? 2 : 4;
+    if (zero1_status ms = check_mv(q.flags, "zero1_arena_plan")) return ms;
+    const size_t mvn = mv_bytes(mv_kind(q.flags), q.shard_len);
     const size_t ws_bytes = zero1_workspace_bytes(q.shard_len, q.W, store_g ? ZERO1_STORE_G : 0);
     const size_t grad_bytes = round_up((size_t)q.grad_elems * 2, unit);
 
@@ -747,8 +811,8 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
     const Slot slot[5] = {
         store_g ? Slot{0, ws_bytes} : Slot{(size_t)q.grad_offset * 2, (size_t)(q.grad_elems - q.grad_offset) * 2},
         {0, S * 4},
-        {0, S * mvb},
-        {0, S * mvb},
+        {0, mvn},
+        {0, mvn},
         {(size_t)q.param_offset * 2, (size_t)(q.param_elems - q.param_offset) * 2},
     };
     const size_t base = round_up(slot[0].before, unit);   // shard start of slot 0

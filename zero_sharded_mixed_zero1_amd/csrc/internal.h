@@ -60,6 +60,9 @@ struct Scal {
     const StepScal* dev;    // non-null: read b1..delta and max_norm from here at run time
 };
 
+// How m and v are stored (8 bits: state8.h).
+enum MvKind : int { kMvF32 = 0, kMvBf16 = 1, kMv8 = 2 };
+
 // How the W-slice sum becomes g: keep it, multiply by the exact 2^-k (W a
 // power of two: identical to dividing), or divide by W.
 enum AvgMode : int { kAvgNone = 0, kAvgMulPow2 = 1, kAvgDiv = 2 };
@@ -130,15 +133,20 @@ hipError_t launch_finalize(const double* partials, int nblocks, double* q_out, h
 // order) and the clip decision for max_norm; workgroup 0 writes it to info_out.
 // clip_eps selects the torch clip convention (max_norm / (norm + 1e-6) < 1).
 hipError_t launch_adamw_flat(const float* g, const Reduce& r, int64_t len, bool vec,
-                             bool mv_bf16, float* master, void* m, void* v,
+                             int mv, float* master, void* m, void* v,
                              uint16_t* param, const Scal& sc, const double* rank_sumsq,
                              int n_ranks, double max_norm, int clip_eps, NormInfo* info_out,
                              int nblocks, int split, hipStream_t s);
 // Phase 2 over a multi-tensor plan (same prologue).
 hipError_t launch_adamw_mta(const float* g, const Reduce& r, const PieceDesc* pieces,
                             const ChunkDesc* chunks, int n_chunks, bool vec,
-                            bool mv_bf16, const Scal& sc, const double* rank_sumsq,
+                            int mv, const Scal& sc, const double* rank_sumsq,
                             int n_ranks, double max_norm, int clip_eps, NormInfo* info_out,
                             int nblocks, int split, hipStream_t s);
+
+// ---- moments in 8 bits from and to fp32 or bf16 (state8.hip).  v: x holds v, the
+// codes its root.
+hipError_t launch_state8_encode(const void* x, int64_t n, bool bf16, bool v, void* state, int nblocks, hipStream_t s);
+hipError_t launch_state8_decode(const void* state, int64_t n, bool bf16, bool v, void* x, int nblocks, hipStream_t s);
 
 }  // namespace z1

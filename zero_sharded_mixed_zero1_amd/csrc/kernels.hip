@@ -43,6 +43,7 @@
 #include <tuple>
 
 #include "internal.h"
+#include "state8.h"
 
 #pragma clang fp contract(off)
 
@@ -540,11 +541,13 @@ __device__ __forceinline__ void block_clip(const ClipArgs& ca, bool& clip, float
 // One element of AdamW: m = b1 m + a1 g, v = b2 v + a2 (g g), then the
 // master moves by sigma m / (sqrt(v) + eps) and is multiplied by the decay
 // factor (decay after the move; decay_first swaps the two).
-__device__ __forceinline__ void adamw_elem(float g, float& p, float& m, float& v, const Scal& c)
+// Returns the root of the new v.
+__device__ __forceinline__ float adamw_elem(float g, float& p, float& m, float& v, const Scal& c)
 {
     const float mn = c.b1 * m + c.a1 * g;
     const float vn = c.b2 * v + c.a2 * (g * g);
-    const float d = sqrtf(vn) + c.eps;
+    const float r = sqrtf(vn);
+    const float d = r + c.eps;
     const float q = mn / d;
     float pn;
     if (c.decay_first) {   // compatibility variant: decay, then update
@@ -557,6 +560,7 @@ __device__ __forceinline__ void adamw_elem(float g, float& p, float& m, float& v
     m = mn;
     v = vn;
     p = pn;
+    return r;
 }
 
 // Where the update finds its arrays: g (fp32 buffer; unused when the gradient
@@ -567,16 +571,128 @@ struct Span {
     void* m;
     void* v;
     uint16_t* param;
+    // 8-bit moments: the words of the span's blocks, and the low 32 bits of the
+    // shard position of its first element
+    uint32_t* mw;
+    uint32_t* vw;
+    uint32_t first;
 };
 
+// Moments in 8 bits (state8.h), the lane's 8 elements of a full tile at state
+// index si: a wave's first quads are one block, its second quads the next.
+typedef uint32_t u32x2w __attribute__((ext_vector_type(2), aligned(4)));
+
+__device__ __forceinline__ void update8_bytes(const Span& sp, int64_t si, const float (&gv)[8], const Scal& c,
+                                              bool clip, float coef)
+{
+    using namespace dev8;
+    const int a = quad_a(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    uint8_t* mp = static_cast<uint8_t*>(sp.m) + si + a;
+    uint8_t* vp = static_cast<uint8_t*>(sp.v) + si + a;
+    const int64_t blk = (si >> 8) + 2 * wave;
+    float p[8];
+    ld8_f32(sp.master + si, p);
+    uint32_t mc[2], vc[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        mc[h] = ld_nt(reinterpret_cast<const uint32_t*>(mp + 256 * h));
+        vc[h] = ld_nt(reinterpret_cast<const uint32_t*>(vp + 256 * h));
+    }
+    const u32x2 mw = ld_nt(reinterpret_cast<const u32x2w*>(sp.mw + blk));
+    const u32x2 vw = ld_nt(reinterpret_cast<const u32x2w*>(sp.vw + blk));
+    u32x2 mwn, vwn;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float m[4], r[4], v[4];
+        decode4(mc[h], scale8(mw[h]), m);
+        decode4(vc[h], scale8(vw[h]), r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float g = clip ? gv[4 * h + j] * coef : gv[4 * h + j];
+            v[j] = r[j] * r[j];
+            r[j] = adamw_elem(g, p[4 * h + j], m[j], v[j], c);
+        }
+        const Top8 tm = top8<false>(m), tr = top8<true>(r);
+        const float im = inverse8(tm.b), ir = inverse8(tr.b);
+        const uint32_t key = key8(sp.first + (uint32_t)si + 512u * wave + 256u * h, mw[h] >> 8) + 4u * (threadIdx.x & 63);
+        uint32_t cm = 0, cr = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t bits = mix32(key + j);
+            cm |= code_m(m[j], im, bits, tm) << (8 * j);
+            cr |= code_r(r[j], ir, bits, tr) << (8 * j);
+        }
+        st_nt(reinterpret_cast<uint32_t*>(mp + 256 * h), cm);
+        st_nt(reinterpret_cast<uint32_t*>(vp + 256 * h), cr);
+        mwn[h] = next_word(mw[h], tm.b);
+        vwn[h] = next_word(vw[h], tr.b);
+    }
+    st8_f32(sp.master + si, p);
+    st8_bf16(sp.param + si, p);
+    if ((threadIdx.x & 63) == 0) {
+        st_nt(reinterpret_cast<u32x2w*>(sp.mw + blk), mwn);
+        st_nt(reinterpret_cast<u32x2w*>(sp.vw + blk), vwn);
+    }
+}
+
+// The same of n <= kTile elements at any alignment: a wave takes a block, lane l
+// its elements l, l + 64, l + 128 and l + 192.  g: the element's gradient by its
+// place in the tile.
+template <typename G>
+__device__ __forceinline__ void update_blocks(const Span& sp, int64_t si, int n, const Scal& c, bool clip, float coef,
+                                              G g)
+{
+    using namespace dev8;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    uint8_t* mp = static_cast<uint8_t*>(sp.m) + si;
+    uint8_t* vp = static_cast<uint8_t*>(sp.v) + si;
+    for (int k = wave; k * kBlock8 < n; k += kThreads / 64) {
+        const int64_t blk = (si >> 8) + k;
+        const uint32_t mw = sp.mw[blk], vw = sp.vw[blk];
+        const float ms = scale8(mw), rs = scale8(vw);
+        float m[4], r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = k * kBlock8 + lane + 64 * i;
+            m[i] = r[i] = 0.0f;
+            if (j < n) {
+                float p = ld_nt(sp.master + si + j);
+                m[i] = __builtin_amdgcn_cvt_f32_fp8(mp[j], 0) * ms;
+                r[i] = __builtin_amdgcn_cvt_f32_fp8(vp[j], 0) * rs;
+                float gj = g(j), v = r[i] * r[i];
+                if (clip) gj = gj * coef;
+                r[i] = adamw_elem(gj, p, m[i], v, c);
+                st_nt(sp.master + si + j, p);
+                st_nt(sp.param + si + j, (uint16_t)bf16_rne_bits(p));
+            }
+        }
+        const Top8 tm = top8<false>(m), tr = top8<true>(r);
+        const float im = inverse8(tm.b), ir = inverse8(tr.b);
+        const uint32_t key = key8(sp.first + (uint32_t)si + (uint32_t)(k * kBlock8), mw >> 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = k * kBlock8 + lane + 64 * i;
+            const uint32_t bits = mix32(key + lane + 64 * i);
+            if (j < n) {
+                mp[j] = (uint8_t)code_m(m[i], im, bits, tm);
+                vp[j] = (uint8_t)code_r(r[i], ir, bits, tr);
+            }
+        }
+        if (lane == 0) {
+            sp.mw[blk] = next_word(mw, tm.b);
+            sp.vw[blk] = next_word(vw, tr.b);
+        }
+    }
+}
+
 // The lane's 8 elements of a full tile at state index si, given their g.
-template <bool MVBF16>
+template <int MV>
 __device__ __forceinline__ void update8(const Span& sp, int64_t si, const float (&gv)[8], const Scal& c, bool clip,
                                         float coef)
 {
     float p[8], m[8], v[8];
     ld8_f32(sp.master + si, p);
-    if constexpr (MVBF16) {
+    if constexpr (MV == kMvBf16) {
         ld8_bf16(static_cast<const uint16_t*>(sp.m) + si, m);
         ld8_bf16(static_cast<const uint16_t*>(sp.v) + si, v);
     } else {
@@ -589,7 +705,7 @@ __device__ __forceinline__ void update8(const Span& sp, int64_t si, const float 
         adamw_elem(gj, p[j], m[j], v[j], c);
     }
     st8_f32(sp.master + si, p);
-    if constexpr (MVBF16) {
+    if constexpr (MV == kMvBf16) {
         st8_bf16(static_cast<uint16_t*>(sp.m) + si, m);
         st8_bf16(static_cast<uint16_t*>(sp.v) + si, v);
     } else {
@@ -600,12 +716,12 @@ __device__ __forceinline__ void update8(const Span& sp, int64_t si, const float 
 }
 
 // One element at state index si, given its g.
-template <bool MVBF16>
+template <int MV>
 __device__ __forceinline__ void update1(const Span& sp, int64_t si, float gj, const Scal& c, bool clip, float coef)
 {
     if (clip) gj = gj * coef;
     float p = ld_nt(sp.master + si), m, v;
-    if constexpr (MVBF16) {
+    if constexpr (MV == kMvBf16) {
         m = bf16_to_f32(ld_nt(static_cast<const uint16_t*>(sp.m) + si));
         v = bf16_to_f32(ld_nt(static_cast<const uint16_t*>(sp.v) + si));
     } else {
@@ -614,7 +730,7 @@ __device__ __forceinline__ void update1(const Span& sp, int64_t si, float gj, co
     }
     adamw_elem(gj, p, m, v, c);
     st_nt(sp.master + si, p);
-    if constexpr (MVBF16) {
+    if constexpr (MV == kMvBf16) {
         st_nt(static_cast<uint16_t*>(sp.m) + si, (uint16_t)bf16_rne_bits(m));
         st_nt(static_cast<uint16_t*>(sp.v) + si, (uint16_t)bf16_rne_bits(v));
     } else {
@@ -626,7 +742,7 @@ __device__ __forceinline__ void update1(const Span& sp, int64_t si, float gj, co
 
 // One tile [0, n) of a span (n <= kTile), g at shard index gi, state at si:
 // vector path when the whole tile is present (and VEC), element path otherwise.
-template <bool VEC, int GSRC, bool MVBF16>
+template <bool VEC, int GSRC, int MV>
 __device__ __forceinline__ void update_tile(const Span& sp, const Reduce& r, int64_t gi, int64_t si, int n,
                                             const Scal& c, bool clip, float coef)
 {
@@ -634,16 +750,20 @@ __device__ __forceinline__ void update_tile(const Span& sp, const Reduce& r, int
         float gv[8];
         if constexpr (GSRC == 0) ld8_g(sp.g + gi, gv);
         else reduce8(r, gi, gv);
-        update8<MVBF16>(sp, si, gv, c, clip, coef);
+        if constexpr (MV == kMv8) update8_bytes(sp, si, gv, c, clip, coef);
+        else update8<MV>(sp, si, gv, c, clip, coef);
+    } else if constexpr (MV == kMv8) {
+        update_blocks(sp, si, n, c, clip, coef,
+                      [&](int j) { return (GSRC == 0) ? ld_g(sp.g + gi + j) : reduce1(r, gi + j); });
     } else {
         for (int j = threadIdx.x; j < n; j += kThreads) {
             const float gj = (GSRC == 0) ? ld_g(sp.g + gi + j) : reduce1(r, gi + j);
-            update1<MVBF16>(sp, si + j, gj, c, clip, coef);
+            update1<MV>(sp, si + j, gj, c, clip, coef);
         }
     }
 }
 
-template <bool VEC, int GSRC, bool MVBF16>
+template <bool VEC, int GSRC, int MV>
 __global__ __launch_bounds__(kThreads) void adamw_flat_kernel(Span sp, Reduce r, int64_t len, Scal c,
                                                               ClipArgs ca, int split)
 {
@@ -656,25 +776,31 @@ __global__ __launch_bounds__(kThreads) void adamw_flat_kernel(Span sp, Reduce r,
     for (int64_t t = u.lo; t < u.hi; t += u.step) {
         const int64_t base = t * kTile;
         const int n = (int)(len - base < kTile ? len - base : kTile);
-        update_tile<VEC, GSRC, MVBF16>(sp, r, base, base, n, c, clip, coef);
+        update_tile<VEC, GSRC, MV>(sp, r, base, base, n, c, clip, coef);
     }
 }
 
 // Span of one chunk's piece, starting at the chunk.
-template <bool MVBF16>
+template <int MV>
 __device__ __forceinline__ Span chunk_span(const PieceDesc& pc, const ChunkDesc& ch)
 {
-    const size_t mvb = MVBF16 ? 2 : 4;
+    const size_t mvb = MV == kMvF32 ? 4 : MV == kMvBf16 ? 2 : 1;
     Span sp;
     sp.g = nullptr;
     sp.master = pc.master + ch.offset;
     sp.m = static_cast<char*>(pc.m) + mvb * ch.offset;
     sp.v = static_cast<char*>(pc.v) + mvb * ch.offset;
     sp.param = pc.param + ch.offset;
+    if constexpr (MV == kMv8) {   // (chunks begin at blocks)
+        const size_t words = state8_words_at(pc.numel) + 4 * (size_t)(ch.offset / kBlock8);
+        sp.mw = reinterpret_cast<uint32_t*>(static_cast<char*>(pc.m) + words);
+        sp.vw = reinterpret_cast<uint32_t*>(static_cast<char*>(pc.v) + words);
+        sp.first = (uint32_t)(pc.shard_offset + ch.offset);
+    }
     return sp;
 }
 
-template <bool VEC, int GSRC, bool MVBF16>
+template <bool VEC, int GSRC, int MV>
 __global__ __launch_bounds__(kThreads) void adamw_mta_kernel(const float* __restrict__ g, Reduce r,
                                                              const PieceDesc* __restrict__ pieces,
                                                              const ChunkDesc* __restrict__ chunks,
@@ -688,12 +814,12 @@ __global__ __launch_bounds__(kThreads) void adamw_mta_kernel(const float* __rest
     for (int64_t k = u.lo; k < u.hi; k += u.step) {
         const ChunkDesc ch = chunks[k];
         const PieceDesc pc = pieces[ch.piece];
-        Span sp = chunk_span<MVBF16>(pc, ch);
+        Span sp = chunk_span<MV>(pc, ch);
         sp.g = g;
         const int64_t g0 = pc.shard_offset + ch.offset;
         for (int sub = 0; sub < ch.len; sub += kTile) {
             const int n = ch.len - sub < kTile ? ch.len - sub : kTile;
-            update_tile<VEC, GSRC, MVBF16>(sp, r, g0 + sub, sub, n, c, clip, coef);
+            update_tile<VEC, GSRC, MV>(sp, r, g0 + sub, sub, n, c, clip, coef);
         }
     }
 }
@@ -786,30 +912,39 @@ hipError_t launch_finalize(const double* partials, int nblocks, double* q_out, h
     return run(finalize_kernel, dim3(1), s, partials, nblocks, q_out);
 }
 
-hipError_t launch_adamw_flat(const float* g, const Reduce& r, int64_t len, bool vec, bool mv_bf16,
+hipError_t launch_adamw_flat(const float* g, const Reduce& r, int64_t len, bool vec, int mv,
                              float* master, void* m, void* v, uint16_t* param, const Scal& sc,
                              const double* rank_sumsq, int n_ranks, double max_norm, int clip_eps,
                              NormInfo* info_out, int nblocks, int split, hipStream_t s)
 {
     const dim3 grid(nblocks);
     const ClipArgs ca{rank_sumsq, n_ranks, max_norm, clip_eps, info_out};
-    const Span sp{g, master, m, v, param};
+    Span sp{g, master, m, v, param, nullptr, nullptr, 0};
+    if (mv == kMv8 && len > 0) {
+        sp.mw = reinterpret_cast<uint32_t*>(static_cast<char*>(m) + state8_words_at(len));
+        sp.vw = reinterpret_cast<uint32_t*>(static_cast<char*>(v) + state8_words_at(len));
+    }
     hipError_t e;
 #define Z1_FLAT(V, GS, MV) e = run(adamw_flat_kernel<V, GS, MV>, grid, s, sp, r, len, sc, ca, split)
     const int gs = g ? 0 : 1;
+#define Z1_FLAT_MV(V, GS)                                \
+    do {                                               \
+        if (mv == kMv8) Z1_FLAT(V, GS, kMv8);          \
+        else if (mv == kMvBf16) Z1_FLAT(V, GS, kMvBf16); \
+        else Z1_FLAT(V, GS, kMvF32);                   \
+    } while (0)
     if (vec) {
-        if (gs == 0) { if (mv_bf16) Z1_FLAT(true, 0, true); else Z1_FLAT(true, 0, false); }
-        else         { if (mv_bf16) Z1_FLAT(true, 1, true); else Z1_FLAT(true, 1, false); }
+        if (gs == 0) Z1_FLAT_MV(true, 0); else Z1_FLAT_MV(true, 1);
     } else {
-        if (gs == 0) { if (mv_bf16) Z1_FLAT(false, 0, true); else Z1_FLAT(false, 0, false); }
-        else         { if (mv_bf16) Z1_FLAT(false, 1, true); else Z1_FLAT(false, 1, false); }
+        if (gs == 0) Z1_FLAT_MV(false, 0); else Z1_FLAT_MV(false, 1);
     }
+#undef Z1_FLAT_MV
 #undef Z1_FLAT
     return e;
 }
 
 hipError_t launch_adamw_mta(const float* g, const Reduce& r, const PieceDesc* pieces, const ChunkDesc* chunks,
-                            int n_chunks, bool vec, bool mv_bf16, const Scal& sc, const double* rank_sumsq,
+                            int n_chunks, bool vec, int mv, const Scal& sc, const double* rank_sumsq,
                             int n_ranks, double max_norm, int clip_eps, NormInfo* info_out, int nblocks,
                             int split, hipStream_t s)
 {
@@ -818,13 +953,18 @@ hipError_t launch_adamw_mta(const float* g, const Reduce& r, const PieceDesc* pi
     hipError_t e;
 #define Z1_MTA(V, GS, MV) e = run(adamw_mta_kernel<V, GS, MV>, grid, s, g, r, pieces, chunks, n_chunks, sc, ca, split)
     const int gs = g ? 0 : 1;
+#define Z1_MTA_MV(V, GS)                                \
+    do {                                               \
+        if (mv == kMv8) Z1_MTA(V, GS, kMv8);          \
+        else if (mv == kMvBf16) Z1_MTA(V, GS, kMvBf16); \
+        else Z1_MTA(V, GS, kMvF32);                   \
+    } while (0)
     if (vec) {
-        if (gs == 0) { if (mv_bf16) Z1_MTA(true, 0, true); else Z1_MTA(true, 0, false); }
-        else         { if (mv_bf16) Z1_MTA(true, 1, true); else Z1_MTA(true, 1, false); }
+        if (gs == 0) Z1_MTA_MV(true, 0); else Z1_MTA_MV(true, 1);
     } else {
-        if (gs == 0) { if (mv_bf16) Z1_MTA(false, 0, true); else Z1_MTA(false, 0, false); }
-        else         { if (mv_bf16) Z1_MTA(false, 1, true); else Z1_MTA(false, 1, false); }
+        if (gs == 0) Z1_MTA_MV(false, 0); else Z1_MTA_MV(false, 1);
     }
+#undef Z1_MTA_MV
 #undef Z1_MTA
     return e;
 }
