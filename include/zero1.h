@@ -14,6 +14,9 @@
  *                new master                                          (3-5: zero1_adamw_step)
  *   1-5 fused over a ragged per-tensor list: zero1_mta_plan + zero1_mta_step.
  * The moments may be held in 8 bits (ZERO1_MV_8BIT, zero1_state8_encode).
+ * For forward and backward passes in 8-bit floating point: the weights' copies,
+ * activations and gradients with a scale for each block of 128, and their products
+ * (zero1_f8_quantize, zero1_f8_product).
  * Beside AdamW, for weight matrices that a rank owns whole: the Muon step
  * (momentum, orthogonalisation by Newton-Schulz products, update), at the end
  * of this header.
@@ -515,6 +518,60 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
 size_t zero1_state8_bytes(int64_t n);
 zero1_status zero1_state8_encode(const void* x, int64_t n, void* state, int which, uint32_t flags, void* stream);
 zero1_status zero1_state8_decode(const void* state, int64_t n, void* x, int which, uint32_t flags, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit matrices
+ * Forward and backward passes in 8-bit floating point around the step: weights
+ * from the bf16 parameters (or the fp32 master) that it writes, activations and
+ * their gradients, each with a scale for each block of 128 along the axis that a
+ * product sums over; and the products, whose bf16 output may be a replica's
+ * gradient buffer that the step reduces.  With W [n, k] a layer's weight, X
+ * [tokens, k] its input and dY [tokens, n] its output's gradient:
+ *   forward        Y  = product(quantize(X),  quantize(W))
+ *   input's        dX = product(quantize(dY), quantize(W)'s transpose)
+ *   weight's       dW = product(quantize(dY)'s transpose, quantize(X)'s transpose)
+ * With blocks of 128 x 128 W and its transpose hold the same values.
+ *
+ * A matrix: rows x cols codes, e4m3 (OCP; e5m2 with ZERO1_E5M2), row i from
+ * codes + i * ld; its columns up to the next multiple of 128 are there too
+ * and hold zeros (zero1_f8_quantize writes them).  The code of (i, k) stands for
+ * itself times 2^(scales[(i / block_rows) * ld_scales + k / 128] - 127).  The scale
+ * byte 255 stands for NaN. */
+#define ZERO1_F32          0x10000u /* src (quantize), d (product) are fp32, else bf16 */
+#define ZERO1_E5M2         0x20000u /* zero1_f8_matrix.flags: codes are e5m2          */
+
+typedef struct zero1_f8_matrix {
+    int64_t rows, cols;     /* >= 0; rows < 2^31 - 255, cols <= 2^23             */
+    int64_t ld;             /* bytes; a multiple of 16, >= cols rounded up to 128, <= 2^24;
+                               0: cols rounded up to 128                         */
+    int64_t ld_scales;      /* bytes; a multiple of 4, >= the blocks of a row; 0: these
+                               rounded up to 4                                   */
+    uint8_t* codes;         /* 16-byte aligned                                   */
+    uint8_t* scales;        /* 4-byte aligned                                    */
+    int32_t block_rows;     /* 1 or 128                                          */
+    uint32_t flags;         /* ZERO1_E5M2                                        */
+} zero1_f8_matrix;
+
+/* zero1_f8_quantize: src (rows x cols, bf16 or fp32 with ZERO1_F32, row stride ld
+ *   elements, 0: cols) into q (rows x cols) and its transpose into qt (cols x rows);
+ *   either may be NULL.  A block's scale is the least power of two (b >= 1) that
+ *   brings its largest finite magnitude to at most the format's largest, 448 or
+ *   57344; codes are to the nearest, ties to even: off by at most 2^-4 (e5m2: 2^-3)
+ *   of the value or 2^-17 (2^-31) of the block's largest (where b > 1).
+ *   NaN stays NaN; an infinity becomes NaN in e4m3 and stays one in e5m2.
+ * zero1_f8_product: d[i][j] = sum over k of a(i, k) b(j, k), a.rows x b.rows, bf16
+ *   (nearest even) or fp32 with ZERO1_F32, row stride ldd elements (0: b.rows);
+ *   added in fp32.  For bf16 the matrix cores add eight neighbouring products at a
+ *   time and drop what is below 2^-13 of the largest of the eight (about 2^-15 of
+ *   the result); for fp32 nothing is dropped, at half the rate.  Without columns:
+ *   zeros.  ws: zero1_f8_product_workspace_bytes
+ *   bytes, 256-byte aligned (NULL where that is 0).  The same operands give the
+ *   same bits.
+ * Written buffers must not overlap any other of the call. */
+zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int64_t ld, const zero1_f8_matrix* q,
+                               const zero1_f8_matrix* qt, uint32_t flags, void* stream);
+size_t zero1_f8_product_workspace_bytes(const zero1_f8_matrix* a, const zero1_f8_matrix* b, uint32_t flags);
+zero1_status zero1_f8_product(const zero1_f8_matrix* a, const zero1_f8_matrix* b, void* d, int64_t ldd, uint32_t flags,
+                              void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- Muon
  * The Muon step on weight matrices that this rank owns whole (the embedding,

@@ -13,6 +13,7 @@ from .binding import (  # noqa: F401
     mta_table_bytes, mta_plan, mta_workspace_bytes, mta_reduce, mta_update, mta_design, mta_step,
     mta_step_static, mta_reduce_range, partials_sum,
     arena_plan, step_scalars_derive, time_next_launch,
+    F32, E5M2, F8Matrix, f8_matrix, f8_quantize, f8_product, f8_product_workspace_bytes,
     MV_8BIT, STATE_M, STATE_V, state8_bytes, state8_encode, state8_decode,
     Matrix, MatrixPlan, MuonHParams, MuonScalars, U_F32, NO_NESTEROV, matrix, muon_scalars_derive,
     muon_table_bytes, muon_plan, muon_workspace_bytes, muon_momentum, orthogonalize, muon_update, muon_step,

@@ -26,6 +26,8 @@ U_F32 = 0x200
 NO_NESTEROV = 0x400
 MV_8BIT = 0x2000
 STATE_M, STATE_V = 0, 1
+F32 = 0x10000
+E5M2 = 0x20000
 MAX_W = 128
 STATIC_MAX_G_ELEMS = 16777216
 # the layout of the structures below and the signatures set in lib(); a
@@ -88,6 +90,11 @@ class ArenaLayout(ctypes.Structure):
                 ("ws", ctypes.c_size_t), ("ws_bytes", ctypes.c_size_t),
                 ("master", ctypes.c_size_t), ("m", ctypes.c_size_t), ("v", ctypes.c_size_t),
                 ("params", ctypes.c_size_t), ("grads", ctypes.c_size_t * 128)]
+
+
+class F8Matrix(ctypes.Structure):
+    _fields_ = [("rows", i64), ("cols", i64), ("ld", i64), ("ld_scales", i64), ("codes", P), ("scales", P),
+                ("block_rows", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 class Matrix(ctypes.Structure):
@@ -198,6 +205,12 @@ def lib():
         L.zero1_state8_encode.restype = i32
         L.zero1_state8_decode.argtypes = [P, i64, P, i32, u32, P]
         L.zero1_state8_decode.restype = i32
+        L.zero1_f8_quantize.argtypes = [P, i64, i64, i64, ctypes.POINTER(F8Matrix), ctypes.POINTER(F8Matrix), u32, P]
+        L.zero1_f8_quantize.restype = i32
+        L.zero1_f8_product_workspace_bytes.argtypes = [ctypes.POINTER(F8Matrix), ctypes.POINTER(F8Matrix), u32]
+        L.zero1_f8_product_workspace_bytes.restype = szt
+        L.zero1_f8_product.argtypes = [ctypes.POINTER(F8Matrix), ctypes.POINTER(F8Matrix), P, i64, u32, P, szt, P]
+        L.zero1_f8_product.restype = i32
         L.zero1_time_next_launch.argtypes = [P, P]
         L.zero1_time_next_launch.restype = i32
         L.zero1_muon_scalars_derive.argtypes = [ctypes.POINTER(MuonHParams), ctypes.POINTER(MuonScalars)]
@@ -454,6 +467,31 @@ def state8_encode(x, n: int, state, which: int, flags: int = 0, stream=None):
 def state8_decode(state, n: int, x, which: int, flags: int = 0, stream=None):
     """What an 8-bit buffer of n elements stands for, as fp32 (bf16 with MV_BF16)."""
     _check(lib().zero1_state8_decode(_addr(state), n, _addr(x), which, flags, _stream(stream)))
+
+
+# ------------------------------------------------------------------ 8-bit matrices
+def f8_matrix(rows: int, cols: int, codes, scales, block_rows: int = 1, flags: int = 0, ld: int = 0,
+              ld_scales: int = 0) -> F8Matrix:
+    """A matrix in 8-bit floating point (zero1_f8_matrix); buffers are tensors or
+    device addresses, strides of 0 the least there are.  flags: E5M2."""
+    return F8Matrix(rows, cols, ld, ld_scales, _addr(codes), _addr(scales), block_rows, flags)
+
+
+def f8_quantize(src, rows: int, cols: int, q: F8Matrix = None, qt: F8Matrix = None, ld: int = 0, flags: int = 0,
+                stream=None):
+    """src (bf16, fp32 with F32) into q and its transpose into qt (zero1_f8_quantize)."""
+    _check(lib().zero1_f8_quantize(_addr(src), rows, cols, ld, ctypes.byref(q) if q is not None else None,
+                                   ctypes.byref(qt) if qt is not None else None, flags, _stream(stream)))
+
+
+def f8_product_workspace_bytes(a: F8Matrix, b: F8Matrix, flags: int = 0) -> int:
+    return lib().zero1_f8_product_workspace_bytes(ctypes.byref(a), ctypes.byref(b), flags)
+
+
+def f8_product(a: F8Matrix, b: F8Matrix, d, ldd: int = 0, flags: int = 0, ws=None, ws_bytes=None, stream=None):
+    """d = a b^T in bf16 (fp32 with F32) (zero1_f8_product)."""
+    w, wb = _ws(ws, ws_bytes)
+    _check(lib().zero1_f8_product(ctypes.byref(a), ctypes.byref(b), _addr(d), ldd, flags, w, wb, _stream(stream)))
 
 
 def _event(e) -> int:

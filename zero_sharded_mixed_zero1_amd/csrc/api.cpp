@@ -754,9 +754,9 @@ static zero1_status state8_common(const char* fn, const void* x, int64_t n, cons
         const size_t xb = flags & ZERO1_MV_BF16 ? 2 : 4;
         if (reinterpret_cast<uintptr_t>(x) % xb) return fail(ZERO1_EINVAL, "%s: x must be aligned to its elements", fn);
         if (!aligned16(state)) return fail(ZERO1_EINVAL, "%s: the 8-bit buffer must be 16-byte aligned", fn);
-        std::vector<Range> rg = {{(uintptr_t)x, (uintptr_t)x + xb * (size_t)n, "x", 0},
-                                 {(uintptr_t)state, (uintptr_t)state + state8_size(n), "state", 0}};
-        if (zero1_status st = check_disjoint(rg)) return st;
+        const uintptr_t xp = (uintptr_t)x, sp = (uintptr_t)state;
+        if (xp < sp + state8_size(n) && sp < xp + xb * (size_t)n)
+            return fail(ZERO1_EINVAL, "%s: buffers overlap: x and the 8-bit buffer", fn);
     }
     return current_device(d);
 }

@@ -1,0 +1,42 @@
+// f8.h -- matrices in 8-bit floating point with a scale for each block of 128:
+// what the host side (f8_api.cpp) and the kernels (f8_quantize.hip,
+// f8_product.hip) share.
+//
+// A matrix of rows x cols is rows of codes (e4m3 or e5m2, OCP), padded with zeros
+// to whole blocks of 128 columns, and one byte b for each block of 128 columns of
+// one row or of 128 rows: a code stands for itself times 2^(b-127).  Why powers of
+// two: the matrix cores take such a scale with each operand, so a block's scale
+// costs the product nothing; and a floating point code loses no precision to it,
+// only up to one binade of the 17 that e4m3 has.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace z1 {
+
+constexpr int kF8Block = 128;
+
+// A matrix as the kernels see it.
+struct F8 {
+    uint8_t* codes;        // NULL: absent (quantize)
+    uint8_t* scales;
+    int64_t rows, cols, ld, ld_scales;
+    int shift;             // row >> shift is the row of its scales: 0 or 7
+    int e5m2;
+};
+
+// Quantizes src (rows x cols, bf16 or fp32) into q, its transpose into qt.
+hipError_t launch_f8_quantize(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, const F8& q,
+                              const F8& qt, hipStream_t s);
+
+// D[i][j] = sum over k of a(i, k) b(j, k).
+struct F8Product {
+    F8 a, b;
+    void* d;
+    int64_t ldd;
+    int f32;               // D is fp32, else bf16
+};
+hipError_t launch_f8_product(const F8Product& p, hipStream_t s);
+
+}  // namespace z1

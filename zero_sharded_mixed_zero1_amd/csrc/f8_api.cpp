@@ -1,0 +1,259 @@
+// f8_api.cpp -- the 8-bit floating point entry points of the C ABI (declared in
+// include/zero1.h): argument checks and launches.  No entry point allocates device
+// memory or synchronizes (except ZERO1_SYNC_CHECK=1).
+#include <hip/hip_runtime.h>
+
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+
+#include "../../include/zero1.h"
+#include "f8.h"
+#include "internal.h"
+
+using namespace z1;
+
+namespace {
+
+// ------------------------------------------------------------------ errors
+zero1_status fail(zero1_status st, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_error(st, buf);
+    return st;
+}
+
+zero1_status ok()
+{
+    set_error(ZERO1_OK, "");
+    return ZERO1_OK;
+}
+
+#define Z1_HIP(call)                                                                      \
+    do {                                                                                  \
+        hipError_t e_ = (call);                                                           \
+        if (e_ != hipSuccess)                                                             \
+            return fail(ZERO1_EHIP, "%s failed: %s", #call, hipGetErrorString(e_));      \
+    } while (0)
+
+zero1_status finish(hipStream_t s)
+{
+    static const bool sync = [] {
+        const char* e = std::getenv("ZERO1_SYNC_CHECK");
+        return e && e[0] && e[0] != '0';
+    }();
+    if (sync) {
+        hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+        Z1_HIP(hipStreamIsCapturing(s, &cs));
+        if (cs == hipStreamCaptureStatusNone) Z1_HIP(hipStreamSynchronize(s));
+        Z1_HIP(hipGetLastError());
+    }
+    return ok();
+}
+
+// ------------------------------------------------------------------ device
+std::mutex g_mu;
+int g_cus[64];   // CUs of each device once probed; -1: not gfx950
+
+zero1_status current_device(int& cus)
+{
+    int dev = 0;
+    Z1_HIP(hipGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return fail(ZERO1_ENOTSUPPORTED, "device index %d out of range", dev);
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (g_cus[dev] == 0) {
+        hipDeviceProp_t p;
+        Z1_HIP(hipGetDeviceProperties(&p, dev));
+        g_cus[dev] = std::strncmp(p.gcnArchName, "gfx950", 6) == 0 ? p.multiProcessorCount : -1;
+    }
+    if (g_cus[dev] < 0) return fail(ZERO1_ENOTSUPPORTED, "device %d is not a gfx950", dev);
+    cus = g_cus[dev];
+    return ZERO1_OK;
+}
+
+// ------------------------------------------------------------------ checks
+constexpr uint32_t kF8Flags = ZERO1_F32;
+constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 256, kMaxCols = (int64_t)1 << 23, kMaxLd = (int64_t)1 << 40;
+
+int64_t blocks(int64_t n) { return (n + kF8Block - 1) / kF8Block; }
+int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+zero1_status check_flags(uint32_t flags, const char* fn)
+{
+    if (flags & ~kF8Flags) return fail(ZERO1_EINVAL, "%s: unknown flag bits 0x%x", fn, flags & ~kF8Flags);
+    return ZERO1_OK;
+}
+
+// A matrix's fields, with the strides of 0 filled in.
+zero1_status check_matrix(const zero1_f8_matrix& m, const char* fn, const char* name, F8& out)
+{
+    if (m.rows < 0 || m.rows > kMaxRows)
+        return fail(ZERO1_EINVAL, "%s: %s.rows=%lld must be in [0, 2^31 - 256]", fn, name, (long long)m.rows);
+    if (m.cols < 0 || m.cols > kMaxCols)
+        return fail(ZERO1_EINVAL, "%s: %s.cols=%lld must be in [0, 2^23]", fn, name, (long long)m.cols);
+    if (m.block_rows != 1 && m.block_rows != kF8Block)
+        return fail(ZERO1_EINVAL, "%s: %s.block_rows=%d must be 1 or 128", fn, name, m.block_rows);
+    if (m.flags & ~ZERO1_E5M2)
+        return fail(ZERO1_EINVAL, "%s: %s: unknown flag bits 0x%x", fn, name, m.flags & ~ZERO1_E5M2);
+    const int64_t wide = up(m.cols, kF8Block), per = blocks(m.cols);
+    out.ld = m.ld ? m.ld : wide;
+    out.ld_scales = m.ld_scales ? m.ld_scales : up(per, 4);
+    if (out.ld < wide || out.ld % 16 || out.ld > kMaxCols * 2)
+        return fail(ZERO1_EINVAL, "%s: %s.ld=%lld must be a multiple of 16, at least %lld and at most 2^24", fn, name,
+                    (long long)out.ld, (long long)wide);
+    if (out.ld_scales < per || out.ld_scales % 4 || out.ld_scales > kMaxLd)
+        return fail(ZERO1_EINVAL, "%s: %s.ld_scales=%lld must be a multiple of 4 and at least %lld", fn, name,
+                    (long long)out.ld_scales, (long long)per);
+    if (m.rows > 0 && m.cols > 0) {
+        if (!m.codes || !m.scales) return fail(ZERO1_EINVAL, "%s: %s: NULL buffer", fn, name);
+        if (reinterpret_cast<uintptr_t>(m.codes) % 16)
+            return fail(ZERO1_EINVAL, "%s: %s.codes must be 16-byte aligned", fn, name);
+        if (reinterpret_cast<uintptr_t>(m.scales) % 4)
+            return fail(ZERO1_EINVAL, "%s: %s.scales must be 4-byte aligned", fn, name);
+    }
+    out.codes = m.codes;
+    out.scales = m.scales;
+    out.rows = m.rows;
+    out.cols = m.cols;
+    out.shift = m.block_rows == 1 ? 0 : 7;
+    out.e5m2 = (m.flags & ZERO1_E5M2) ? 1 : 0;
+    return ZERO1_OK;
+}
+
+struct Range {
+    uintptr_t lo, hi;
+    const char* what;
+};
+
+// The bytes from a matrix's first element to its last; empty where it has none.
+Range range_of(const void* p, int64_t rows, int64_t ld_bytes, int64_t row_bytes, const char* what)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    if (!p || rows <= 0 || row_bytes <= 0) return Range{lo, lo, what};
+    return Range{lo, lo + (uintptr_t)(rows - 1) * (uintptr_t)ld_bytes + (uintptr_t)row_bytes, what};
+}
+
+Range codes_of(const F8& m, const char* what) { return range_of(m.codes, m.rows, m.ld, up(m.cols, kF8Block), what); }
+Range scales_of(const F8& m, const char* what)
+{
+    return range_of(m.scales, m.rows > 0 ? ((m.rows - 1) >> m.shift) + 1 : 0, m.ld_scales, blocks(m.cols), what);
+}
+
+// None of the first n_out ranges (written) overlaps another.
+zero1_status check_disjoint(const char* fn, const Range* r, int n, int n_out)
+{
+    for (int i = 0; i < n_out; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (r[i].lo < r[i].hi && r[j].lo < r[j].hi && r[i].lo < r[j].hi && r[j].lo < r[i].hi)
+                return fail(ZERO1_EINVAL, "%s: buffers overlap: %s and %s", fn, r[i].what, r[j].what);
+    return ZERO1_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int64_t ld, const zero1_f8_matrix* q,
+                               const zero1_f8_matrix* qt, uint32_t flags, void* stream)
+{
+    const char* fn = "zero1_f8_quantize";
+    zero1_status st;
+    if ((st = check_flags(flags, fn))) return st;
+    if (!q && !qt) return fail(ZERO1_EINVAL, "%s: q and qt are both NULL", fn);
+    if (rows < 0 || cols < 0) return fail(ZERO1_EINVAL, "%s: rows=%lld and cols=%lld must be >= 0", fn, (long long)rows, (long long)cols);
+    F8 fq, ft;
+    std::memset(&fq, 0, sizeof fq);
+    std::memset(&ft, 0, sizeof ft);
+    if (q) {
+        if ((st = check_matrix(*q, fn, "q", fq))) return st;
+        if (q->rows != rows || q->cols != cols)
+            return fail(ZERO1_EINVAL, "%s: q is %lld x %lld, src %lld x %lld", fn, (long long)q->rows, (long long)q->cols,
+                        (long long)rows, (long long)cols);
+    }
+    if (qt) {
+        if ((st = check_matrix(*qt, fn, "qt", ft))) return st;
+        if (qt->rows != cols || qt->cols != rows)
+            return fail(ZERO1_EINVAL, "%s: qt is %lld x %lld, src's transpose %lld x %lld", fn, (long long)qt->rows,
+                        (long long)qt->cols, (long long)cols, (long long)rows);
+    }
+    if (ld == 0) ld = cols;
+    const int64_t eb = flags & ZERO1_F32 ? 4 : 2;
+    if (ld < cols || ld > kMaxLd) return fail(ZERO1_EINVAL, "%s: ld=%lld must be at least cols=%lld", fn, (long long)ld, (long long)cols);
+    if (rows > 0 && cols > 0) {
+        if (!src) return fail(ZERO1_EINVAL, "%s: src is NULL", fn);
+        if (reinterpret_cast<uintptr_t>(src) % eb) return fail(ZERO1_EINVAL, "%s: src must be aligned to its elements", fn);
+    }
+    const Range r[5] = {codes_of(fq, "q.codes"), scales_of(fq, "q.scales"), codes_of(ft, "qt.codes"),
+                        scales_of(ft, "qt.scales"), range_of(src, rows, ld * eb, cols * eb, "src")};
+    if ((st = check_disjoint(fn, r, 5, 4))) return st;
+    if (blocks(rows) * blocks(cols) > (int64_t)1 << 24)
+        return fail(ZERO1_EINVAL, "%s: more than 2^24 blocks of 128 x 128", fn);
+    int cus = 0;
+    if ((st = current_device(cus))) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (rows > 0 && cols > 0) Z1_HIP(launch_f8_quantize(src, (flags & ZERO1_F32) != 0, rows, cols, ld, fq, ft, s));
+    return finish(s);
+}
+
+// Shared checks of the product and its workspace's size.
+static zero1_status product_of(const zero1_f8_matrix* a, const zero1_f8_matrix* b, uint32_t flags, const char* fn,
+                               F8Product& p)
+{
+    zero1_status st;
+    if ((st = check_flags(flags, fn))) return st;
+    if (!a || !b) return fail(ZERO1_EINVAL, "%s: a or b is NULL", fn);
+    if ((st = check_matrix(*a, fn, "a", p.a))) return st;
+    if ((st = check_matrix(*b, fn, "b", p.b))) return st;
+    if (a->cols != b->cols)
+        return fail(ZERO1_EINVAL, "%s: a has %lld columns, b %lld", fn, (long long)a->cols, (long long)b->cols);
+    p.f32 = (flags & ZERO1_F32) ? 1 : 0;
+    p.d = nullptr;
+    p.ldd = b->rows;
+    return ZERO1_OK;
+}
+
+size_t zero1_f8_product_workspace_bytes(const zero1_f8_matrix* a, const zero1_f8_matrix* b, uint32_t flags)
+{
+    F8Product p;
+    if (product_of(a, b, flags, "zero1_f8_product_workspace_bytes", p)) return 0;
+    return 0;
+}
+
+zero1_status zero1_f8_product(const zero1_f8_matrix* a, const zero1_f8_matrix* b, void* d, int64_t ldd, uint32_t flags,
+                              void* ws, size_t ws_bytes, void* stream)
+{
+    const char* fn = "zero1_f8_product";
+    (void)ws;
+    (void)ws_bytes;
+    zero1_status st;
+    F8Product p;
+    if ((st = product_of(a, b, flags, fn, p))) return st;
+    const int64_t eb = p.f32 ? 4 : 2;
+    if (ldd == 0) ldd = p.b.rows;
+    if (ldd < p.b.rows || ldd > kMaxLd)
+        return fail(ZERO1_EINVAL, "%s: ldd=%lld must be at least b's rows, %lld", fn, (long long)ldd, (long long)p.b.rows);
+    if (p.a.rows > 0 && p.b.rows > 0) {
+        if (!d) return fail(ZERO1_EINVAL, "%s: d is NULL", fn);
+        if (reinterpret_cast<uintptr_t>(d) % eb) return fail(ZERO1_EINVAL, "%s: d must be aligned to its elements", fn);
+    }
+    const Range r[5] = {range_of(d, p.a.rows, ldd * eb, p.b.rows * eb, "d"), codes_of(p.a, "a.codes"),
+                        scales_of(p.a, "a.scales"), codes_of(p.b, "b.codes"), scales_of(p.b, "b.scales")};
+    if ((st = check_disjoint(fn, r, 5, 1))) return st;
+    if (blocks(p.a.rows) * blocks(p.b.rows) > (int64_t)1 << 24)
+        return fail(ZERO1_EINVAL, "%s: more than 2^24 tiles of 128 x 128", fn);
+    int cus = 0;
+    if ((st = current_device(cus))) return st;
+    p.d = d;
+    p.ldd = ldd;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p.a.rows > 0 && p.b.rows > 0) Z1_HIP(launch_f8_product(p, s));
+    return finish(s);
+}
+
+}  // extern "C"
