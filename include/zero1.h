@@ -543,8 +543,8 @@ typedef struct zero1_f8_matrix {
     int64_t rows, cols;     /* >= 0; rows < 2^31 - 255, cols <= 2^23             */
     int64_t ld;             /* bytes; a multiple of 16, >= cols rounded up to 128, <= 2^24;
                                0: cols rounded up to 128                         */
-    int64_t ld_scales;      /* bytes; a multiple of 4, >= the blocks of a row; 0: these
-                               rounded up to 4                                   */
+    int64_t ld_scales;      /* bytes; a multiple of 4, >= the blocks of a row, <= 2^24; 0:
+                               these rounded up to 4 (rows of scales are read in fours) */
     uint8_t* codes;         /* 16-byte aligned                                   */
     uint8_t* scales;        /* 4-byte aligned                                    */
     int32_t block_rows;     /* 1 or 128                                          */

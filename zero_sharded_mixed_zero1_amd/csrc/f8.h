@@ -36,6 +36,7 @@ struct F8Product {
     void* d;
     int64_t ldd;
     int f32;               // D is fp32, else bf16
+    int vec;               // D and its rows begin at multiples of 16 bytes
 };
 hipError_t launch_f8_product(const F8Product& p, hipStream_t s);
 

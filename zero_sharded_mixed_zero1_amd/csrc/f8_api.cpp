@@ -107,8 +107,8 @@ zero1_status check_matrix(const zero1_f8_matrix& m, const char* fn, const char* 
     if (out.ld < wide || out.ld % 16 || out.ld > kMaxCols * 2)
         return fail(ZERO1_EINVAL, "%s: %s.ld=%lld must be a multiple of 16, at least %lld and at most 2^24", fn, name,
                     (long long)out.ld, (long long)wide);
-    if (out.ld_scales < per || out.ld_scales % 4 || out.ld_scales > kMaxLd)
-        return fail(ZERO1_EINVAL, "%s: %s.ld_scales=%lld must be a multiple of 4 and at least %lld", fn, name,
+    if (out.ld_scales < per || out.ld_scales % 4 || out.ld_scales > kMaxCols * 2)
+        return fail(ZERO1_EINVAL, "%s: %s.ld_scales=%lld must be a multiple of 4, at least %lld and at most 2^24", fn, name,
                     (long long)out.ld_scales, (long long)per);
     if (m.rows > 0 && m.cols > 0) {
         if (!m.codes || !m.scales) return fail(ZERO1_EINVAL, "%s: %s: NULL buffer", fn, name);
@@ -215,6 +215,7 @@ static zero1_status product_of(const zero1_f8_matrix* a, const zero1_f8_matrix* 
     p.f32 = (flags & ZERO1_F32) ? 1 : 0;
     p.d = nullptr;
     p.ldd = b->rows;
+    p.vec = 0;
     return ZERO1_OK;
 }
 
@@ -251,6 +252,7 @@ zero1_status zero1_f8_product(const zero1_f8_matrix* a, const zero1_f8_matrix* b
     if ((st = current_device(cus))) return st;
     p.d = d;
     p.ldd = ldd;
+    p.vec = reinterpret_cast<uintptr_t>(d) % 16 == 0 && ldd * eb % 16 == 0;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (p.a.rows > 0 && p.b.rows > 0) Z1_HIP(launch_f8_product(p, s));
     return finish(s);
