@@ -30,6 +30,10 @@ struct F8 {
 hipError_t launch_f8_quantize(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, const F8& q,
                               const F8& qt, hipStream_t s);
 
+// Which kernel a product takes (f8_product.hip): rows of A by rows of B of a
+// workgroup's tile; thin: few rows of A, four or eight waves.
+enum F8Kind : int { kF8Thin4, kF8Thin8, kF8Tile64, kF8Tile128, kF8Tile128Deep, kF8Tile128x256, kF8Tile256 };
+
 // D[i][j] = sum over k of a(i, k) b(j, k).
 struct F8Product {
     F8 a, b;
@@ -37,6 +41,10 @@ struct F8Product {
     int64_t ldd;
     int f32;               // D is fp32, else bf16
     int vec;               // D and its rows begin at multiples of 16 bytes
+    int kind;              // F8Kind
+    int parts, part_steps; // the summed axis in parts of so many blocks of 128
+    float* sums;           // parts > 1: their sums, rows of ld_sums, part_elems a part
+    int64_t ld_sums, part_elems;
 };
 hipError_t launch_f8_product(const F8Product& p, hipStream_t s);
 

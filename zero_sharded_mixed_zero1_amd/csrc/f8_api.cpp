@@ -201,6 +201,22 @@ zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int6
     return finish(s);
 }
 
+// Kernel and parts of a product.
+static void choose(F8Product& p)
+{
+    const int64_t m = p.a.rows, n = p.b.rows, per = blocks(p.a.cols);
+    p.kind = m <= 32 ? kF8Thin4 : m <= 1024 ? kF8Tile128 : kF8Tile256;
+    p.parts = 1;
+    if (const char* e = std::getenv("F8_KIND")) p.kind = std::atoi(e);
+    if (const char* e = std::getenv("F8_PARTS")) p.parts = std::atoi(e);
+    p.part_steps = (int)((per + p.parts - 1) / p.parts);
+    if (p.part_steps < 1) p.part_steps = 1;
+    p.parts = per > 0 ? (int)((per + p.part_steps - 1) / p.part_steps) : 1;
+    p.sums = nullptr;
+    p.ld_sums = up(n, 4);
+    p.part_elems = m * p.ld_sums;
+}
+
 // Shared checks of the product and its workspace's size.
 static zero1_status product_of(const zero1_f8_matrix* a, const zero1_f8_matrix* b, uint32_t flags, const char* fn,
                                F8Product& p)
@@ -216,6 +232,7 @@ static zero1_status product_of(const zero1_f8_matrix* a, const zero1_f8_matrix* 
     p.d = nullptr;
     p.ldd = b->rows;
     p.vec = 0;
+    choose(p);
     return ZERO1_OK;
 }
 
@@ -223,15 +240,13 @@ size_t zero1_f8_product_workspace_bytes(const zero1_f8_matrix* a, const zero1_f8
 {
     F8Product p;
     if (product_of(a, b, flags, "zero1_f8_product_workspace_bytes", p)) return 0;
-    return 0;
+    return p.parts > 1 ? (size_t)p.parts * (size_t)p.part_elems * sizeof(float) : 0;
 }
 
 zero1_status zero1_f8_product(const zero1_f8_matrix* a, const zero1_f8_matrix* b, void* d, int64_t ldd, uint32_t flags,
                               void* ws, size_t ws_bytes, void* stream)
 {
     const char* fn = "zero1_f8_product";
-    (void)ws;
-    (void)ws_bytes;
     zero1_status st;
     F8Product p;
     if ((st = product_of(a, b, flags, fn, p))) return st;
@@ -252,6 +267,13 @@ zero1_status zero1_f8_product(const zero1_f8_matrix* a, const zero1_f8_matrix* b
     if ((st = current_device(cus))) return st;
     p.d = d;
     p.ldd = ldd;
+    if (p.parts > 1) {
+        const size_t need = (size_t)p.parts * (size_t)p.part_elems * sizeof(float);
+        if (!ws) return fail(ZERO1_EWORKSPACE, "workspace is NULL (need %zu bytes)", need);
+        if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(ZERO1_EWORKSPACE, "workspace must be 256-byte aligned");
+        if (ws_bytes < need) return fail(ZERO1_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+        p.sums = static_cast<float*>(ws);
+    }
     p.vec = reinterpret_cast<uintptr_t>(d) % 16 == 0 && ldd * eb % 16 == 0;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (p.a.rows > 0 && p.b.rows > 0) Z1_HIP(launch_f8_product(p, s));

@@ -115,6 +115,9 @@ struct Tile {
     static_assert(kLds <= 160 * 1024 && kRows % 64 == 0 && kCols % 64 == 0 && kLines / 8 % kWaves == 0, "tile");
 };
 
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+
 // Tiles of D in an order that keeps what an XCD works on at once (workgroup b runs on
 // XCD b % 8) close to a square: each XCD takes one contiguous eighth of the tiles
 // in bands of 8 tile rows, down a band's columns first.
@@ -127,24 +130,28 @@ __device__ __forceinline__ void tile_at(int64_t b, int64_t tiles_m, int64_t tile
     j = in / high;
 }
 
-// EXACT: widened to bf16 (D fp32).
-template <typename T, int WR, int WC, int PX, int QY, int S, int FA, int FB, typename D>
+// EXACT: widened to bf16.  Each of p.parts workgroups of a tile adds up p.part_steps
+// blocks of the summed axis; where there are more than one, they leave their sums
+// in fp32 for join_kernel.
+template <typename T, int WR, int WC, int PX, int QY, int S, int FA, int FB, bool EXACT, typename D>
 __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
 {
-    constexpr bool EXACT = sizeof(D) == 4;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wi = wave / WC, wj = wave % WC;
+    const int64_t tiles_m = (p.a.rows + T::kRows - 1) / T::kRows, tiles_n = (p.b.rows + T::kCols - 1) / T::kCols;
+    const int64_t part = blockIdx.x / (tiles_m * tiles_n);
     int64_t ti, tj;
-    tile_at(blockIdx.x, (p.a.rows + T::kRows - 1) / T::kRows, (p.b.rows + T::kCols - 1) / T::kCols, ti, tj);
+    tile_at(blockIdx.x - part * (tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
     const int64_t m0 = ti * T::kRows, n0 = tj * T::kCols;
-    const int steps = (int)((p.a.cols + kF8Block - 1) / kF8Block);
+    const int from = (int)part * p.part_steps;
+    const int steps = min(p.part_steps, (int)((p.a.cols + kF8Block - 1) / kF8Block) - from);
 
     // what this wave loads: lines of 128 bytes (A's rows, then B's), eight a load,
     // their 16-byte slots permuted on the way; then 64 rows' scales of four blocks.
     // Rows past the end repeat the last one.
-    const uint8_t* const ca = p.a.codes + m0 * p.a.ld;
-    const uint8_t* const cb = p.b.codes + n0 * p.b.ld;
+    const uint8_t* const ca = p.a.codes + m0 * p.a.ld + (int64_t)from * kF8Block;
+    const uint8_t* const cb = p.b.codes + n0 * p.b.ld + (int64_t)from * kF8Block;
     const uint8_t* const sa = p.a.scales + (m0 >> p.a.shift) * p.a.ld_scales;
     const uint8_t* const sb = p.b.scales + (n0 >> p.b.shift) * p.b.ld_scales;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
@@ -164,18 +171,22 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
         if (first < T::kRows) soff[l] = (uint32_t)(((m0 + min(line, last_a)) >> p.a.shift) - (m0 >> p.a.shift)) * (uint32_t)p.a.ld_scales;
         else soff[l] = (uint32_t)(((n0 + min(line - T::kRows, last_b)) >> p.b.shift) - (n0 >> p.b.shift)) * (uint32_t)p.b.ld_scales;
     }
-    auto issue = [&](int kb, int buf) {
-        const uint32_t at = lds0 + buf * T::kStage;
-#pragma unroll
-        for (int l = 0; l < T::kLoads; ++l) {
-            const int first = (wave * T::kLoads + l) * 8;
-            load_1k((first < T::kRows ? ca : cb) + (int64_t)kb * kF8Block, off[l], at + first * kLine);
-        }
+    auto issue_scales = [&](int t, uint32_t at) {
 #pragma unroll
         for (int l = 0; l < T::kScaleLoads; ++l) {
             const int first = min(wave * T::kScaleLoads + l, T::kLines / 64 - 1) * 64;
-            load_256((first < T::kRows ? sa : sb) + (kb & ~3), soff[l], at + T::kLines * kLine + first * 4);
+            load_256((first < T::kRows ? sa : sb) + ((from + t) & ~3), soff[l], at + T::kLines * kLine + first * 4);
         }
+    };
+    auto issue = [&](int t, int buf) {
+        const uint32_t at = lds0 + buf * T::kStage;
+        const uint8_t *la = ca + (int64_t)t * kF8Block, *lb = cb + (int64_t)t * kF8Block;
+#pragma unroll
+        for (int l = 0; l < T::kLoads; ++l) {
+            const int first = (wave * T::kLoads + l) * 8;
+            load_1k(first < T::kRows ? la : lb, off[l], at + first * kLine);
+        }
+        issue_scales(t, at);
     };
 
     f32x16 acc[PX][QY];
@@ -199,67 +210,26 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
         u32x4 v[2];
         i32x8 f;
     };
-    struct Frag {
-        Codes p[PX], q[QY];
+    const uint8_t* const lds_p = lds + wi * 32 * PX * kLine;
+    const uint8_t* const lds_q = lds + (T::kRows + wj * 32 * QY) * kLine;
+    auto read_p = [&](Codes& v, int buf, int x, int h) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) v.v[c] = *reinterpret_cast<const u32x4*>(lds_p + buf * T::kStage + x * 32 * kLine + place[h][c]);
     };
-    int ep[PX], eq[QY];
-    auto read = [&](Frag& f, int buf, int h) {
-        const uint8_t* a = lds + buf * T::kStage + wi * 32 * PX * kLine;
-        const uint8_t* b = lds + buf * T::kStage + (T::kRows + wj * 32 * QY) * kLine;
+    auto read_q = [&](Codes (&v)[QY], int buf, int h) {
 #pragma unroll
         for (int y = 0; y < QY; ++y)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) f.q[y].v[c] = *reinterpret_cast<const u32x4*>(b + y * 32 * kLine + place[h][c]);
-#pragma unroll
-        for (int x = 0; x < PX; ++x)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) f.p[x].v[c] = *reinterpret_cast<const u32x4*>(a + x * 32 * kLine + place[h][c]);
+            for (int c = 0; c < 2; ++c) v[y].v[c] = *reinterpret_cast<const u32x4*>(lds_q + buf * T::kStage + y * 32 * kLine + place[h][c]);
     };
-    auto read_scales = [&](int buf, int kb) {
-        const uint8_t* e = lds + buf * T::kStage + T::kLines * kLine + (kb & 3) + 4 * (lane & 31);
+    auto read_scales = [&](int (&ep)[PX], int (&eq)[QY], int buf, int t) {
+        const uint8_t* e = lds + buf * T::kStage + T::kLines * kLine + ((from + t) & 3) + 4 * (lane & 31);
 #pragma unroll
         for (int x = 0; x < PX; ++x) ep[x] = e[4 * (wi * 32 * PX + 32 * x)];
 #pragma unroll
         for (int y = 0; y < QY; ++y) eq[y] = e[4 * (T::kRows + wj * 32 * QY + 32 * y)];
     };
-    auto multiply = [&](const Frag& f) {
-        if constexpr (!EXACT) {
-#pragma unroll
-            for (int x = 0; x < PX; ++x)
-#pragma unroll
-                for (int y = 0; y < QY; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.q[y].f, f.p[x].f, acc[x][y], FB, FA, 0, eq[y], 0, ep[x]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                bf16x8 wp[PX], wq[QY];
-#pragma unroll
-                for (int x = 0; x < PX; ++x) wp[x] = widen8<FA>((uint32_t)f.p[x].f[2 * j], (uint32_t)f.p[x].f[2 * j + 1], power(ep[x]));
-#pragma unroll
-                for (int y = 0; y < QY; ++y) wq[y] = widen8<FB>((uint32_t)f.q[y].f[2 * j], (uint32_t)f.q[y].f[2 * j + 1], power(eq[y]));
-#pragma unroll
-                for (int x = 0; x < PX; ++x)
-#pragma unroll
-                    for (int y = 0; y < QY; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wq[y], wp[x], acc[x][y], 0, 0, 0);
-            }
-        }
-    };
-    // the order that a half is scheduled in: its MFMAs with the LDS reads of the
-    // next spread between them
-    auto spread = [] {
-        if constexpr (!EXACT) {
-            constexpr int kMfma = PX * QY, kReads = 2 * (PX + QY), kEach = (kReads + kMfma - 1) / kMfma;
-#pragma unroll
-            for (int i = 0; i < kMfma; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
-            }
-        }
-    };
 
-    // each half's operands are read from LDS while the half before is multiplied;
-    // the barrier lies between the halves, when this wave's reads of stage t are
-    // done and its loads of stage t + 1 have arrived
     int put = 0, get = 0;   // buffers: the next one to load into, the one to read
     auto next = [](int b) { return b + 1 == S ? 0 : b + 1; };
 #pragma unroll
@@ -268,33 +238,83 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
             issue(k, put);
             put = next(put);
         }
+    // A stage is 2 PX turns, each of the QY MFMAs of 32 rows and one half of the
+    // block.  A turn's operands are read from LDS in the turn before; at the last turn
+    // this wave's reads of the stage are done, so there lies the barrier after
+    // which the next stage is read and the stage after the following loaded.  (All
+    // of a half's operands read ahead instead takes 40 registers more and 4 % more
+    // time at 8192 x 11008 x 4096.)  EXACT: a turn is a half of the block, so that
+    // each code is widened once.
+    int ep[PX], eq[QY], np[PX], nq[QY];
+    constexpr int kTurns = EXACT ? 2 : 2 * PX;
+    Codes rp[EXACT ? 2 * PX : 2], rq[2][QY];
+    auto stage = [&](int t, auto more_, auto last_) {
+        constexpr bool more = decltype(more_)::value, last = decltype(last_)::value;
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            if (i == kTurns - 1) {
+                if constexpr (!last) {
+                    if constexpr (more) stage_wait<(S - 2) * T::kInFlight>();   // stages t + 2 .. t + S - 1 may be under way
+                    else stage_wait<0>();
+                    __syncthreads();
+                    get = next(get);
+                }
+                // (the last round reads the last stage again)
+                read_q(rq[0], get, 0);
+                read_scales(np, nq, get, last ? t : t + 1);
+            }
+            if (EXACT ? i == 0 : i == PX - 1) read_q(rq[1], get, 1);
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int x = 0; x < PX; ++x) read_p(rp[(1 - i) * PX + x], get, x, 1 - i);
+            } else {
+                read_p(rp[(i + 1) & 1], get, (i + 1) % PX, (i + 1) % kTurns / PX);
+            }
+            if constexpr (more) {
+                if (i == kTurns - 1) issue(t + S, put);
+            }
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    bf16x8 wp[PX], wq[QY];
+#pragma unroll
+                    for (int x = 0; x < PX; ++x)
+                        wp[x] = widen8<FA>((uint32_t)rp[i * PX + x].f[2 * j], (uint32_t)rp[i * PX + x].f[2 * j + 1], power(ep[x]));
+#pragma unroll
+                    for (int y = 0; y < QY; ++y)
+                        wq[y] = widen8<FB>((uint32_t)rq[i][y].f[2 * j], (uint32_t)rq[i][y].f[2 * j + 1], power(eq[y]));
+#pragma unroll
+                    for (int x = 0; x < PX; ++x)
+#pragma unroll
+                        for (int y = 0; y < QY; ++y) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wq[y], wp[x], acc[x][y], 0, 0, 0);
+                }
+            } else {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int y = 0; y < QY; ++y)
+                    acc[i % PX][y] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(rq[i / PX][y].f, rp[i & 1].f, acc[i % PX][y], FB, FA, 0,
+                                                                                     eq[y], 0, ep[i % PX]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if constexpr (more) put = next(put);
+#pragma unroll
+        for (int x = 0; x < PX; ++x) ep[x] = np[x];
+#pragma unroll
+        for (int y = 0; y < QY; ++y) eq[y] = nq[y];
+    };
     if (steps > 0) {
-        Frag f0, f1;
         if (steps > S - 1) stage_wait<(S - 1) * T::kInFlight>();
         else stage_wait<0>();
         __syncthreads();
-        read(f0, get, 0);
-        read_scales(get, 0);
-        for (int t = 0; t < steps; ++t) {
-            read(f1, get, 1);
-            multiply(f0);
-            spread();
-            if (t + 1 < steps) {
-                if (t + S - 1 < steps) stage_wait<(S - 2) * T::kInFlight>();   // stages t + 2 .. t + S - 1 may be under way
-                else stage_wait<0>();
-                __syncthreads();
-                if (t + S < steps) {
-                    issue(t + S, put);
-                    put = next(put);
-                }
-                get = next(get);
-            }
-            // (the last round reads the last stage again: the loop stays one block)
-            read(f0, get, 0);
-            multiply(f1);
-            spread();
-            read_scales(get, t + 1 < steps ? t + 1 : t);
-        }
+        read_q(rq[0], get, 0);
+        read_scales(ep, eq, get, 0);
+#pragma unroll
+        for (int x = 0; x < (EXACT ? PX : 1); ++x) read_p(rp[x], get, x, 0);
+        int t = 0;
+        for (; t + S < steps; ++t) stage(t, Yes{}, No{});
+        for (; t + 1 < steps; ++t) stage(t, No{}, No{});
+        stage(t, No{}, Yes{});
     }
     __syncthreads();   // the stages are free for the way out
 
@@ -302,7 +322,7 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
     constexpr int kVec = 16 / (int)sizeof(D), kRowVecs = 32 * QY / kVec, kPitch = T::kPitch / 4 * (int)sizeof(D) + (sizeof(D) == 2 ? 8 : 0);
     static_assert(kPitch % 16 == 0, "rows in LDS begin at 16 bytes");
     uint8_t* out = lds + wave * 32 * T::kPitch;
-    D* const d = static_cast<D*>(p.d);
+    D* const d = static_cast<D*>(p.d) + part * p.part_elems;
     const bool vec = p.vec != 0;
 #pragma unroll
     for (int x = 0; x < PX; ++x) {
@@ -335,20 +355,207 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
     }
 }
 
-template <int FA, int FB, typename D, int WR, int WC, int PX, int QY, int S>
+// D from the parts' sums, added in the parts' order: four columns a lane.
+template <typename D>
+__global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict__ sums, int parts, int64_t part_elems,
+                                                        int64_t lds, int64_t rows, int64_t cols, D* __restrict__ d,
+                                                        int64_t ldd, int vec)
+{
+    const int64_t per = (cols + 3) / 4, at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (at >= rows * per) return;
+    const int64_t m = at / per, n = at % per * 4;
+    const float* s = sums + m * lds + n;   // (rows of sums are padded to whole quads)
+    f32x4 v = *reinterpret_cast<const f32x4*>(s);
+    for (int k = 1; k < parts; ++k) v += *reinterpret_cast<const f32x4*>(s + k * part_elems);
+    D* o = d + m * ldd + n;
+    if (vec && n + 4 <= cols) {
+        narrow4(v, o);
+    } else {
+        D e[4];
+        narrow4(v, e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < cols) o[j] = e[j];
+    }
+}
+
+// Few rows of A (at most AR): what counts is reading B once, at the rate of memory.  A
+// workgroup takes 32 rows of B; its waves take the blocks of the summed axis in
+// turn, each with a ring of R blocks in LDS of its own, so that nothing waits for
+// another wave until they add up their sums at the end.
+template <int NW, int R, int AR>
+struct Thin {
+    static constexpr int kBytesB = 32 * kLine, kBytesA = AR * kLine, kSlot = kBytesB + kBytesA + 256;
+    static constexpr int kLoads = (32 + AR) / 8 + 1;
+    static constexpr int kPitch = 36;                                  // floats of a row of sums in LDS
+    static constexpr int kRing = NW * R * kSlot, kSums = NW * 32 * kPitch * 4;
+    static constexpr int kLds = kRing > kSums ? kRing : kSums;
+    static_assert(kLds <= 160 * 1024, "LDS of a CU");
+};
+
+__device__ __forceinline__ void load_256_at(const uint8_t* lane_base, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(lane_base) : "memory");
+}
+
+template <typename T, int NW, int R, int AR, int FA, int FB, typename D>
+__global__ __launch_bounds__(64 * NW) void thin_kernel(F8Product p)
+{
+    constexpr bool EXACT = sizeof(D) == 4;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * 32;
+    const int last_a = (int)p.a.rows - 1, last_b = (int)(p.b.rows - 1 - n0 < 31 ? p.b.rows - 1 - n0 : 31);
+    const int blocks = (int)((p.a.cols + kF8Block - 1) / kF8Block), mine = (blocks - wave + NW - 1) / NW;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + wave * R * T::kSlot;
+    const uint8_t* const cb = p.b.codes + n0 * p.b.ld;
+    uint32_t off_b[4], off_a[AR / 8];
+#pragma unroll
+    for (int l = 0; l < 4; ++l) {
+        const int line = 8 * l + (lane >> 3);
+        off_b[l] = (uint32_t)min(line, last_b) * (uint32_t)p.b.ld + 16 * ((lane & 7) ^ slot_key(line));
+    }
+#pragma unroll
+    for (int l = 0; l < AR / 8; ++l) {
+        const int line = 8 * l + (lane >> 3);
+        off_a[l] = (uint32_t)min(line, last_a) * (uint32_t)p.a.ld + 16 * ((lane & 7) ^ slot_key(line));
+    }
+    // lanes 0-31: the scales of B's rows, 32-63: of A's
+    const uint8_t* const scales = lane < 32
+        ? p.b.scales + ((n0 + min(lane, last_b)) >> p.b.shift) * p.b.ld_scales
+        : p.a.scales + ((int64_t)min(lane - 32, last_a) >> p.a.shift) * p.a.ld_scales;
+    auto issue = [&](int i, int slot) {
+        const int kb = wave + i * NW;
+        const uint32_t at = lds0 + slot * T::kSlot;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) load_1k(cb + (int64_t)kb * kF8Block, off_b[l], at + 1024 * l);
+#pragma unroll
+        for (int l = 0; l < AR / 8; ++l) load_1k(p.a.codes + (int64_t)kb * kF8Block, off_a[l], at + T::kBytesB + 1024 * l);
+        load_256_at(scales + (kb & ~3), at + T::kBytesB + T::kBytesA);
+    };
+    f32x16 acc;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+        if (k < mine) issue(k, k);
+    const int row_a = (lane & 31) & (AR - 1);
+    int slot = 0;
+    for (int i = 0; i < mine; ++i) {
+        if (i + R <= mine) stage_wait<(R - 1) * T::kLoads>();
+        else stage_wait<0>();
+        const uint8_t* b = lds + (wave * R + slot) * T::kSlot;
+        const uint8_t* a = b + T::kBytesB;
+        union Codes {
+            u32x4 v[2];
+            i32x8 f;
+        } q[2], u[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int s = 4 * h + 2 * c + (lane >> 5);
+                q[h].v[c] = *reinterpret_cast<const u32x4*>(b + (lane & 31) * kLine + 16 * (s ^ slot_key(lane & 31)));
+                u[h].v[c] = *reinterpret_cast<const u32x4*>(a + row_a * kLine + 16 * (s ^ slot_key(row_a)));
+            }
+        const uint8_t* e = a + T::kBytesA + ((wave + i * NW) & 3);
+        const int eq = e[4 * (lane & 31)], ep = e[4 * (32 + (lane & 31))];
+        // the slot has been read: its next block may come
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (i + R < mine) issue(i + R, slot);
+        slot = slot + 1 == R ? 0 : slot + 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bf16x8 wq = widen8<FB>((uint32_t)q[h].f[2 * j], (uint32_t)q[h].f[2 * j + 1], power(eq));
+                    const bf16x8 wp = widen8<FA>((uint32_t)u[h].f[2 * j], (uint32_t)u[h].f[2 * j + 1], power(ep));
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wq, wp, acc, 0, 0, 0);
+                }
+            } else {
+                acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[h].f, u[h].f, acc, FB, FA, 0, eq, 0, ep);
+            }
+        }
+    }
+    __syncthreads();   // the rings are free for the sums
+    float* const sums = reinterpret_cast<float*>(lds);
+    if ((lane & 31) <= last_a) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<f32x4*>(sums + (wave * 32 + (lane & 31)) * T::kPitch + 8 * g + 4 * (lane >> 5)) =
+                f32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+    }
+    __syncthreads();
+    for (int at = threadIdx.x; at < 32 * (last_a + 1); at += 64 * NW) {
+        const int m = at >> 5, n = at & 31;
+        if (n > last_b) continue;
+        float v = sums[m * T::kPitch + n];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v += sums[(w * 32 + m) * T::kPitch + n];
+        static_cast<D*>(p.d)[m * p.ldd + n0 + n] = (D)v;
+    }
+}
+
+// ------------------------------------------------------------------ launchers
+template <int FA, int FB, bool EXACT, typename D, int WR, int WC, int PX, int QY, int S>
 void launch_tile(const F8Product& p, hipStream_t s)
 {
     using T = Tile<WR, WC, PX, QY, S>;
-    const int64_t grid = (p.a.rows + T::kRows - 1) / T::kRows * ((p.b.rows + T::kCols - 1) / T::kCols);
-    tile_kernel<T, WR, WC, PX, QY, S, FA, FB, D><<<dim3((uint32_t)grid), dim3(T::kThr), T::kLds, s>>>(p);
+    const int64_t tiles = (p.a.rows + T::kRows - 1) / T::kRows * ((p.b.rows + T::kCols - 1) / T::kCols);
+    const dim3 grid((uint32_t)(tiles * p.parts));
+    if (p.parts == 1) {
+        tile_kernel<T, WR, WC, PX, QY, S, FA, FB, EXACT, D><<<grid, dim3(T::kThr), T::kLds, s>>>(p);
+        return;
+    }
+    F8Product q = p;
+    q.d = p.sums;
+    q.ldd = p.ld_sums;
+    q.vec = 1;
+    tile_kernel<T, WR, WC, PX, QY, S, FA, FB, EXACT, float><<<grid, dim3(T::kThr), T::kLds, s>>>(q);
+    const int64_t quads = p.a.rows * ((p.b.rows + 3) / 4);
+    join_kernel<D><<<dim3((uint32_t)((quads + kThreads - 1) / kThreads)), kThreads, 0, s>>>(
+        p.sums, p.parts, p.part_elems, p.ld_sums, p.a.rows, p.b.rows, static_cast<D*>(p.d), p.ldd, p.vec);
+}
+
+template <int FA, int FB, typename D, int NW, int AR>
+void launch_thin(const F8Product& p, hipStream_t s)
+{
+    constexpr int R = NW == 8 && AR == 32 ? 2 : 3;   // what LDS holds
+    using T = Thin<NW, R, AR>;
+    thin_kernel<T, NW, R, AR, FA, FB, D><<<dim3((uint32_t)((p.b.rows + 31) / 32)), dim3(64 * NW), T::kLds, s>>>(p);
+}
+
+template <int FA, int FB, typename D>
+void launch_kind(const F8Product& p, hipStream_t s)
+{
+    constexpr bool EXACT = sizeof(D) == 4;
+    switch (p.kind) {
+    case kF8Thin4:
+        if (p.a.rows <= 8) launch_thin<FA, FB, D, 4, 8>(p, s);
+        else if (p.a.rows <= 16) launch_thin<FA, FB, D, 4, 16>(p, s);
+        else launch_thin<FA, FB, D, 4, 32>(p, s);
+        break;
+    case kF8Thin8:
+        if (p.a.rows <= 8) launch_thin<FA, FB, D, 8, 8>(p, s);
+        else if (p.a.rows <= 16) launch_thin<FA, FB, D, 8, 16>(p, s);
+        else launch_thin<FA, FB, D, 8, 32>(p, s);
+        break;
+    case kF8Tile64: launch_tile<FA, FB, EXACT, D, 2, 2, 1, 1, 4>(p, s); break;
+    case kF8Tile128: launch_tile<FA, FB, EXACT, D, 2, 2, 2, 2, 2>(p, s); break;
+    case kF8Tile128Deep: launch_tile<FA, FB, EXACT, D, 2, 2, 2, 2, 4>(p, s); break;
+    default:
+        if constexpr (EXACT) launch_tile<FA, FB, EXACT, D, 2, 2, 2, 2, 2>(p, s);
+        else if (p.kind == kF8Tile128x256) launch_tile<FA, FB, EXACT, D, 2, 4, 2, 2, 3>(p, s);
+        else launch_tile<FA, FB, EXACT, D, 2, 4, 4, 2, 2>(p, s);
+    }
 }
 
 template <int FA, int FB>
 void launch(const F8Product& p, hipStream_t s)
 {
-    if (p.f32) launch_tile<FA, FB, float, 2, 2, 2, 2, 2>(p, s);
-    else if (p.a.rows > 1024) launch_tile<FA, FB, __bf16, 2, 2, 4, 4, 2>(p, s);
-    else launch_tile<FA, FB, __bf16, 2, 2, 2, 2, 2>(p, s);
+    if (p.f32) launch_kind<FA, FB, float>(p, s);
+    else launch_kind<FA, FB, __bf16>(p, s);
 }
 
 }  // namespace
