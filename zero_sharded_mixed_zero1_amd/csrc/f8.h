@@ -30,9 +30,9 @@ struct F8 {
 hipError_t launch_f8_quantize(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, const F8& q,
                               const F8& qt, hipStream_t s);
 
-// Which kernel a product takes (f8_product.hip): rows of A by rows of B of a
-// workgroup's tile; thin: few rows of A, four or eight waves.
-enum F8Kind : int { kF8Thin4, kF8Thin8, kF8Tile64, kF8Tile128, kF8Tile128Deep, kF8Tile128x256, kF8Tile256 };
+// Which kernel a product takes (f8_product.hip): few rows of A, or tiles of 64 x 64,
+// 128 x 128 or 256 x 256 of D (the last into bf16 only).
+enum F8Kind : int { kF8Thin, kF8Tile64, kF8Tile128, kF8Tile256 };
 
 // D[i][j] = sum over k of a(i, k) b(j, k).
 struct F8Product {
@@ -43,6 +43,8 @@ struct F8Product {
     int vec;               // D and its rows begin at multiples of 16 bytes
     int kind;              // F8Kind
     int parts, part_steps; // the summed axis in parts of so many blocks of 128
+    int64_t whole;         // 256: tiles of a workgroup each; the others' workgroups take
+    int bands;             // 256 / bands rows
     float* sums;           // parts > 1: their sums, rows of ld_sums, part_elems a part
     int64_t ld_sums, part_elems;
 };

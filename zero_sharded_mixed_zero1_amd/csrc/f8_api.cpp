@@ -205,10 +205,17 @@ zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int6
 static void choose(F8Product& p)
 {
     const int64_t m = p.a.rows, n = p.b.rows, per = blocks(p.a.cols);
-    p.kind = m <= 32 ? kF8Thin4 : m <= 1024 ? kF8Tile128 : kF8Tile256;
+    p.kind = m <= 32 ? kF8Thin : m <= 512 ? kF8Tile64 : m <= 1024 || p.f32 ? kF8Tile128 : kF8Tile256;
     p.parts = 1;
     if (const char* e = std::getenv("F8_KIND")) p.kind = std::atoi(e);
     if (const char* e = std::getenv("F8_PARTS")) p.parts = std::atoi(e);
+    if (p.f32 && p.kind == kF8Tile256) p.kind = kF8Tile128;
+    const int64_t tiles = (m + 255) / 256 * ((n + 255) / 256), rest = tiles % 256;
+    p.whole = tiles - rest;
+    p.bands = rest > 128 ? 1 : rest > 64 ? 2 : 4;
+    if (p.bands == 1) { p.whole = tiles; p.bands = 2; }
+    if (const char* e = std::getenv("F8_BANDS")) { p.bands = std::atoi(e); if (p.bands == 1) { p.whole = tiles; p.bands = 2; } }
+    if (p.kind == kF8Tile256) p.parts = 1;
     p.part_steps = (int)((per + p.parts - 1) / p.parts);
     if (p.part_steps < 1) p.part_steps = 1;
     p.parts = per > 0 ? (int)((per + p.part_steps - 1) / p.part_steps) : 1;

@@ -118,13 +118,17 @@ struct Tile {
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
 
-// Tiles of D in an order that keeps what an XCD works on at once (workgroup b runs on
-// XCD b % 8) close to a square: each XCD takes one contiguous eighth of the tiles
-// in bands of 8 tile rows, down a band's columns first.
-__device__ __forceinline__ void tile_at(int64_t b, int64_t tiles_m, int64_t tiles_n, int64_t& i, int64_t& j)
+// Workgroup b of n runs on XCD b % 8: each XCD takes one contiguous eighth.
+__device__ __forceinline__ int64_t xcd_part(int64_t b, int64_t n)
 {
-    const int64_t n = tiles_m * tiles_n, q = n / 8, rest = n % 8, x = b % 8;
-    const int64_t t = x * q + (x < rest ? x : rest) + b / 8;
+    const int64_t x = b % 8, q = n / 8, rest = n % 8;
+    return x * q + (x < rest ? x : rest) + b / 8;
+}
+
+// Tile t of D, in an order that keeps what an XCD works on at once close to a square:
+// in bands of 8 tile rows, down a band's columns first.
+__device__ __forceinline__ void tile_at(int64_t t, int64_t tiles_m, int64_t tiles_n, int64_t& i, int64_t& j)
+{
     const int64_t band = t / (8 * tiles_n), high = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8, in = t - band * 8 * tiles_n;
     i = band * 8 + in % high;
     j = in / high;
@@ -133,17 +137,12 @@ __device__ __forceinline__ void tile_at(int64_t b, int64_t tiles_m, int64_t tile
 // EXACT: widened to bf16.  Each of p.parts workgroups of a tile adds up p.part_steps
 // blocks of the summed axis; where there are more than one, they leave their sums
 // in fp32 for join_kernel.
-template <typename T, int WR, int WC, int PX, int QY, int S, int FA, int FB, bool EXACT, typename D>
-__global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
+template <int WR, int WC, int PX, int QY, int S, int FA, int FB, bool EXACT, typename D>
+__device__ __forceinline__ void tile(const F8Product& p, uint8_t* lds, int64_t m0, int64_t n0, int64_t part)
 {
-    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    using T = Tile<WR, WC, PX, QY, S>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wi = wave / WC, wj = wave % WC;
-    const int64_t tiles_m = (p.a.rows + T::kRows - 1) / T::kRows, tiles_n = (p.b.rows + T::kCols - 1) / T::kCols;
-    const int64_t part = blockIdx.x / (tiles_m * tiles_n);
-    int64_t ti, tj;
-    tile_at(blockIdx.x - part * (tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
-    const int64_t m0 = ti * T::kRows, n0 = tj * T::kCols;
     const int from = (int)part * p.part_steps;
     const int steps = min(p.part_steps, (int)((p.a.cols + kF8Block - 1) / kF8Block) - from);
 
@@ -355,6 +354,40 @@ __global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
     }
 }
 
+template <int WR, int WC, int PX, int QY, int S, int FA, int FB, bool EXACT, typename D>
+__global__ __launch_bounds__(64 * WR * WC) void tile_kernel(F8Product p)
+{
+    using T = Tile<WR, WC, PX, QY, S>;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int64_t tiles_m = (p.a.rows + T::kRows - 1) / T::kRows, tiles_n = (p.b.rows + T::kCols - 1) / T::kCols;
+    const int64_t part = blockIdx.x / (tiles_m * tiles_n);
+    int64_t i, j;
+    tile_at(xcd_part(blockIdx.x - part * (tiles_m * tiles_n), tiles_m * tiles_n), tiles_m, tiles_n, i, j);
+    tile<WR, WC, PX, QY, S, FA, FB, EXACT, D>(p, lds, i * T::kRows, j * T::kCols, part);
+}
+
+// Tiles of 256 x 256, the first p.whole of them by one workgroup each; the others,
+// which would leave CUs without one in the last round, by p.bands (2 or 4) workgroups
+// of 128 or 64 rows.
+template <int FA, int FB, typename D>
+__global__ __launch_bounds__(512) void big_kernel(F8Product p)
+{
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int64_t tiles_m = (p.a.rows + 255) / 256, tiles_n = (p.b.rows + 255) / 256;
+    int64_t i, j;
+    if (blockIdx.x < p.whole) {
+        tile_at(xcd_part(blockIdx.x, p.whole), tiles_m, tiles_n, i, j);
+        tile<2, 4, 4, 2, 2, FA, FB, false, D>(p, lds, i * 256, j * 256, 0);
+        return;
+    }
+    const int64_t u = xcd_part(blockIdx.x - p.whole, (tiles_m * tiles_n - p.whole) * p.bands);
+    tile_at(p.whole + u / p.bands, tiles_m, tiles_n, i, j);
+    const int64_t m0 = i * 256 + u % p.bands * (256 / p.bands);
+    if (m0 >= p.a.rows) return;
+    if (p.bands == 2) tile<2, 4, 2, 2, 3, FA, FB, false, D>(p, lds, m0, j * 256, 0);
+    else tile<2, 4, 1, 2, 3, FA, FB, false, D>(p, lds, m0, j * 256, 0);
+}
+
 // D from the parts' sums, added in the parts' order: four columns a lane.
 template <typename D>
 __global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict__ sums, int parts, int64_t part_elems,
@@ -505,25 +538,33 @@ void launch_tile(const F8Product& p, hipStream_t s)
     const int64_t tiles = (p.a.rows + T::kRows - 1) / T::kRows * ((p.b.rows + T::kCols - 1) / T::kCols);
     const dim3 grid((uint32_t)(tiles * p.parts));
     if (p.parts == 1) {
-        tile_kernel<T, WR, WC, PX, QY, S, FA, FB, EXACT, D><<<grid, dim3(T::kThr), T::kLds, s>>>(p);
+        tile_kernel<WR, WC, PX, QY, S, FA, FB, EXACT, D><<<grid, dim3(T::kThr), T::kLds, s>>>(p);
         return;
     }
     F8Product q = p;
     q.d = p.sums;
     q.ldd = p.ld_sums;
     q.vec = 1;
-    tile_kernel<T, WR, WC, PX, QY, S, FA, FB, EXACT, float><<<grid, dim3(T::kThr), T::kLds, s>>>(q);
+    tile_kernel<WR, WC, PX, QY, S, FA, FB, EXACT, float><<<grid, dim3(T::kThr), T::kLds, s>>>(q);
     const int64_t quads = p.a.rows * ((p.b.rows + 3) / 4);
     join_kernel<D><<<dim3((uint32_t)((quads + kThreads - 1) / kThreads)), kThreads, 0, s>>>(
         p.sums, p.parts, p.part_elems, p.ld_sums, p.a.rows, p.b.rows, static_cast<D*>(p.d), p.ldd, p.vec);
 }
 
+template <int FA, int FB, typename D>
+void launch_big(const F8Product& p, hipStream_t s)
+{
+    const int64_t n = (p.a.rows + 255) / 256 * ((p.b.rows + 255) / 256);
+    constexpr int lds = Tile<2, 4, 2, 2, 3>::kLds;
+    static_assert(lds >= Tile<2, 4, 4, 2, 2>::kLds && lds >= Tile<2, 4, 1, 2, 3>::kLds, "LDS of the largest of the three");
+    big_kernel<FA, FB, D><<<dim3((uint32_t)(p.whole + (n - p.whole) * p.bands)), dim3(512), lds, s>>>(p);
+}
+
 template <int FA, int FB, typename D, int NW, int AR>
 void launch_thin(const F8Product& p, hipStream_t s)
 {
-    constexpr int R = NW == 8 && AR == 32 ? 2 : 3;   // what LDS holds
-    using T = Thin<NW, R, AR>;
-    thin_kernel<T, NW, R, AR, FA, FB, D><<<dim3((uint32_t)((p.b.rows + 31) / 32)), dim3(64 * NW), T::kLds, s>>>(p);
+    using T = Thin<NW, 3, AR>;
+    thin_kernel<T, NW, 3, AR, FA, FB, D><<<dim3((uint32_t)((p.b.rows + 31) / 32)), dim3(64 * NW), T::kLds, s>>>(p);
 }
 
 template <int FA, int FB, typename D>
@@ -531,23 +572,15 @@ void launch_kind(const F8Product& p, hipStream_t s)
 {
     constexpr bool EXACT = sizeof(D) == 4;
     switch (p.kind) {
-    case kF8Thin4:
+    case kF8Thin:
         if (p.a.rows <= 8) launch_thin<FA, FB, D, 4, 8>(p, s);
         else if (p.a.rows <= 16) launch_thin<FA, FB, D, 4, 16>(p, s);
         else launch_thin<FA, FB, D, 4, 32>(p, s);
         break;
-    case kF8Thin8:
-        if (p.a.rows <= 8) launch_thin<FA, FB, D, 8, 8>(p, s);
-        else if (p.a.rows <= 16) launch_thin<FA, FB, D, 8, 16>(p, s);
-        else launch_thin<FA, FB, D, 8, 32>(p, s);
-        break;
     case kF8Tile64: launch_tile<FA, FB, EXACT, D, 2, 2, 1, 1, 4>(p, s); break;
     case kF8Tile128: launch_tile<FA, FB, EXACT, D, 2, 2, 2, 2, 2>(p, s); break;
-    case kF8Tile128Deep: launch_tile<FA, FB, EXACT, D, 2, 2, 2, 2, 4>(p, s); break;
     default:
-        if constexpr (EXACT) launch_tile<FA, FB, EXACT, D, 2, 2, 2, 2, 2>(p, s);
-        else if (p.kind == kF8Tile128x256) launch_tile<FA, FB, EXACT, D, 2, 4, 2, 2, 3>(p, s);
-        else launch_tile<FA, FB, EXACT, D, 2, 4, 4, 2, 2>(p, s);
+        if constexpr (!EXACT) launch_big<FA, FB, D>(p, s);
     }
 }
 
