@@ -524,3 +524,14 @@ def test_small_changes_add_up(env):
     assert float(d.square().mean() / exact_m.square().mean()) <= 0.021
     # (mean of 65,536: six standard errors)
     assert abs(float(d.mean())) <= 6 * float(d.std()) / n ** 0.5
+
+
+def test_calls_run_on_torchs_current_stream(env):
+    from zero_sharded_mixed_zero1_amd import binding
+    torch, dev = env
+    side = torch.cuda.Stream()
+    assert binding._stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert binding._stream(None) == side.cuda_stream == torch.cuda.current_stream().cuda_stream
+    assert binding._stream(side) == side.cuda_stream
+    assert binding._stream(None) == torch.cuda.current_stream().cuda_stream != side.cuda_stream

@@ -201,27 +201,71 @@ zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int6
     return finish(s);
 }
 
+// What a workgroup takes, in us: a block of 128 of the summed axis where its CU has
+// one workgroup and where it has two, and what comes beside the blocks.  From
+// products of 64 to 8192 rows by 512 to 11008 by 768 to 11008 on an MI355X; the
+// choice is that of the least measured time in all but a few of them, where it is
+// within 15 % of that (1024 x 4096 x 4096: tiles of 64 27.7 us, 128 26.3, 256 in bands of
+// 64 rows 22.8; 512 x 4096 x 4096: 15.9, 25.0, 20.3; 2048 x 4096 x 4096: 52, 34.7, 34.9;
+// 8192 x 11008 x 4096: 607, 407, 326).
+struct TileCost {
+    int side;
+    double one, two, fixed;
+};
+static constexpr TileCost kCosts[2][2] = {{{64, 0.26, 0.44, 1.5}, {128, 0.73, 1.04, 2.0}},    // into bf16
+                                          {{64, 0.44, 0.70, 1.5}, {128, 0.93, 1.78, 2.0}}};   // into fp32
+static constexpr double kBandCost[3] = {1.7, 0.95, 0.64}, kBandFixed[3] = {4.0, 3.0, 2.5};     // 256, 128, 64 rows of 256
+static constexpr double kJoinFixed = 3.0, kJoinBytes = 6e6;                                    // us, bytes a us
+constexpr int kMaxParts = 16, kChip = 256;   // CUs the rule counts with (it decides speed, not results' bits alone)
+
 // Kernel and parts of a product.
 static void choose(F8Product& p)
 {
     const int64_t m = p.a.rows, n = p.b.rows, per = blocks(p.a.cols);
-    p.kind = m <= 32 ? kF8Thin : m <= 512 ? kF8Tile64 : m <= 1024 || p.f32 ? kF8Tile128 : kF8Tile256;
     p.parts = 1;
-    if (const char* e = std::getenv("F8_KIND")) p.kind = std::atoi(e);
-    if (const char* e = std::getenv("F8_PARTS")) p.parts = std::atoi(e);
-    if (p.f32 && p.kind == kF8Tile256) p.kind = kF8Tile128;
-    const int64_t tiles = (m + 255) / 256 * ((n + 255) / 256), rest = tiles % 256;
-    p.whole = tiles - rest;
-    p.bands = rest > 128 ? 1 : rest > 64 ? 2 : 4;
-    if (p.bands == 1) { p.whole = tiles; p.bands = 2; }
-    if (const char* e = std::getenv("F8_BANDS")) { p.bands = std::atoi(e); if (p.bands == 1) { p.whole = tiles; p.bands = 2; } }
-    if (p.kind == kF8Tile256) p.parts = 1;
-    p.part_steps = (int)((per + p.parts - 1) / p.parts);
-    if (p.part_steps < 1) p.part_steps = 1;
-    p.parts = per > 0 ? (int)((per + p.part_steps - 1) / p.part_steps) : 1;
+    p.part_steps = (int)(per > 0 ? per : 1);
+    p.whole = 0;
+    p.bands = 2;
     p.sums = nullptr;
     p.ld_sums = up(n, 4);
     p.part_elems = m * p.ld_sums;
+    if (m <= 32) {
+        p.kind = kF8Thin;
+        return;
+    }
+    double best = 1e300;
+    for (int k = 0; k < 2; ++k) {
+        const TileCost& c = kCosts[p.f32][k];
+        const int64_t tiles = (m + c.side - 1) / c.side * ((n + c.side - 1) / c.side);
+        for (int parts = 1; parts <= kMaxParts; parts *= 2) {
+            const int64_t steps = per > 0 ? (per + parts - 1) / parts : 1;
+            const int64_t groups = tiles * (per > 0 ? (per + steps - 1) / steps : 1);
+            if (parts > 1 && (steps < 2 || tiles * parts > 2 * kChip)) break;
+            const double t = groups <= kChip ? steps * c.one + c.fixed
+                                             : (double)((groups + 2 * kChip - 1) / (2 * kChip)) * (steps * c.two + c.fixed);
+            const double join = parts > 1 ? kJoinFixed + 8.0 * parts * (double)m * (double)n / kJoinBytes : 0.0;
+            if (t + join < best) {
+                best = t + join;
+                p.kind = k == 0 ? kF8Tile64 : kF8Tile128;
+                p.part_steps = (int)steps;
+                p.parts = (int)(per > 0 ? (per + steps - 1) / steps : 1);
+            }
+        }
+    }
+    if (!p.f32) {
+        const int64_t tiles = (m + 255) / 256 * ((n + 255) / 256), rest = tiles % kChip;
+        const int bands = rest == 0 || rest > kChip / 2 ? 1 : rest > kChip / 4 ? 2 : 4;
+        const int64_t whole = bands == 1 ? tiles : tiles - rest;
+        double t = (double)((whole + kChip - 1) / kChip) * (per * kBandCost[0] + kBandFixed[0]);
+        if (bands > 1) t += per * kBandCost[bands / 2] + kBandFixed[bands / 2];
+        if (t < best) {
+            p.kind = kF8Tile256;
+            p.parts = 1;
+            p.part_steps = (int)(per > 0 ? per : 1);
+            p.whole = whole;
+            p.bands = bands == 1 ? 2 : bands;
+        }
+    }
 }
 
 // Shared checks of the product and its workspace's size.

@@ -563,8 +563,9 @@ void launch_big(const F8Product& p, hipStream_t s)
 template <int FA, int FB, typename D, int NW, int AR>
 void launch_thin(const F8Product& p, hipStream_t s)
 {
-    using T = Thin<NW, 3, AR>;
-    thin_kernel<T, NW, 3, AR, FA, FB, D><<<dim3((uint32_t)((p.b.rows + 31) / 32)), dim3(64 * NW), T::kLds, s>>>(p);
+    constexpr int R = AR == 32 ? 2 : 3;   // two workgroups a CU
+    using T = Thin<NW, R, AR>;
+    thin_kernel<T, NW, R, AR, FA, FB, D><<<dim3((uint32_t)((p.b.rows + 31) / 32)), dim3(64 * NW), T::kLds, s>>>(p);
 }
 
 template <int FA, int FB, typename D>
