@@ -112,13 +112,15 @@ def random_bits(first, counts, n):
 
 
 def encode_random(x, bits16, which):
-    """Codes and exponent bytes of fp32 values, rounded by 16 random bits each: binary32's own bits of x 2^(7-b),
-    scaled so that its exponent field is the code's."""
+    """Codes and exponent bytes of fp32 values rounded by 16 random bits each: floor(|x| / step + u / 65536) steps, in 64
+    bits (exact: a binary32 value over a power of two, and 16 bits beside its 24)."""
     b = exponents(x)
-    inv = (2.0 ** (127.0 - per_element(b, x.size))).astype(np.float32)
-    with np.errstate(under="ignore"):
-        u = (np.abs(np.where(np.isfinite(x), x, 0)).astype(np.float32) * inv * np.float32(2.0 ** -120)).view(np.uint32)
-    code = (u.astype(np.int64) + (bits16.astype(np.int64) << 4)) >> 20
+    y = np.abs(np.where(np.isfinite(x), x, 0)).astype(np.float64) * 2.0 ** (127.0 - per_element(b, x.size))
+    _, e = np.frexp(y)
+    e = np.where(y > 0, np.maximum(e - 1, -6), -6)          # the binade; below 2^-6 steps are equal
+    k = np.floor(y / 2.0 ** (e - 3.0) + bits16.astype(np.float64) / 65536).astype(np.int64)
+    # k steps of 2^(e - 3): 8 to 16 in the binade of e (16: the next one's first), 0 to 8 below
+    code = k + (e + 6) * 8
     return _finish(x, code, which), b
 
 

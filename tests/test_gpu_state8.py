@@ -535,3 +535,51 @@ def test_calls_run_on_torchs_current_stream(env):
         assert binding._stream(None) == side.cuda_stream == torch.cuda.current_stream().cuda_stream
     assert binding._stream(side) == side.cuda_stream
     assert binding._stream(None) == torch.cuda.current_stream().cuda_stream != side.cuda_stream
+
+
+def test_rounding_at_its_borders(env):
+    """Magnitudes and bits at which the sum just reaches, or just misses, the next code, in every binade of the codes and
+    below the smallest normal one, where binary32's scaled bits are rounded to 2^-29 of a unit first."""
+    torch, dev = env
+    rng = np.random.default_rng(9)
+    n = 256 * 512
+    first, counts = 0, np.zeros(ref.blocks(n), np.uint32)
+    bits = ref.random_bits(first, counts, n).astype(np.int64)
+    for which, half in ((ref.M, bits & 0xFFFF), (ref.V, bits >> 16)):
+        # a value whose fraction of a code's step is 1 - u / 65536 give or take less than 2^-20
+        e = rng.integers(-9, 7, n)
+        step = 2.0 ** (np.maximum(e, -6) - 3)
+        k = np.floor(2.0 ** e / step + rng.integers(0, 8, n) * (e >= -6))
+        near = (1 - half / 65536.0) + rng.choice([-1, -0.75, -0.5, -0.25, 0, 0.25, 0.5, 1], n) * 2.0 ** -20
+        y = (k + np.clip(near, 0, 1 - 2.0 ** -20)) * step
+        y[::256] = 200.0                                   # the block's largest
+        x = y.astype(np.float32)
+        # a step that leaves x: m = 0 * m + 1 * g (beta1 = 0), r = sqrt(0 * v + 1 * g^2); g fp32
+        hp = dict(lr=0.0, beta1=0.0, beta2=0.0, eps=1e-8, weight_decay=0.0, max_norm=math.inf, step=1)
+        m, v = (torch.zeros(z.state8_bytes(n), dtype=torch.uint8, device=dev) for _ in range(2))
+        master, param = torch.zeros(n, device=dev), torch.zeros(n, dtype=torch.int16, device=dev)
+        z.adamw_step(torch.from_numpy(x).to(dev), None, 0, n, master, m, v, param, hp, torch.ones(1, dtype=torch.float64, device=dev),
+                     1, flags=z.MV_8BIT)
+        r = np.sqrt(x * x) if which == ref.V else np.sqrt(x * x)
+        want = ref.round_step(x, r, np.zeros(ref.blocks(n), np.uint32), np.zeros(ref.blocks(n), np.uint32), first)
+        gc, gw = ref.split(m.cpu().numpy(), n)
+        assert np.array_equal(gw, want[1]) and np.array_equal(gc, want[0]), f"m: {(gc != want[0]).sum()} differ"
+        gc, gw = ref.split(v.cpu().numpy(), n)
+        assert np.array_equal(gw, want[3]) and np.array_equal(gc, want[2]), f"v: {(gc != want[2]).sum()} differ"
+
+
+def test_param_is_the_nearest_bf16_of_any_master(env):
+    """Masters of every kind of bits through a step that changes none of them."""
+    torch, dev = env
+    n = 1 << 20
+    u = np.random.default_rng(4).integers(0, 1 << 32, n, dtype=np.uint64).astype(np.uint32)
+    u[:8] = [0x3F808000, 0x3F818000, 0x7F7FFFFF, 0x7F7F8000, 0x00008000, 0x00018000, 0x80000000, 0x7F800000]
+    u[2048:4096] &= 0x807FFFFF                             # subnormals
+    x = u.view(np.float32)
+    hp = dict(lr=0.0, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.0, max_norm=math.inf, step=1)
+    m, v = (torch.zeros(z.state8_bytes(n), dtype=torch.uint8, device=dev) for _ in range(2))
+    master, param = torch.from_numpy(x.copy()).to(dev), torch.zeros(n, dtype=torch.int16, device=dev)
+    g = torch.full((n,), 1e-3, device=dev)
+    z.adamw_step(g, None, 0, n, master, m, v, param, hp, torch.ones(1, dtype=torch.float64, device=dev), 1, flags=z.MV_8BIT)
+    assert_f32_equal(master.cpu().numpy(), x, "master")
+    assert_bf16_equal(to_np_u16(param), bf16_bits(x), "param")

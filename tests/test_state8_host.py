@@ -103,15 +103,18 @@ def test_reference_nearest_is_within_half_a_step():
 
 
 def test_reference_random_is_floor_plus_share():
-    x = _sample(50_000, 1)
+    """Against exact rational arithmetic."""
+    from fractions import Fraction
+    x = _sample(3000, 1)
     bits = np.random.default_rng(2).integers(0, 65536, x.size).astype(np.uint64)
     codes, b = ref.encode_random(x, bits, ref.M)
-    y = np.abs(x.astype(np.float64)) * 2.0 ** (127.0 - ref.per_element(b, x.size))
-    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(y, 1e-30))), -6) - 3)
-    want = np.floor(y / step + bits.astype(np.float64) / 65536) * step
-    got = np.abs(ref.E4M3[codes])
-    # binary32 keeps 2^-29 of a unit below the format's smallest normal: a floor in 2^19 may go the other way
-    assert (got != want).mean() < 1e-4 and (np.abs(got - want) <= step).all()
+    for xi, u, c, bi in zip(x, bits, codes, ref.per_element(b, x.size)):
+        y = abs(Fraction(float(xi))) / (Fraction(2) ** (int(bi) - 127))
+        e = -6
+        while Fraction(2) ** (e + 1) <= y:
+            e += 1
+        step = Fraction(2) ** (e - 3)
+        assert Fraction(float(abs(ref.E4M3[c]))) == (y / step + Fraction(int(u), 65536)).__floor__() * step
 
 
 def test_reference_random_rounding_is_right_on_average():

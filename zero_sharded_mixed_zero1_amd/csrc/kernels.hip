@@ -151,6 +151,20 @@ __device__ __forceinline__ void st8_bf16(uint16_t* p, const float (&x)[8])
     st_nt(reinterpret_cast<u32x2*>(p + a + 256), w);
 }
 
+// The same by the conversion instruction (nearest even; another NaN's payload).
+__device__ __forceinline__ void st8_bf16_cvt(uint16_t* p, const float (&x)[8])
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x[2 * k], x[2 * k + 1]}), bf16x2));
+    const int a = quad_a();
+    st_nt(reinterpret_cast<u32x2*>(p + a), u32x2{w[0], w[1]});
+    st_nt(reinterpret_cast<u32x2*>(p + a + 256), u32x2{w[2], w[3]});
+}
+
 __device__ __forceinline__ void ld8_f32(const float* p, float (&x)[8])
 {
     const int a = quad_a();
@@ -613,22 +627,17 @@ __device__ __forceinline__ void update8_bytes(const Span& sp, int64_t si, const 
             r[j] = adamw_elem(g, p[4 * h + j], m[j], v[j], c);
         }
         const Top8 tm = top8<false>(m), tr = top8<true>(r);
-        const float im = inverse8(tm.b), ir = inverse8(tr.b);
         const uint32_t key = key8(sp.first + (uint32_t)si + 512u * wave + 256u * h, mw[h] >> 8) + 4u * (threadIdx.x & 63);
-        uint32_t cm = 0, cr = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t bits = mix32(key + j);
-            cm |= code_m(m[j], im, bits, tm) << (8 * j);
-            cr |= code_r(r[j], ir, bits, tr) << (8 * j);
-        }
+        const uint32_t bits[4] = {mix32(key), mix32(key + 1), mix32(key + 2), mix32(key + 3)};
+        uint32_t cm, cr;
+        codes4(m, r, bits, tm, tr, cm, cr);
         st_nt(reinterpret_cast<uint32_t*>(mp + 256 * h), cm);
         st_nt(reinterpret_cast<uint32_t*>(vp + 256 * h), cr);
         mwn[h] = next_word(mw[h], tm.b);
         vwn[h] = next_word(vw[h], tr.b);
     }
     st8_f32(sp.master + si, p);
-    st8_bf16(sp.param + si, p);
+    st8_bf16_cvt(sp.param + si, p);
     if ((threadIdx.x & 63) == 0) {
         st_nt(reinterpret_cast<u32x2w*>(sp.mw + blk), mwn);
         st_nt(reinterpret_cast<u32x2w*>(sp.vw + blk), vwn);
@@ -667,15 +676,14 @@ __device__ __forceinline__ void update_blocks(const Span& sp, int64_t si, int n,
             }
         }
         const Top8 tm = top8<false>(m), tr = top8<true>(r);
-        const float im = inverse8(tm.b), ir = inverse8(tr.b);
         const uint32_t key = key8(sp.first + (uint32_t)si + (uint32_t)(k * kBlock8), mw >> 8);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int j = k * kBlock8 + lane + 64 * i;
             const uint32_t bits = mix32(key + lane + 64 * i);
             if (j < n) {
-                mp[j] = (uint8_t)code_m(m[i], im, bits, tm);
-                vp[j] = (uint8_t)code_r(r[i], ir, bits, tr);
+                mp[j] = (uint8_t)code_m(m[i], bits, tm);
+                vp[j] = (uint8_t)code_r(r[i], bits, tr);
             }
         }
         if (lane == 0) {

@@ -62,6 +62,8 @@ __device__ __forceinline__ void decode4(uint32_t codes, float scale, float (&x)[
     x[0] = a[0] * scale; x[1] = a[1] * scale; x[2] = b[0] * scale; x[3] = b[1] * scale;
 }
 
+__device__ __forceinline__ float inverse8(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+
 // The exponent byte of a block from the largest of its values' abs_bits, and
 // whether any of them is infinite, NaN or in the last binade.  Infinite ones and NaN
 // leave the others' scale alone (the largest finite one sets it) and get NaN's
@@ -75,10 +77,10 @@ struct Top8 {
 template <bool V, int N>
 __device__ __forceinline__ Top8 top8(const float (&x)[N])
 {
-    uint32_t t = 0;
+    float f = 0.0f;   // (the maximum that NaN goes through: three operands, magnitudes for free)
 #pragma unroll
-    for (int i = 0; i < N; ++i) t = max(t, abs_bits(x[i]));
-    t = wave_max(t);
+    for (int i = 0; i < N; ++i) f = __builtin_elementwise_maximum(f, fabsf(x[i]));
+    uint32_t t = wave_max(abs_bits(f));
     const bool special = t >= kHugeBits[V];
     if (t >= kInfBits) {
         t = 0;
@@ -107,37 +109,64 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x)
 // the same state and gradients give the same bits, in a replayed graph too.
 __device__ __forceinline__ uint32_t key8(uint32_t first, uint32_t count) { return mix32(mix32(first) + count); }
 
-// Code of x >= 0 (its magnitude): 2^-120 brings the format's exponent 0 to binary32's,
-// so that the bits above the twentieth are the code, subnormals included.
-__device__ __forceinline__ uint32_t code_random(float x, float inv, uint32_t bits16)
+// x's code, rounded by 16 bits, into byte J of `old`.  The instruction divides by the
+// scale (a power of two) and adds the upper 20 of its 32 random bits below the last
+// bit kept: floor(|x| / step + u / 65536) steps, over the whole range of codes.
+template <int J>
+__device__ __forceinline__ uint32_t put_random(uint32_t old, float x, float scale, uint32_t bits16_high)
 {
-    const uint32_t u = __float_as_uint((fabsf(x) * inv) * 0x1p-120f);
-    return (u + (bits16 << 4)) >> 20;
+    return (uint32_t)__builtin_amdgcn_cvt_scalef32_sr_fp8_f32((int)old, x, bits16_high, scale, J);
 }
 
-__device__ __forceinline__ float inverse8(uint32_t b) { return __uint_as_float((254u - b) << 23); }
-
-// The code of a value in a block with special ones (see top8).
+// A code in a block with special values (see top8).
 template <bool V>
-__device__ __forceinline__ uint32_t held8(float x, uint32_t c, uint32_t sign, const Top8& t)
+__device__ __forceinline__ uint32_t held8(float x, uint32_t code, const Top8& t)
 {
+    uint32_t c = code & 0x7fu;
     if (t.b == kLastB[V]) c = min(c, kLast8);
-    return abs_bits(x) >= kInfBits ? kNan8 : c | sign;
+    return abs_bits(x) >= kInfBits ? kNan8 : c | (code & 0x80u);
 }
 
 // m's code, and r's: a root that is not zero does not become zero (m / (0 + eps)
 // would throw the parameter off), it stays at the smallest step.
-__device__ __forceinline__ uint32_t code_m(float m, float inv, uint32_t bits, const Top8& t)
+__device__ __forceinline__ uint32_t code_m(float m, uint32_t bits, const Top8& t)
 {
-    const uint32_t c = code_random(m, inv, bits & 0xffffu), sign = (__float_as_uint(m) >> 24) & 0x80u;
-    return t.special ? held8<false>(m, c, sign, t) : c | sign;
+    const uint32_t c = put_random<0>(0, m, scale8(t.b), bits << 16) & 0xffu;
+    return t.special ? held8<false>(m, c, t) : c;
 }
 
-__device__ __forceinline__ uint32_t code_r(float r, float inv, uint32_t bits, const Top8& t)
+__device__ __forceinline__ uint32_t code_r(float r, uint32_t bits, const Top8& t)
 {
-    uint32_t c = code_random(r, inv, bits >> 16);
+    uint32_t c = put_random<0>(0, r, scale8(t.b), bits & 0xffff0000u) & 0xffu;
     c = max(c, r > 0.0f ? 1u : 0u);
-    return t.special ? held8<true>(r, c, 0, t) : c;
+    return t.special ? held8<true>(r, c & 0x7fu, t) : c;
+}
+
+// Four codes of m and of r from their elements' bits.  The instructions' own for all
+// blocks but those with special values and, of r, quads with a code of zero (which
+// may stand for a root that is not zero).
+__device__ __forceinline__ void codes4(const float (&m)[4], const float (&r)[4], const uint32_t (&bits)[4],
+                                       const Top8& tm, const Top8& tr, uint32_t& cm, uint32_t& cr)
+{
+    const float sm = scale8(tm.b), sr = scale8(tr.b);
+    cm = put_random<0>(0, m[0], sm, bits[0] << 16);
+    cm = put_random<1>(cm, m[1], sm, bits[1] << 16);
+    cm = put_random<2>(cm, m[2], sm, bits[2] << 16);
+    cm = put_random<3>(cm, m[3], sm, bits[3] << 16);
+    cr = put_random<0>(0, r[0], sr, bits[0] & 0xffff0000u);
+    cr = put_random<1>(cr, r[1], sr, bits[1] & 0xffff0000u);
+    cr = put_random<2>(cr, r[2], sr, bits[2] & 0xffff0000u);
+    cr = put_random<3>(cr, r[3], sr, bits[3] & 0xffff0000u);
+    if (tm.special) {
+        cm = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cm |= code_m(m[j], bits[j], tm) << (8 * j);
+    }
+    if (tr.special || __any(((cr - 0x01010101u) & ~cr & 0x80808080u) != 0)) {
+        cr = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cr |= code_r(r[j], bits[j], tr) << (8 * j);
+    }
 }
 
 __device__ __forceinline__ uint32_t next_word(uint32_t word, uint32_t b) { return ((word & ~255u) + 256u) | b; }

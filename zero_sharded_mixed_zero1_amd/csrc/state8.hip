@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void encode_kernel(const T* __restrict__ 
         for (int i = 0; i < 4; ++i) {
             c[i] = code_near(y[i] * inv);
             if constexpr (V) c[i] = max(c[i] & 0x7fu, y[i] > 0.0f ? 1u : 0u);   // (the root of -0 is -0)
-            if (t.special) c[i] = held8<V>(y[i], c[i] & 0x7fu, c[i] & 0x80u, t);
+            if (t.special) c[i] = held8<V>(y[i], c[i], t);
         }
         if (whole) {
             *reinterpret_cast<uint32_t*>(codes + at + 4 * lane) = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
