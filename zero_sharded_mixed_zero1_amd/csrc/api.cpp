@@ -165,6 +165,16 @@ Shape update_shape(int64_t units, const DevInfo& d)
     return Shape{grid_for(units, d, big ? kUpdatePerCu : 0), big ? 8 : 1};
 }
 
+// With 8-bit moments (less to move for each tile) a workgroup takes one tile, each
+// XCD's in its own contiguous eighth past kMaxPartials units (adamw8_kernel).
+Shape update8_shape(int64_t units)
+{
+    const bool big = units > kMaxPartials;
+    if (units > (int64_t)1 << 22) units = (int64_t)1 << 22;   // 2^33 elements: fewer than 2^31 threads a launch
+    const int64_t n = big ? (units + 7) / 8 * 8 : units;
+    return Shape{(int)(n > 0 ? n : 1), big ? 8 : 1};
+}
+
 // few: the few-slice sum-of-squares pass (few_slice_pass), whose loads of
 // several tiles at once keep enough in flight with 6 workgroups per CU: the
 // W=1 pass over a 7e9 shard takes 2.14 ms there and 2.39 ms at 8 per CU.
@@ -464,7 +474,7 @@ zero1_status zero1_adamw_step(const float* g, const uint16_t* const* grads, int 
     hipStream_t s = static_cast<hipStream_t>(stream);
     // always launched (also for len == 0) so that info_out is written
     const Scal sc = scalars(hp, flags);
-    const Shape sh = update_shape(tiles(len, vec), d);
+    const Shape sh = mv == kMv8 ? update8_shape(tiles(len, vec)) : update_shape(tiles(len, vec), d);
     const int nb = sh.grid;
     Z1_HIP(launch_adamw_flat(g, r, len, vec, mv, master, m, v, param_bf16, sc, rank_sumsq, n_ranks,
                              hp->max_norm, (flags & ZERO1_CLIP_EPS) ? 1 : 0,
@@ -677,9 +687,10 @@ zero1_status zero1_mta_update(const uint16_t* const* grads, int W, int64_t begin
     const char* tb = static_cast<const char*>(plan->table);
     const PieceDesc* pd = reinterpret_cast<const PieceDesc*>(tb);
     const ChunkDesc* cd = reinterpret_cast<const ChunkDesc*>(tb + round_up(sizeof(PieceDesc) * plan->n_pieces, 256));
-    const Shape sh = update_shape(plan->n_chunks, d);
+    const MvKind mv = mv_kind(plan->flags);
+    const Shape sh = mv == kMv8 ? update8_shape(plan->n_chunks) : update_shape(plan->n_chunks, d);
     const int nb = sh.grid;
-    Z1_HIP(launch_adamw_mta(w.g, r, pd, cd, plan->n_chunks, vec, mv_kind(plan->flags), scalars(hp, flags),
+    Z1_HIP(launch_adamw_mta(w.g, r, pd, cd, plan->n_chunks, vec, mv, scalars(hp, flags),
                             rank_sumsq, n_ranks, hp->max_norm, (flags & ZERO1_CLIP_EPS) ? 1 : 0,
                             reinterpret_cast<NormInfo*>(info_out), nb, sh.split, s));
     return finish(s);

@@ -593,54 +593,72 @@ struct Span {
 };
 
 // Moments in 8 bits (state8.h), the lane's 8 elements of a full tile at state
-// index si: a wave's first quads are one block, its second quads the next.
+// index si: a wave's first quads are one block, its second quads the next.  The
+// codes and words take the default cache policy: the words of a tile are 32 bytes
+// that four waves read and write (with the non-temporal hint 202 M parameters at W = 1
+// take 6 % longer), and moments of up to 100 M parameters stay in the MALL where
+// nothing comes between two steps.
 typedef uint32_t u32x2w __attribute__((ext_vector_type(2), aligned(4)));
 
-__device__ __forceinline__ void update8_bytes(const Span& sp, int64_t si, const float (&gv)[8], const Scal& c,
-                                              bool clip, float coef)
-{
-    using namespace dev8;
-    const int a = quad_a(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    uint8_t* mp = static_cast<uint8_t*>(sp.m) + si + a;
-    uint8_t* vp = static_cast<uint8_t*>(sp.v) + si + a;
-    const int64_t blk = (si >> 8) + 2 * wave;
+struct Bytes8 {   // as loaded
     float p[8];
-    ld8_f32(sp.master + si, p);
-    uint32_t mc[2], vc[2];
+    uint32_t m[2], v[2];
+    u32x2w mw, vw;
+};
+
+__device__ __forceinline__ int64_t first_block(int64_t si)
+{
+    return (si >> 8) + 2 * __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+}
+
+__device__ __forceinline__ void load_bytes(const Span& sp, int64_t si, Bytes8& t)
+{
+    const int a = quad_a();
+    const uint8_t* m = static_cast<const uint8_t*>(sp.m) + si + a;
+    const uint8_t* v = static_cast<const uint8_t*>(sp.v) + si + a;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        mc[h] = ld_nt(reinterpret_cast<const uint32_t*>(mp + 256 * h));
-        vc[h] = ld_nt(reinterpret_cast<const uint32_t*>(vp + 256 * h));
+        t.m[h] = *gbl(reinterpret_cast<const uint32_t*>(m + 256 * h));
+        t.v[h] = *gbl(reinterpret_cast<const uint32_t*>(v + 256 * h));
     }
-    const u32x2 mw = ld_nt(reinterpret_cast<const u32x2w*>(sp.mw + blk));
-    const u32x2 vw = ld_nt(reinterpret_cast<const u32x2w*>(sp.vw + blk));
-    u32x2 mwn, vwn;
+    t.mw = *gbl(reinterpret_cast<const u32x2w*>(sp.mw + first_block(si)));
+    t.vw = *gbl(reinterpret_cast<const u32x2w*>(sp.vw + first_block(si)));
+    ld8_f32(sp.master + si, t.p);
+}
+
+__device__ __forceinline__ void update_bytes(const Span& sp, int64_t si, Bytes8& t, const float (&gv)[8], const Scal& c,
+                                             bool clip, float coef)
+{
+    using namespace dev8;
+    const int a = quad_a();
+    const uint32_t first = sp.first + (uint32_t)si + 512u * (uint32_t)(threadIdx.x >> 6);
+    u32x2w mwn, vwn;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float m[4], r[4], v[4];
-        decode4(mc[h], scale8(mw[h]), m);
-        decode4(vc[h], scale8(vw[h]), r);
+        decode4(t.m[h], scale8(t.mw[h]), m);
+        decode4(t.v[h], scale8(t.vw[h]), r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float g = clip ? gv[4 * h + j] * coef : gv[4 * h + j];
             v[j] = r[j] * r[j];
-            r[j] = adamw_elem(g, p[4 * h + j], m[j], v[j], c);
+            r[j] = adamw_elem(g, t.p[4 * h + j], m[j], v[j], c);
         }
         const Top8 tm = top8<false>(m), tr = top8<true>(r);
-        const uint32_t key = key8(sp.first + (uint32_t)si + 512u * wave + 256u * h, mw[h] >> 8) + 4u * (threadIdx.x & 63);
+        const uint32_t key = key8(first + 256u * h, t.mw[h] >> 8) + 4u * (threadIdx.x & 63);
         const uint32_t bits[4] = {mix32(key), mix32(key + 1), mix32(key + 2), mix32(key + 3)};
         uint32_t cm, cr;
         codes4(m, r, bits, tm, tr, cm, cr);
-        st_nt(reinterpret_cast<uint32_t*>(mp + 256 * h), cm);
-        st_nt(reinterpret_cast<uint32_t*>(vp + 256 * h), cr);
-        mwn[h] = next_word(mw[h], tm.b);
-        vwn[h] = next_word(vw[h], tr.b);
+        *gbl(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(sp.m) + si + a + 256 * h)) = cm;
+        *gbl(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(sp.v) + si + a + 256 * h)) = cr;
+        mwn[h] = next_word(t.mw[h], tm.b);
+        vwn[h] = next_word(t.vw[h], tr.b);
     }
-    st8_f32(sp.master + si, p);
-    st8_bf16_cvt(sp.param + si, p);
+    st8_f32(sp.master + si, t.p);
+    st8_bf16_cvt(sp.param + si, t.p);
     if ((threadIdx.x & 63) == 0) {
-        st_nt(reinterpret_cast<u32x2w*>(sp.mw + blk), mwn);
-        st_nt(reinterpret_cast<u32x2w*>(sp.vw + blk), vwn);
+        *gbl(reinterpret_cast<u32x2w*>(sp.mw + first_block(si))) = mwn;
+        *gbl(reinterpret_cast<u32x2w*>(sp.vw + first_block(si))) = vwn;
     }
 }
 
@@ -758,11 +776,7 @@ __device__ __forceinline__ void update_tile(const Span& sp, const Reduce& r, int
         float gv[8];
         if constexpr (GSRC == 0) ld8_g(sp.g + gi, gv);
         else reduce8(r, gi, gv);
-        if constexpr (MV == kMv8) update8_bytes(sp, si, gv, c, clip, coef);
-        else update8<MV>(sp, si, gv, c, clip, coef);
-    } else if constexpr (MV == kMv8) {
-        update_blocks(sp, si, n, c, clip, coef,
-                      [&](int j) { return (GSRC == 0) ? ld_g(sp.g + gi + j) : reduce1(r, gi + j); });
+        update8<MV>(sp, si, gv, c, clip, coef);
     } else {
         for (int j = threadIdx.x; j < n; j += kThreads) {
             const float gj = (GSRC == 0) ? ld_g(sp.g + gi + j) : reduce1(r, gi + j);
@@ -831,6 +845,74 @@ __global__ __launch_bounds__(kThreads) void adamw_mta_kernel(const float* __rest
         }
     }
 }
+
+// Gradient slices of a lane's 8 elements in one go: exactly FEW (1 to 4) of them, or
+// g itself (FEW = 0), or any number (FEW = -1).
+template <int FEW>
+__device__ __forceinline__ void gradient8(const float* g, const Reduce& r, int64_t e, float (&s)[8])
+{
+    if constexpr (FEW == 0) {
+        ld8_g(g + e, s);
+    } else if constexpr (FEW < 0) {
+        reduce8(r, e, s);
+    } else {
+        Raw x[FEW];
+#pragma unroll
+        for (int w = 0; w < FEW; ++w) x[w] = ld_raw(r.gp.p[w] + e);
+        raw_init(s, x[0]);
+#pragma unroll
+        for (int w = 1; w < FEW; ++w) raw_add(s, x[w]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = average(r, s[j]);
+    }
+}
+
+// The update with 8-bit moments, flat (one span of len elements) or over a plan's
+// chunks.  A workgroup takes one tile where the grid has as many: each tile moves half
+// of what it does with fp32 moments, so more of them have to be under way (a step of
+// 200 M parameters at W = 1 takes 655 us so, 703 in a persistent grid of 32 workgroups a
+// CU and 742 of 8), and the slices of W = 1 to 4 are loaded by code of their own (635;
+// the kernel has 70 registers then and not 88).
+//
+// HBM-bound: 16 bytes a parameter at W = 1 (5.8 TB/s), 18 with g from the workspace
+// (the 117 M of a step at W = 8: 6.1).
+template <bool VEC, int FEW, bool FLAT>
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(Span flat, Reduce r, const PieceDesc* __restrict__ pieces,
+                                                          const ChunkDesc* __restrict__ chunks, int64_t units,
+                                                          int64_t len, Scal c, ClipArgs ca, int split)
+{
+    use_device_scalars(c, ca.max_norm);
+    bool clip;
+    float coef;
+    block_clip(ca, clip, coef);
+    const Units u = xcd_units(units, split);
+    for (int64_t k = u.lo; k < u.hi; k += u.step) {
+        Span sp = flat;
+        int64_t gi = k * kTile, si = gi;
+        int n;
+        if constexpr (FLAT) {
+            n = (int)(len - gi < kTile ? len - gi : kTile);
+        } else {
+            const ChunkDesc ch = chunks[k];
+            const PieceDesc pc = pieces[ch.piece];
+            sp = chunk_span<kMv8>(pc, ch);
+            gi = pc.shard_offset + ch.offset;
+            si = 0;
+            n = ch.len;
+        }
+        if (VEC && n == kTile) {
+            Bytes8 t;
+            float gv[8];
+            load_bytes(sp, si, t);
+            gradient8<FEW>(flat.g, r, gi, gv);
+            update_bytes(sp, si, t, gv, c, clip, coef);
+        } else {
+            update_blocks(sp, si, n, c, clip, coef,
+                          [&](int j) { return (FEW == 0) ? ld_g(flat.g + gi + j) : reduce1(r, gi + j); });
+        }
+    }
+}
+static_assert(kChunkElems == kTile, "a chunk is a tile");
 
 // ------------------------------------------------------------- launch helper
 // Timing events requested for the next launch on this thread
@@ -933,13 +1015,28 @@ hipError_t launch_adamw_flat(const float* g, const Reduce& r, int64_t len, bool 
         sp.vw = reinterpret_cast<uint32_t*>(static_cast<char*>(v) + state8_words_at(len));
     }
     hipError_t e;
+    if (mv == kMv8) {
+        const int64_t units = (len + kTile - 1) / kTile;
+        const PieceDesc* pieces = nullptr;
+        const ChunkDesc* chunks = nullptr;
+#define Z1_8(V, FEW) return run(adamw8_kernel<V, FEW, true>, grid, s, sp, r, pieces, chunks, units, len, sc, ca, split)
+        if (!vec) { if (g) Z1_8(false, 0); else Z1_8(false, -1); }
+        if (g) Z1_8(true, 0);
+        switch (r.W) {
+        case 1: Z1_8(true, 1);
+        case 2: Z1_8(true, 2);
+        case 3: Z1_8(true, 3);
+        case 4: Z1_8(true, 4);
+        default: Z1_8(true, -1);
+        }
+#undef Z1_8
+    }
 #define Z1_FLAT(V, GS, MV) e = run(adamw_flat_kernel<V, GS, MV>, grid, s, sp, r, len, sc, ca, split)
     const int gs = g ? 0 : 1;
-#define Z1_FLAT_MV(V, GS)                                \
-    do {                                               \
-        if (mv == kMv8) Z1_FLAT(V, GS, kMv8);          \
-        else if (mv == kMvBf16) Z1_FLAT(V, GS, kMvBf16); \
-        else Z1_FLAT(V, GS, kMvF32);                   \
+#define Z1_FLAT_MV(V, GS)                           \
+    do {                                            \
+        if (mv == kMvBf16) Z1_FLAT(V, GS, kMvBf16); \
+        else Z1_FLAT(V, GS, kMvF32);                \
     } while (0)
     if (vec) {
         if (gs == 0) Z1_FLAT_MV(true, 0); else Z1_FLAT_MV(true, 1);
@@ -959,13 +1056,27 @@ hipError_t launch_adamw_mta(const float* g, const Reduce& r, const PieceDesc* pi
     const dim3 grid(nblocks);
     const ClipArgs ca{rank_sumsq, n_ranks, max_norm, clip_eps, info_out};
     hipError_t e;
+    if (mv == kMv8) {
+        const Span sp{g, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0};
+        const int64_t units = n_chunks, len = 0;
+#define Z1_8(V, FEW) return run(adamw8_kernel<V, FEW, false>, grid, s, sp, r, pieces, chunks, units, len, sc, ca, split)
+        if (!vec) { if (g) Z1_8(false, 0); else Z1_8(false, -1); }
+        if (g) Z1_8(true, 0);
+        switch (r.W) {
+        case 1: Z1_8(true, 1);
+        case 2: Z1_8(true, 2);
+        case 3: Z1_8(true, 3);
+        case 4: Z1_8(true, 4);
+        default: Z1_8(true, -1);
+        }
+#undef Z1_8
+    }
 #define Z1_MTA(V, GS, MV) e = run(adamw_mta_kernel<V, GS, MV>, grid, s, g, r, pieces, chunks, n_chunks, sc, ca, split)
     const int gs = g ? 0 : 1;
-#define Z1_MTA_MV(V, GS)                                \
-    do {                                               \
-        if (mv == kMv8) Z1_MTA(V, GS, kMv8);          \
-        else if (mv == kMvBf16) Z1_MTA(V, GS, kMvBf16); \
-        else Z1_MTA(V, GS, kMvF32);                   \
+#define Z1_MTA_MV(V, GS)                           \
+    do {                                           \
+        if (mv == kMvBf16) Z1_MTA(V, GS, kMvBf16); \
+        else Z1_MTA(V, GS, kMvF32);                \
     } while (0)
     if (vec) {
         if (gs == 0) Z1_MTA_MV(true, 0); else Z1_MTA_MV(true, 1);

@@ -142,9 +142,9 @@ __device__ __forceinline__ uint32_t code_r(float r, uint32_t bits, const Top8& t
     return t.special ? held8<true>(r, c & 0x7fu, t) : c;
 }
 
-// Four codes of m and of r from their elements' bits.  The instructions' own for all
-// blocks but those with special values and, of r, quads with a code of zero (which
-// may stand for a root that is not zero).
+// Four codes of m and of r from their elements' bits: an instruction a code, but in
+// blocks with special values and, of r, where a lane has a code of zero (which may
+// stand for a root that is not zero).
 __device__ __forceinline__ void codes4(const float (&m)[4], const float (&r)[4], const uint32_t (&bits)[4],
                                        const Top8& tm, const Top8& tr, uint32_t& cm, uint32_t& cr)
 {
