@@ -406,7 +406,7 @@ zero1_status zero1_mta_step_static(const uint16_t* const* grads, int W, int64_t 
  * sum of zero1_partials_sum (and of an empty zero1_shard_reduce /
  * zero1_grad_norm).  The request is dropped when that call returns, whether
  * or not it launched anything; a later request replaces an earlier one.  The
- * Muon calls neither take it nor drop it.
+ * Muon calls, the 8-bit conversions, quantize and product neither take it nor drop it.
  *
  * The events are created and owned by the caller (hipEventCreate, timing
  * enabled, on the device the step runs on) and must outlive the kernel.
@@ -506,7 +506,7 @@ zero1_status zero1_arena_plan(const zero1_arena_request* req, zero1_arena_layout
  * that by up to 2^-16 of the largest.
  *
  * zero1_state8_bytes: bytes of a buffer of n elements (0 for n <= 0).
- * zero1_state8_encode: x (n fp32, or bf16 with ZERO1_MV_BF16; any alignment of
+ * zero1_state8_encode: x (n <= 2^34 fp32, or bf16 with ZERO1_MV_BF16; any alignment of
  *   its element) to codes, to the nearest, ties to even, and counts of 0.
  *   which: ZERO1_STATE_M, or ZERO1_STATE_V for x >= 0 held by its root (a
  *   negative x: NaN).
@@ -563,8 +563,9 @@ typedef struct zero1_f8_matrix {
  *   added in fp32.  For bf16 the matrix cores add eight neighbouring products at a
  *   time and drop what is below 2^-13 of the largest of the eight (about 2^-15 of
  *   the result); for fp32 nothing is dropped, at half the rate.  Without columns:
- *   zeros.  ws: zero1_f8_product_workspace_bytes
- *   bytes, 256-byte aligned (NULL where that is 0).  The same operands give the
+ *   zeros.  d has at most 2^21 blocks of 128 x 128.  ws: zero1_f8_product_workspace_bytes
+ *   bytes (0 too for arguments that the product rejects), 256-byte aligned (NULL where
+ *   that is 0); every byte is written before it is read.  The same operands give the
  *   same bits.
  * Written buffers must not overlap any other of the call. */
 zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int64_t ld, const zero1_f8_matrix* q,

@@ -60,8 +60,8 @@ def test_quantize_refuses():
     assert "q.scales and src" in _einval(lambda: f(s=FAKE + (1 << 36)))
     assert "q.codes and qt.codes" in _einval(lambda: f(qt=_m(300, 100, FAKE, scales=FAKE + (1 << 40))))
     assert "q.scales and qt.scales" in _einval(lambda: f(qt=_m(300, 100, FAKE + (1 << 40), scales=FAKE + (1 << 36) + 396)))
-    many = _m(1 << 30, 1 << 12)
-    assert "2^24" in _einval(lambda: z.f8_quantize(1 << 50, 1 << 30, 1 << 12, q=z.f8_matrix(1 << 30, 1 << 12, 1 << 45, 1 << 47), stream=0)) and many.rows
+    many = z.f8_matrix(1 << 30, 1 << 12, 1 << 45, 1 << 47)
+    assert "2^23" in _einval(lambda: z.f8_quantize(1 << 50, 1 << 30, 1 << 12, q=many, stream=0))
 
 
 def test_product_refuses():
@@ -73,6 +73,9 @@ def test_product_refuses():
     assert "aligned to its elements" in _einval(lambda: f(d=d + 1))
     assert "aligned to its elements" in _einval(lambda: f(d=d + 2, flags=z.F32))
     assert "unknown flag" in _einval(lambda: f(flags=0x10))
+    tall = z.f8_matrix(1 << 30, 128, 1 << 45, 1 << 47)
+    assert "2^21" in _einval(lambda: f(a=_m(1, 128), b=tall, d=1 << 50))
+    assert "2^21" in _einval(lambda: f(a=tall, b=_m(1, 128), d=1 << 50))
     for at in (FAKE + 38_399, FAKE + (1 << 36) + 396, FAKE + (1 << 40), FAKE + (1 << 40) + (1 << 36)):
         assert "d and" in _einval(lambda: f(d=at // 2 * 2))
 

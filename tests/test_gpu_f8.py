@@ -216,6 +216,41 @@ def test_product_of_whole_numbers_is_exact(env, m, n, k, blocks):
     assert np.array_equal(got, widen(bf16_bits(want.astype(np.float32))))
 
 
+# tiles of 256 in bands of 64 rows, of 128 rows, whole, whole ones and bands of either; of 128; of 64 with the summed axis in parts;
+# of 128 (into fp32) in parts
+LARGE = [(1100, 2304, 1000), (2200, 2500, 1500), (5000, 5000, 130), (4100, 4200, 260), (4100, 5400, 260), (1500, 4096, 300), (300, 300, 8000), (2304, 768, 8192),
+         (40, 3000, 8192), (20, 11008, 1000)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE, ids=["x".join(map(str, p)) for p in LARGE])
+@pytest.mark.parametrize("blocks", [(1, 128), (128, 1)], ids=["rows-tiles", "tiles-rows"])
+def test_large_product_of_whole_numbers_is_exact(env, m, n, k, blocks):
+    """Every tile shape, whole and cut by the edges, the workspace full of NaN before the call."""
+    torch, dev = env
+    a, va = whole_numbers(env, m, k, m + k, blocks[0], False)
+    b, vb = whole_numbers(env, n, k, n + k + 1, blocks[1], k % 3 == 0)
+    want = (torch.from_numpy(va).to(dev) @ torch.from_numpy(vb).to(dev).T).float().cpu().numpy()   # exact in 64 bits
+    for f32 in (True, False):
+        ws = torch.full((max(256, z.f8_product_workspace_bytes(a.m, b.m, z.F32 if f32 else 0)),), 0xFF, dtype=torch.uint8, device=dev)
+        got = product(env, a, b, f32, ws=ws, ld_more=5)
+        assert np.array_equal(got, want if f32 else widen(bf16_bits(want))), f"f32={f32}: {(got != want).sum()} of {got.size}"
+
+
+def test_the_workspace_is_checked(env):
+    torch, dev = env
+    a, _ = whole_numbers(env, 300, 8000, 1, 1, False)
+    b, _ = whole_numbers(env, 300, 8000, 2, 128, False)
+    need = z.f8_product_workspace_bytes(a.m, b.m)
+    assert need > 0
+    d = torch.zeros(300, 300, dtype=torch.bfloat16, device=dev)
+    ws = torch.zeros(need + 256, dtype=torch.uint8, device=dev)
+    for bad, word in ((None, "NULL"), (ws[:need - 1], "needs"), (ws[8:], "256-byte")):
+        with pytest.raises(z.Zero1Error) as e:
+            z.f8_product(a.m, b.m, d, ws=bad)
+        assert e.value.name == "ZERO1_EWORKSPACE" and word in e.value.message
+    assert (d == 0).all()
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 200, 300), (130, 140, 260), (300, 520, 1100)])
 def test_product_strides(env, m, n, k):
     a, va = whole_numbers(env, m, k, 1, 1, False, wide=16, more=4)
@@ -288,7 +323,7 @@ def test_two_streams_and_a_captured_product(env):
     """Two products at once on two streams with workspaces of their own; and one captured, replayed between eager work
     on operands that change."""
     torch, dev = env
-    shapes = [(5, 2000, 4096), (300, 520, 1100), (1, 512, 8192)]
+    shapes = [(5, 2000, 4096), (300, 300, 8000), (1, 512, 8192)]
     ops = [(whole_numbers(env, m, k, m, 1, False), whole_numbers(env, n, k, n, 128, False)) for m, n, k in shapes]
     streams = [torch.cuda.Stream() for _ in ops]
     ds = [torch.zeros(a.rows, b.rows, device=dev) for (a, _), (b, _) in ops]

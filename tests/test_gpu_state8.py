@@ -583,3 +583,64 @@ def test_param_is_the_nearest_bf16_of_any_master(env):
     z.adamw_step(g, None, 0, n, master, m, v, param, hp, torch.ones(1, dtype=torch.float64, device=dev), 1, flags=z.MV_8BIT)
     assert_f32_equal(master.cpu().numpy(), x, "master")
     assert_bf16_equal(to_np_u16(param), bf16_bits(x), "param")
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_long_flat_step(env, given):
+    """The flat step past the size where each XCD walks its own part of the tiles, with a ragged tail."""
+    torch, dev = env
+    n, W = (1 << 24) + 2053, 2
+    G, gd = grads_of(torch, dev, n, W, 43, 1)
+    g = oracle.shard_reduce(G)
+    rs = np.array([0.3])
+    mc, mw = ref.encode_nearest(values(n, 1), ref.M)
+    vc, vw = ref.encode_nearest(np.abs(values(n, 2)), ref.V)
+    master = values(n, 3)
+    m, v = Buf(torch, dev, ref.size(n)), Buf(torch, dev, ref.size(n))
+    m.put(ref.join(mc, mw))
+    v.put(ref.join(vc, vw))
+    md = torch.from_numpy(master.copy()).to(dev)
+    param = torch.zeros(n, dtype=torch.int16, device=dev)
+    hp = dict(HP, step=5)
+    z.adamw_step(torch.from_numpy(g).to(dev) if given else None, None if given else gd, 0, n, md, m.view, v.view, param, hp,
+                 torch.from_numpy(rs).to(dev), 1, flags=z.MV_8BIT)
+    mm, vv, p = ref.decode(mc, mw, ref.M), ref.decode(vc, vw, ref.V), np.zeros(n, np.uint16)
+    clip, coef = oracle.clip_coef(oracle.global_norm(rs), HP["max_norm"])
+    oracle.adamw(g, master, mm, vv, p, oracle.adamw_scalars(HP["lr"], HP["beta1"], HP["beta2"], HP["eps"], HP["weight_decay"], 5), clip, coef)
+    want = ref.round_step(mm, np.sqrt(vv), mw, vw, 0)
+    assert_f32_equal(md.cpu().numpy(), master, "master")
+    assert_bf16_equal(to_np_u16(param), p, "param")
+    for buf, c, w in ((m, 0, 1), (v, 2, 3)):
+        gc, gw = ref.split(buf.get(), n)
+        assert np.array_equal(gw, want[w]) and np.array_equal(gc, want[c]) and buf.guards_hold()
+
+
+@pytest.mark.parametrize("skew", [0, 1])
+@pytest.mark.parametrize("W", [1, 3, 6, 64])
+def test_flat_step_of_misaligned_slices(env, W, skew):
+    """Slices, master and parameters off every vector's alignment; lengths around the tile and the quad."""
+    torch, dev = env
+    for n in (1, 2, 3, 5, 2047, 2049, 2050, 2051, 4099):
+        begin = 3 * skew
+        G = [synth.bf16(n + begin, synth.grad_key(7, 1, w), 0, 0.02, 1) for w in range(W)]
+        gd = [to_dev_u16(torch, x, dev) for x in G]
+        g = oracle.shard_reduce([x[begin:] for x in G])
+        rs = np.array([oracle.sumsq(g)])
+        mc, mw = ref.encode_nearest(values(n, n), ref.M)
+        vc, vw = ref.encode_nearest(np.abs(values(n, n + 1)), ref.V)
+        master, p = values(n, n + 2), np.zeros(n, np.uint16)
+        m, v, ms, pr = Buf(torch, dev, ref.size(n)), Buf(torch, dev, ref.size(n)), Buf(torch, dev, 4 * n, skew=4 * skew), Buf(torch, dev, 2 * n, skew=2 * skew)
+        m.put(ref.join(mc, mw))
+        v.put(ref.join(vc, vw))
+        ms.put(master)
+        z.adamw_step(None, gd, begin, n, ms.view, m.view, v.view, pr.view, dict(HP, step=2), torch.from_numpy(rs).to(dev), 1, flags=z.MV_8BIT)
+        mm, vv = ref.decode(mc, mw, ref.M), ref.decode(vc, vw, ref.V)
+        clip, coef = oracle.clip_coef(oracle.global_norm(rs), HP["max_norm"])
+        oracle.adamw(g, master, mm, vv, p, oracle.adamw_scalars(HP["lr"], HP["beta1"], HP["beta2"], HP["eps"], HP["weight_decay"], 2), clip, coef)
+        want = ref.round_step(mm, np.sqrt(vv), mw, vw, 0)
+        assert_f32_equal(ms.get(np.float32), master, f"master n={n}")
+        assert_bf16_equal(pr.get(np.uint16), p, f"param n={n}")
+        for buf, c, w in ((m, 0, 1), (v, 2, 3)):
+            gc, gw = ref.split(buf.get(), n)
+            assert np.array_equal(gw, want[w]) and np.array_equal(gc, want[c]) and buf.guards_hold()
+        assert ms.guards_hold() and pr.guards_hold()

@@ -28,7 +28,7 @@ def test_conversions_refuse():
     x, s = FAKE, FAKE + (1 << 30)
     for f in (lambda n, x, s, w, fl=0: enc(x, n, s, w, flags=fl, stream=0), lambda n, x, s, w, fl=0: dec(s, n, x, w, flags=fl, stream=0)):
         assert "n=-1" in _einval(lambda: f(-1, x, s, 0))
-        assert "2^40" in _einval(lambda: f((1 << 40) + 1, x, s, 0))
+        assert "2^34" in _einval(lambda: f((1 << 34) + 1, x, s, 0))
         assert "which" in _einval(lambda: f(10, x, s, 2))
         assert "NULL" in _einval(lambda: f(10, 0, s, 0))
         assert "NULL" in _einval(lambda: f(10, x, 0, 0))

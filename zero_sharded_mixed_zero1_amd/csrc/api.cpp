@@ -616,6 +616,11 @@ zero1_status zero1_mta_reduce(const uint16_t* const* grads, int W, int64_t begin
     if (!sumsq_out) return fail(ZERO1_EINVAL, "sumsq_out is NULL");
     zero1_status st = mta_common(grads, W, begin, plan, flags, ws, ws_bytes, r, vec, store_g, d, w);
     if (st) return st;
+    // (the slices' alignment alone, not the pieces': an 8-bit plan's update goes by neither)
+    if (plan->flags & ZERO1_MV_8BIT) {
+        vec = true;
+        for (int k = 0; k < W; ++k) vec = vec && aligned16(grads[k] + begin);
+    }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Shape sh = reduce_shape(tiles(plan->shard_len, vec), d, few_slice_pass(vec, w.g != nullptr, true, W));
     const int nb = sh.grid;
@@ -757,7 +762,7 @@ static zero1_status state8_common(const char* fn, const void* x, int64_t n, cons
                                   DevInfo& d)
 {
     if (zero1_status fs = check_flags(flags, kAllFlags, fn)) return fs;
-    if (n < 0 || n > (int64_t)1 << 40) return fail(ZERO1_EINVAL, "%s: n=%lld must be in [0, 2^40]", fn, (long long)n);
+    if (n < 0 || n > (int64_t)1 << 34) return fail(ZERO1_EINVAL, "%s: n=%lld must be in [0, 2^34]", fn, (long long)n);
     if (which != ZERO1_STATE_M && which != ZERO1_STATE_V)
         return fail(ZERO1_EINVAL, "%s: which=%d must be ZERO1_STATE_M or ZERO1_STATE_V", fn, which);
     if (n > 0) {
@@ -778,8 +783,7 @@ zero1_status zero1_state8_encode(const void* x, int64_t n, void* state, int whic
     if (zero1_status st = state8_common("zero1_state8_encode", x, n, state, which, flags, d)) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (n > 0)
-        Z1_HIP(launch_state8_encode(x, n, flags & ZERO1_MV_BF16, which == ZERO1_STATE_V, state,
-                                    grid_for(tiles(n, true), d, kReducePerCu), s));
+        Z1_HIP(launch_state8_encode(x, n, flags & ZERO1_MV_BF16, which == ZERO1_STATE_V, state, s));
     return finish(s);
 }
 
@@ -789,8 +793,7 @@ zero1_status zero1_state8_decode(const void* state, int64_t n, void* x, int whic
     if (zero1_status st = state8_common("zero1_state8_decode", x, n, state, which, flags, d)) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (n > 0)
-        Z1_HIP(launch_state8_decode(state, n, flags & ZERO1_MV_BF16, which == ZERO1_STATE_V, x,
-                                    grid_for(tiles(n, true), d, kReducePerCu), s));
+        Z1_HIP(launch_state8_decode(state, n, flags & ZERO1_MV_BF16, which == ZERO1_STATE_V, x, s));
     return finish(s);
 }
 

@@ -80,6 +80,7 @@ zero1_status current_device(int& cus)
 // ------------------------------------------------------------------ checks
 constexpr uint32_t kF8Flags = ZERO1_F32;
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 256, kMaxCols = (int64_t)1 << 23, kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxGrid = (int64_t)1 << 23;   // workgroups of 256: 2^31 threads a launch
 
 int64_t blocks(int64_t n) { return (n + kF8Block - 1) / kF8Block; }
 int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -192,8 +193,7 @@ zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int6
     const Range r[5] = {codes_of(fq, "q.codes"), scales_of(fq, "q.scales"), codes_of(ft, "qt.codes"),
                         scales_of(ft, "qt.scales"), range_of(src, rows, ld * eb, cols * eb, "src")};
     if ((st = check_disjoint(fn, r, 5, 4))) return st;
-    if (blocks(rows) * blocks(cols) > (int64_t)1 << 24)
-        return fail(ZERO1_EINVAL, "%s: more than 2^24 blocks of 128 x 128", fn);
+    if (blocks(rows) * blocks(cols) > kMaxGrid) return fail(ZERO1_EINVAL, "%s: more than 2^23 blocks of 128 x 128", fn);
     int cus = 0;
     if ((st = current_device(cus))) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -240,7 +240,7 @@ static void choose(F8Product& p)
         for (int parts = 1; parts <= kMaxParts; parts *= 2) {
             const int64_t steps = per > 0 ? (per + parts - 1) / parts : 1;
             const int64_t groups = tiles * (per > 0 ? (per + steps - 1) / steps : 1);
-            if (parts > 1 && (steps < 2 || tiles * parts > 2 * kChip)) break;
+            if (groups > kMaxGrid || (parts > 1 && (steps < 2 || tiles * parts > 2 * kChip))) break;
             const double t = groups <= kChip ? steps * c.one + c.fixed
                                              : (double)((groups + 2 * kChip - 1) / (2 * kChip)) * (steps * c.two + c.fixed);
             const double join = parts > 1 ? kJoinFixed + 8.0 * parts * (double)m * (double)n / kJoinBytes : 0.0;
@@ -312,8 +312,8 @@ zero1_status zero1_f8_product(const zero1_f8_matrix* a, const zero1_f8_matrix* b
     const Range r[5] = {range_of(d, p.a.rows, ldd * eb, p.b.rows * eb, "d"), codes_of(p.a, "a.codes"),
                         scales_of(p.a, "a.scales"), codes_of(p.b, "b.codes"), scales_of(p.b, "b.scales")};
     if ((st = check_disjoint(fn, r, 5, 1))) return st;
-    if (blocks(p.a.rows) * blocks(p.b.rows) > (int64_t)1 << 24)
-        return fail(ZERO1_EINVAL, "%s: more than 2^24 tiles of 128 x 128", fn);
+    if (blocks(p.a.rows) * blocks(p.b.rows) > kMaxGrid / 4)   // (32 rows of B a workgroup where A has few)
+        return fail(ZERO1_EINVAL, "%s: d has more than 2^21 blocks of 128 x 128", fn);
     int cus = 0;
     if ((st = current_device(cus))) return st;
     p.d = d;

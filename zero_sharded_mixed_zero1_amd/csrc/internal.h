@@ -146,7 +146,7 @@ hipError_t launch_adamw_mta(const float* g, const Reduce& r, const PieceDesc* pi
 
 // ---- moments in 8 bits from and to fp32 or bf16 (state8.hip).  v: x holds v, the
 // codes its root.
-hipError_t launch_state8_encode(const void* x, int64_t n, bool bf16, bool v, void* state, int nblocks, hipStream_t s);
-hipError_t launch_state8_decode(const void* state, int64_t n, bool bf16, bool v, void* x, int nblocks, hipStream_t s);
+hipError_t launch_state8_encode(const void* x, int64_t n, bool bf16, bool v, void* state, hipStream_t s);
+hipError_t launch_state8_decode(const void* state, int64_t n, bool bf16, bool v, void* x, hipStream_t s);
 
 }  // namespace z1

@@ -151,18 +151,13 @@ __device__ __forceinline__ void st8_bf16(uint16_t* p, const float (&x)[8])
     st_nt(reinterpret_cast<u32x2*>(p + a + 256), w);
 }
 
-// The same by the conversion instruction (nearest even; another NaN's payload).
-__device__ __forceinline__ void st8_bf16_cvt(uint16_t* p, const float (&x)[8])
+// Two nearest-even bf16 by the conversion instruction (another NaN's payload than
+// bf16_rne_bits').
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x[2 * k], x[2 * k + 1]}), bf16x2));
-    const int a = quad_a();
-    st_nt(reinterpret_cast<u32x2*>(p + a), u32x2{w[0], w[1]});
-    st_nt(reinterpret_cast<u32x2*>(p + a + 256), u32x2{w[2], w[3]});
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
 __device__ __forceinline__ void ld8_f32(const float* p, float (&x)[8])
@@ -600,113 +595,196 @@ struct Span {
 // nothing comes between two steps.
 typedef uint32_t u32x2w __attribute__((ext_vector_type(2), aligned(4)));
 
+// A tile of a plan's piece or of a flat shard, n of its kTile elements present.  Its
+// quads are loaded and stored whole at any alignment of their elements (gfx950's
+// vector accesses need no more); one that the end cuts, element by element.  What is
+// not there counts as zero.
+typedef f32x4 f32x4e __attribute__((aligned(4)));
+typedef u32x2 u32x2e __attribute__((aligned(2)));
+
 struct Bytes8 {   // as loaded
     float p[8];
     uint32_t m[2], v[2];
-    u32x2w mw, vw;
+    u32x2 mw, vw;
 };
+
+// How many of quad h's elements are there, of a tile of n (4: the whole quad).
+template <bool WHOLE>
+__device__ __forceinline__ int present(int n, int h)
+{
+    const int left = n - (quad_a() + 256 * h);
+    return WHOLE || left > 4 ? 4 : left;
+}
+
+// Whether block h of the wave's two has any.
+template <bool WHOLE>
+__device__ __forceinline__ bool block_there(int n, int h)
+{
+    return WHOLE || (int)(threadIdx.x & ~63u) * 8 + 256 * h < n;
+}
 
 __device__ __forceinline__ int64_t first_block(int64_t si)
 {
     return (si >> 8) + 2 * __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 }
 
-__device__ __forceinline__ void load_bytes(const Span& sp, int64_t si, Bytes8& t)
+template <bool WHOLE>
+__device__ __forceinline__ void load_bytes(const Span& sp, int64_t si, int n, Bytes8& t)
 {
     const int a = quad_a();
-    const uint8_t* m = static_cast<const uint8_t*>(sp.m) + si + a;
-    const uint8_t* v = static_cast<const uint8_t*>(sp.v) + si + a;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        t.m[h] = *gbl(reinterpret_cast<const uint32_t*>(m + 256 * h));
-        t.v[h] = *gbl(reinterpret_cast<const uint32_t*>(v + 256 * h));
+        const float* p = sp.master + si + a + 256 * h;
+        const uint8_t* m = static_cast<const uint8_t*>(sp.m) + si + a + 256 * h;
+        const uint8_t* v = static_cast<const uint8_t*>(sp.v) + si + a + 256 * h;
+        f32x4 q = {0, 0, 0, 0};
+        t.m[h] = t.v[h] = t.mw[h] = t.vw[h] = 0;
+        if (block_there<WHOLE>(n, h)) {
+            t.mw[h] = *gbl(sp.mw + first_block(si) + h);
+            t.vw[h] = *gbl(sp.vw + first_block(si) + h);
+        }
+        const int c = present<WHOLE>(n, h);
+        if (c == 4) {
+            t.m[h] = *gbl(reinterpret_cast<const uint32_t*>(m));
+            t.v[h] = *gbl(reinterpret_cast<const uint32_t*>(v));
+            q = ld_nt(reinterpret_cast<const f32x4e*>(p));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < c) {
+                    t.m[h] |= (uint32_t)*gbl(m + j) << (8 * j);
+                    t.v[h] |= (uint32_t)*gbl(v + j) << (8 * j);
+                    q[j] = ld_nt(p + j);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t.p[4 * h + j] = q[j];
     }
-    t.mw = *gbl(reinterpret_cast<const u32x2w*>(sp.mw + first_block(si)));
-    t.vw = *gbl(reinterpret_cast<const u32x2w*>(sp.vw + first_block(si)));
-    ld8_f32(sp.master + si, t.p);
 }
 
-__device__ __forceinline__ void update_bytes(const Span& sp, int64_t si, Bytes8& t, const float (&gv)[8], const Scal& c,
-                                             bool clip, float coef)
+// The lane's gradients: g itself (FEW = 0), or the average of exactly FEW (1 to 4) or of
+// any number (FEW = -1) of slices, loaded together and added in rank order.
+template <int FEW, bool WHOLE>
+__device__ __forceinline__ void gradient8(const float* g, const Reduce& r, int64_t e, int n, float (&s)[8])
+{
+    const int a = quad_a();
+    constexpr int N = FEW > 0 ? FEW : 1;
+    f32x4 q[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    u32x2 x[2][N] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = present<WHOLE>(n, h);
+        const int64_t at = e + a + 256 * h;
+        if (c == 4) {
+            if constexpr (FEW == 0) {
+                q[h] = ld_g(reinterpret_cast<const f32x4e*>(g + at));
+            } else {
+#pragma unroll
+                for (int w = 0; w < N; ++w) x[h][w] = ld_nt(reinterpret_cast<const u32x2e*>(r.gp.p[w] + at));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < c) {
+                    if constexpr (FEW == 0) {
+                        q[h][j] = ld_g(g + at + j);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < N; ++w) x[h][w][j >> 1] |= (uint32_t)ld_nt(r.gp.p[w] + at + j) << (16 * (j & 1));
+                    }
+                }
+        }
+    }
+    if constexpr (FEW == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = q[j >> 2][j & 3];
+    } else {
+        auto add = [&](bool first, const u32x2& lo, const u32x2& hi) {
+            const Raw raw{lo, hi};
+            if (first) raw_init(s, raw);
+            else raw_add(s, raw);
+        };
+#pragma unroll
+        for (int w = 0; w < N; ++w) add(w == 0, x[0][w], x[1][w]);
+        if constexpr (FEW < 0) {
+            constexpr int B = 4;   // slices under way together
+            for (int w0 = 1; w0 < r.W; w0 += B) {
+                u32x2 y[2][B] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = present<WHOLE>(n, h);
+                    const int64_t at = e + a + 256 * h;
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {
+                        if (w0 + k >= r.W) continue;
+                        const uint16_t* p = r.gp.p[w0 + k] + at;
+                        if (c == 4) {
+                            y[h][k] = ld_nt(reinterpret_cast<const u32x2e*>(p));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 3; ++j)
+                                if (j < c) y[h][k][j >> 1] |= (uint32_t)ld_nt(p + j) << (16 * (j & 1));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                    if (w0 + k < r.W) add(false, y[0][k], y[1][k]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = average(r, s[j]);
+    }
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void update_bytes(const Span& sp, int64_t si, int n, Bytes8& t, const float (&gv)[8],
+                                             const Scal& c, bool clip, float coef)
 {
     using namespace dev8;
     const int a = quad_a();
     const uint32_t first = sp.first + (uint32_t)si + 512u * (uint32_t)(threadIdx.x >> 6);
-    u32x2w mwn, vwn;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float m[4], r[4], v[4];
+        float m[4], r[4], v[4], p[4];
         decode4(t.m[h], scale8(t.mw[h]), m);
         decode4(t.v[h], scale8(t.vw[h]), r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float g = clip ? gv[4 * h + j] * coef : gv[4 * h + j];
+            p[j] = t.p[4 * h + j];
             v[j] = r[j] * r[j];
-            r[j] = adamw_elem(g, t.p[4 * h + j], m[j], v[j], c);
+            r[j] = adamw_elem(g, p[j], m[j], v[j], c);
         }
         const Top8 tm = top8<false>(m), tr = top8<true>(r);
         const uint32_t key = key8(first + 256u * h, t.mw[h] >> 8) + 4u * (threadIdx.x & 63);
         const uint32_t bits[4] = {mix32(key), mix32(key + 1), mix32(key + 2), mix32(key + 3)};
         uint32_t cm, cr;
         codes4(m, r, bits, tm, tr, cm, cr);
-        *gbl(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(sp.m) + si + a + 256 * h)) = cm;
-        *gbl(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(sp.v) + si + a + 256 * h)) = cr;
-        mwn[h] = next_word(t.mw[h], tm.b);
-        vwn[h] = next_word(t.vw[h], tr.b);
-    }
-    st8_f32(sp.master + si, t.p);
-    st8_bf16_cvt(sp.param + si, t.p);
-    if ((threadIdx.x & 63) == 0) {
-        *gbl(reinterpret_cast<u32x2w*>(sp.mw + first_block(si))) = mwn;
-        *gbl(reinterpret_cast<u32x2w*>(sp.vw + first_block(si))) = vwn;
-    }
-}
-
-// The same of n <= kTile elements at any alignment: a wave takes a block, lane l
-// its elements l, l + 64, l + 128 and l + 192.  g: the element's gradient by its
-// place in the tile.
-template <typename G>
-__device__ __forceinline__ void update_blocks(const Span& sp, int64_t si, int n, const Scal& c, bool clip, float coef,
-                                              G g)
-{
-    using namespace dev8;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    uint8_t* mp = static_cast<uint8_t*>(sp.m) + si;
-    uint8_t* vp = static_cast<uint8_t*>(sp.v) + si;
-    for (int k = wave; k * kBlock8 < n; k += kThreads / 64) {
-        const int64_t blk = (si >> 8) + k;
-        const uint32_t mw = sp.mw[blk], vw = sp.vw[blk];
-        const float ms = scale8(mw), rs = scale8(vw);
-        float m[4], r[4];
+        const uint32_t lo = bf16_pair(p[0], p[1]), hi = bf16_pair(p[2], p[3]);
+        uint8_t* mp = static_cast<uint8_t*>(sp.m) + si + a + 256 * h;
+        uint8_t* vp = static_cast<uint8_t*>(sp.v) + si + a + 256 * h;
+        float* pp = sp.master + si + a + 256 * h;
+        uint16_t* bp = sp.param + si + a + 256 * h;
+        const int there = present<WHOLE>(n, h);
+        if (there == 4) {
+            *gbl(reinterpret_cast<uint32_t*>(mp)) = cm;
+            *gbl(reinterpret_cast<uint32_t*>(vp)) = cr;
+            st_nt(reinterpret_cast<f32x4e*>(pp), f32x4e{p[0], p[1], p[2], p[3]});
+            st_nt(reinterpret_cast<u32x2e*>(bp), u32x2e{lo, hi});
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = k * kBlock8 + lane + 64 * i;
-            m[i] = r[i] = 0.0f;
-            if (j < n) {
-                float p = ld_nt(sp.master + si + j);
-                m[i] = __builtin_amdgcn_cvt_f32_fp8(mp[j], 0) * ms;
-                r[i] = __builtin_amdgcn_cvt_f32_fp8(vp[j], 0) * rs;
-                float gj = g(j), v = r[i] * r[i];
-                if (clip) gj = gj * coef;
-                r[i] = adamw_elem(gj, p, m[i], v, c);
-                st_nt(sp.master + si + j, p);
-                st_nt(sp.param + si + j, (uint16_t)bf16_rne_bits(p));
-            }
+            for (int j = 0; j < 3; ++j)
+                if (j < there) {
+                    *gbl(mp + j) = (uint8_t)(cm >> (8 * j));
+                    *gbl(vp + j) = (uint8_t)(cr >> (8 * j));
+                    st_nt(pp + j, p[j]);
+                    st_nt(bp + j, (uint16_t)((j & 2 ? hi : lo) >> (16 * (j & 1))));
+                }
         }
-        const Top8 tm = top8<false>(m), tr = top8<true>(r);
-        const uint32_t key = key8(sp.first + (uint32_t)si + (uint32_t)(k * kBlock8), mw >> 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = k * kBlock8 + lane + 64 * i;
-            const uint32_t bits = mix32(key + lane + 64 * i);
-            if (j < n) {
-                mp[j] = (uint8_t)code_m(m[i], bits, tm);
-                vp[j] = (uint8_t)code_r(r[i], bits, tr);
-            }
-        }
-        if (lane == 0) {
-            sp.mw[blk] = next_word(mw, tm.b);
-            sp.vw[blk] = next_word(vw, tr.b);
+        if ((threadIdx.x & 63) == 0 && block_there<WHOLE>(n, h)) {
+            *gbl(sp.mw + first_block(si) + h) = next_word(t.mw[h], tm.b);
+            *gbl(sp.vw + first_block(si) + h) = next_word(t.vw[h], tr.b);
         }
     }
 }
@@ -846,27 +924,6 @@ __global__ __launch_bounds__(kThreads) void adamw_mta_kernel(const float* __rest
     }
 }
 
-// Gradient slices of a lane's 8 elements in one go: exactly FEW (1 to 4) of them, or
-// g itself (FEW = 0), or any number (FEW = -1).
-template <int FEW>
-__device__ __forceinline__ void gradient8(const float* g, const Reduce& r, int64_t e, float (&s)[8])
-{
-    if constexpr (FEW == 0) {
-        ld8_g(g + e, s);
-    } else if constexpr (FEW < 0) {
-        reduce8(r, e, s);
-    } else {
-        Raw x[FEW];
-#pragma unroll
-        for (int w = 0; w < FEW; ++w) x[w] = ld_raw(r.gp.p[w] + e);
-        raw_init(s, x[0]);
-#pragma unroll
-        for (int w = 1; w < FEW; ++w) raw_add(s, x[w]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = average(r, s[j]);
-    }
-}
-
 // The update with 8-bit moments, flat (one span of len elements) or over a plan's
 // chunks.  A workgroup takes one tile where the grid has as many: each tile moves half
 // of what it does with fp32 moments, so more of them have to be under way (a step of
@@ -876,7 +933,7 @@ __device__ __forceinline__ void gradient8(const float* g, const Reduce& r, int64
 //
 // HBM-bound: 16 bytes a parameter at W = 1 (5.8 TB/s), 18 with g from the workspace
 // (the 117 M of a step at W = 8: 6.1).
-template <bool VEC, int FEW, bool FLAT>
+template <int FEW, bool FLAT>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(Span flat, Reduce r, const PieceDesc* __restrict__ pieces,
                                                           const ChunkDesc* __restrict__ chunks, int64_t units,
                                                           int64_t len, Scal c, ClipArgs ca, int split)
@@ -900,15 +957,16 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(Span flat, Reduce r, c
             si = 0;
             n = ch.len;
         }
-        if (VEC && n == kTile) {
-            Bytes8 t;
-            float gv[8];
-            load_bytes(sp, si, t);
-            gradient8<FEW>(flat.g, r, gi, gv);
-            update_bytes(sp, si, t, gv, c, clip, coef);
+        Bytes8 t;
+        float gv[8];
+        if (n == kTile) {
+            load_bytes<true>(sp, si, n, t);
+            gradient8<FEW, true>(flat.g, r, gi, n, gv);
+            update_bytes<true>(sp, si, n, t, gv, c, clip, coef);
         } else {
-            update_blocks(sp, si, n, c, clip, coef,
-                          [&](int j) { return (FEW == 0) ? ld_g(flat.g + gi + j) : reduce1(r, gi + j); });
+            load_bytes<false>(sp, si, n, t);
+            gradient8<FEW, false>(flat.g, r, gi, n, gv);
+            update_bytes<false>(sp, si, n, t, gv, c, clip, coef);
         }
     }
 }
@@ -1019,15 +1077,14 @@ hipError_t launch_adamw_flat(const float* g, const Reduce& r, int64_t len, bool 
         const int64_t units = (len + kTile - 1) / kTile;
         const PieceDesc* pieces = nullptr;
         const ChunkDesc* chunks = nullptr;
-#define Z1_8(V, FEW) return run(adamw8_kernel<V, FEW, true>, grid, s, sp, r, pieces, chunks, units, len, sc, ca, split)
-        if (!vec) { if (g) Z1_8(false, 0); else Z1_8(false, -1); }
-        if (g) Z1_8(true, 0);
+#define Z1_8(FEW) return run(adamw8_kernel<FEW, true>, grid, s, sp, r, pieces, chunks, units, len, sc, ca, split)
+        if (g) Z1_8(0);
         switch (r.W) {
-        case 1: Z1_8(true, 1);
-        case 2: Z1_8(true, 2);
-        case 3: Z1_8(true, 3);
-        case 4: Z1_8(true, 4);
-        default: Z1_8(true, -1);
+        case 1: Z1_8(1);
+        case 2: Z1_8(2);
+        case 3: Z1_8(3);
+        case 4: Z1_8(4);
+        default: Z1_8(-1);
         }
 #undef Z1_8
     }
@@ -1059,15 +1116,14 @@ hipError_t launch_adamw_mta(const float* g, const Reduce& r, const PieceDesc* pi
     if (mv == kMv8) {
         const Span sp{g, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0};
         const int64_t units = n_chunks, len = 0;
-#define Z1_8(V, FEW) return run(adamw8_kernel<V, FEW, false>, grid, s, sp, r, pieces, chunks, units, len, sc, ca, split)
-        if (!vec) { if (g) Z1_8(false, 0); else Z1_8(false, -1); }
-        if (g) Z1_8(true, 0);
+#define Z1_8(FEW) return run(adamw8_kernel<FEW, false>, grid, s, sp, r, pieces, chunks, units, len, sc, ca, split)
+        if (g) Z1_8(0);
         switch (r.W) {
-        case 1: Z1_8(true, 1);
-        case 2: Z1_8(true, 2);
-        case 3: Z1_8(true, 3);
-        case 4: Z1_8(true, 4);
-        default: Z1_8(true, -1);
+        case 1: Z1_8(1);
+        case 2: Z1_8(2);
+        case 3: Z1_8(3);
+        case 4: Z1_8(4);
+        default: Z1_8(-1);
         }
 #undef Z1_8
     }

@@ -6,9 +6,10 @@
 // the root.  decode: the product of code and scale, which fp32 holds exactly;
 // squared for v.
 //
-// HBM-bound: 5 bytes an element.  A wave takes a block, lane l its elements 4 l to
-// 4 l + 3 where x allows vector access, and l, l + 64, ... where it does not and in
-// a short last block.
+// HBM-bound: 5 bytes an element (fp32).  A workgroup takes a tile of 2048, a wave two
+// blocks of it, a lane a quad of each: whole quads at any alignment of x (gfx950's
+// vector accesses need no more than the elements'), the one that the end cuts
+// element by element.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,8 +23,11 @@ namespace {
 
 using namespace dev8;
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+template <typename T>
+struct Quad {
+    typedef T Plain __attribute__((ext_vector_type(4)));
+    typedef Plain Any __attribute__((aligned(sizeof(T))));
+};
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
@@ -38,124 +42,139 @@ __device__ __forceinline__ void narrow(float x, uint16_t& o)   // to the nearest
 // Code to the nearest, ties to even.
 __device__ __forceinline__ uint32_t code_near(float y) { return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, y, 0, false) & 0xffu; }
 
-template <typename T, bool VEC, bool V>
+// Where the lane's quad h of tile blockIdx.x begins, and how many of its elements
+// there are.
+__device__ __forceinline__ int64_t quad_at(int h)
+{
+    return (int64_t)blockIdx.x * kTile + 512 * (int)(threadIdx.x >> 6) + 256 * h + 4 * (int)(threadIdx.x & 63);
+}
+
+__device__ __forceinline__ int present(int64_t at, int64_t n) { return n - at > 4 ? 4 : (int)(n - at); }
+
+template <typename T, bool V>
 __global__ __launch_bounds__(kThreads) void encode_kernel(const T* __restrict__ x, int64_t n, uint8_t* __restrict__ codes,
                                                           uint32_t* __restrict__ words)
 {
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    const int lane = threadIdx.x & 63;
-    const int64_t blocks = state8_blocks(n), step = (int64_t)gridDim.x * (kThreads / 64);
-    for (int64_t k = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); k < blocks; k += step) {
-        const int64_t at = k * kBlock8;
-        const bool whole = VEC && at + kBlock8 <= n;
-        float y[4];
-        if (whole) {
-            const T4 q = *reinterpret_cast<const T4*>(x + at + 4 * lane);
+    float y[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = widen(q[i]);
+    for (int h = 0; h < 2; ++h) {
+        const int64_t at = quad_at(h);
+        const int c = present(at, n);
+        typename Quad<T>::Plain q = {0, 0, 0, 0};
+        if (c == 4) {
+            q = *reinterpret_cast<const typename Quad<T>::Any*>(x + at);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t e = at + lane + 64 * i;
-                y[i] = e < n ? widen(x[e]) : 0.0f;
-            }
+            for (int j = 0; j < 3; ++j)
+                if (j < c) q[j] = x[at + j];
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[h][j] = widen((T)q[j]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
         if constexpr (V) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = sqrtf(y[i]);
+            for (int j = 0; j < 4; ++j) y[h][j] = sqrtf(y[h][j]);
         }
-        const Top8 t = top8<V>(y);
+        const Top8 t = top8<V>(y[h]);
         const float inv = inverse8(t.b);
-        uint32_t c[4];
+        uint32_t word = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c[i] = code_near(y[i] * inv);
-            if constexpr (V) c[i] = max(c[i] & 0x7fu, y[i] > 0.0f ? 1u : 0u);   // (the root of -0 is -0)
-            if (t.special) c[i] = held8<V>(y[i], c[i], t);
+        for (int j = 0; j < 4; ++j) {
+            uint32_t c = code_near(y[h][j] * inv);
+            if constexpr (V) c = max(c & 0x7fu, y[h][j] > 0.0f ? 1u : 0u);   // (the root of -0 is -0)
+            if (t.special) c = held8<V>(y[h][j], c, t);
+            word |= c << (8 * j);
         }
-        if (whole) {
-            *reinterpret_cast<uint32_t*>(codes + at + 4 * lane) = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+        const int64_t at = quad_at(h);
+        const int c = present(at, n);
+        if (c == 4) {
+            *reinterpret_cast<uint32_t*>(codes + at) = word;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t e = at + lane + 64 * i;
-                if (e < n) codes[e] = (uint8_t)c[i];
-            }
+            for (int j = 0; j < 3; ++j)
+                if (j < c) codes[at + j] = (uint8_t)(word >> (8 * j));
         }
-        if (lane == 0) words[k] = t.b;
+        if ((threadIdx.x & 63) == 0 && c > 0) words[at >> 8] = t.b;
     }
 }
 
-template <typename T, bool VEC, bool V>
+template <typename T, bool V>
 __global__ __launch_bounds__(kThreads) void decode_kernel(const uint8_t* __restrict__ codes,
                                                           const uint32_t* __restrict__ words, int64_t n,
                                                           T* __restrict__ x)
 {
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    const int lane = threadIdx.x & 63;
-    const int64_t blocks = state8_blocks(n), step = (int64_t)gridDim.x * (kThreads / 64);
-    for (int64_t k = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); k < blocks; k += step) {
-        const int64_t at = k * kBlock8;
-        const float scale = scale8(words[k]);
-        if (VEC && at + kBlock8 <= n) {
-            float y[4];
-            decode4(*reinterpret_cast<const uint32_t*>(codes + at + 4 * lane), scale, y);
-            T4 q;
+    uint32_t w[2] = {0, 0}, b[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                T o;
-                narrow(V ? y[i] * y[i] : y[i], o);
-                q[i] = o;
-            }
-            *reinterpret_cast<T4*>(x + at + 4 * lane) = q;
+    for (int h = 0; h < 2; ++h) {
+        const int64_t at = quad_at(h);
+        const int c = present(at, n);
+        if (c > 0) b[h] = words[at >> 8];
+        if (c == 4) {
+            w[h] = *reinterpret_cast<const uint32_t*>(codes + at);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t e = at + lane + 64 * i;
-                if (e < n) {
-                    const float y = __builtin_amdgcn_cvt_f32_fp8(codes[e], 0) * scale;
-                    narrow(V ? y * y : y, x[e]);
-                }
-            }
+            for (int j = 0; j < 3; ++j)
+                if (j < c) w[h] |= (uint32_t)codes[at + j] << (8 * j);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t at = quad_at(h);
+        const int c = present(at, n);
+        float y[4];
+        decode4(w[h], scale8(b[h]), y);
+        typename Quad<T>::Plain q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            T o;
+            narrow(V ? y[j] * y[j] : y[j], o);
+            q[j] = o;
+        }
+        if (c == 4) {
+            __builtin_nontemporal_store((typename Quad<T>::Any)q, reinterpret_cast<typename Quad<T>::Any*>(x + at));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < c) x[at + j] = q[j];
         }
     }
 }
 
 }  // namespace
 
-hipError_t launch_state8_encode(const void* x, int64_t n, bool bf16, bool v, void* state, int nblocks, hipStream_t s)
+hipError_t launch_state8_encode(const void* x, int64_t n, bool bf16, bool v, void* state, hipStream_t s)
 {
     uint8_t* codes = static_cast<uint8_t*>(state);
     uint32_t* words = reinterpret_cast<uint32_t*>(codes + state8_words_at(n));
-    const bool vec = reinterpret_cast<uintptr_t>(x) % (bf16 ? 8 : 16) == 0;
-#define Z1_ENC(T, VEC, V) encode_kernel<T, VEC, V><<<nblocks, kThreads, 0, s>>>(static_cast<const T*>(x), n, codes, words)
-#define Z1_ENC_T(T)                                                                   \
-    do {                                                                              \
-        if (vec) { if (v) Z1_ENC(T, true, true); else Z1_ENC(T, true, false); }       \
-        else     { if (v) Z1_ENC(T, false, true); else Z1_ENC(T, false, false); }     \
-    } while (0)
-    if (bf16) Z1_ENC_T(uint16_t);
-    else Z1_ENC_T(float);
-#undef Z1_ENC_T
-#undef Z1_ENC
+    const dim3 grid((uint32_t)((n + kTile - 1) / kTile));
+    if (bf16) {
+        const uint16_t* h = static_cast<const uint16_t*>(x);
+        if (v) encode_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(h, n, codes, words);
+        else encode_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(h, n, codes, words);
+    } else {
+        const float* f = static_cast<const float*>(x);
+        if (v) encode_kernel<float, true><<<grid, kThreads, 0, s>>>(f, n, codes, words);
+        else encode_kernel<float, false><<<grid, kThreads, 0, s>>>(f, n, codes, words);
+    }
     return hipGetLastError();
 }
 
-hipError_t launch_state8_decode(const void* state, int64_t n, bool bf16, bool v, void* x, int nblocks, hipStream_t s)
+hipError_t launch_state8_decode(const void* state, int64_t n, bool bf16, bool v, void* x, hipStream_t s)
 {
     const uint8_t* codes = static_cast<const uint8_t*>(state);
     const uint32_t* words = reinterpret_cast<const uint32_t*>(codes + state8_words_at(n));
-    const bool vec = reinterpret_cast<uintptr_t>(x) % (bf16 ? 8 : 16) == 0;
-#define Z1_DEC(T, VEC, V) decode_kernel<T, VEC, V><<<nblocks, kThreads, 0, s>>>(codes, words, n, static_cast<T*>(x))
-#define Z1_DEC_T(T)                                                                   \
-    do {                                                                              \
-        if (vec) { if (v) Z1_DEC(T, true, true); else Z1_DEC(T, true, false); }       \
-        else     { if (v) Z1_DEC(T, false, true); else Z1_DEC(T, false, false); }     \
-    } while (0)
-    if (bf16) Z1_DEC_T(uint16_t);
-    else Z1_DEC_T(float);
-#undef Z1_DEC_T
-#undef Z1_DEC
+    const dim3 grid((uint32_t)((n + kTile - 1) / kTile));
+    if (bf16) {
+        uint16_t* h = static_cast<uint16_t*>(x);
+        if (v) decode_kernel<uint16_t, true><<<grid, kThreads, 0, s>>>(codes, words, n, h);
+        else decode_kernel<uint16_t, false><<<grid, kThreads, 0, s>>>(codes, words, n, h);
+    } else {
+        float* f = static_cast<float*>(x);
+        if (v) decode_kernel<float, true><<<grid, kThreads, 0, s>>>(codes, words, n, f);
+        else decode_kernel<float, false><<<grid, kThreads, 0, s>>>(codes, words, n, f);
+    }
     return hipGetLastError();
 }
 
