@@ -307,6 +307,23 @@ def test_product_of_nan_and_extreme_scales(env):
         assert np.isnan(got[bad]).all() and np.array_equal(got[~bad], widen(bf16_bits(want)))
 
 
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_product_at_the_ends_of_the_range(env, m):
+    """Elements down to 2^-127 (fp32: bf16 holds them; 2^-136 counts as zero there), results below binary32's normal ones,
+    and elements beyond 2^128 (fp32: infinite)."""
+    n, k = 40, 128
+    one, least, most = 0x38, 0x01, 0x7E
+    for sa, sb, code, f32_zero, f32_inf in ((0, 127, one, 0, 0), (1, 110, one, 0, 0), (100, 20, one, 0, 0), (1, 127, least, 1, 0),
+                                            (0, 254, most, 0, 1), (1, 1, most, 0, 0)):
+        a = Mat(env, m, k).put(np.full((m, k), code, np.uint8), np.full((m, 1), sa, np.uint8))
+        b = Mat(env, n, k).put(np.full((n, k), most if code == most else one, np.uint8), np.full((n, 1), sb, np.uint8))
+        want = np.float32(k * ref.E4M3[code] * 2.0 ** (sa - 127) * ref.E4M3[most if code == most else one] * 2.0 ** (sb - 127))
+        got = product(env, a, b, True)
+        assert (got == (0.0 if f32_zero else np.inf if f32_inf else want)).all(), (sa, sb, got[0, 0], want)
+        got = product(env, a, b, False)
+        assert (got == widen(bf16_bits(np.array([want])))[0]).all(), (sa, sb, got[0, 0], want)
+
+
 def test_rows_past_the_end_do_not_matter(env):
     """What lies behind the operands (guards of NaN codes) does not reach d."""
     for m, n, k in ((1, 3, 128), (130, 131, 384), (17, 250, 200)):
