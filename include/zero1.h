@@ -102,9 +102,9 @@ typedef enum zero1_status {
 
 /* m and v are stored in 8 bits: each buffer is one of zero1_state8_bytes(numel)
  * bytes, 16-byte aligned (the layout and the rounding: zero1_state8_encode); zero
- * bytes before the first step.  Exclusive with ZERO1_MV_BF16.  A step takes 2W + 18
- * bytes a parameter of a W = 1..4 step's 2W + 30 with fp32 moments, and the state is
- * 6 bytes of 12. */
+ * bytes before the first step.  Exclusive with ZERO1_MV_BF16.  A step that reads the
+ * slices twice moves 4W + 14 bytes a parameter (fp32 moments: 4W + 26), one that keeps
+ * g 2W + 22 (2W + 34); master, m and v take 6 bytes a parameter (12). */
 #define ZERO1_MV_8BIT      0x2000u
 
 /* Compatibility variants (not the pages' step; off by default):
