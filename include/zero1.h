@@ -566,8 +566,8 @@ typedef struct zero1_f8_matrix {
  *   of a or b (code times scale) counts as zero below 2^-133 and as infinite from 2^128
  *   on.  Without columns: zeros.  d has at most 2^21 blocks of 128 x 128.  ws: zero1_f8_product_workspace_bytes
  *   bytes (0 too for arguments that the product rejects), 256-byte aligned (NULL where
- *   that is 0); what it holds before the call does not matter.  The same operands give the
- *   same bits.
+ *   that is 0); what it holds before the call does not matter, and calls that may overlap
+ *   (streams, captured graphs) take one each.  The same operands give the same bits.
  * Written buffers must not overlap any other of the call. */
 zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int64_t ld, const zero1_f8_matrix* q,
                                const zero1_f8_matrix* qt, uint32_t flags, void* stream);

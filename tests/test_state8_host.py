@@ -38,6 +38,8 @@ def test_conversions_refuse():
         assert "overlap" in _einval(lambda: f(1000, x, x + 3984, 0))
         assert "overlap" in _einval(lambda: f(1000, x + 1000, x, 1))
         assert "unknown flag" in _einval(lambda: f(10, x, s, 0, 0x1000))
+        assert "do not apply" in _einval(lambda: f(10, x, s, 0, z.MV_8BIT))
+        assert "do not apply" in _einval(lambda: f(10, x, s, 0, z.STORE_G))
 
 
 def _piece(n, off, at, m=None, v=None):

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libzero1.so")
 SOURCES = [os.path.join(HERE, "csrc", "api.cpp"), os.path.join(HERE, "csrc", "kernels.hip"),
            os.path.join(HERE, "csrc", "state8.hip"), os.path.join(HERE, "csrc", "f8_api.cpp"),
-           os.path.join(HERE, "csrc", "f8_quantize.hip"), os.path.join(HERE, "csrc", "f8_product.hip"), os.path.join(HERE, "csrc", "static_ws.hip"), os.path.join(HERE, "csrc", "muon_api.cpp"),
+           os.path.join(HERE, "csrc", "f8_quantize.hip"), os.path.join(HERE, "csrc", "f8_product.hip"),
+           os.path.join(HERE, "csrc", "static_ws.hip"), os.path.join(HERE, "csrc", "muon_api.cpp"),
            os.path.join(HERE, "csrc", "muon.hip"), os.path.join(HERE, "csrc", "newton_schulz.hip"),
            os.path.join(HERE, "csrc", "ns_thin.hip")]
 # bandwidth calibration kernels used by bench.py (not part of the step library)

@@ -761,7 +761,7 @@ size_t zero1_state8_bytes(int64_t n) { return state8_size(n); }
 static zero1_status state8_common(const char* fn, const void* x, int64_t n, const void* state, int which, uint32_t flags,
                                   DevInfo& d)
 {
-    if (zero1_status fs = check_flags(flags, kAllFlags, fn)) return fs;
+    if (zero1_status fs = check_flags(flags, ZERO1_MV_BF16, fn)) return fs;
     if (n < 0 || n > (int64_t)1 << 34) return fail(ZERO1_EINVAL, "%s: n=%lld must be in [0, 2^34]", fn, (long long)n);
     if (which != ZERO1_STATE_M && which != ZERO1_STATE_V)
         return fail(ZERO1_EINVAL, "%s: which=%d must be ZERO1_STATE_M or ZERO1_STATE_V", fn, which);

