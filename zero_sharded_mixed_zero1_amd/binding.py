@@ -487,8 +487,11 @@ def state8_decode(state, n: int, x, which: int, flags: int = 0, stream=None):
 def f8_matrix(rows: int, cols: int, codes, scales, block_rows: int = 1, flags: int = 0, ld: int = 0,
               ld_scales: int = 0) -> F8Matrix:
     """A matrix in 8-bit floating point (zero1_f8_matrix); buffers are tensors or
-    device addresses, strides of 0 the least there are.  flags: E5M2."""
-    return F8Matrix(rows, cols, ld, ld_scales, _addr(codes), _addr(scales), block_rows, flags)
+    device addresses, strides of 0 the least there are.  flags: E5M2.  Tensors
+    live as long as the matrix does."""
+    out = F8Matrix(rows, cols, ld, ld_scales, _addr(codes), _addr(scales), block_rows, flags)
+    out.buffers = (codes, scales)
+    return out
 
 
 def f8_quantize(src, rows: int, cols: int, q: F8Matrix = None, qt: F8Matrix = None, ld: int = 0, flags: int = 0,

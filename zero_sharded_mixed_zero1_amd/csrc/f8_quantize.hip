@@ -9,8 +9,13 @@
 // the way (magnitudes are compared as 16-bit numbers, codes made from pairs).
 //
 // HBM-bound: 2 or 4 bytes an element in, one out for each output.  8192 x 4096 bf16 into
-// both 31.5 us (4.3 TB/s; without the pairs, an element at a time, 48), 11008 x 4096 fp32
-// with blocks of 128 x 128 into both 54.5 (5.0 TB/s).
+// both 32 us (4.2 TB/s; without the pairs, an element at a time, 48), 11008 x 4096 fp32
+// with blocks of 128 x 128 into both 54.2 (5.0 TB/s).  A forward pass multiplies the codes
+// next and the backward pass reads the transpose much later, so the transpose is stored
+// non-temporally and the codes are not: into the transpose alone 19.2 us (23.8), and the
+// weight's and the input's conversion with the product behind them, 2048 x 4096 x 4096,
+// 57.9 (59.2).  Both so: 8192 x 4096 27.0 us alone, but the product then reads from
+// memory (512 x 4096 x 4096 38.5 all together, 35.8 without either, 35.4 as it is).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -273,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const typename F::El
             const int64_t out = (int64_t)cb * kF8Block + line;
             u32x4 v = *reinterpret_cast<const u32x4*>(turned + line * kF8Block + 16 * (seg ^ (key >> 1)));
             if (key & 1) v = u32x4{v[2], v[3], v[0], v[1]};
-            if (out < cols) *reinterpret_cast<u32x4*>(qt.codes + out * qt.ld + (int64_t)rb * kF8Block + 16 * seg) = v;
+            if (out < cols) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(qt.codes + out * qt.ld + (int64_t)rb * kF8Block + 16 * seg));
         }
     }
 }
