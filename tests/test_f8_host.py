@@ -2,6 +2,8 @@
 compare with against its own definition."""
 from __future__ import annotations
 
+import weakref
+
 import numpy as np
 import pytest
 
@@ -96,3 +98,20 @@ def test_reference_rounds_within_half_a_step():
 def test_reference_scales_at_the_borders():
     x = np.array([[448.0], [449.0], [np.nextafter(np.float32(448), np.float32(500))], [0.0], [2.0 ** -149], [1.75], [224.0], [224.1]], np.float32)
     assert ref.exponents(x, 1, False)[:, 0].tolist() == [127, 128, 128, 1, 1, 119, 126, 127]
+
+
+class _Tensor:   # what the binding asks of a tensor
+    is_cuda = True
+
+    def data_ptr(self):
+        return FAKE
+
+
+def test_a_matrix_keeps_its_tensors():
+    codes, scales = _Tensor(), _Tensor()
+    alive = weakref.ref(codes)
+    m = z.f8_matrix(128, 128, codes, scales)
+    del codes, scales
+    assert alive() is not None and m.codes == FAKE
+    del m
+    assert alive() is None
