@@ -1,0 +1,87 @@
+// The 8-bit matrices' entry points at the edges of what zero1.h allows, checked
+// without a GPU: f8_api.cpp linked with the stand-ins below for the HIP runtime and
+// the kernels' launchers, which count their calls.
+#include <hip/hip_runtime.h>
+
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <string>
+
+#include "../../include/zero1.h"
+#include "../../zero_sharded_mixed_zero1_amd/csrc/f8.h"
+
+using namespace z1;
+
+#define REQUIRE(cond)                                                                                    \
+    do {                                                                                                 \
+        if (!(cond)) {                                                                                   \
+            std::printf("%s:%d: %s (%s)\n", __FILE__, __LINE__, #cond, g_error.c_str());                 \
+            std::exit(1);                                                                                \
+        }                                                                                                \
+    } while (0)
+
+static std::string g_error;
+static int g_quantized, g_multiplied;
+
+// ------------------------------------------------------------------ stand-ins
+extern "C" {
+hipError_t hipGetDevice(int* d) { *d = 0; return hipSuccess; }
+hipError_t hipGetDeviceProperties(hipDeviceProp_t* p, int)
+{
+    std::memset(p, 0, sizeof *p);
+    std::strcpy(p->gcnArchName, "gfx950:sramecc+:xnack-");
+    p->multiProcessorCount = 256;
+    return hipSuccess;
+}
+const char* hipGetErrorString(hipError_t) { return "error"; }
+hipError_t hipGetLastError(void) { return hipSuccess; }
+hipError_t hipStreamIsCapturing(hipStream_t, hipStreamCaptureStatus*) { return hipSuccess; }
+hipError_t hipStreamSynchronize(hipStream_t) { return hipSuccess; }
+}
+
+namespace z1 {
+int set_error(int st, const char* msg) { g_error = msg; return st; }
+hipError_t launch_f8_quantize(const void*, bool, int64_t, int64_t, int64_t, const F8&, const F8&, hipStream_t)
+{
+    ++g_quantized;
+    return hipSuccess;
+}
+hipError_t launch_f8_product(const F8Product&, hipStream_t)
+{
+    ++g_multiplied;
+    return hipSuccess;
+}
+}  // namespace z1
+
+static uint8_t* at(int k) { return reinterpret_cast<uint8_t*>((uintptr_t)1 << 44 | (uintptr_t)k << 40); }
+
+static zero1_f8_matrix matrix(int64_t rows, int64_t cols, int k)
+{
+    return zero1_f8_matrix{rows, cols, 0, 0, at(2 * k), at(2 * k + 1), 1, 0};
+}
+
+// A product without rows is an empty call: no workspace, nothing launched, whatever the
+// other sizes.
+static void empty_products()
+{
+    for (int64_t rows : {1, 7, 32, 33, 64, 300, 5000})
+        for (int64_t k : {0, 1, 128, 8192, 1 << 23})
+            for (uint32_t flags : {0u, (uint32_t)ZERO1_F32}) {
+                const zero1_f8_matrix some = matrix(rows, k, 0), none = matrix(0, k, 1);
+                g_multiplied = 0;
+                REQUIRE(zero1_f8_product_workspace_bytes(&some, &none, flags) == 0);
+                REQUIRE(zero1_f8_product_workspace_bytes(&none, &some, flags) == 0);
+                REQUIRE(zero1_f8_product(&some, &none, at(8), 0, flags, nullptr, 0, nullptr) == ZERO1_OK);
+                REQUIRE(zero1_f8_product(&none, &some, at(8), 0, flags, nullptr, 0, nullptr) == ZERO1_OK);
+                REQUIRE(zero1_f8_product(&none, &none, nullptr, 0, flags, nullptr, 0, nullptr) == ZERO1_OK);
+                REQUIRE(g_multiplied == 0);
+            }
+}
+
+int main()
+{
+    empty_products();
+    std::printf("all ok\n");
+    return 0;
+}

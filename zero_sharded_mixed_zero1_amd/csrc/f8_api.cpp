@@ -229,7 +229,7 @@ static void choose(F8Product& p)
     p.sums = nullptr;
     p.ld_sums = up(n, 4);
     p.part_elems = m * p.ld_sums;
-    if (m <= 32) {
+    if (m <= 32 || n == 0) {   // (without rows of B nothing is launched, and no workspace asked for)
         p.kind = kF8Thin;
         return;
     }
