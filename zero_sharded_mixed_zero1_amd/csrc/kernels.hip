@@ -623,14 +623,24 @@ struct Span {
 // that four waves read and write (with the non-temporal hint 202 M parameters at W = 1
 // take 6 % longer), and moments of up to 100 M parameters stay in the MALL where
 // nothing comes between two steps.
-typedef uint32_t u32x2w __attribute__((ext_vector_type(2), aligned(4)));
 
 // A tile of a plan's piece or of a flat shard, n of its kTile elements present.  Its
 // quads are loaded and stored whole at any alignment of their elements (gfx950's
 // vector accesses need no more); one that the end cuts, element by element.  What is
-// not there counts as zero.
+// not there counts as zero.  The accesses of such quads are functions of their own:
+// ld_nt and its like, given these types, would deduce the plain vector's alignment.
 typedef f32x4 f32x4e __attribute__((aligned(4)));
 typedef u32x2 u32x2e __attribute__((aligned(2)));
+typedef __attribute__((address_space(1))) f32x4e* f32x4e_ptr;
+typedef __attribute__((address_space(1))) u32x2e* u32x2e_ptr;
+typedef const __attribute__((address_space(1))) f32x4e* f32x4e_cptr;
+typedef const __attribute__((address_space(1))) u32x2e* u32x2e_cptr;
+
+__device__ __forceinline__ f32x4 quad_ld(const float* p) { return *(f32x4e_cptr)gbl(p); }
+__device__ __forceinline__ f32x4 quad_ld_nt(const float* p) { return __builtin_nontemporal_load((f32x4e_cptr)gbl(p)); }
+__device__ __forceinline__ u32x2 quad_ld_nt(const uint16_t* p) { return __builtin_nontemporal_load((u32x2e_cptr)gbl(p)); }
+__device__ __forceinline__ void quad_st_nt(float* p, f32x4 v) { __builtin_nontemporal_store((f32x4e)v, (f32x4e_ptr)gbl(p)); }
+__device__ __forceinline__ void quad_st_nt(uint16_t* p, u32x2 v) { __builtin_nontemporal_store((u32x2e)v, (u32x2e_ptr)gbl(p)); }
 
 struct Bytes8 {   // as loaded
     float p[8];
@@ -677,7 +687,7 @@ __device__ __forceinline__ void load_bytes(const Span& sp, int64_t si, int n, By
         if (c == 4) {
             t.m[h] = *gbl(reinterpret_cast<const uint32_t*>(m));
             t.v[h] = *gbl(reinterpret_cast<const uint32_t*>(v));
-            q = ld_nt(reinterpret_cast<const f32x4e*>(p));
+            q = quad_ld_nt(p);
         } else {
 #pragma unroll
             for (int j = 0; j < 3; ++j)
@@ -707,10 +717,10 @@ __device__ __forceinline__ void gradient8(const float* g, const Reduce& r, int64
         const int64_t at = e + a + 256 * h;
         if (c == 4) {
             if constexpr (FEW == 0) {
-                q[h] = ld_g(reinterpret_cast<const f32x4e*>(g + at));
+                q[h] = quad_ld(g + at);
             } else {
 #pragma unroll
-                for (int w = 0; w < N; ++w) x[h][w] = ld_nt(reinterpret_cast<const u32x2e*>(r.gp.p[w] + at));
+                for (int w = 0; w < N; ++w) x[h][w] = quad_ld_nt(r.gp.p[w] + at);
             }
         } else {
 #pragma unroll
@@ -749,7 +759,7 @@ __device__ __forceinline__ void gradient8(const float* g, const Reduce& r, int64
                         if (w0 + k >= r.W) continue;
                         const uint16_t* p = r.gp.p[w0 + k] + at;
                         if (c == 4) {
-                            y[h][k] = ld_nt(reinterpret_cast<const u32x2e*>(p));
+                            y[h][k] = quad_ld_nt(p);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 3; ++j)
@@ -800,8 +810,8 @@ __device__ __forceinline__ void update_bytes(const Span& sp, int64_t si, int n, 
         if (there == 4) {
             *gbl(reinterpret_cast<uint32_t*>(mp)) = cm;
             *gbl(reinterpret_cast<uint32_t*>(vp)) = cr;
-            st_nt(reinterpret_cast<f32x4e*>(pp), f32x4e{p[0], p[1], p[2], p[3]});
-            st_nt(reinterpret_cast<u32x2e*>(bp), u32x2e{lo, hi});
+            quad_st_nt(pp, f32x4{p[0], p[1], p[2], p[3]});
+            quad_st_nt(bp, u32x2{lo, hi});
         } else {
 #pragma unroll
             for (int j = 0; j < 3; ++j)
