@@ -3,13 +3,19 @@
 //
 // Into bf16: v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 x 64 codes by 32 x 64 and
 // takes a scale for each operand's row, so two instructions are one block of 128,
-// scales included.  It adds groups of eight products after aligning them to the
-// group's largest, and what lies below 2^-13 of that is dropped (found by adding
-// powers of two; beyond the groups sums keep fp32's 24 bits): 1e-5 to 6e-5 of the
-// result on random operands, a hundredth of bf16's own rounding.
-// Into fp32 that would be the largest error there is, so codes are widened to bf16
+// scales included.  It adds groups of eight neighbouring products, each cut toward
+// zero to a multiple of 2^(E - 13), E the largest sum of two codes' exponents in the
+// group (one below the smallest normal code counts as that; zeros do not count; found by
+// adding powers of two and products of 15 by 15; beyond the groups sums keep
+// fp32's 24 bits).  On random operands that takes 1e-5 to 8e-5 of the result, a
+// hundredth of bf16's own rounding; at worst 7 * 2^-13 of each group's largest product,
+// whatever the result is, so a sum that cancels may lose most of what is left.  Taken
+// all the same, because the way without it costs: 8192 x 11008 x 4096 takes 610 us by
+// the bf16 instructions and 310 so, 2048 x 4096 x 4096 63 and 39, 1 x 1024 x 8192 8.6
+// and 6.1, 1 x 11008 x 4096 12.4 and 11.5.
+// Into fp32 the cuts would be the largest error there is, so codes are widened to bf16
 // with their scales (each exactly) and multiplied as bf16, which adds to
-// 24 bits (7e-8), at half the rate.
+// 24 bits (7e-8), at half the rate: the way for sums that cancel.
 //
 // The operands are swapped (B's rows first), so that a lane holds four neighbouring
 // columns of D: acc[x][y][r] = D[32 x + (lane & 31)][32 y + 8 (r >> 2) + 4 (lane >>
