@@ -573,7 +573,8 @@ typedef struct zero1_f8_matrix {
  *   bytes (0 too for arguments that the product rejects), 256-byte aligned (NULL where
  *   that is 0); what it holds before the call does not matter, and calls that may overlap
  *   (streams, captured graphs) take one each.  The same operands give the same bits.
- * Written buffers must not overlap any other of the call. */
+ * Written buffers, what is used of the workspace among them, must not overlap any other of
+ * the call. */
 zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int64_t ld, const zero1_f8_matrix* q,
                                const zero1_f8_matrix* qt, uint32_t flags, void* stream);
 size_t zero1_f8_product_workspace_bytes(const zero1_f8_matrix* a, const zero1_f8_matrix* b, uint32_t flags);

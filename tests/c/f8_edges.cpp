@@ -79,9 +79,37 @@ static void empty_products()
             }
 }
 
+// The workspace is written: it may not lie over d or what is read, and need not keep
+// clear of anything where it is not used.
+static void workspaces()
+{
+    const zero1_f8_matrix a = matrix(300, 8000, 0), b = matrix(300, 8000, 1);
+    const size_t need = zero1_f8_product_workspace_bytes(&a, &b, 0);
+    REQUIRE(need > 0 && need % 4 == 0);
+    const int64_t ld = 8064, lds = 64;   // (of both: bytes of a row of codes, of scales)
+    g_multiplied = 0;
+    const struct { uint8_t* p; size_t bytes; const char* what; } others[] = {
+        {at(8), 2 * 300 * 300, "d"}, {a.codes, (size_t)(300 * ld), "a.codes"}, {a.scales, (size_t)(300 * lds), "a.scales"},
+        {b.codes, (size_t)(300 * ld), "b.codes"}, {b.scales, (size_t)(300 * lds), "b.scales"}};
+    for (const auto& o : others) {
+        for (uint8_t* ws : {o.p, o.p + 256, o.p + (o.bytes - 256) / 256 * 256, o.p - (need - 1) / 256 * 256}) {
+            REQUIRE(zero1_f8_product(&a, &b, at(8), 0, 0, ws, need, nullptr) == ZERO1_EINVAL);
+            REQUIRE(g_error.find("overlap") != std::string::npos && g_error.find("workspace") != std::string::npos &&
+                    g_error.find(o.what) != std::string::npos);
+        }
+        // just beside it; and a longer buffer, of which the call takes only what it needs
+        REQUIRE(zero1_f8_product(&a, &b, at(8), 0, 0, o.p + (o.bytes + 255) / 256 * 256, need, nullptr) == ZERO1_OK);
+        REQUIRE(zero1_f8_product(&a, &b, at(8), 0, 0, o.p - (need + 255) / 256 * 256, need + 4096, nullptr) == ZERO1_OK);
+    }
+    REQUIRE(g_multiplied == 10);
+    const zero1_f8_matrix few = matrix(7, 8000, 0);   // takes none
+    REQUIRE(zero1_f8_product(&few, &b, at(8), 0, 0, at(8), 4096, nullptr) == ZERO1_OK && g_multiplied == 11);
+}
+
 int main()
 {
     empty_products();
+    workspaces();
     std::printf("all ok\n");
     return 0;
 }

@@ -323,6 +323,8 @@ zero1_status zero1_f8_product(const zero1_f8_matrix* a, const zero1_f8_matrix* b
         if (!ws) return fail(ZERO1_EWORKSPACE, "workspace is NULL (need %zu bytes)", need);
         if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(ZERO1_EWORKSPACE, "workspace must be 256-byte aligned");
         if (ws_bytes < need) return fail(ZERO1_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+        const Range w[6] = {range_of(ws, 1, 0, (int64_t)need, "workspace"), r[0], r[1], r[2], r[3], r[4]};
+        if ((st = check_disjoint(fn, w, 6, 1))) return st;
         p.sums = static_cast<float*>(ws);
     }
     p.vec = reinterpret_cast<uintptr_t>(d) % 16 == 0 && ldd * eb % 16 == 0;
