@@ -106,10 +106,45 @@ static void workspaces()
     REQUIRE(zero1_f8_product(&few, &b, at(8), 0, 0, at(8), 4096, nullptr) == ZERO1_OK && g_multiplied == 11);
 }
 
+// Strides and rows within their limits whose product passes 64 bits, or the end of the
+// address space: no memory is that large, and the index arithmetic would wrap.
+static void beyond_any_memory()
+{
+    const int64_t wide = (int64_t)1 << 40;
+    g_quantized = g_multiplied = 0;
+    auto refused = [](zero1_status st, const char* what) {
+        return st == ZERO1_EINVAL && g_error.find("address space") != std::string::npos && g_error.find(what) != std::string::npos;
+    };
+    for (uint32_t flags : {0u, (uint32_t)ZERO1_F32}) {
+        for (int64_t rows : {(int64_t)1 << 23, ((int64_t)1 << 24) + 1, ((int64_t)1 << 24) + 3, (int64_t)1 << 30}) {
+            const zero1_f8_matrix q = matrix(rows, 100, 0);
+            REQUIRE(refused(zero1_f8_quantize(at(8), rows, 100, wide, &q, nullptr, flags, nullptr), "src"));
+        }
+        // rows * ld * element wraps to a few bytes behind 2^64
+        const zero1_f8_matrix q = matrix(((int64_t)1 << 26) + 1, 100, 0), qt = matrix(100, ((int64_t)1 << 23) - 5, 1);
+        REQUIRE(refused(zero1_f8_quantize(at(8), q.rows, 100, (int64_t)1 << (flags ? 36 : 37), &q, nullptr, flags, nullptr), "src"));
+        REQUIRE(refused(zero1_f8_quantize(at(8), qt.cols, 100, wide, nullptr, &qt, flags, nullptr), "src"));
+        for (int64_t rows : {(int64_t)1 << 23, ((int64_t)1 << 24) + 1, (int64_t)1 << 28}) {
+            const zero1_f8_matrix a = matrix(rows, 256, 0), b = matrix(5, 256, 1);
+            REQUIRE(refused(zero1_f8_product(&a, &b, at(8), wide, flags, nullptr, 0, nullptr), " d "));
+        }
+    }
+    zero1_f8_matrix a = matrix(1 << 20, 256, 0), b = matrix(5, 256, 1);
+    a.codes = reinterpret_cast<uint8_t*>(~(uintptr_t)0 << 20);
+    REQUIRE(refused(zero1_f8_product(&a, &b, at(8), 0, 0, nullptr, 0, nullptr), "a.codes"));
+    REQUIRE(refused(zero1_f8_quantize(at(8), a.rows, a.cols, 0, &a, nullptr, 0, nullptr), "q.codes"));
+    REQUIRE(g_quantized == 0 && g_multiplied == 0);
+    // the widest rows that fit are taken
+    a = matrix(1000, 256, 0);
+    REQUIRE(zero1_f8_quantize(at(8), 1000, 256, wide, &a, nullptr, ZERO1_F32, nullptr) == ZERO1_OK && g_quantized == 1);
+    REQUIRE(zero1_f8_product(&a, &b, at(8), wide, ZERO1_F32, nullptr, 0, nullptr) == ZERO1_OK && g_multiplied == 1);
+}
+
 int main()
 {
     empty_products();
     workspaces();
+    beyond_any_memory();
     std::printf("all ok\n");
     return 0;
 }

@@ -132,12 +132,15 @@ struct Range {
     const char* what;
 };
 
-// The bytes from a matrix's first element to its last; empty where it has none.
+// The bytes from a matrix's first element to its last; empty where it has none.  Where
+// the last lies past the end of the address space (2^63: the kernels' offsets are signed),
+// hi is the largest address.
 Range range_of(const void* p, int64_t rows, int64_t ld_bytes, int64_t row_bytes, const char* what)
 {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
     if (!p || rows <= 0 || row_bytes <= 0) return Range{lo, lo, what};
-    return Range{lo, lo + (uintptr_t)(rows - 1) * (uintptr_t)ld_bytes + (uintptr_t)row_bytes, what};
+    const unsigned __int128 hi = lo + (unsigned __int128)(rows - 1) * (uint64_t)ld_bytes + (uint64_t)row_bytes;
+    return Range{lo, hi > (uint64_t)1 << 63 ? UINTPTR_MAX : (uintptr_t)hi, what};
 }
 
 Range codes_of(const F8& m, const char* what) { return range_of(m.codes, m.rows, m.ld, up(m.cols, kF8Block), what); }
@@ -146,9 +149,12 @@ Range scales_of(const F8& m, const char* what)
     return range_of(m.scales, m.rows > 0 ? ((m.rows - 1) >> m.shift) + 1 : 0, m.ld_scales, blocks(m.cols), what);
 }
 
-// None of the first n_out ranges (written) overlaps another.
+// Every range lies in the address space; none of the first n_out (written) overlaps another.
 zero1_status check_disjoint(const char* fn, const Range* r, int n, int n_out)
 {
+    for (int i = 0; i < n; ++i)
+        if (r[i].lo < r[i].hi && r[i].hi == UINTPTR_MAX)
+            return fail(ZERO1_EINVAL, "%s: %s reaches past the end of the address space", fn, r[i].what);
     for (int i = 0; i < n_out; ++i)
         for (int j = i + 1; j < n; ++j)
             if (r[i].lo < r[i].hi && r[j].lo < r[j].hi && r[i].lo < r[j].hi && r[j].lo < r[i].hi)
