@@ -571,7 +571,9 @@ typedef struct zero1_f8_matrix {
  *   of a or b (code times scale) counts as zero below 2^-133 and as infinite from 2^128
  *   on.  Without columns: zeros.  d has at most 2^21 blocks of 128 x 128.  ws: zero1_f8_product_workspace_bytes
  *   bytes (0 too for arguments that the product rejects), 256-byte aligned (NULL where
- *   that is 0); what it holds before the call does not matter, and calls that may overlap
+ *   that is 0).  The size goes by the shape and does not grow with it (b 4096 x 4096,
+ *   into bf16: 8192 rows of a need none, 64 need 4 MiB), so a buffer for several shapes is
+ *   the largest of what each asks for; what it holds before the call does not matter, and calls that may overlap
  *   (streams, captured graphs) take one each.  The same operands give the same bits.
  * Written buffers, what is used of the workspace among them, must not overlap any other of
  * the call. */

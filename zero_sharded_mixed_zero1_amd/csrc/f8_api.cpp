@@ -213,7 +213,7 @@ zero1_status zero1_f8_quantize(const void* src, int64_t rows, int64_t cols, int6
 // choice is that of the least measured time in all but a few of them, where it is
 // within 15 % of that (1024 x 4096 x 4096: tiles of 64 27.7 us, 128 26.3, 256 in bands of
 // 64 rows 22.8; 512 x 4096 x 4096: 15.9, 25.0, 20.3; 2048 x 4096 x 4096: 52, 34.7, 34.9;
-// 8192 x 11008 x 4096: 607, 407, 326).
+// 8192 x 11008 x 4096: 607, 407, 326; one session's, another's differ by up to 5 %).
 struct TileCost {
     int side;
     double one, two, fixed;

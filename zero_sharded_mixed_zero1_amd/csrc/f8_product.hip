@@ -21,8 +21,8 @@
 // columns of D: acc[x][y][r] = D[32 x + (lane & 31)][32 y + 8 (r >> 2) + 4 (lane >>
 // 5) + (r & 3)].
 //
-// What bounds it: at 8192 x 11008 x 4096 (318 us, 2.3 PFLOP/s) the clock that power
-// leaves (1.8 GHz, the matrix cores busy 63 % of it; operands that lie in L2 gain 5 to
+// What bounds it: at 8192 x 11008 x 4096 (321 us among other passes, 2.3 PFLOP/s; by
+// itself under the profiler 332) the clock that power leaves (1.8 GHz, the matrix cores busy 63 % of it; operands that lie in L2 gain 5 to
 // 10 %); between 512 and 2048 rows whole rounds of the chip and the first stages' latency
 // (2048 x 4096 x 4096 34.9 us, 2.0 PFLOP/s; into fp32 60, 1.1); up to 32 rows memory (1 x
 // 11008 x 4096 10.2 us, 4.4 TB/s).

@@ -968,8 +968,11 @@ __global__ __launch_bounds__(kThreads) void adamw_mta_kernel(const float* __rest
 // chunks.  A workgroup takes one tile where the grid has as many: each tile moves half
 // of what it does with fp32 moments, so more of them have to be under way (a step of
 // 200 M parameters at W = 1 takes 655 us so, 703 in a persistent grid of 32 workgroups a
-// CU and 742 of 8), and the slices of W = 1 to 4 are loaded by code of their own (635;
-// the kernel has 70 registers then and not 88).
+// CU and 742 of 8), and the slices of W = 1 to 4 are loaded by code of their own, all
+// under way together: the update alone takes 92.2 us at 30 M parameters and W = 2 (100.3
+// by the loop over any number), 10.6 at 1.55 M and W = 3 (11.3), 570 at 202 M and W = 1
+// (578), the same at 2^18 and at 202 M and W = 4; 75 to 79 registers (over a plan 75 by
+// the loop, flat 84).
 //
 // HBM-bound: 16 bytes a parameter at W = 1 (5.8 TB/s), 18 with g from the workspace
 // (the 117 M of a step at W = 8: 6.1).
